@@ -9,8 +9,8 @@
  * collective.
  *
  * Conventions shared by every call
- *   - Every tensor is a DEVICE pointer, row-major and contiguous, owned by the
- *     caller.  Arrays of per-rank pointers (x_chunks, chunks) are HOST arrays
+ *   - Every tensor is a DEVICE pointer, row-major and contiguous (unless the
+ *     call takes a row stride), owned by the caller.  Arrays of per-rank pointers (x_chunks, chunks) are HOST arrays
  *     of device pointers.  Every device pointer must address memory of the
  *     CUDA device current on the calling thread, and `stream` must belong to
  *     that device: the library launches there and does not look up where a
@@ -37,7 +37,8 @@
  *     bit-identical to whole tiles.
  *   - Pointers must be 16-byte aligned and row pitches multiples of 16 bytes
  *     (the tensor-memory-accelerator copies need it); otherwise
- *     MC2_ERR_UNSUPPORTED.
+ *     MC2_ERR_UNSUPPORTED.  The operators around the linears (from
+ *     mc2_add_rms_norm on) take other layouts too, as each says.
  */
 #ifndef MC2_GB300_H
 #define MC2_GB300_H
@@ -297,6 +298,151 @@ int mc2_alltoall_quant_mm_no_alloc(const void *const *chunks, int rank_size, int
                                    void *out, void *alltoall_out, int8_t *q_out, float *x1_scale_out,
                                    int32_t *acc_out, void *stream);
 
+/*
+ * Operators around the fused linears.  The rows of their matrices may be
+ * strided (ld*: elements from one row to the next, at least the row's length,
+ * the same in every row), so a slice of a wider tensor is passed as it is.
+ * They take any sizes from 1 and any alignment that suits the element type;
+ * sizes and layouts that the fast kernels cannot take run on a plain kernel,
+ * which each call's comment names.
+ */
+
+/*
+ * Residual RMS norm with an optional 8-bit output, the step before a fused
+ * linear (the codes and scales are what mc2_alltoall_quant_mm takes in
+ * x1_quant_mode 3, or mc2_quant_all_reduce in its two layouts).
+ *
+ *   s[t, j]  = x[t, j] + residual[t, j]          (x alone without a residual)
+ *   rstd[t]  = 1 / sqrt(mean_j s[t, j]^2 + eps)
+ *   y[t, j]  = s[t, j] * rstd[t] * weight[j]
+ *   out = y and residual_out = s, each rounded once (nearest-even) to dtype
+ *
+ *   The codes are made from the unrounded y, by quant_mode:
+ *     MC2_QUANT_NONE               none: q_out and scale_out are NULL
+ *     MC2_QUANT_PERTOKEN_DYNAMIC   scale[t] = max_j |y[t, j]| / Q, fp32 (m)
+ *     MC2_QUANT_PERGROUP           the same for each 128 columns, fp32 (m, ceil(h / 128))
+ *     MC2_QUANT_MX                 2^(floor(log2 max|y|) - E) for each 32 columns, at least
+ *                                  2^-127, as e8m0 codes (m, ceil(h / 32)); fp8 codes only
+ *   with Q = 127, 448, 57344 and E = -, 8, 15 for MC2_I8, MC2_F8E4M3, MC2_F8E5M2;
+ *   q = y / scale, rounded to nearest-even and saturated at Q.  Where the scale is
+ *   not above zero (a zero row, a scale that underflows, a NaN) the codes are 0; a
+ *   row or group that holds a NaN has a NaN scale.
+ *
+ *   All arithmetic is fp32 (the mean of squares must be within its range).
+ *
+ *   x             (m, h) of dtype, rows ldx apart
+ *   residual      NULL or (m, h), rows ldr apart
+ *   weight        (h) of weight_dtype: dtype or MC2_F32
+ *   m, h          1 <= m <= INT32_MAX, 1 <= h <= 2^30
+ *   eps           finite, >= 0
+ *   dtype         MC2_F16, MC2_BF16 or MC2_F32
+ *   out           (m, h), rows ldo apart; may be NULL when there are codes; may be x or
+ *                 residual itself (same stride)
+ *   residual_out  NULL or (m, h), rows ldro apart (with a residual only); may be x or
+ *                 residual itself (same stride), not out
+ *   rstd_out      NULL or fp32 (m), what mc2_rms_norm_grad takes
+ *   q_out         (m, h) contiguous codes;  scale_out contiguous
+ *
+ * Returns MC2_OK or a negative mc2_status; nothing is launched on error.
+ */
+int mc2_add_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                     int weight_dtype, int64_t m, int64_t h, float eps, int dtype, void *out, int64_t ldo,
+                     void *residual_out, int64_t ldro, float *rstd_out, int quant_mode, int q_dtype, void *q_out,
+                     void *scale_out, void *stream);
+
+/*
+ * Gradient of the residual RMS norm (of its unquantised output).
+ *
+ *   xhat = x * rstd,  g = dy * weight,  c[t] = mean_j g[t, j] xhat[t, j]
+ *   dx[t, j] = rstd[t] (g[t, j] - xhat[t, j] c[t]) (+ dres[t, j])
+ *   dw[j]    = sum_t dy[t, j] xhat[t, j]
+ *
+ *   x is the tensor that was normalised: residual_out of the forward call (x
+ *   itself without a residual).  dx is the gradient of both the forward call's
+ *   x and its residual; dres is the gradient that arrives at residual_out.
+ *   Sums are fp32, in an order that only m and h set; dx and dw are
+ *   rounded once, dw to weight_dtype.
+ *
+ *   dy, x         (m, h) of dtype;  rstd fp32 (m);  weight (h) of weight_dtype
+ *   dres          NULL or (m, h)
+ *   dx            (m, h); may be dy, x or dres itself (same stride)
+ *   dw            NULL or (h) of weight_dtype
+ *   workspace     with dw: device scratch of at least the bytes the query returns,
+ *                 16-byte aligned, no initialisation; reusable by calls ordered on one stream
+ *
+ * Returns MC2_OK or a negative mc2_status; nothing is launched on error.
+ */
+int mc2_rms_norm_grad_workspace(int64_t m, int64_t h, size_t *bytes);
+int mc2_rms_norm_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *weight, int weight_dtype,
+                      const float *rstd, const void *dres, int64_t lddres, int64_t m, int64_t h, int dtype, void *dx,
+                      int64_t lddx, void *dw, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Activations of the fused-epilogue products. */
+typedef enum {
+    MC2_ACT_NONE = 0,
+    MC2_ACT_RELU = 1,      /* max(z, 0) */
+    MC2_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+    MC2_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    MC2_ACT_SILU = 4       /* z / (1 + e^-z) */
+} mc2_activation;
+
+/*
+ * Matrix product with bias, activation and residual in its epilogue.
+ *
+ *   z   = x @ w^T (+ bias)              (w_is_nk != 0; x @ w otherwise)
+ *   out = act(z) (+ residual),  preact = z
+ *
+ *   Sums are fp32; z is rounded once where it is stored, and out once (from
+ *   the unrounded z).
+ *
+ *   x         (m, k), rows ldx apart
+ *   w         (n, k) (the nn.Linear layout) or (k, n), rows ldw apart
+ *   m, n, k   1 to INT32_MAX
+ *   bias      NULL or (n);  residual NULL or (m, n), rows ldr apart
+ *   act       an mc2_activation
+ *   dtype     MC2_F16 or MC2_BF16 for every tensor
+ *   out       (m, n), rows ldo apart; may be residual itself (same stride)
+ *   preact    NULL or (m, n), rows ldp apart (what mc2_matmul_act_grad and
+ *             mc2_act_grad take)
+ *   Where a matrix is not 16-byte aligned or its stride is not a multiple of 8
+ *   elements, a plain kernel without tensor cores does the work.
+ *
+ * Returns MC2_OK or a negative mc2_status; nothing is launched on error.
+ */
+int mc2_matmul_bias_act(const void *x, int64_t ldx, const void *w, int64_t ldw, int w_is_nk, int64_t m, int64_t n,
+                        int64_t k, const void *bias, int act, const void *residual, int64_t ldr, int dtype, void *out,
+                        int64_t ldo, void *preact, int64_t ldp, void *stream);
+
+/*
+ * The backward product of a linear layer, with the derivative of the
+ * activation that made the layer's input in its epilogue.
+ *
+ *   dz = (dy @ w) * act'(z)             (w_is_nk != 0; dy @ w^T otherwise)
+ *
+ *   For h = act(z), y = h @ w^T this is the gradient of z; the weight's and
+ *   the bias's come from mc2_matmul_weight_grad(dy, h).
+ *
+ *   dy        (m, n), rows lddy apart
+ *   w         the forward layer's weight: (n, k) (w_is_nk != 0) or (k, n), rows ldw apart
+ *   z         (m, k), rows ldz apart;  dz (m, k), rows lddz apart; dz may be z itself
+ *             (same stride)
+ *   Other arguments, and the layouts that the plain kernel takes, as in mc2_matmul_bias_act.
+ *
+ * Returns MC2_OK or a negative mc2_status; nothing is launched on error.
+ */
+int mc2_matmul_act_grad(const void *dy, int64_t lddy, const void *w, int64_t ldw, int w_is_nk, const void *z,
+                        int64_t ldz, int act, int64_t m, int64_t n, int64_t k, int dtype, void *dz, int64_t lddz,
+                        void *stream);
+
+/*
+ * Gradient through an activation alone: dz = dy * act'(z), elementwise over
+ * (m, n) matrices with rows lddy, ldz and lddz apart, for an output of
+ * mc2_matmul_bias_act whose gradient did not come from a linear layer.
+ * dz may be dy or z itself (same stride).  dtype MC2_F16 or MC2_BF16.
+ */
+int mc2_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int act, int64_t m, int64_t n, int dtype,
+                 void *dz, int64_t lddz, void *stream);
+
 /* Name of a status code (static string). */
 const char *mc2_status_str(int status);
 
@@ -323,6 +469,8 @@ int mc2_device_status(void);
  *   mc2_all_gather_mm, mc2_matmul_reduce_scatter   1: the GEMM
  *   mc2_matmul_weight_grad     1: the GEMM (which also forms db)
  *   mc2_quant_all_reduce       1: the reduction
+ *   mc2_add_rms_norm, mc2_matmul_bias_act, mc2_matmul_act_grad, mc2_act_grad   1
+ *   mc2_rms_norm_grad          1, or 2 with dw: the gradient, the sum of its shares of dw
  *   mc2_alltoall_quant_mm      x1_quant_mode 7: 2 (the fused quant and x2
  *                              widening, the GEMM), or 3 when rank_size*h > 32768
  *                              or h % 8 != 0 (the quant, the x2 widening, the

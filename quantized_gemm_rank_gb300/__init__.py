@@ -11,6 +11,14 @@ cannot be built or loaded, importing the functions raises.
   mc2_matmul_reduce_scatter  out_j = (sum_r X_r @ W_r^T)[rows of rank j] (+ bias)
   mc2_matmul_weight_grad   dw = dy^T @ x, db = dy.sum(0)
   mc2_quant_all_reduce     out = sum_r dequant(x_r, scales_r)  (int8/fp8 codes)
+
+and, around the linears:
+
+  mc2_add_rms_norm         out = rmsnorm(x + residual) * weight, and its 8-bit codes with scales
+  mc2_rms_norm_grad        its gradient
+  mc2_matmul_bias_act      out = act(x @ w^T + bias) + residual
+  mc2_matmul_act_grad      dz = (dy @ w) * act'(z)
+  mc2_act_grad             dz = dy * act'(z)
 """
 from __future__ import annotations
 
@@ -33,8 +41,11 @@ MC2_ERR_TIMEOUT = -7
 
 MC2_F16, MC2_BF16, MC2_F32, MC2_I8 = 1, 2, 3, 4
 MC2_F8E4M3, MC2_F8E5M2, MC2_E8M0 = 5, 6, 7
+QUANT_NONE = 0
 QUANT_PERCHANNEL = 2
 QUANT_PERTOKEN = 3
+QUANT_PERGROUP = 4
+QUANT_MX = 6
 QUANT_PERTOKEN_DYNAMIC = 7
 
 _P = ctypes.c_void_p
@@ -73,6 +84,22 @@ def lib() -> ctypes.CDLL:
         L.mc2_alltoall_quant_mm_no_alloc.argtypes = [_P, _INT, _I64, _I64, _INT, _P, _P, _P, _P, _INT, _INT, _INT,
                                                      _I64, _P, _P, _P, _P, _P, _P]
         L.mc2_alltoall_quant_mm_no_alloc.restype = _INT
+        L.mc2_add_rms_norm.argtypes = [_P, _I64, _P, _I64, _P, _INT, _I64, _I64, ctypes.c_float, _INT, _P, _I64,
+                                       _P, _I64, _P, _INT, _INT, _P, _P, _P]
+        L.mc2_add_rms_norm.restype = _INT
+        L.mc2_rms_norm_grad_workspace.argtypes = [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)]
+        L.mc2_rms_norm_grad_workspace.restype = _INT
+        L.mc2_rms_norm_grad.argtypes = [_P, _I64, _P, _I64, _P, _INT, _P, _P, _I64, _I64, _I64, _INT, _P, _I64,
+                                        _P, _P, ctypes.c_size_t, _P]
+        L.mc2_rms_norm_grad.restype = _INT
+        L.mc2_matmul_bias_act.argtypes = [_P, _I64, _P, _I64, _INT, _I64, _I64, _I64, _P, _INT, _P, _I64, _INT,
+                                          _P, _I64, _P, _I64, _P]
+        L.mc2_matmul_bias_act.restype = _INT
+        L.mc2_matmul_act_grad.argtypes = [_P, _I64, _P, _I64, _INT, _P, _I64, _INT, _I64, _I64, _I64, _INT, _P,
+                                          _I64, _P]
+        L.mc2_matmul_act_grad.restype = _INT
+        L.mc2_act_grad.argtypes = [_P, _I64, _P, _I64, _INT, _I64, _I64, _INT, _P, _I64, _P]
+        L.mc2_act_grad.restype = _INT
         L.mc2_status_str.argtypes = [_INT]
         L.mc2_status_str.restype = ctypes.c_char_p
         L.mc2_last_error.argtypes = []
@@ -425,6 +452,256 @@ def mc2_alltoall_quant_mm_no_alloc(chunks: Sequence[torch.Tensor], x2: torch.Ten
     return {"out": out, "q": q_out, "x1_scale": x1_scale_out, "acc": acc_out, "alltoall_out": alltoall_out}
 
 
+# ------------------------------------------------------------------ around the linears
+# These calls take matrices whose rows are strided (a slice of a wider tensor),
+# and tensors of more dimensions, whose last one is the row: (b, s, h) is the
+# (b * s, h) problem.
+
+def _rows(t: torch.Tensor, shape, dtype, what: str, cur: int):
+    """The tensor's device pointer and its row stride in elements, once its shape, dtype, device and
+    layout are right: rows of adjacent elements at one stride."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != cur:
+        _refuse(t, shape, dtype, what, cur)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    cols = shape[-1]
+    ld = None
+    ok = cols == 1 or t.stride(-1) == 1
+    rows = 1                      # rows below the dimension looked at
+    for d in range(t.dim() - 2, -1, -1):
+        if shape[d] == 1:
+            continue
+        if ld is None:
+            ld = t.stride(d)
+        elif t.stride(d) != rows * ld:
+            ok = False
+        rows *= shape[d]
+    if ld is None:
+        ld = cols
+    if not ok or ld < cols:
+        raise ValueError(f"{what} must have rows of adjacent elements at one stride, got strides {t.stride()} "
+                         f"for shape {tuple(shape)}")
+    return t.data_ptr(), ld
+
+
+def _opt_rows(t: Optional[torch.Tensor], shape, dtype, what: str, cur: int):
+    return (None, 0) if t is None else _rows(t, shape, dtype, what, cur)
+
+
+def _leading(t: torch.Tensor, what: str) -> int:
+    """The number of rows of a tensor of two or more dimensions."""
+    if t.dim() == 2:
+        return t.shape[0]
+    if t.dim() < 2:
+        raise ValueError(f"{what} must have at least 2 dimensions, got {t.dim()}")
+    rows = 1
+    for n in t.shape[:-1]:
+        rows *= n
+    return rows
+
+
+_QNORM = {torch.int8: MC2_I8, torch.float8_e4m3fn: MC2_F8E4M3, torch.float8_e5m2: MC2_F8E5M2}
+
+
+def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, quant_mode: int = QUANT_NONE, q_dtype: torch.dtype = torch.int8,
+                     with_out: Optional[bool] = None, with_rstd: bool = False, out: Optional[torch.Tensor] = None,
+                     residual_out: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                     q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """RMS norm of x + residual, with 8-bit codes for the fused linear that follows.
+
+    x, residual (..., h) of fp16, bf16 or fp32; weight (h) of x's type or fp32.
+    quant_mode: QUANT_NONE; QUANT_PERTOKEN_DYNAMIC (scale fp32, one per row: what
+    mc2_alltoall_quant_mm takes in mode 3); QUANT_PERGROUP (fp32, one per 128
+    columns) or QUANT_MX (e8m0 codes as uint8, one per 32 columns), the layouts of
+    mc2_quant_all_reduce.  q_dtype: int8, float8_e4m3fn or float8_e5m2.  The 16-bit
+    ``out`` is made when there are no codes, when it is given, or by ``with_out``.
+    Returns dict(out, residual, rstd, q, scale): the sum that was normalised is
+    ``residual`` (None without a residual); outputs not asked for are None.
+    """
+    cur = _current_device()
+    shape, dt, dev = x.shape, x.dtype, x.device
+    m, h = _leading(x, "x"), shape[-1]
+    xp, ldx = _rows(x, shape, dt, "x", cur)
+    wt = weight.dtype
+    wp = _arg(weight, (h,), wt, "weight", cur)
+    rp, ldr = _opt_rows(residual, shape, dt, "residual", cur)
+    op, ldo, rop, ldro = None, 0, None, 0
+    if out is not None or with_out or (with_out is None and quant_mode == QUANT_NONE):
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=dev)
+        op, ldo = _rows(out, shape, dt, "out", cur)
+    if residual is not None:
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=dt, device=dev)
+    if residual_out is not None:
+        rop, ldro = _rows(residual_out, shape, dt, "residual_out", cur)
+    sp = None
+    if rstd is not None or with_rstd:
+        if rstd is None:
+            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        sp = _arg(rstd, shape[:-1], torch.float32, "rstd", cur)
+    qp, scp, qd = None, None, 0
+    if quant_mode != QUANT_NONE:
+        if q_dtype not in _QNORM:
+            raise ValueError(f"q_dtype must be int8, float8_e4m3fn or float8_e5m2, got {q_dtype}")
+        qd = _QNORM[q_dtype]
+        if q is None:
+            q = torch.empty(shape, dtype=q_dtype, device=dev)
+        qp = _arg(q, shape, q_dtype, "q", cur)
+        sshape, sdt = shape[:-1], torch.float32
+        if quant_mode == QUANT_PERGROUP:
+            sshape = (*sshape, -(-h // 128))
+        elif quant_mode == QUANT_MX:
+            sshape, sdt = (*sshape, -(-h // 32)), torch.uint8
+        if scale is None:
+            scale = torch.empty(sshape, dtype=sdt, device=dev)
+        scp = _arg(scale, sshape, sdt, "scale", cur)
+    elif q is not None or scale is not None:
+        raise ValueError("q and scale need a quant_mode")
+    _need_device(cur)
+    _check(lib().mc2_add_rms_norm(xp, ldx, rp, ldr, wp, _dtype_code(wt), m, h, eps, _dtype_code(dt), op, ldo, rop,
+                                  ldro, sp, quant_mode, qd, qp, scp, _stream(stream, cur)))
+    return {"out": out if op is not None else None, "residual": residual_out, "rstd": rstd, "q": q, "scale": scale}
+
+
+def mc2_rms_norm_grad_workspace(m: int, h: int) -> int:
+    nbytes = ctypes.c_size_t(0)
+    _check(lib().mc2_rms_norm_grad_workspace(m, h, ctypes.byref(nbytes)))
+    return int(nbytes.value)
+
+
+def mc2_rms_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *,
+                      dres: Optional[torch.Tensor] = None, with_weight: bool = True,
+                      dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of mc2_add_rms_norm's ``out``.
+
+    x is what was normalised (the forward call's ``residual`` output, or x itself
+    without one) and rstd its ``rstd``; dres is the gradient that arrives at the
+    ``residual`` output.  Returns (dx, dw): dx is the gradient of both x and the
+    residual, dw of the weight (None without ``with_weight``).
+    """
+    cur = _current_device()
+    shape, dt, dev = x.shape, x.dtype, x.device
+    m, h = _leading(x, "x"), shape[-1]
+    xp, ldx = _rows(x, shape, dt, "x", cur)
+    dyp, lddy = _rows(dy, shape, dt, "dy", cur)
+    wt = weight.dtype
+    wp = _arg(weight, (h,), wt, "weight", cur)
+    sp = _arg(rstd, shape[:-1], torch.float32, "rstd", cur)
+    drp, lddr = _opt_rows(dres, shape, dt, "dres", cur)
+    if dx is None:
+        dx = torch.empty(shape, dtype=dt, device=dev)
+    dxp, lddx = _rows(dx, shape, dt, "dx", cur)
+    dwp, wsp, nbytes = None, None, 0
+    if with_weight or dw is not None:
+        if dw is None:
+            dw = torch.empty((h,), dtype=wt, device=dev)
+        dwp = _arg(dw, (h,), wt, "dw", cur)
+        _need_device(cur)
+        if workspace is None:
+            workspace = torch.empty(mc2_rms_norm_grad_workspace(m, h), dtype=torch.uint8, device=dev)
+        wsp = _arg(workspace, workspace.shape, workspace.dtype, "workspace", cur)
+        nbytes = workspace.numel() * workspace.element_size()
+    _need_device(cur)
+    _check(lib().mc2_rms_norm_grad(dyp, lddy, xp, ldx, wp, _dtype_code(wt), sp, drp, lddr, m, h, _dtype_code(dt), dxp,
+                                   lddx, dwp, wsp, nbytes, _stream(stream, cur)))
+    return dx, dw
+
+
+_ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _activation(name: str) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}, got {name!r}")
+    return _ACTIVATIONS[name]
+
+
+def mc2_matmul_bias_act(x: torch.Tensor, w: torch.Tensor, *, w_is_nk: bool = True,
+                        bias: Optional[torch.Tensor] = None, activation: str = "none",
+                        residual: Optional[torch.Tensor] = None, with_preact: bool = False,
+                        out: Optional[torch.Tensor] = None, preact: Optional[torch.Tensor] = None, stream=None):
+    """out = act(x @ w^T + bias) + residual, in one kernel.
+
+    x (..., k); w (n, k), or (k, n) with ``w_is_nk=False``; bias (n); residual
+    (..., n); all of one 16-bit type.  activation: "none", "relu", "gelu" (by erf),
+    "gelu_tanh" or "silu".  Returns (out, preact): preact = x @ w^T + bias, with
+    ``with_preact`` or when given, is what the gradients take.
+    """
+    cur = _current_device()
+    act = _activation(activation)
+    dt, dev = x.dtype, x.device
+    m, k = _leading(x, "x"), x.shape[-1]
+    if w.dim() != 2:
+        raise ValueError(f"w must have 2 dimensions, got {w.dim()}")
+    n = w.shape[0] if w_is_nk else w.shape[1]
+    xp, ldx = _rows(x, x.shape, dt, "x", cur)
+    wp, ldw = _rows(w, (n, k) if w_is_nk else (k, n), dt, "w", cur)
+    bp = _opt(bias, (n,), dt, "bias", cur)
+    oshape = (*x.shape[:-1], n)
+    rp, ldr = _opt_rows(residual, oshape, dt, "residual", cur)
+    if out is None:
+        out = torch.empty(oshape, dtype=dt, device=dev)
+    op, ldo = _rows(out, oshape, dt, "out", cur)
+    pp, ldp = None, 0
+    if with_preact or preact is not None:
+        if preact is None:
+            preact = torch.empty(oshape, dtype=dt, device=dev)
+        pp, ldp = _rows(preact, oshape, dt, "preact", cur)
+    _need_device(cur)
+    _check(lib().mc2_matmul_bias_act(xp, ldx, wp, ldw, w_is_nk, m, n, k, bp, act, rp, ldr, _dtype_code(dt), op, ldo,
+                                     pp, ldp, _stream(stream, cur)))
+    return out, preact
+
+
+def mc2_matmul_act_grad(dy: torch.Tensor, w: torch.Tensor, z: torch.Tensor, *, activation: str, w_is_nk: bool = True,
+                        dz: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dz = (dy @ w) * act'(z): the gradient of z for y = act(z) @ w^T.
+
+    dy (..., n); w (n, k), or (k, n) with ``w_is_nk=False``; z (..., k), the forward
+    call's ``preact``.  The layer's dW and dB are mc2_matmul_weight_grad(dy, act(z)).
+    """
+    cur = _current_device()
+    act = _activation(activation)
+    dt = dy.dtype
+    m, n = _leading(dy, "dy"), dy.shape[-1]
+    if w.dim() != 2:
+        raise ValueError(f"w must have 2 dimensions, got {w.dim()}")
+    k = w.shape[1] if w_is_nk else w.shape[0]
+    dyp, lddy = _rows(dy, dy.shape, dt, "dy", cur)
+    wp, ldw = _rows(w, (n, k) if w_is_nk else (k, n), dt, "w", cur)
+    zshape = (*dy.shape[:-1], k)
+    zp, ldz = _rows(z, zshape, dt, "z", cur)
+    if dz is None:
+        dz = torch.empty(zshape, dtype=dt, device=dy.device)
+    dzp, lddz = _rows(dz, zshape, dt, "dz", cur)
+    _need_device(cur)
+    _check(lib().mc2_matmul_act_grad(dyp, lddy, wp, ldw, w_is_nk, zp, ldz, act, m, n, k, _dtype_code(dt), dzp, lddz,
+                                     _stream(stream, cur)))
+    return dz
+
+
+def mc2_act_grad(dy: torch.Tensor, z: torch.Tensor, *, activation: str, dz: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """dz = dy * act'(z), elementwise: the gradient of mc2_matmul_bias_act's
+    ``preact`` for a gradient ``dy`` of its ``out``."""
+    cur = _current_device()
+    act = _activation(activation)
+    shape, dt = dy.shape, dy.dtype
+    m = _leading(dy, "dy")
+    dyp, lddy = _rows(dy, shape, dt, "dy", cur)
+    zp, ldz = _rows(z, shape, dt, "z", cur)
+    if dz is None:
+        dz = torch.empty(shape, dtype=dt, device=dy.device)
+    dzp, lddz = _rows(dz, shape, dt, "dz", cur)
+    _need_device(cur)
+    _check(lib().mc2_act_grad(dyp, lddy, zp, ldz, act, m, shape[-1], _dtype_code(dt), dzp, lddz,
+                              _stream(stream, cur)))
+    return dz
+
+
 def mc2_device_status() -> int:
     """Synchronise and return (and clear) the kernels' bounded-wait status."""
     return int(lib().mc2_device_status())
@@ -456,9 +733,11 @@ __all__ = [
     "mc2_matmul_reduce_scatter", "mc2_matmul_weight_grad", "mc2_quant_all_reduce",
     "mc2_alltoall_quant_mm_workspace", "mc2_alltoall_quant_mm",
     "mc2_alltoall_quant_mm_no_alloc",
+    "mc2_add_rms_norm", "mc2_rms_norm_grad_workspace", "mc2_rms_norm_grad", "mc2_matmul_bias_act",
+    "mc2_matmul_act_grad", "mc2_act_grad",
     "NO_ALLOC_SCRATCH_BYTES", "mc2_device_status", "mc2_set_launch_events", "mc2_test_expire_next_flag_waits",
     "MC2_OK", "MC2_ERR_NULL", "MC2_ERR_SHAPE", "MC2_ERR_DTYPE", "MC2_ERR_UNSUPPORTED", "MC2_ERR_WORKSPACE",
     "MC2_ERR_CUDA", "MC2_ERR_TIMEOUT", "MC2_F16", "MC2_BF16", "MC2_F32", "MC2_I8",
     "MC2_F8E4M3", "MC2_F8E5M2", "MC2_E8M0",
-    "QUANT_PERCHANNEL", "QUANT_PERTOKEN", "QUANT_PERTOKEN_DYNAMIC",
+    "QUANT_NONE", "QUANT_PERCHANNEL", "QUANT_PERTOKEN", "QUANT_PERGROUP", "QUANT_MX", "QUANT_PERTOKEN_DYNAMIC",
 ]

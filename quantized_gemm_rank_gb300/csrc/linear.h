@@ -1,0 +1,40 @@
+// linear.h -- the fused-epilogue matrix product's kernels, as the C entry points call them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace mc2 {
+
+// What the epilogue does with the second matrix it reads (aux, the shape of out):
+//   AUX_NONE      out = act(acc + bias)
+//   AUX_RESIDUAL  out = act(acc + bias) + aux
+//   AUX_ACT_GRAD  out = acc * act'(aux)
+enum AuxMode : int { AUX_NONE = 0, AUX_RESIDUAL = 1, AUX_ACT_GRAD = 2 };
+
+// out (m, n) from x (m, k) and w, (n, k) when w_nk or (k, n); strides are in
+// elements, from row to row.  All tensors are of one 16-bit type.
+struct LinearParams {
+    const void *x, *w, *bias, *aux;
+    void *out, *preact;
+    int64_t ldx, ldw, ldaux, ldo, ldp;
+    int m, n, k;
+    int w_nk;
+    int act;        // ActKind
+    int aux_mode;   // AuxMode
+};
+
+cudaError_t launch_linear_any(bool bf16, const LinearParams &p, cudaStream_t stream);
+
+// dz = dy * act'(z), (m, n)
+struct ActGradParams {
+    const void *dy, *z;
+    void *dz;
+    int64_t lddy, ldz, lddz;
+    int64_t m, n;
+    int act;
+};
+cudaError_t launch_act_grad(bool bf16, const ActGradParams &p, int num_sms, cudaStream_t stream);
+
+}  // namespace mc2

@@ -1,0 +1,143 @@
+// linear_kernels.cu -- matrix product with bias, activation and residual in its
+// epilogue, and the activation's derivative in the backward product.
+//
+//   z[i, j]   = sum_l x[i, l] W[l, j] + bias[j]
+//   out[i, j] = act(z[i, j]) + residual[i, j],  preact = z        (forward)
+//   out[i, j] = (sum_l x[i, l] W[l, j]) act'(aux[i, j])           (backward)
+// Sums and the epilogue are fp32; each output is rounded once.
+#include "linear.h"
+
+#include <type_traits>
+
+#include "num.cuh"
+#include "sm103_ptx.cuh"
+
+namespace mc2 {
+
+namespace {
+
+// The epilogue of one element: acc with the bias and aux of its place.
+template <int kAct>
+__device__ __forceinline__ float epilogue_one(float z, float aux, int aux_mode) {
+    if (aux_mode == AUX_ACT_GRAD) return z * act_derivative_f<kAct>(aux);
+    const float o = act_f<kAct>(z);
+    return aux_mode == AUX_RESIDUAL ? o + aux : o;
+}
+
+// Any sizes, strides and alignments: a 64 x 64 tile a block, 4 x 4 outputs a
+// thread, the operands staged through shared memory 16 columns at a time with
+// element loads.
+template <int kT, int kAct>
+__global__ void __launch_bounds__(256) linear_any_kernel(const __grid_constant__ LinearParams p) {
+    using T = typename Elem<kT>::type;
+    __shared__ float xs[16][64 + 4], ws[16][64 + 4];
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int64_t n_tiles = (p.n + 63) / 64;
+    const int m0 = static_cast<int>(blockIdx.x / n_tiles) * 64, n0 = static_cast<int>(blockIdx.x % n_tiles) * 64;
+    const T *x = static_cast<const T *>(p.x), *w = static_cast<const T *>(p.w);
+    float acc[4][4] = {};
+    for (int k0 = 0; k0 < p.k; k0 += 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = tid + 256 * i, r = e >> 4, c = e & 15;
+            xs[c][r] = (m0 + r < p.m && k0 + c < p.k) ? Elem<kT>::load(x + (m0 + r) * p.ldx + k0 + c) : 0.0f;
+            if (p.w_nk) {
+                ws[c][r] = (n0 + r < p.n && k0 + c < p.k) ? Elem<kT>::load(w + (n0 + r) * p.ldw + k0 + c) : 0.0f;
+            } else {
+                const int kr = e >> 6, nc = e & 63;
+                ws[kr][nc] = (n0 + nc < p.n && k0 + kr < p.k) ? Elem<kT>::load(w + (k0 + kr) * p.ldw + n0 + nc) : 0.0f;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int l = 0; l < 16; ++l) {
+            float a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = xs[l][ty * 4 + i], b[i] = ws[l][tx * 4 + i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
+            if (r >= p.m || c >= p.n) continue;
+            float z = acc[i][j];
+            if (p.bias) z += Elem<kT>::load(static_cast<const T *>(p.bias) + c);
+            if (p.preact) Elem<kT>::store(static_cast<T *>(p.preact) + r * p.ldp + c, z);
+            const float aux = p.aux_mode != AUX_NONE ? Elem<kT>::load(static_cast<const T *>(p.aux) + r * p.ldaux + c) : 0.0f;
+            Elem<kT>::store(static_cast<T *>(p.out) + r * p.ldo + c, epilogue_one<kAct>(z, aux, p.aux_mode));
+        }
+}
+
+template <int kT, int kAct>
+__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradParams p) {
+    using T = typename Elem<kT>::type;
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    const int64_t total = p.m * p.n, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total; e += step) {
+        const int64_t r = e / p.n, c = e - r * p.n;
+        const float d = Elem<kT>::load(static_cast<const T *>(p.dy) + r * p.lddy + c);
+        const float z = Elem<kT>::load(static_cast<const T *>(p.z) + r * p.ldz + c);
+        Elem<kT>::store(static_cast<T *>(p.dz) + r * p.lddz + c, d * act_derivative_f<kAct>(z));
+    }
+}
+
+template <class K, class... A>
+cudaError_t launch(K kern, unsigned grid, unsigned block, cudaStream_t stream, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// f(std::integral_constant<int, act>) for a run-time activation
+template <class F>
+cudaError_t with_act(int act, F f) {
+    switch (act) {
+        case ACT_RELU: return f(std::integral_constant<int, ACT_RELU>{});
+        case ACT_GELU: return f(std::integral_constant<int, ACT_GELU>{});
+        case ACT_GELU_TANH: return f(std::integral_constant<int, ACT_GELU_TANH>{});
+        case ACT_SILU: return f(std::integral_constant<int, ACT_SILU>{});
+        default: return f(std::integral_constant<int, ACT_NONE>{});
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_any(bool bf16, const LinearParams &p, cudaStream_t stream) {
+    const int64_t tiles = ((p.m + 63ll) / 64) * ((p.n + 63ll) / 64);
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    return with_act(p.act, [&](auto a) {
+        constexpr int kAct = decltype(a)::value;
+        return bf16 ? launch(linear_any_kernel<ELEM_BF16, kAct>, static_cast<unsigned>(tiles), 256, stream, p)
+                    : launch(linear_any_kernel<ELEM_F16, kAct>, static_cast<unsigned>(tiles), 256, stream, p);
+    });
+}
+
+cudaError_t launch_act_grad(bool bf16, const ActGradParams &p, int num_sms, cudaStream_t stream) {
+    const int64_t blocks = (p.m * p.n + 255) / 256;
+    const unsigned grid = static_cast<unsigned>(blocks < 64ll * num_sms ? blocks : 64ll * num_sms);
+    return with_act(p.act, [&](auto a) {
+        constexpr int kAct = decltype(a)::value;
+        return bf16 ? launch(act_grad_kernel<ELEM_BF16, kAct>, grid, 256, stream, p)
+                    : launch(act_grad_kernel<ELEM_F16, kAct>, grid, 256, stream, p);
+    });
+}
+
+}  // namespace mc2

@@ -11,12 +11,16 @@
 #include <cstring>
 
 #include "gemm_tcgen05.cuh"
+#include "host.h"
 #include "internal.h"
 #include "mc2_gb300.h"
 
 namespace {
-
 thread_local char g_last_error[512] = "";
+}  // namespace
+
+namespace mc2 {
+namespace host {
 
 int fail(int status, const char *fmt, ...) {
     va_list ap;
@@ -26,42 +30,31 @@ int fail(int status, const char *fmt, ...) {
     return status;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+void clear_error() { g_last_error[0] = '\0'; }
 
 // ------------------------------------------------------------------ launch events
 // The caller's events that mc2_set_launch_events installed on this thread:
 // events[0] is recorded before a call's first kernel launch, events[i] after
 // its i-th, on the call's stream.
 constexpr int kMaxLaunchEvents = 8;
-thread_local cudaEvent_t g_launch_events[kMaxLaunchEvents];
-thread_local int g_num_launch_events = 0;
+static thread_local cudaEvent_t g_launch_events[kMaxLaunchEvents];
+static thread_local int g_num_launch_events = 0;
 
-// Records the installed events of one call, in launch order.
-class LaunchMarks {
-  public:
-    explicit LaunchMarks(cudaStream_t s) : s_(s) { mark(); }
-    // after each kernel launch of the call
-    void launched() { mark(); }
-
-  private:
-    void mark() {
-        if (next_ < g_num_launch_events) cudaEventRecord(g_launch_events[next_], s_);
-        ++next_;
-    }
-    cudaStream_t s_;
-    int next_ = 0;
-};
+void LaunchMarks::mark() {
+    if (next_ < g_num_launch_events) cudaEventRecord(g_launch_events[next_], s_);
+    ++next_;
+}
 
 // One-shot test hook (mc2_test_expire_next_flag_waits): the wait limit the next
 // AlltoAllQuantMatmul GEMM on this thread runs with, 0 when not armed.
-thread_local uint64_t g_expire_next_flag_waits_ns = 0;
+static thread_local uint64_t g_expire_next_flag_waits_ns = 0;
 
 // ------------------------------------------------------------------ driver entry point
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeTiledFn encode_fn() {
+static EncodeTiledFn encode_fn() {
     static std::atomic<EncodeTiledFn> fn{nullptr};
     EncodeTiledFn f = fn.load(std::memory_order_relaxed);
     if (!f) {
@@ -85,10 +78,10 @@ EncodeTiledFn encode_fn() {
 // up to 11).  Direct-mapped: a key that hashes to an occupied slot replaces it.
 struct MapKey {
     const void *base;
-    uint64_t inner, outer;
+    uint64_t inner, outer, pitch;
     uint32_t box_inner, box_outer, groups;  // groups 0: a 2-D map
     bool operator==(const MapKey &o) const {
-        return base == o.base && inner == o.inner && outer == o.outer && box_inner == o.box_inner &&
+        return base == o.base && inner == o.inner && outer == o.outer && pitch == o.pitch && box_inner == o.box_inner &&
                box_outer == o.box_outer && groups == o.groups;
     }
 };
@@ -99,11 +92,12 @@ struct MapCacheSlot {
     CUtensorMap map;
     bool used;
 };
-thread_local MapCacheSlot g_map_cache[kMapCacheSlots];
+static thread_local MapCacheSlot g_map_cache[kMapCacheSlots];
 
-MapCacheSlot &map_slot(const MapKey &k) {
+static MapCacheSlot &map_slot(const MapKey &k) {
     uint64_t h = reinterpret_cast<uintptr_t>(k.base) * 0x9E3779B97F4A7C15ull;
     h ^= (k.inner * 0xC2B2AE3D27D4EB4Full) ^ (k.outer * 0x165667B19E3779F9ull);
+    h ^= k.pitch * 0x9E3779B185EBCA87ull;
     h ^= (static_cast<uint64_t>(k.box_inner) << 32 | k.box_outer) * 0x27D4EB2F165667C5ull + k.groups;
     h ^= h >> 29;
     return g_map_cache[h % kMapCacheSlots];
@@ -112,8 +106,9 @@ MapCacheSlot &map_slot(const MapKey &k) {
 // 2-D map over a row-major (outer, inner) matrix with 16-bit elements and a
 // 128-byte swizzle; out-of-range box elements read as zero.
 bool make_map16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint32_t box_inner,
-                uint32_t box_outer) {
-    const MapKey key{base, inner, outer, box_inner, box_outer, 0};
+                uint32_t box_outer, uint64_t pitch) {
+    if (pitch == 0) pitch = inner;
+    const MapKey key{base, inner, outer, pitch, box_inner, box_outer, 0};
     MapCacheSlot &slot = map_slot(key);
     if (slot.used && slot.key == key) {
         *m = slot.map;
@@ -122,7 +117,7 @@ bool make_map16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {inner * 2};
+    cuuint64_t strides[1] = {pitch * 2};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
@@ -136,14 +131,15 @@ bool make_map16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer
 }
 
 // N-major B (outer = k rows, inner = n columns, 16-bit) as a 3-D map
-// [inner / 64][outer][64] (strides inner * 2 and 128 bytes), so one copy of box
+// [inner / 64][outer][64] (strides pitch * 2 and 128 bytes), so one copy of box
 // {64, box_outer, groups} brings `groups` 64-column slices, slice j landing
 // 8 KiB after slice j - 1 (the layout of that many 2-D boxes).  Only for
 // inner % 64 == 0: a partial last group would read into the next row.
 bool make_map16_nmajor3d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint32_t box_outer,
-                         uint32_t groups) {
+                         uint32_t groups, uint64_t pitch) {
     if (inner % 64 != 0) return false;
-    const MapKey key{base, inner, outer, 64, box_outer, groups};
+    if (pitch == 0) pitch = inner;
+    const MapKey key{base, inner, outer, pitch, 64, box_outer, groups};
     MapCacheSlot &slot = map_slot(key);
     if (slot.used && slot.key == key) {
         *m = slot.map;
@@ -152,7 +148,7 @@ bool make_map16_nmajor3d(CUtensorMap *m, const void *base, uint64_t inner, uint6
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {64, outer, inner / 64};
-    cuuint64_t strides[2] = {inner * 2, 128};
+    cuuint64_t strides[2] = {pitch * 2, 128};
     cuuint32_t box[3] = {64, box_outer, groups};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, estr,
@@ -164,11 +160,6 @@ bool make_map16_nmajor3d(CUtensorMap *m, const void *base, uint64_t inner, uint6
     slot.used = true;
     return true;
 }
-
-struct DeviceInfo {
-    int device = -1;
-    int num_sms = 0;
-};
 
 int current_device(DeviceInfo *info) {
     int dev = 0;
@@ -193,7 +184,13 @@ int current_device(DeviceInfo *info) {
     return MC2_OK;
 }
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per bounded device-side wait
+}  // namespace host
+}  // namespace mc2
+
+namespace {
+
+using namespace mc2::host;
+
 constexpr int kKBlockTiles = 1024 / mc2::kBK;      // k-tiles per exact fp32 K block (1024 * 127^2 < 2^24)
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
