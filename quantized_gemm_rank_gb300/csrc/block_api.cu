@@ -61,12 +61,24 @@ int check_product(int64_t m, int64_t n, int64_t k, int act, int dtype) {
 }
 
 // The product itself, its arguments checked: the kernel that takes its sizes and layout.
-int product(const char *what, bool bf16, const mc2::LinearParams &p, void *stream) {
+int product(const char *what, bool bf16, mc2::LinearParams &p, void *stream) {
     DeviceInfo dev;
     if (int st = current_device(&dev)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // the stride of a single row is free: one that the tensor copies take
+    const auto one_row = [](int rows, int64_t cols, int64_t &ld) {
+        if (rows == 1) ld = (cols + 7) / 8 * 8;
+    };
+    one_row(p.m, p.k, p.ldx);
+    one_row(p.w_nk ? p.n : p.k, p.w_nk ? p.k : p.n, p.ldw);
+    one_row(p.m, p.n, p.ldo);
+    one_row(p.m, p.n, p.ldp);
+    one_row(p.m, p.n, p.ldaux);
     LaunchMarks marks(s);
-    cudaError_t e = mc2::launch_linear_any(bf16, p, s);
+    cudaError_t e = !mc2::linear_layout_fits(p) ? mc2::launch_linear_any(bf16, p, s)
+                    : mc2::linear_prefers_split(p, dev.num_sms)
+                        ? mc2::launch_linear_split(bf16, p, dev.num_sms, s)
+                        : mc2::launch_linear_tiles(bf16, p, dev.num_sms, s);
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
     marks.launched();
     return MC2_OK;

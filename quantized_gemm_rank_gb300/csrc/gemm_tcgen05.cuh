@@ -69,6 +69,7 @@
 
 #include <type_traits>
 
+#include "epilogue.cuh"
 #include "sm103_ptx.cuh"
 
 namespace mc2 {
@@ -156,6 +157,11 @@ struct GemmParams {
     // swizzle; used when rs_tma (out_rows % 32 == 0: a warp's 32 rows are one rank's)
     CUtensorMap out_rank_maps[kMaxAMaps];
     int rs_tma;
+    // fused-epilogue instantiations only (kEpi): see epilogue.cuh
+    CUtensorMap aux_map;   // the second matrix the epilogue reads, box and swizzle as out_map
+    CUtensorMap pre_map;   // the pre-activation output, the same
+    int has_aux, has_pre;
+    Activation act;
 };
 
 // ---------------------------------------------------------------------------
@@ -350,27 +356,6 @@ struct TileWalk {
     }
 };
 
-template <bool kBF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (kBF16) {
-        __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<uint32_t *>(&v);
-    } else {
-        __half2 v = __floats2half2_rn(a, b);
-        return *reinterpret_cast<uint32_t *>(&v);
-    }
-}
-
-template <bool kBF16>
-__device__ __forceinline__ float load16(const void *base, int idx) {
-    const uint16_t v = reinterpret_cast<const uint16_t *>(base)[idx];
-    if constexpr (kBF16) {
-        return __uint_as_float(static_cast<uint32_t>(v) << 16);
-    } else {
-        return __half2float(__ushort_as_half(v));
-    }
-}
-
 // Store 32 consecutive 16-bit outputs (columns col0 .. col0+31) of the row that
 // starts at row_ptr, masked at n.
 __device__ __forceinline__ void store_row32_16(uint16_t *row_ptr, int n, int col0, const uint32_t (&pk)[16]) {
@@ -388,10 +373,13 @@ __device__ __forceinline__ void store_row32_16(uint16_t *row_ptr, int n, int col
 
 // kDyn: one CTA pair launched per tile, balanced at run time by cluster launch
 // control (float path only: no stream-K tail).  kNarrow: see TileCfg (float
-// path, one CTA per tile, n <= 64).
-template <int kG, bool kBF16, bool kIntPath, bool kRS = false, bool kDyn = false, bool kNarrow = false>
+// path, one CTA per tile, n <= 64).  kEpi: the epilogue's form (EpiMode); other
+// than EPI_PLAIN a float-path form.
+template <int kG, bool kBF16, bool kIntPath, bool kRS = false, bool kDyn = false, bool kNarrow = false,
+          int kEpi = EPI_PLAIN>
 __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_constant__ GemmParams p) {
     static_assert(!kDyn || (kG == 2 && !kIntPath), "run-time tiles are a CTA-pair float-path form");
+    static_assert(kEpi == EPI_PLAIN || (!kIntPath && !kRS && !kNarrow), "the fused epilogue is a float-path form");
     static_assert(!kNarrow || (kG == 1 && !kIntPath && !kRS && !kDyn), "the narrow tile is a one-CTA float-path form");
     constexpr bool kTmaOut = true;  // epilogue stores through shared slabs and TMA (see the epilogue)
     using Cfg = TileCfg<kG, kTmaOut, kNarrow>;
@@ -863,7 +851,13 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
         const int half = (warp - 4) >> 2;     // which 128 of the 256 columns
         const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
         uint32_t acc_iter = 0;
-        uint32_t skr_phase = 0;   // phase of this warp's stream-K partial barrier
+        uint32_t skr_phase = 0;   // phase of this warp's stream-K partial barrier (kEpi: of its aux barrier)
+        // one lane asks for 32 rows x 64 columns of the second matrix, into the warp's slab
+        auto load_aux = [&](int e, int col, int row0) {
+            const uint32_t bar = ptx::smem_u32(&skr_bar[e]);
+            ptx::mbar_arrive_expect_tx(bar, kEpiSlabBytes);
+            ptx::tma_load_2d(ptx::smem_u32(epi_stage) + e * kEpiSlabBytes, &p.aux_map, col, row0, bar);
+        };
         TileWalk<kDyn> walk = walk0;
         Work w;
         while (walk.template next<kPair>(w, p, abort_flag)) {
@@ -872,6 +866,15 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
             const int row = mb * Cfg::kTileM + kBM * static_cast<int>(cr) + 32 * q + lane;
             const int colh = nb * kBN + half * 128;
             bool ok = true;
+            if constexpr (kEpi != EPI_PLAIN) {
+                // The first slab of the second matrix comes in while the MMAs run: the slab
+                // it lands in is free once the previous tile's stores have read it.  With a
+                // pre-activation output the slab is needed for that first.
+                if (p.has_aux && !p.has_pre && colh < p.n && lane == 0) {
+                    ptx::bulk_wait_group_read<0>();
+                    load_aux(warp - 4, colh, mb * Cfg::kTileM + kBM * static_cast<int>(cr) + 32 * q);
+                }
+            }
             if constexpr (kIntPath) {
                 // This warp's 128 column scales and biases are read only after the tile's
                 // last K block; fetching their lines into L1 now takes those reads (eight
@@ -926,7 +929,14 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 }
                 ++acc_iter;
             }
-            if (!ok) break;
+            if (!ok) {
+                if constexpr (kEpi != EPI_PLAIN) {
+                    // a copy asked for above lands before the CTA can exit
+                    if (p.has_aux && !p.has_pre && colh < p.n)
+                        (void)ptx::mbar_wait(ptx::smem_u32(&skr_bar[warp - 4]), skr_phase, p.wait_limit_ns);
+                }
+                break;
+            }
             if constexpr (kIntPath) {
                 if (w.kind != WORK_FULL) {
                     // stream-K: this thread's 128 int32 sums in slot (unit, cta), laid out
@@ -1069,7 +1079,80 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     }
                 }
             };
-            if constexpr (!kIntPath) {
+            if constexpr (kEpi != EPI_PLAIN) {
+                // Per 64-column slab: the pre-activation leaves first (if asked for), the
+                // second matrix's slab comes in, and the outputs overwrite it in place.
+#pragma unroll
+                for (int sl = 0; sl < 2; ++sl) {
+                    const int scol = colh + sl * 64;
+                    if (!ok || scol >= p.n) continue;
+                    uint8_t *mine = slab + lane * 128;
+                    const uint32_t bar = ptx::smem_u32(&skr_bar[warp - 4]);
+                    if (p.bias16 != nullptr) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float b8[8];
+                            load_bias8<kBF16>(p.bias16, scol + 8 * j, p.n, b8);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                sum[sl * 64 + 8 * j + i] = __fadd_rn(sum[sl * 64 + 8 * j + i], b8[i]);
+                        }
+                    }
+                    if (p.has_pre) {
+                        if (lane == 0) ptx::bulk_wait_group_read<0>();
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            uint32_t pk[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                pk[i] = pack2<kBF16>(sum[sl * 64 + 8 * j + 2 * i], sum[sl * 64 + 8 * j + 2 * i + 1]);
+                            *reinterpret_cast<uint4 *>(mine + ((j ^ (lane & 7)) << 4)) =
+                                make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_2d(&p.pre_map, scol, slab_row0, ptx::smem_u32(slab));
+                            ptx::bulk_commit_group();
+                        }
+                    }
+                    // the slab's previous store has finished reading it
+                    if (lane == 0) ptx::bulk_wait_group_read<0>();
+                    __syncwarp();
+                    if (p.has_aux) {
+                        if ((sl != 0 || p.has_pre) && lane == 0) load_aux(warp - 4, scol, slab_row0);
+                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, skr_phase, p.wait_limit_ns))) {
+                            *abort_flag = 1;
+                            if (p.status && lane == 0) atomicExch(p.status, -7);
+                            ok = false;
+                            continue;
+                        }
+                        skr_phase ^= 1u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint4 *slot = reinterpret_cast<uint4 *>(mine + ((j ^ (lane & 7)) << 4));
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = sum[sl * 64 + 8 * j + i];
+                        uint4 a = make_uint4(0, 0, 0, 0);
+                        if (p.has_aux) a = *slot;
+                        epilogue8<kBF16, kEpi>(v, a, p.act, p.has_aux != 0);
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) pk[i] = pack2<kBF16>(v[2 * i], v[2 * i + 1]);
+                        *slot = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_2d(omap, scol, slab_row0, ptx::smem_u32(slab));
+                        ptx::bulk_commit_group();
+                    }
+                }
+                if (!ok) break;
+            } else if constexpr (!kIntPath) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int col0 = colh + c * 32;

@@ -25,7 +25,19 @@ struct LinearParams {
     int aux_mode;   // AuxMode
 };
 
+// Any sizes and layouts, without tensor cores.
 cudaError_t launch_linear_any(bool bf16, const LinearParams &p, cudaStream_t stream);
+
+// The tensor-core kernels take 16-byte aligned matrices whose strides are multiples
+// of 8 elements (the tensor copies' rule); the strides of single rows are set here.
+bool linear_layout_fits(const LinearParams &p);
+// A CTA pair per 256 x 256 tile: products of many rows.
+cudaError_t launch_linear_tiles(bool bf16, const LinearParams &p, int num_sms, cudaStream_t stream);
+// The weight's columns as the tile's rows, the contraction split over a cluster:
+// products whose tiles would not fill the device.
+cudaError_t launch_linear_split(bool bf16, const LinearParams &p, int num_sms, cudaStream_t stream);
+// Which of the two is expected to be faster for these sizes.
+bool linear_prefers_split(const LinearParams &p, int num_sms);
 
 // dz = dy * act'(z), (m, n)
 struct ActGradParams {

@@ -47,6 +47,24 @@ constexpr float kSqrtHalf = 0.70710678118654752f;     // 1 / sqrt(2)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;   // 1 / sqrt(2 pi)
 constexpr float kSqrt2OverPi = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
+constexpr float kTanhLimit = 14.0f;    // e^-2u(14) = e^-218 and e^104 are beyond fp32's range
+constexpr float kSiluLimit = 104.0f;
+
+// z sigmoid(t) with t = z (c1 + c2 z^2).  The sigmoid is 0 or 1 in fp32 from |z| =
+// limit on, and is taken at z clamped to that, which keeps t finite (0 times
+// infinity otherwise); a NaN passes the comparisons unchanged.
+__device__ __forceinline__ float sigmoid_form(float z, float c1, float c2, float limit) {
+    const float c = z > limit ? limit : (z < -limit ? -limit : z);
+    return z * sigmoid_f(c * fmaf(c2, c * c, c1));
+}
+
+// Its derivative, s + z s (1 - s) t'(z), at the same clamped z (see below).
+__device__ __forceinline__ float sigmoid_form_derivative(float z, float c1, float c2, float limit) {
+    const float c = z > limit ? limit : (z < -limit ? -limit : z);
+    const float zz = c * c;
+    const float s = sigmoid_f(c * fmaf(c2, zz, c1));
+    return fmaf(c * s * (1.0f - s), fmaf(3.0f * c2, zz, c1), s);
+}
 
 // relu  max(z, 0) (a NaN stays a NaN)
 // gelu  z (1 + erf(z / sqrt 2)) / 2
@@ -57,8 +75,9 @@ template <int kAct>
 __device__ __forceinline__ float act_f(float z) {
     if constexpr (kAct == ACT_RELU) return z < 0.0f ? 0.0f : z;
     if constexpr (kAct == ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-    if constexpr (kAct == ACT_GELU_TANH) return z * sigmoid_f(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
-    if constexpr (kAct == ACT_SILU) return z * sigmoid_f(z);
+    if constexpr (kAct == ACT_GELU_TANH)
+        return sigmoid_form(z, 2.0f * kSqrt2OverPi, 2.0f * kSqrt2OverPi * kGeluCubic, kTanhLimit);
+    if constexpr (kAct == ACT_SILU) return sigmoid_form(z, 1.0f, 0.0f, kSiluLimit);
     return z;
 }
 
@@ -73,17 +92,9 @@ __device__ __forceinline__ float act_derivative_f(float z) {
         const float c = z > 14.0f ? 14.0f : (z < -14.0f ? -14.0f : z);
         return 0.5f * (1.0f + erff(c * kSqrtHalf)) + c * kInvSqrt2Pi * __expf(-0.5f * c * c);
     }
-    if constexpr (kAct == ACT_GELU_TANH) {
-        // s + z s (1 - s) 2 u'(z), s = sigmoid(2u)
-        const float c = z > 14.0f ? 14.0f : (z < -14.0f ? -14.0f : z);
-        const float s = sigmoid_f(2.0f * kSqrt2OverPi * (c + kGeluCubic * c * c * c));
-        return s + c * s * (1.0f - s) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * c * c);
-    }
-    if constexpr (kAct == ACT_SILU) {
-        const float c = z > 88.0f ? 88.0f : (z < -88.0f ? -88.0f : z);
-        const float s = sigmoid_f(c);
-        return s * (1.0f + c * (1.0f - s));
-    }
+    if constexpr (kAct == ACT_GELU_TANH)
+        return sigmoid_form_derivative(z, 2.0f * kSqrt2OverPi, 2.0f * kSqrt2OverPi * kGeluCubic, kTanhLimit);
+    if constexpr (kAct == ACT_SILU) return sigmoid_form_derivative(z, 1.0f, 0.0f, kSiluLimit);
     return 1.0f;
 }
 

@@ -137,6 +137,26 @@ def test_odd_widths_in_aligned_rows(m, n, k):
     assert (wide[:, n:] == 9).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 72, 67), (40, 136, 131), (500, 264, 1021), (1300, 77, 5), (2100, 1100, 77)])
+@pytest.mark.parametrize("w_is_nk", [True, False])
+def test_odd_depths_in_aligned_rows(m, n, k, w_is_nk):
+    """k (and n) odd in rows of a stride that is a multiple of 8: what lies between a row's end
+    and the next row's start (here NaN) enters no sum."""
+    def padded(t):
+        big = torch.full((t.shape[0], t.shape[1] + (-t.shape[1] % 8) + 8), float("nan"), dtype=t.dtype, device="cuda")
+        big[:, :t.shape[1]] = t
+        return big[:, :t.shape[1]]
+
+    x, w, bias, res = make(m, n, k, BF16, 6, w_is_nk)
+    z, size = product(x, w, w_is_nk)
+    z = z + bias.double()
+    ref = plain_act(z, "silu") + res.double()
+    out, pre = mc2.mc2_matmul_bias_act(padded(x), padded(w), w_is_nk=w_is_nk, bias=bias, activation="silu",
+                                       residual=padded(res), with_preact=True)
+    within(pre, z, acc_bound(k, size) + UNIT[BF16] * z.abs() + 2.0 ** -23 * z.abs() + 1e-38, "preact")
+    within(out, ref, 1.2 * acc_bound(k, size) + OWN_ACT * (1 + z.abs()) + (UNIT[BF16] + 2.0 ** -22) * ref.abs() + 1e-38, "out")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("w_is_nk", [True, False])
 @pytest.mark.parametrize("m,n,k", [(1, 264, 1040), (20, 520, 712), (140, 136, 328), (1090, 272, 328), (350, 1000, 72)])
