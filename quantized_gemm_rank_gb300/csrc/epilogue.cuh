@@ -1,4 +1,4 @@
-// epilogue.cuh -- the fused epilogues of the 16-bit matrix products, on eight
+// epilogue.cuh -- the fused epilogues of the 16-bit matrix products, on some
 // consecutive columns at a time.  All arithmetic is fp32; each output is rounded once.
 #pragma once
 
@@ -82,50 +82,45 @@ __device__ __forceinline__ void load_bias8(const void *bias, int col, int n, flo
     }
 }
 
-// v: z of eight columns (EPI_FORWARD) or the product (EPI_BACKWARD); a: their aux.
-template <bool kBF16, int kEpi>
-__device__ __forceinline__ void epilogue8(float (&v)[8], const uint4 &a, const Activation &act, bool has_aux) {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    float x[8];
+// v: z of kN columns, a multiple of 8 (EPI_FORWARD), or the product (EPI_BACKWARD);
+// a: their aux, eight columns a vector.
+template <bool kBF16, int kEpi, int kN>
+__device__ __forceinline__ void epilogue(float (&v)[kN], const uint4 (&a)[kN / 8], const Activation &act, bool has_aux) {
+    auto aux = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<kBF16>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
+        for (int j = 0; j < kN / 8; ++j) {
+            const uint32_t w[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack2<kBF16>(w[i]);
+                f(v[8 * j + 2 * i], x.x);
+                f(v[8 * j + 2 * i + 1], x.y);
+            }
+        }
+    };
     if constexpr (kEpi == EPI_FORWARD) {
         switch (act.form) {   // the same in every thread
             case CASE_RELU:
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = act_f<ACT_RELU>(v[i]);
+                for (int i = 0; i < kN; ++i) v[i] = act_f<ACT_RELU>(v[i]);
                 break;
             case CASE_ERF:
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = act_f<ACT_GELU>(v[i]);
+                for (int i = 0; i < kN; ++i) v[i] = act_f<ACT_GELU>(v[i]);
                 break;
             case CASE_SIGMOID:
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = sigmoid_form(v[i], act.c1, act.c2, act.limit);
+                for (int i = 0; i < kN; ++i) v[i] = sigmoid_form(v[i], act.c1, act.c2, act.limit);
                 break;
             default: break;
         }
-        if (has_aux) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], x[i]);
-        }
+        if (has_aux) aux([](float &z, float x) { z = __fadd_rn(z, x); });
     } else {
         switch (act.form) {
-            case CASE_RELU:
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= act_derivative_f<ACT_RELU>(x[i]);
-                break;
-            case CASE_ERF:
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= act_derivative_f<ACT_GELU>(x[i]);
-                break;
+            case CASE_RELU: aux([](float &z, float x) { z *= act_derivative_f<ACT_RELU>(x); }); break;
+            case CASE_ERF: aux([](float &z, float x) { z *= act_derivative_f<ACT_GELU>(x); }); break;
             case CASE_SIGMOID:
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= sigmoid_form_derivative(x[i], act.c1, act.c2, act.limit);
+                aux([&](float &z, float x) { z *= sigmoid_form_derivative(x, act.c1, act.c2, act.limit); });
                 break;
             default: break;
         }

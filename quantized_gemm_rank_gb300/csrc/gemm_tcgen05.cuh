@@ -867,13 +867,119 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
             const int colh = nb * kBN + half * 128;
             bool ok = true;
             if constexpr (kEpi != EPI_PLAIN) {
-                // The first slab of the second matrix comes in while the MMAs run: the slab
-                // it lands in is free once the previous tile's stores have read it.  With a
+                // The tile is one K block: its sums are read from TMEM where they are used, in
+                // a short loop (kept in registers, 128 of them could only be indexed by
+                // unrolled code past the instruction cache's size: an (8192, 8192) output with
+                // k = 1024 and gelu took 159 us that way and takes 123 this way, with k = 7168, a
+                // bias and the pre-activation 816 and 588).
+                const int row0 = mb * Cfg::kTileM + kBM * static_cast<int>(cr) + 32 * q;
+                uint8_t *const slab = epi_stage + (warp - 4) * kEpiSlabBytes;
+                uint8_t *const mine = slab + lane * 128;
+                const uint32_t bar = ptx::smem_u32(&skr_bar[warp - 4]);
+                const bool some = colh < p.n;
+                // The first slab of the second matrix comes in while the MMAs run; it is
+                // free once the previous tile's stores have read it.  With a
                 // pre-activation output the slab is needed for that first.
-                if (p.has_aux && !p.has_pre && colh < p.n && lane == 0) {
+                const bool early = p.has_aux && !p.has_pre && some;
+                if (early && lane == 0) {
                     ptx::bulk_wait_group_read<0>();
-                    load_aux(warp - 4, colh, mb * Cfg::kTileM + kBM * static_cast<int>(cr) + 32 * q);
+                    load_aux(warp - 4, colh, row0);
                 }
+                const uint32_t b = acc_iter & 1u;
+                const bool got = wait_or_abort<kPair>(ptx::smem_u32(&tfull_bar[b]), (acc_iter >> 1) & 1u, p, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    // a copy asked for above lands before the CTA can exit
+                    if (early) (void)ptx::mbar_wait(bar, skr_phase, p.wait_limit_ns);
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t acc = tmem_base + lane_addr + b * kBN + half * 128;
+                // kCols sums of this lane's row with their bias
+                constexpr int kCols = 32;
+                auto sums = [&](int c, float (&v)[kCols]) {
+                    uint32_t r[kCols];
+                    ptx::tmem_ld_32x32b_x32(acc + c, r);
+                    ptx::tmem_ld_wait32(r);
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) v[i] = __uint_as_float(r[i]);
+                    if (p.bias16 != nullptr) {
+#pragma unroll
+                        for (int j = 0; j < kCols / 8; ++j) {
+                            float b8[8];
+                            load_bias8<kBF16>(p.bias16, colh + c + 8 * j, p.n, b8);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[8 * j + i] = __fadd_rn(v[8 * j + i], b8[i]);
+                        }
+                    }
+                };
+                // ... rounded, to their place in the slab (vectors j0, j0 + 1, ...)
+                auto put = [&](int j0, const float (&v)[kCols]) {
+#pragma unroll
+                    for (int j = 0; j < kCols / 8; ++j)
+                        *reinterpret_cast<uint4 *>(mine + (((j0 + j) ^ (lane & 7)) << 4)) =
+                            make_uint4(pack2<kBF16>(v[8 * j], v[8 * j + 1]), pack2<kBF16>(v[8 * j + 2], v[8 * j + 3]),
+                                       pack2<kBF16>(v[8 * j + 4], v[8 * j + 5]), pack2<kBF16>(v[8 * j + 6], v[8 * j + 7]));
+                };
+                for (int sl = 0; sl < 2 && ok; ++sl) {
+                    const int scol = colh + sl * 64;
+                    if (scol >= p.n) break;
+                    // the slab leaves once every lane has written it
+                    auto send = [&](const CUtensorMap *map) {
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_2d(map, scol, row0, ptx::smem_u32(slab));
+                            ptx::bulk_commit_group();
+                            // ... and is free again once the copy has read it
+                            ptx::bulk_wait_group_read<0>();
+                        }
+                        __syncwarp();
+                    };
+                    if (p.has_pre) {
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += kCols) {
+                            float v[kCols];
+                            sums(sl * 64 + c, v);
+                            put(c / 8, v);
+                        }
+                        send(&p.pre_map);
+                    }
+                    if (p.has_aux) {
+                        if ((sl != 0 || p.has_pre) && lane == 0) load_aux(warp - 4, scol, row0);
+                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, skr_phase, p.wait_limit_ns))) {
+                            *abort_flag = 1;
+                            if (p.status && lane == 0) atomicExch(p.status, -7);
+                            ok = false;
+                            break;
+                        }
+                        skr_phase ^= 1u;
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += kCols) {
+                        float v[kCols];
+                        sums(sl * 64 + c, v);
+                        uint4 a[kCols / 8];
+#pragma unroll
+                        for (int j = 0; j < kCols / 8; ++j)
+                            a[j] = p.has_aux ? *reinterpret_cast<const uint4 *>(mine + (((c / 8 + j) ^ (lane & 7)) << 4))
+                                             : make_uint4(0, 0, 0, 0);
+                        epilogue<kBF16, kEpi>(v, a, p.act, p.has_aux != 0);
+                        put(c / 8, v);
+                    }
+                    send(&p.out_map);
+                }
+                // every sum has been read: the accumulator is free
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (kPair)
+                        ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&tempty_bar[b]), 0));
+                    else
+                        ptx::mbar_arrive(ptx::smem_u32(&tempty_bar[b]));
+                }
+                ++acc_iter;
+                if (!ok) break;
+                continue;
             }
             if constexpr (kIntPath) {
                 // This warp's 128 column scales and biases are read only after the tile's
@@ -929,14 +1035,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 }
                 ++acc_iter;
             }
-            if (!ok) {
-                if constexpr (kEpi != EPI_PLAIN) {
-                    // a copy asked for above lands before the CTA can exit
-                    if (p.has_aux && !p.has_pre && colh < p.n)
-                        (void)ptx::mbar_wait(ptx::smem_u32(&skr_bar[warp - 4]), skr_phase, p.wait_limit_ns);
-                }
-                break;
-            }
+            if (!ok) break;
             if constexpr (kIntPath) {
                 if (w.kind != WORK_FULL) {
                     // stream-K: this thread's 128 int32 sums in slot (unit, cta), laid out
@@ -1079,80 +1178,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     }
                 }
             };
-            if constexpr (kEpi != EPI_PLAIN) {
-                // Per 64-column slab: the pre-activation leaves first (if asked for), the
-                // second matrix's slab comes in, and the outputs overwrite it in place.
-#pragma unroll
-                for (int sl = 0; sl < 2; ++sl) {
-                    const int scol = colh + sl * 64;
-                    if (!ok || scol >= p.n) continue;
-                    uint8_t *mine = slab + lane * 128;
-                    const uint32_t bar = ptx::smem_u32(&skr_bar[warp - 4]);
-                    if (p.bias16 != nullptr) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float b8[8];
-                            load_bias8<kBF16>(p.bias16, scol + 8 * j, p.n, b8);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                sum[sl * 64 + 8 * j + i] = __fadd_rn(sum[sl * 64 + 8 * j + i], b8[i]);
-                        }
-                    }
-                    if (p.has_pre) {
-                        if (lane == 0) ptx::bulk_wait_group_read<0>();
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            uint32_t pk[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                pk[i] = pack2<kBF16>(sum[sl * 64 + 8 * j + 2 * i], sum[sl * 64 + 8 * j + 2 * i + 1]);
-                            *reinterpret_cast<uint4 *>(mine + ((j ^ (lane & 7)) << 4)) =
-                                make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                        }
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            ptx::tma_store_2d(&p.pre_map, scol, slab_row0, ptx::smem_u32(slab));
-                            ptx::bulk_commit_group();
-                        }
-                    }
-                    // the slab's previous store has finished reading it
-                    if (lane == 0) ptx::bulk_wait_group_read<0>();
-                    __syncwarp();
-                    if (p.has_aux) {
-                        if ((sl != 0 || p.has_pre) && lane == 0) load_aux(warp - 4, scol, slab_row0);
-                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, skr_phase, p.wait_limit_ns))) {
-                            *abort_flag = 1;
-                            if (p.status && lane == 0) atomicExch(p.status, -7);
-                            ok = false;
-                            continue;
-                        }
-                        skr_phase ^= 1u;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        uint4 *slot = reinterpret_cast<uint4 *>(mine + ((j ^ (lane & 7)) << 4));
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = sum[sl * 64 + 8 * j + i];
-                        uint4 a = make_uint4(0, 0, 0, 0);
-                        if (p.has_aux) a = *slot;
-                        epilogue8<kBF16, kEpi>(v, a, p.act, p.has_aux != 0);
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) pk[i] = pack2<kBF16>(v[2 * i], v[2 * i + 1]);
-                        *slot = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    }
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        ptx::tma_store_2d(omap, scol, slab_row0, ptx::smem_u32(slab));
-                        ptx::bulk_commit_group();
-                    }
-                }
-                if (!ok) break;
-            } else if constexpr (!kIntPath) {
+            if constexpr (!kIntPath) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int col0 = colh + c * 32;

@@ -31,7 +31,8 @@ constexpr int kSplitThreads = 256;
 constexpr int kBlockSteps = 1024 / kDepth;   // stages of one accumulator
 constexpr uint32_t kWBytes = kTileN * kDepth * 2;
 constexpr uint32_t kSmemPerSm = 228 * 1024;
-constexpr uint32_t kSmemOverhead = 1024 + 272;   // the system's, and this kernel's static shared memory
+constexpr uint32_t kSmemStatic = 272;            // this kernel's static shared memory
+constexpr uint32_t kSmemOverhead = 1024 + kSmemStatic;   // with the system's part of each CTA's
 
 struct SplitParams {
     CUtensorMap w_map, x_map;
@@ -248,9 +249,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __
         }
         const bool vec = p.aligned != 0;
         if (p.preact) store8<kBF16>(p.preact, row * p.ldp, col, p.n, vec, v);
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (p.aux) a = load8(p.aux, row * p.ldaux, col, p.n, vec);
-        epilogue8<kBF16, kEpi>(v, a, p.act, p.aux != nullptr);
+        uint4 a[1] = {make_uint4(0, 0, 0, 0)};
+        if (p.aux) a[0] = load8(p.aux, row * p.ldaux, col, p.n, vec);
+        epilogue<kBF16, kEpi>(v, a, p.act, p.aux != nullptr);
         store8<kBF16>(p.out, row * p.ldo, col, p.n, vec, v);
     }
     __syncwarp();
@@ -317,7 +318,8 @@ cudaError_t launch_split(const SplitParams &p, const SplitShape &s, cudaStream_t
     thread_local unsigned long long ready_ctx = 0;
     const unsigned long long ctx = current_context_id();
     if (ctx == 0 || ctx != ready_ctx) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             227 * 1024 - kSmemStatic);
         if (e != cudaSuccess) return e;
         ready_ctx = ctx;
     }

@@ -70,7 +70,7 @@ cudaError_t launch_linear_tiles(bool bf16, const LinearParams &lp, int num_sms, 
     p.num_a_maps = 1;
     p.a_mode = A_SINGLE;
     p.m = lp.m, p.n = lp.n, p.k = lp.k;
-    p.kblock_tiles = 1024 / kBK;
+    p.kblock_tiles = (lp.k + kBK - 1) / kBK;   // one K block a tile
     p.out = lp.out;
     p.bias16 = lp.bias;
     p.act = activation_of(lp.act);

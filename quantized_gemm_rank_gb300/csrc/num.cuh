@@ -66,6 +66,23 @@ __device__ __forceinline__ float sigmoid_form_derivative(float z, float c1, floa
     return fmaf(c * s * (1.0f - s), fmaf(3.0f * c2, zz, c1), s);
 }
 
+// The normal distribution at z: Phi(z) = (1 + erf(z / sqrt 2)) / 2 and, for the
+// derivative, e^(-z^2 / 2).  erf by Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26: for x >= 0, erf x = 1 - (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x),
+// to 1.5e-7; its exponential is the density's, so the derivative costs little more
+// than the value.  Infinities give the limits (e^-inf = 0, t = 0), a NaN stays one.
+__device__ __forceinline__ float normal_cdf(float z, float &expo) {
+    const float x = fabsf(z) * kSqrtHalf;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    expo = __expf(-x * x);
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    const float tail = 0.5f * q * t * expo;   // Phi(-|z|)
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
 // relu  max(z, 0) (a NaN stays a NaN)
 // gelu  z (1 + erf(z / sqrt 2)) / 2
 // gelu_tanh  z (1 + tanh u) / 2 with u = sqrt(2/pi) (z + 0.044715 z^3); as
@@ -74,7 +91,10 @@ __device__ __forceinline__ float sigmoid_form_derivative(float z, float c1, floa
 template <int kAct>
 __device__ __forceinline__ float act_f(float z) {
     if constexpr (kAct == ACT_RELU) return z < 0.0f ? 0.0f : z;
-    if constexpr (kAct == ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    if constexpr (kAct == ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    }
     if constexpr (kAct == ACT_GELU_TANH)
         return sigmoid_form(z, 2.0f * kSqrt2OverPi, 2.0f * kSqrt2OverPi * kGeluCubic, kTanhLimit);
     if constexpr (kAct == ACT_SILU) return sigmoid_form(z, 1.0f, 0.0f, kSiluLimit);
@@ -90,7 +110,9 @@ __device__ __forceinline__ float act_derivative_f(float z) {
     if constexpr (kAct == ACT_GELU) {
         // Phi(z) + z phi(z)
         const float c = z > 14.0f ? 14.0f : (z < -14.0f ? -14.0f : z);
-        return 0.5f * (1.0f + erff(c * kSqrtHalf)) + c * kInvSqrt2Pi * __expf(-0.5f * c * c);
+        float e;
+        const float cdf = normal_cdf(c, e);
+        return fmaf(c * kInvSqrt2Pi, e, cdf);
     }
     if constexpr (kAct == ACT_GELU_TANH)
         return sigmoid_form_derivative(z, 2.0f * kSqrt2OverPi, 2.0f * kSqrt2OverPi * kGeluCubic, kTanhLimit);
