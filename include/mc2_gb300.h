@@ -325,8 +325,8 @@ int mc2_alltoall_quant_mm_no_alloc(const void *const *chunks, int rank_size, int
  *                                  2^-127, as e8m0 codes (m, ceil(h / 32)); fp8 codes only
  *   with Q = 127, 448, 57344 and E = -, 8, 15 for MC2_I8, MC2_F8E4M3, MC2_F8E5M2;
  *   q = y / scale, rounded to nearest-even and saturated at Q.  Where the scale is
- *   not above zero (a zero row, a scale that underflows, a NaN) the codes are 0; a
- *   row or group that holds a NaN has a NaN scale.
+ *   not above zero or not finite (a zero row, a scale that underflows, a NaN) the
+ *   codes are 0; a row or group that holds a NaN has a NaN scale.
  *
  *   All arithmetic is fp32 (the mean of squares must be within its range).
  *

@@ -140,9 +140,19 @@ def _dtype_code(dt: torch.dtype) -> int:
     return _DTYPE_CODES[dt]
 
 
+_raw_device = None   # the current device's index, once CUDA is known to be there
+
+
 def _current_device() -> int:
     """The CUDA device the library launches on, or -1 without CUDA."""
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+    global _raw_device
+    if _raw_device is not None:
+        return _raw_device()
+    if not torch.cuda.is_available():
+        return -1
+    cur = torch.cuda.current_device()   # (initialises CUDA, once)
+    _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return cur
 
 
 # Every tensor goes to the library as a bare pointer, and its kernels trust the
@@ -462,9 +472,9 @@ def _rows(t: torch.Tensor, shape, dtype, what: str, cur: int):
     layout are right: rows of adjacent elements at one stride."""
     if t.shape != shape or t.dtype != dtype or t.get_device() != cur:
         _refuse(t, shape, dtype, what, cur)
-    if t.is_contiguous():
-        return t.data_ptr(), shape[-1]
     cols = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), cols
     ld = None
     ok = cols == 1 or t.stride(-1) == 1
     rows = 1                      # rows below the dimension looked at
@@ -528,14 +538,16 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optiona
     rp, ldr = _opt_rows(residual, shape, dt, "residual", cur)
     op, ldo, rop, ldro = None, 0, None, 0
     if out is not None or with_out or (with_out is None and quant_mode == QUANT_NONE):
-        if out is None:
+        if out is None: 
             out = torch.empty(shape, dtype=dt, device=dev)
-        op, ldo = _rows(out, shape, dt, "out", cur)
-    if residual is not None:
-        if residual_out is None:
-            residual_out = torch.empty(shape, dtype=dt, device=dev)
+            op, ldo = out.data_ptr(), h
+        else:
+            op, ldo = _rows(out, shape, dt, "out", cur)
     if residual_out is not None:
         rop, ldro = _rows(residual_out, shape, dt, "residual_out", cur)
+    elif residual is not None:
+        residual_out = torch.empty(shape, dtype=dt, device=dev)
+        rop, ldro = residual_out.data_ptr(), h
     sp = None
     if rstd is not None or with_rstd:
         if rstd is None:
@@ -548,7 +560,9 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optiona
         qd = _QNORM[q_dtype]
         if q is None:
             q = torch.empty(shape, dtype=q_dtype, device=dev)
-        qp = _arg(q, shape, q_dtype, "q", cur)
+            qp = q.data_ptr()
+        else:
+            qp = _arg(q, shape, q_dtype, "q", cur)
         sshape, sdt = shape[:-1], torch.float32
         if quant_mode == QUANT_PERGROUP:
             sshape = (*sshape, -(-h // 128))
@@ -556,7 +570,9 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optiona
             sshape, sdt = (*sshape, -(-h // 32)), torch.uint8
         if scale is None:
             scale = torch.empty(sshape, dtype=sdt, device=dev)
-        scp = _arg(scale, sshape, sdt, "scale", cur)
+            scp = scale.data_ptr()
+        else:
+            scp = _arg(scale, sshape, sdt, "scale", cur)
     elif q is not None or scale is not None:
         raise ValueError("q and scale need a quant_mode")
     _need_device(cur)
@@ -593,17 +609,24 @@ def mc2_rms_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, r
     drp, lddr = _opt_rows(dres, shape, dt, "dres", cur)
     if dx is None:
         dx = torch.empty(shape, dtype=dt, device=dev)
-    dxp, lddx = _rows(dx, shape, dt, "dx", cur)
+        dxp, lddx = dx.data_ptr(), h
+    else:
+        dxp, lddx = _rows(dx, shape, dt, "dx", cur)
     dwp, wsp, nbytes = None, None, 0
     if with_weight or dw is not None:
         if dw is None:
             dw = torch.empty((h,), dtype=wt, device=dev)
-        dwp = _arg(dw, (h,), wt, "dw", cur)
+            dwp = dw.data_ptr()
+        else:
+            dwp = _arg(dw, (h,), wt, "dw", cur)
         _need_device(cur)
         if workspace is None:
-            workspace = torch.empty(mc2_rms_norm_grad_workspace(m, h), dtype=torch.uint8, device=dev)
-        wsp = _arg(workspace, workspace.shape, workspace.dtype, "workspace", cur)
-        nbytes = workspace.numel() * workspace.element_size()
+            nbytes = mc2_rms_norm_grad_workspace(m, h)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            wsp = workspace.data_ptr()
+        else:
+            wsp = _arg(workspace, workspace.shape, workspace.dtype, "workspace", cur)
+            nbytes = workspace.numel() * workspace.element_size()
     _need_device(cur)
     _check(lib().mc2_rms_norm_grad(dyp, lddy, xp, ldx, wp, _dtype_code(wt), sp, drp, lddr, m, h, _dtype_code(dt), dxp,
                                    lddx, dwp, wsp, nbytes, _stream(stream, cur)))
@@ -644,12 +667,15 @@ def mc2_matmul_bias_act(x: torch.Tensor, w: torch.Tensor, *, w_is_nk: bool = Tru
     rp, ldr = _opt_rows(residual, oshape, dt, "residual", cur)
     if out is None:
         out = torch.empty(oshape, dtype=dt, device=dev)
-    op, ldo = _rows(out, oshape, dt, "out", cur)
+        op, ldo = out.data_ptr(), n
+    else:
+        op, ldo = _rows(out, oshape, dt, "out", cur)
     pp, ldp = None, 0
-    if with_preact or preact is not None:
-        if preact is None:
-            preact = torch.empty(oshape, dtype=dt, device=dev)
+    if preact is not None:
         pp, ldp = _rows(preact, oshape, dt, "preact", cur)
+    elif with_preact:
+        preact = torch.empty(oshape, dtype=dt, device=dev)
+        pp, ldp = preact.data_ptr(), n
     _need_device(cur)
     _check(lib().mc2_matmul_bias_act(xp, ldx, wp, ldw, w_is_nk, m, n, k, bp, act, rp, ldr, _dtype_code(dt), op, ldo,
                                      pp, ldp, _stream(stream, cur)))
@@ -676,7 +702,9 @@ def mc2_matmul_act_grad(dy: torch.Tensor, w: torch.Tensor, z: torch.Tensor, *, a
     zp, ldz = _rows(z, zshape, dt, "z", cur)
     if dz is None:
         dz = torch.empty(zshape, dtype=dt, device=dy.device)
-    dzp, lddz = _rows(dz, zshape, dt, "dz", cur)
+        dzp, lddz = dz.data_ptr(), k
+    else:
+        dzp, lddz = _rows(dz, zshape, dt, "dz", cur)
     _need_device(cur)
     _check(lib().mc2_matmul_act_grad(dyp, lddy, wp, ldw, w_is_nk, zp, ldz, act, m, n, k, _dtype_code(dt), dzp, lddz,
                                      _stream(stream, cur)))
@@ -695,7 +723,9 @@ def mc2_act_grad(dy: torch.Tensor, z: torch.Tensor, *, activation: str, dz: Opti
     zp, ldz = _rows(z, shape, dt, "z", cur)
     if dz is None:
         dz = torch.empty(shape, dtype=dt, device=dy.device)
-    dzp, lddz = _rows(dz, shape, dt, "dz", cur)
+        dzp, lddz = dz.data_ptr(), shape[-1]
+    else:
+        dzp, lddz = _rows(dz, shape, dt, "dz", cur)
     _need_device(cur)
     _check(lib().mc2_act_grad(dyp, lddy, zp, ldz, act, m, shape[-1], _dtype_code(dt), dzp, lddz,
                               _stream(stream, cur)))

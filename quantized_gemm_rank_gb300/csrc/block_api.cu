@@ -145,7 +145,7 @@ int mc2_add_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t l
     p.qkind = q_dtype == MC2_F8E4M3 ? mc2::Q_E4M3 : (q_dtype == MC2_F8E5M2 ? mc2::Q_E5M2 : mc2::Q_I8);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     LaunchMarks marks(s);
-    cudaError_t e = mc2::launch_add_rms_norm(elem_kind(dtype), p, s);
+    cudaError_t e = mc2::launch_add_rms_norm(elem_kind(dtype), p, dev.num_sms, s);
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "RMS norm launch: %s", cudaGetErrorString(e));
     marks.launched();
     return MC2_OK;
@@ -155,7 +155,7 @@ int mc2_rms_norm_grad_workspace(int64_t m, int64_t h, size_t *bytes) {
     clear_error();
     if (!bytes) return fail(MC2_ERR_NULL, "bytes is NULL");
     if (int st = check_norm_sizes(m, h)) return st;
-    *bytes = static_cast<size_t>(mc2::norm_grad_parts(m)) * static_cast<size_t>(h) * 4;
+    *bytes = static_cast<size_t>(mc2::norm_grad_parts(m, h, 2)) * static_cast<size_t>(h) * 4;
     return MC2_OK;
 }
 

@@ -24,19 +24,17 @@ struct NormGradParams {
     const void *dy, *x, *w, *dres;
     const float *rstd;
     void *dx, *dw;
-    float *parts;   // norm_grad_parts(m) rows of h fp32 (with dw)
+    float *parts;   // norm_grad_parts() rows of h fp32 (with dw)
     int64_t lddy, ldx, lddres, lddx;
     int64_t m;
     int h;
     int w_f32;
 };
 
-// Shares of dw that the gradient's blocks leave in the workspace, at most.
-constexpr int kNormGradMaxParts = 304;
-
 // kind: ELEM_F16, ELEM_BF16 or ELEM_F32, the type of x and the outputs
-cudaError_t launch_add_rms_norm(int kind, const NormParams &p, cudaStream_t stream);
-int norm_grad_parts(int64_t m);
+cudaError_t launch_add_rms_norm(int kind, const NormParams &p, int num_sms, cudaStream_t stream);
+// Shares of dw that the gradient's blocks leave in the workspace (more for 2-byte elements than for 4).
+int norm_grad_parts(int64_t m, int64_t h, int elem_size);
 cudaError_t launch_rms_norm_grad(int kind, const NormGradParams &p, cudaStream_t stream);
 // dw from the shares that launch_rms_norm_grad left
 cudaError_t launch_rms_norm_dw(int kind, const NormGradParams &p, cudaStream_t stream);
