@@ -82,20 +82,16 @@ __device__ __forceinline__ void load_bias8(const void *bias, int col, int n, flo
     }
 }
 
-// v: z of kN columns, a multiple of 8 (EPI_FORWARD), or the product (EPI_BACKWARD);
-// a: their aux, eight columns a vector.
+// v: z of kN columns (EPI_FORWARD), or the product (EPI_BACKWARD); a: their aux, two
+// columns a word.
 template <bool kBF16, int kEpi, int kN>
-__device__ __forceinline__ void epilogue(float (&v)[kN], const uint4 (&a)[kN / 8], const Activation &act, bool has_aux) {
+__device__ __forceinline__ void epilogue(float (&v)[kN], const uint32_t (&a)[kN / 2], const Activation &act, bool has_aux) {
     auto aux = [&](auto f) {
 #pragma unroll
-        for (int j = 0; j < kN / 8; ++j) {
-            const uint32_t w[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = unpack2<kBF16>(w[i]);
-                f(v[8 * j + 2 * i], x.x);
-                f(v[8 * j + 2 * i + 1], x.y);
-            }
+        for (int i = 0; i < kN / 2; ++i) {
+            const float2 x = unpack2<kBF16>(a[i]);
+            f(v[2 * i], x.x);
+            f(v[2 * i + 1], x.y);
         }
     };
     if constexpr (kEpi == EPI_FORWARD) {

@@ -958,11 +958,13 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     for (int c = 0; c < 64; c += kCols) {
                         float v[kCols];
                         sums(sl * 64 + c, v);
-                        uint4 a[kCols / 8];
+                        uint32_t a[kCols / 2];
 #pragma unroll
-                        for (int j = 0; j < kCols / 8; ++j)
-                            a[j] = p.has_aux ? *reinterpret_cast<const uint4 *>(mine + (((c / 8 + j) ^ (lane & 7)) << 4))
-                                             : make_uint4(0, 0, 0, 0);
+                        for (int j = 0; j < kCols / 8; ++j) {
+                            uint4 t = make_uint4(0, 0, 0, 0);
+                            if (p.has_aux) t = *reinterpret_cast<const uint4 *>(mine + (((c / 8 + j) ^ (lane & 7)) << 4));
+                            a[4 * j] = t.x, a[4 * j + 1] = t.y, a[4 * j + 2] = t.z, a[4 * j + 3] = t.w;
+                        }
                         epilogue<kBF16, kEpi>(v, a, p.act, p.has_aux != 0);
                         put(c / 8, v);
                     }

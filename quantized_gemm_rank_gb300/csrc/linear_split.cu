@@ -2,17 +2,28 @@
 // few rows (a decode step, a short chunk) or a small output.
 //
 // What bounds it is reading the weight once, so every SM has to read.  The
-// weight's columns are the MMA's 128 rows and the tokens its N columns (16 to
-// 256), so a single token wastes a 16-wide MMA and no weight traffic; the
-// contraction is split over the CTAs of a cluster, whose partial sums are added
-// in shared memory, in rank order (the result does not depend on timing).
+// weight's columns are the MMA's rows and the tokens its N columns (16 to 256), so
+// a single token wastes a 16-wide MMA and no weight traffic; the contraction is
+// split over the CTAs (or CTA pairs) of a cluster, which send one another
+// their partial sums by bulk copies between shared memories and add them in rank
+// order (the result does not depend on timing).
+//   kG = 1  up to 64 tokens: a CTA takes 128 columns, M = 128
+//   kG = 2  more tokens: a CTA pair takes 256 columns, M = 256; each CTA loads 128
+//           columns of the weight and half the tokens, which halves what the
+//           tokens cost in L2 reads (at 256 tokens and one CTA per 128 columns
+//           those reads, 48 KiB a 64-deep stage, set the time)
 //   warp 0      TMA producer (one lane)
-//   warp 1      TMEM allocation, MMA issue
-//   warps 4-7   partial sums from TMEM to shared memory
-//   all warps   the sum over the cluster, and the epilogue, eight columns a thread
+//   warp 1      TMEM allocation, MMA issue (the pair's first CTA)
+//   all warps   then: partial sums from TMEM to shared memory, the sum over the
+//               cluster, and the epilogue, four columns a thread
+// (Reading the other CTAs' sums with loads ran at 9 bytes a clock: 7.3 us for a pair's
+// 256 x 256 sums, the longest part of the call.)
 // The tensor core adds at the size of its running sum, so each 1024-deep part of
 // the contraction goes to an accumulator of its own while TMEM has room, and
 // these are added in fp32 with round-to-nearest.
+#include <atomic>
+#include <cmath>
+
 #include "epilogue.cuh"
 #include "host.h"
 #include "internal.h"
@@ -31,7 +42,7 @@ constexpr int kSplitThreads = 256;
 constexpr int kBlockSteps = 1024 / kDepth;   // stages of one accumulator
 constexpr uint32_t kWBytes = kTileN * kDepth * 2;
 constexpr uint32_t kSmemPerSm = 228 * 1024;
-constexpr uint32_t kSmemStatic = 272;            // this kernel's static shared memory
+constexpr uint32_t kSmemStatic = 288;            // this kernel's static shared memory
 constexpr uint32_t kSmemOverhead = 1024 + kSmemStatic;   // with the system's part of each CTA's
 
 struct SplitParams {
@@ -42,66 +53,122 @@ struct SplitParams {
     int m, n, steps;          // steps: 64-deep stages of the whole contraction
     int w_kn;                 // the weight is (k, n): read M-major
     int rows;                 // tokens a tile (MMA N), a multiple of 16
-    int m_tiles, split;       // token tiles; CTAs a cluster
+    int m_tiles, split;       // token tiles; CTAs (or pairs) that share a tile's contraction
     int stages, accs, tmem_cols;
-    int aligned;              // out, aux and preact rows are 16-byte aligned
+    uint32_t recv_off;        // the other CTAs' sums arrive here, (split - 1) slots of ceil(rows / split) rows
+    int late;                 // ... which the ring reaches into: only once the whole cluster's MMAs are done
+    int prefetch;             // the weight's first stages into L2 ahead of time
     Activation act;
     int *status;
     uint64_t wait_limit_ns;
 };
 
-// A float4 of a CTA of this cluster (shared::cluster address).
-__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
+// Four columns of a row, of which the first `n` (4 or more: all) are in it; whole ones in one access.
 template <bool kBF16>
-__device__ __forceinline__ void store8(void *base, int64_t row_off, int col, int n, bool aligned, const float (&v)[8]) {
-    uint16_t *p = static_cast<uint16_t *>(base) + row_off + col;
-    uint32_t pk[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pk[i] = pack2<kBF16>(v[2 * i], v[2 * i + 1]);
-    if (aligned && col + 8 <= n) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+__device__ __forceinline__ void store4(uint16_t *p, int n, const float *v) {
+    const uint32_t pk[2] = {pack2<kBF16>(v[0], v[1]), pack2<kBF16>(v[2], v[3])};
+    if (n >= 4) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pk[0], pk[1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < n) p[i] = static_cast<uint16_t>(pk[i >> 1] >> ((i & 1) * 16));
+        for (int i = 0; i < 3; ++i)
+            if (i < n) p[i] = static_cast<uint16_t>(pk[i >> 1] >> ((i & 1) * 16));
     }
 }
 
-__device__ __forceinline__ uint4 load8(const void *base, int64_t row_off, int col, int n, bool aligned) {
-    const uint16_t *p = static_cast<const uint16_t *>(base) + row_off + col;
-    if (aligned && col + 8 <= n) return *reinterpret_cast<const uint4 *>(p);
-    uint32_t w[4] = {};
+__device__ __forceinline__ void load4(const uint16_t *p, int n, uint32_t *w) {
+    if (n >= 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = w[1] = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (col + i < n) w[i >> 1] |= static_cast<uint32_t>(p[i]) << ((i & 1) * 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 3; ++i)
+            if (i < n) w[i >> 1] |= static_cast<uint32_t>(p[i]) << ((i & 1) * 16);
+    }
 }
 
-template <bool kBF16, int kEpi>
+// The tokens first + warp * kT, ... < last of a tile (kT a warp at a time, four columns a
+// lane): the partial sums in rank order, the epilogue, the outputs.
+template <bool kBF16, int kEpi, int kT>
+__device__ __forceinline__ void finish(const SplitParams &p, int m0, int first, int last, int rank, int col, const float4 *own,
+                                       const float4 *recv) {
+    const int warp = threadIdx.x >> 5;
+    const int n = p.n - col;   // columns from here on, > 0
+    const int slot = (last - first) * (kTileN / 4);
+    float b4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) b4[i] = load16<kBF16>(p.bias, col + i);
+    }
+#pragma unroll 1
+    for (int t = first + warp * kT; t < last; t += kSplitThreads / 32 * kT) {
+        const int64_t row = m0 + t;
+        const int count = last - t;   // tokens left: those past the last repeat it and are not stored
+        uint32_t aux[2 * kT] = {};
+        if (p.aux) {
+            const uint16_t *from = static_cast<const uint16_t *>(p.aux) + row * p.ldaux + col;
+#pragma unroll
+            for (int u = 0; u < kT; ++u) load4(from + (u < count ? u : 0) * p.ldaux, n, &aux[2 * u]);
+        }
+        float v[4 * kT];
+#pragma unroll
+        for (int i = 0; i < 4 * kT; ++i) v[i] = 0.0f;
+        const float4 *at = recv + (t - first) * (kTileN / 4);
+        for (int r = 0; r < p.split; ++r) {
+            const float4 *from = r == rank ? own + t * (kTileN / 4) : at;
+            if (r != rank) at += slot;
+#pragma unroll
+            for (int u = 0; u < kT; ++u) {
+                const float4 s = from[(u < count ? u : 0) * (kTileN / 4)];
+                v[4 * u] = __fadd_rn(v[4 * u], s.x), v[4 * u + 1] = __fadd_rn(v[4 * u + 1], s.y);
+                v[4 * u + 2] = __fadd_rn(v[4 * u + 2], s.z), v[4 * u + 3] = __fadd_rn(v[4 * u + 3], s.w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * kT; ++i) v[i] = __fadd_rn(v[i], b4[i & 3]);
+        if (p.preact) {
+            uint16_t *to = static_cast<uint16_t *>(p.preact) + row * p.ldp + col;
+#pragma unroll
+            for (int u = 0; u < kT; ++u)
+                if (u < count) store4<kBF16>(to + u * p.ldp, n, &v[4 * u]);
+        }
+        epilogue<kBF16, kEpi>(v, aux, p.act, p.aux != nullptr);
+        uint16_t *to = static_cast<uint16_t *>(p.out) + row * p.ldo + col;
+#pragma unroll
+        for (int u = 0; u < kT; ++u)
+            if (u < count) store4<kBF16>(to + u * p.ldo, n, &v[4 * u]);
+    }
+}
+
+template <bool kBF16, int kEpi, int kG>
 __global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __grid_constant__ SplitParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar;
+    __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, recv_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.stages;
-    const uint32_t stage_bytes = kWBytes + static_cast<uint32_t>(p.rows) * kDepth * 2;
-    const int rank = p.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
-    const int tile = blockIdx.x / p.split;
-    const int n0 = tile / p.m_tiles * kTileN;            // clusters next to one another share the weight's tile
+    const int ctas = p.split * kG;                       // of the cluster
+    const int crank = ctas > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    const int half = kG == 2 ? crank & 1 : 0;            // of the pair
+    const int rank = crank / kG;                         // share of the contraction
+    const int x_rows = p.rows / kG;                      // tokens this CTA loads
+    const uint32_t stage_bytes = kWBytes + static_cast<uint32_t>(x_rows) * kDepth * 2;
+    const int tile = blockIdx.x / ctas;
+    // clusters next to one another share the weight's tile
+    const int n0 = (tile / p.m_tiles * kG + half) * kTileN;
     const int m0 = tile % p.m_tiles * p.rows;
     const int step0 = static_cast<int>(static_cast<int64_t>(p.steps) * rank / p.split);
     const int count = static_cast<int>(static_cast<int64_t>(p.steps) * (rank + 1) / p.split) - step0;
+
+    // the tile's tokens, and this CTA's share of them to finish
+    const int live = min(p.rows, p.m - m0);
+    const int t0 = live * rank / p.split, t1 = live * (rank + 1) / p.split;
+    const uint32_t recv_bytes = static_cast<uint32_t>((p.split - 1) * (t1 - t0)) * (kTileN * 4);
 
     if (threadIdx.x == 0) {
         failed = 0;
@@ -110,59 +177,95 @@ __global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __
             ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
         }
         ptx::mbar_init(ptx::smem_u32(&done_bar), 1);
+        ptx::mbar_init(ptx::smem_u32(&recv_bar), 1);
         ptx::fence_mbar_init();
+        if (recv_bytes) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&recv_bar), recv_bytes);
     }
     if (warp == 1) {
-        ptx::tmem_alloc<1>(ptx::smem_u32(&tmem_slot), static_cast<uint32_t>(p.tmem_cols));
-        ptx::tmem_relinquish<1>();
+        ptx::tmem_alloc<kG>(ptx::smem_u32(&tmem_slot), static_cast<uint32_t>(p.tmem_cols));
+        ptx::tmem_relinquish<kG>();
     }
     ptx::tc_fence_before();
     __syncthreads();
+    // the barriers of the cluster are ready (one CTA a share: when its sums are sent)
+    if constexpr (kG == 2)
+        ptx::cluster_sync();
+    else if (ctas > 1)
+        ptx::cluster_arrive_relaxed();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&p.w_map);
+        ptx::prefetch_tmap(&p.x_map);
+        // The weight's first stages into L2 while the stream's previous kernel ends.  Nothing is
+        // read by this: were that kernel to write the weight, L2 would hold what it wrote.
+        for (int i = 0; i < min(count, S) && p.prefetch; ++i) {
+            const int k0 = (step0 + i) * kDepth;
+            if (p.w_kn) {
+                ptx::tma_prefetch_2d(&p.w_map, n0, k0);
+                ptx::tma_prefetch_2d(&p.w_map, n0 + 64, k0);
+            } else {
+                ptx::tma_prefetch_2d(&p.w_map, k0, n0);
+            }
+        }
+    }
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
 
     if (warp == 0 && lane == 0) {
-        ptx::prefetch_tmap(&p.w_map);
-        ptx::prefetch_tmap(&p.x_map);
         int stage = 0, issued = 0;
         uint32_t phase = 1;
         bool ok = true;
+        auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
+            if constexpr (kG == 2)
+                ptx::tma_load_2d_pair(dst, m, c0, c1, bar);
+            else
+                ptx::tma_load_2d(dst, m, c0, c1, bar);
+        };
         for (int i = 0; i < count; ++i) {
-            const uint32_t full = ptx::smem_u32(&full_bar[stage]);
             if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), phase, p.wait_limit_ns)) {
                 ok = false;
                 break;
             }
+            const uint32_t mine = ptx::smem_u32(&full_bar[stage]);
+            const uint32_t full = kG == 2 && half ? ptx::mapa(mine, crank - 1) : mine;
             const uint32_t sw = ptx::smem_u32(smem) + stage * stage_bytes;
             const int k0 = (step0 + i) * kDepth;
-            ptx::mbar_arrive_expect_tx(full, stage_bytes);
+            // (the pair's first CTA counts the bytes of both)
+            if (!half) ptx::mbar_arrive_expect_tx(mine, stage_bytes * kG);
             if (p.w_kn) {
-                ptx::tma_load_2d(sw, &p.w_map, n0, k0, full);
-                ptx::tma_load_2d(sw + kWBytes / 2, &p.w_map, n0 + 64, k0, full);
+                load(sw, &p.w_map, n0, k0, full);
+                load(sw + kWBytes / 2, &p.w_map, n0 + 64, k0, full);
             } else {
-                ptx::tma_load_2d(sw, &p.w_map, k0, n0, full);
+                load(sw, &p.w_map, k0, n0, full);
             }
-            ptx::tma_load_2d(sw + kWBytes, &p.x_map, k0, m0, full);
+            load(sw + kWBytes, &p.x_map, k0, m0 + half * x_rows, full);
             ++issued;
             if (++stage == S) stage = 0, phase ^= 1u;
         }
         if (!ok) {
             atomicExch(&failed, 1);
             // the copies in flight land before the CTA can exit
-            for (int back = 1; back <= S && back <= issued; ++back) {
+            for (int back = 1; back <= S && back <= issued && !half; ++back) {
                 const int i = issued - back;
                 (void)ptx::mbar_wait(ptx::smem_u32(&full_bar[i % S]), static_cast<uint32_t>((i / S) & 1), p.wait_limit_ns);
             }
+            ptx::nanosleep(20000);
         }
-    } else if (warp == 1) {
-        const uint32_t idesc = ptx::idesc_f16(kBF16, false, kTileN, p.rows, p.w_kn != 0);
+    } else if (warp == 1 && !half) {
+        const uint32_t idesc = ptx::idesc_f16(kBF16, false, kTileN * kG, p.rows, p.w_kn != 0);
         const uint32_t s0 = ptx::smem_u32(smem);
         const uint64_t w_desc0 = p.w_kn ? ptx::smem_desc_sw128(s0, kDepth * 128, 1024) : ptx::smem_desc_sw128(s0, 16, 1024);
         const uint64_t x_desc0 = ptx::smem_desc_sw128(s0 + kWBytes, 16, 1024);
         const uint32_t w_kk = p.w_kn ? (2048u >> 4) : (32u >> 4);
         const uint32_t x_kk = 32u >> 4;
+        const uint16_t pair = static_cast<uint16_t>(3u << crank);
+        auto commit = [&](uint64_t *bar) {
+            if constexpr (kG == 2)
+                ptx::mma_commit_pair(ptx::smem_u32(bar), pair);
+            else
+                ptx::mma_commit<1>(ptx::smem_u32(bar));
+        };
         int stage = 0, in_block = 0, acc = 0, blocks = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -176,11 +279,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __
             const uint64_t off = static_cast<uint64_t>(stage) * (stage_bytes >> 4);
             const uint32_t d = tmem + static_cast<uint32_t>(acc * p.rows);
             // an accumulator's first stage starts it from zero
-            ptx::mma_f16_ss<1>(d, w_desc0 + off, x_desc0 + off, idesc, in_block > 0 || blocks >= p.accs ? 1u : 0u);
+            ptx::mma_f16_ss<kG>(d, w_desc0 + off, x_desc0 + off, idesc, in_block > 0 || blocks >= p.accs ? 1u : 0u);
 #pragma unroll
             for (int kk = 1; kk < kDepth / 16; ++kk)
-                ptx::mma_f16_ss<1>(d, w_desc0 + off + kk * w_kk, x_desc0 + off + kk * x_kk, idesc, 1u);
-            ptx::mma_commit<1>(ptx::smem_u32(&empty_bar[stage]));
+                ptx::mma_f16_ss<kG>(d, w_desc0 + off + kk * w_kk, x_desc0 + off + kk * x_kk, idesc, 1u);
+            commit(&empty_bar[stage]);
             if (++stage == S) stage = 0, phase ^= 1u;
             if (++in_block == kBlockSteps) {
                 in_block = 0;
@@ -190,115 +293,121 @@ __global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __
         }
         if (!ok && lane == 0) atomicExch(&failed, 1);
         // (also after giving up: the MMAs issued so far complete before TMEM is freed)
-        ptx::mma_commit_local<1>(ptx::smem_u32(&done_bar));
+        commit(&done_bar);
     }
     __syncwarp();
     // every thread waits (bounded) for the MMAs: from here on the ring is idle
     if (!ptx::mbar_wait(ptx::smem_u32(&done_bar), 0u, p.wait_limit_ns)) atomicExch(&failed, 1);
     __syncthreads();
-    const bool ok = failed == 0;
+    bool ok = failed == 0;
+    if (kG == 1 && ctas > 1) ptx::cluster_wait();
+    if (p.late) ptx::cluster_sync();
     float *part = reinterpret_cast<float *>(smem);   // [rows][128], over the ring
-    if (warp >= 4 && ok) {
+    if (ok) {
+        // warp w reads TMEM lanes 32 (w % 4) on, every other 16 tokens, two loads at a time
         ptx::tc_fence_after();
         const int q = warp & 3;
         const int used = min(p.accs, (count + kBlockSteps - 1) / kBlockSteps);
-        for (int c = 0; c < p.rows; c += 16) {
-            float sum[16];
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        for (int c = 16 * (warp >> 2); c < p.rows; c += 64) {
+            const bool two = c + 32 < p.rows;
+            float sum[2][16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+            for (int i = 0; i < 16; ++i) sum[0][i] = sum[1][i] = 0.0f;
             for (int a = 0; a < used; ++a) {
-                uint32_t r[16];
-                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * q) << 16) + a * p.rows + c, r);
-                ptx::tmem_ld_wait();
+                uint32_t r0[16], r1[16];
+                ptx::tmem_ld_32x32b_x16(lanes + a * p.rows + c, r0);
+                ptx::tmem_ld_32x32b_x16(lanes + a * p.rows + (two ? c + 32 : c), r1);
+                ptx::tmem_ld_wait16(r0);
+                ptx::tmem_ld_wait16(r1);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum[i] = __fadd_rn(sum[i], __uint_as_float(r[i]));
+                for (int i = 0; i < 16; ++i) {
+                    sum[0][i] = __fadd_rn(sum[0][i], __uint_as_float(r0[i]));
+                    sum[1][i] = __fadd_rn(sum[1][i], __uint_as_float(r1[i]));
+                }
             }
+            float *to = part + c * kTileN + 32 * q + lane;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[(c + i) * kTileN + 32 * q + lane] = sum[i];
+            for (int i = 0; i < 16; ++i) {
+                to[i * kTileN] = sum[0][i];
+                if (two) to[(i + 32) * kTileN] = sum[1][i];
+            }
         }
         ptx::tc_fence_before();
     }
-    if (!ok && threadIdx.x == 0 && p.status) atomicExch(p.status, -7);
-    __syncwarp();
-    if (p.split > 1)
-        ptx::cluster_sync();
-    else
-        __syncthreads();
-    // this CTA's share of the tile's tokens, the partial sums of all CTAs in rank order
-    const int t0 = p.rows * rank / p.split, t1 = p.rows * (rank + 1) / p.split;
-    const uint32_t part0 = ptx::smem_u32(part);
-    for (int e = t0 * 16 + static_cast<int>(threadIdx.x); e < t1 * 16 && ok; e += kSplitThreads) {
-        const int t = e >> 4, col = n0 + (e & 15) * 8;
-        const int row = m0 + t;
-        if (row >= p.m || col >= p.n) continue;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        const uint32_t at = part0 + static_cast<uint32_t>(e) * 32u;
-        for (int r = 0; r < p.split; ++r) {
-            const uint32_t a = p.split > 1 ? ptx::mapa(at, r) : at;
-            const float4 lo = load_cluster4(a), hi = load_cluster4(a + 16);
-            v[0] = __fadd_rn(v[0], lo.x), v[1] = __fadd_rn(v[1], lo.y), v[2] = __fadd_rn(v[2], lo.z), v[3] = __fadd_rn(v[3], lo.w);
-            v[4] = __fadd_rn(v[4], hi.x), v[5] = __fadd_rn(v[5], hi.y), v[6] = __fadd_rn(v[6], hi.z), v[7] = __fadd_rn(v[7], hi.w);
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
+    if (p.split > 1) {
+        // each other CTA's share of the tokens goes to it: its slot of this rank, among the
+        // ranks without its own
+        if (threadIdx.x < p.split && static_cast<int>(threadIdx.x) != rank) {
+            const int r = threadIdx.x, first = live * r / p.split, n = live * (r + 1) / p.split - first;
+            const uint32_t bytes = static_cast<uint32_t>(n) * (kTileN * 4);
+            if (bytes)
+                ptx::bulk_copy_to_cta(ptx::mapa(ptx::smem_u32(smem) + p.recv_off + (rank < r ? rank : rank - 1) * bytes, r * kG + half),
+                                      ptx::smem_u32(part) + static_cast<uint32_t>(first) * (kTileN * 4), bytes,
+                                      ptx::mapa(ptx::smem_u32(&recv_bar), r * kG + half));
         }
-        if (p.bias) {
-            float b[8];
-            load_bias8<kBF16>(p.bias, col, p.n, b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], b[i]);
-        }
-        const bool vec = p.aligned != 0;
-        if (p.preact) store8<kBF16>(p.preact, row * p.ldp, col, p.n, vec, v);
-        uint4 a[1] = {make_uint4(0, 0, 0, 0)};
-        if (p.aux) a[0] = load8(p.aux, row * p.ldaux, col, p.n, vec);
-        epilogue<kBF16, kEpi>(v, a, p.act, p.aux != nullptr);
-        store8<kBF16>(p.out, row * p.ldo, col, p.n, vec, v);
+        if (recv_bytes && !ptx::mbar_wait(ptx::smem_u32(&recv_bar), 0u, p.wait_limit_ns)) ok = false;
+        __syncwarp();
+        ptx::cluster_arrive_relaxed();   // (what this CTA was sent is here)
     }
+    if (!ok && p.status) atomicExch(p.status, -7);
+    const int col = n0 + 4 * lane;
+    if (ok && col < p.n) {
+        const float4 *own = reinterpret_cast<const float4 *>(part) + lane;
+        const float4 *recv = reinterpret_cast<const float4 *>(smem + p.recv_off) + lane;
+        // four tokens at a time hide one another's latency, where there are that many
+        if (t1 - t0 <= kSplitThreads / 32)
+            finish<kBF16, kEpi, 1>(p, m0, t0, t1, rank, col, own, recv);
+        else
+            finish<kBF16, kEpi, 4>(p, m0, t0, t1, rank, col, own, recv);
+    }
+    // no CTA leaves while its sums are on their way to another, nor half a pair before its MMAs' other half
     __syncwarp();
     if (p.split > 1)
-        ptx::cluster_sync();   // no CTA leaves while another reads its sums
-    else
-        __syncthreads();
+        ptx::cluster_wait();
+    else if constexpr (kG == 2)
+        ptx::cluster_sync();
+    __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc<1>(tmem, static_cast<uint32_t>(p.tmem_cols));
+        ptx::tmem_dealloc<kG>(tmem, static_cast<uint32_t>(p.tmem_cols));
     }
 }
 
-// The shape of a launch for one number of tokens a tile.
+// The shape of a launch.
 struct SplitShape {
-    int rows, m_tiles, split, stages, accs, tmem_cols, per_sm;
-    uint32_t smem;
+    int group, rows, m_tiles, split, per_sm, stages, accs, tmem_cols, late, prefetch;
+    uint32_t smem, recv_off;
     int64_t tiles;
+    float us;   // what it is expected to take
 };
 
-SplitShape split_shape(const LinearParams &p, int num_sms) {
-    SplitShape s = {};
-    s.rows = p.m <= 16 ? 16 : (p.m <= 32 ? 32 : (p.m <= 64 ? 64 : (p.m <= 128 ? 128 : 256)));
-    s.m_tiles = (p.m + s.rows - 1) / s.rows;
-    s.tiles = static_cast<int64_t>(s.m_tiles) * ((p.n + kTileN - 1) / kTileN);
-    const int steps = (p.k + kDepth - 1) / kDepth;
-    // short stages leave room for two CTAs an SM (and half of TMEM each)
-    s.per_sm = s.rows <= 64 ? 2 : 1;
-    const int64_t slots = static_cast<int64_t>(num_sms) * s.per_sm;
-    int split = static_cast<int>(slots / s.tiles);
-    if (split > kMaxCluster) split = kMaxCluster;
-    if (split > steps) split = steps;
-    if (split < 1) split = 1;
-    s.split = split;
-    const int most = (steps + split - 1) / split;   // stages of one CTA
-    const uint32_t stage = kWBytes + static_cast<uint32_t>(s.rows) * kDepth * 2;
+// Fetching the weight's first stages into L2 ahead of the stream's previous kernel's end
+// pays where two CTAs share each SM (one token, 4096 x 4096: 8.7 -> 7.8 us), and costs
+// where the loads follow at once (1024 x 8192, 64 CTAs: 7.2 -> 7.9).
+bool prefetch_pays(const SplitShape &s, int num_sms) { return s.group == 1 && s.tiles * s.split > num_sms; }
+
+// Shared memory and TMEM of a launch whose tiles and split are chosen.
+void fit_split(SplitShape &s, int steps, int num_sms) {
+    const int most = (steps + s.split - 1) / s.split;   // stages of one CTA
+    const uint32_t stage = kWBytes + static_cast<uint32_t>(s.rows / s.group) * kDepth * 2;
     const uint32_t room = s.per_sm == 2 ? 110u * 1024u : 220u * 1024u;
-    s.stages = static_cast<int>(room / stage);
+    const uint32_t sums = static_cast<uint32_t>(s.rows) * kTileN * 4;   // this CTA's, over the ring
+    const uint32_t recv = static_cast<uint32_t>((s.split - 1) * ((s.rows + s.split - 1) / s.split)) * kTileN * 4;
+    // the others' sums beside the ring where that leaves it four stages, over it otherwise
+    s.stages = static_cast<int>((room - recv) / stage);
+    s.late = s.stages < 4 && s.stages < most;
+    if (s.late) s.stages = static_cast<int>(room / stage);
     if (s.stages > kMaxStages) s.stages = kMaxStages;
     if (s.stages > most) s.stages = most;
-    uint32_t bytes = s.stages * stage;
-    const uint32_t sums = static_cast<uint32_t>(s.rows) * kTileN * 4;
-    if (bytes < sums) bytes = sums;
+    const uint32_t ring = s.stages * stage;
+    s.recv_off = s.late || ring < sums ? sums : ring;
+    const uint32_t bytes = ring > s.recv_off + recv ? ring : s.recv_off + recv;
     s.smem = bytes + 1024;   // (slack to align the ring)
     const int blocks = (most + kBlockSteps - 1) / kBlockSteps;
-    const int cols = s.per_sm == 2 ? 256 : 512;
-    s.accs = cols / s.rows;
+    s.accs = (s.per_sm == 2 ? 256 : 512) / s.rows;
     if (s.accs > blocks) s.accs = blocks;
     s.tmem_cols = 32;
     while (s.tmem_cols < s.accs * s.rows) s.tmem_cols *= 2;
@@ -309,12 +418,93 @@ SplitShape split_shape(const LinearParams &p, int num_sms) {
     // CTAs that fit beside one another find their columns free.
     const uint32_t share = static_cast<uint32_t>(s.tmem_cols) * (kSmemPerSm / 512) - kSmemOverhead;
     if (s.smem < share) s.smem = share;
-    return s;
+    s.prefetch = prefetch_pays(s, num_sms);
 }
 
-template <bool kBF16, int kEpi>
+// Clusters of `ctas` CTAs, `per_sm` an SM, that the device runs at once.  A cluster stays
+// inside one GPC, so fewer than the SMs would hold; asked once for each kind.
+int64_t clusters_at_once(int ctas, int per_sm, int num_sms) {
+    if (ctas == 1) return static_cast<int64_t>(num_sms) * per_sm;
+    static std::atomic<int> known[64][kMaxCluster + 1][2];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return num_sms * per_sm / ctas;
+    std::atomic<int> &slot = known[dev][ctas][per_sm - 1];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n == 0) {
+        const int smem = per_sm == 2 ? 112 * 1024 : 222 * 1024;
+        auto kern = linear_split_kernel<true, EPI_FORWARD, 1>;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas * num_sms), 1, 1);
+        cfg.blockDim = dim3(kSplitThreads, 1, 1);
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - kSmemStatic) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = num_sms * per_sm / ctas > 0 ? num_sms * per_sm / ctas : 1;
+        }
+        slot.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// What a shape takes, in us, fitted to measurements on GB300: launch, set-up and the cluster's
+// barriers; the stages, at the 110 bytes a ns that an SM receives and the rate of device
+// memory, which reads the weight once (the root of the squares' sum, since the two do
+// not overlap wholly); and per token of the tile the way from TMEM to the output, and to
+// the other CTAs.  Over 50 shapes (1 to 1274 tokens, 64 to 16384 columns and depth) the
+// shape it chose took at most 8% more than the best one, but for three.
+float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sms) {
+    const int64_t clusters = clusters_at_once(s.group * s.split, s.per_sm, num_sms);
+    const int64_t units = s.tiles;   // a cluster each
+    const float waves = static_cast<float>((units + clusters - 1) / clusters);
+    const int64_t resident = (units < clusters ? units : clusters) * s.group * s.split;
+    const float beside = resident > num_sms ? static_cast<float>(resident) / num_sms : 1.0f;
+    const float stage = static_cast<float>(kWBytes) + static_cast<float>(s.rows / s.group) * kDepth * 2;
+    const float stages = waves * (static_cast<float>(steps) / s.split) * stage * beside / 110e3f;
+    const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 2.0f / 6.9e6f;
+    const float stream = sqrtf(stages * stages + read * read);
+    float join = 0.012f * s.rows;
+    if (s.split > 1) join += 0.5f + 0.016f * s.rows * (s.split - 1) / s.split + (s.rows > 128 ? 1.5f : 0.0f);
+    const float ahead = prefetch_pays(s, num_sms) ? 0.8f : 0.0f;
+    return 3.3f + (s.group == 2 ? 0.6f : 0.0f) + stream + waves * join - ahead;
+}
+
+SplitShape best_split(const LinearParams &p, int num_sms) {
+    const int steps = (p.k + kDepth - 1) / kDepth;
+    SplitShape best = {};
+    // tiles of at most 64 tokens by single CTAs; of 64, 128 or 256 by pairs
+    const struct { int group, most; } forms[4] = {{1, 64}, {2, 64}, {2, 128}, {2, 256}};
+    for (const auto &f : forms) {
+        if (f.group == 2 && p.m <= 32) continue;
+        if (f.group == 2 && f.most > 64 && p.m <= f.most / 2) continue;   // the smaller tile does the same
+        SplitShape s = {};
+        s.group = f.group;
+        const int unit = f.group == 1 ? 16 : 32, cols = kTileN * f.group;
+        s.m_tiles = (p.m + f.most - 1) / f.most;
+        s.rows = ((p.m + s.m_tiles - 1) / s.m_tiles + unit - 1) / unit * unit;
+        s.tiles = static_cast<int64_t>(s.m_tiles) * ((p.n + cols - 1) / cols);
+        // two CTAs an SM where their stages are short: 32 tokens, 4096 x 4096, 9.2 us against 9.3;
+        // 64 tokens: 11.3 against 9.9
+        s.per_sm = f.group == 1 && s.rows <= 32 ? 2 : 1;
+        for (s.split = 1; s.split <= kMaxCluster / f.group && s.split <= steps; ++s.split) {
+            s.us = split_us(s, p, steps, num_sms);
+            if (best.group == 0 || s.us < best.us) best = s;
+        }
+    }
+    fit_split(best, steps, num_sms);
+    return best;
+}
+
+template <bool kBF16, int kEpi, int kG>
 cudaError_t launch_split(const SplitParams &p, const SplitShape &s, cudaStream_t stream) {
-    auto kern = linear_split_kernel<kBF16, kEpi>;
+    auto kern = linear_split_kernel<kBF16, kEpi, kG>;
     thread_local unsigned long long ready_ctx = 0;
     const unsigned long long ctx = current_context_id();
     if (ctx == 0 || ctx != ready_ctx) {
@@ -328,15 +518,15 @@ cudaError_t launch_split(const SplitParams &p, const SplitShape &s, cudaStream_t
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(s.split);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(s.split * kG);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(s.tiles * s.split), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(s.tiles * s.split * kG), 1, 1);
     cfg.blockDim = dim3(kSplitThreads, 1, 1);
     cfg.dynamicSmemBytes = s.smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = s.split > 1 ? 2 : 1;
+    cfg.numAttrs = s.split * kG > 1 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -351,19 +541,24 @@ bool linear_layout_fits(const LinearParams &p) {
 }
 
 bool linear_prefers_split(const LinearParams &p, int num_sms) {
-    (void)num_sms;
     // the tiles' outputs leave by tensor copies, which write whole 16-byte units: a row
     // that ends inside one would have up to 7 elements past its end overwritten
     if (p.n % 8 != 0) return true;
-    return p.m <= 256;
+    if (p.m <= 64) return true;
+    // the 256 x 256 tiles: 5.7 us and 0.28 a 64-deep stage for each wave of them (4096 deep, 1,
+    // 3 and 4 waves: 23.2, 60.9 and 79.0 us; 100 deep: 6.3).  Where the two cross, at (m, 4096) with k = 4096:
+    // 384 tokens 16.8 us split against 23.3, 512 tokens 21.2 against 23.4, 777 24.8 against 24.5.
+    const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256), pairs = num_sms / 2;
+    const float us = 5.7f + 0.28f * static_cast<float>((tiles + pairs - 1) / pairs) * ((p.k + kDepth - 1) / kDepth);
+    return best_split(p, num_sms).us < us;
 }
 
 cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, cudaStream_t stream) {
-    const SplitShape s = split_shape(lp, num_sms);
-    if (s.tiles * s.split > INT32_MAX) return cudaErrorInvalidValue;
+    const SplitShape s = best_split(lp, num_sms);
+    if (s.tiles * s.split * s.group > INT32_MAX) return cudaErrorInvalidValue;
     SplitParams p = {};
     const uint64_t m = lp.m, n = lp.n, k = lp.k;
-    bool ok = host::make_map16(&p.x_map, lp.x, k, m, kDepth, static_cast<uint32_t>(s.rows), lp.ldx);
+    bool ok = host::make_map16(&p.x_map, lp.x, k, m, kDepth, static_cast<uint32_t>(s.rows / s.group), lp.ldx);
     ok = ok && (lp.w_nk ? host::make_map16(&p.w_map, lp.w, k, n, kDepth, kTileN, lp.ldw)
                         : host::make_map16(&p.w_map, lp.w, n, k, 64, kDepth, lp.ldw));
     if (!ok) return cudaErrorInvalidValue;
@@ -374,13 +569,17 @@ cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, 
     p.w_kn = !lp.w_nk;
     p.rows = s.rows, p.m_tiles = s.m_tiles, p.split = s.split;
     p.stages = s.stages, p.accs = s.accs, p.tmem_cols = s.tmem_cols;
-    p.aligned = 1;   // linear_layout_fits
+    p.recv_off = s.recv_off, p.late = s.late, p.prefetch = s.prefetch;
     p.act = activation_of(lp.act);
     p.status = device_status_word();
     p.wait_limit_ns = host::kWaitLimitNs;
-    if (lp.aux_mode == AUX_ACT_GRAD)
-        return bf16 ? launch_split<true, EPI_BACKWARD>(p, s, stream) : launch_split<false, EPI_BACKWARD>(p, s, stream);
-    return bf16 ? launch_split<true, EPI_FORWARD>(p, s, stream) : launch_split<false, EPI_FORWARD>(p, s, stream);
+    const bool back = lp.aux_mode == AUX_ACT_GRAD;
+    if (s.group == 1) {
+        if (back) return bf16 ? launch_split<true, EPI_BACKWARD, 1>(p, s, stream) : launch_split<false, EPI_BACKWARD, 1>(p, s, stream);
+        return bf16 ? launch_split<true, EPI_FORWARD, 1>(p, s, stream) : launch_split<false, EPI_FORWARD, 1>(p, s, stream);
+    }
+    if (back) return bf16 ? launch_split<true, EPI_BACKWARD, 2>(p, s, stream) : launch_split<false, EPI_BACKWARD, 2>(p, s, stream);
+    return bf16 ? launch_split<true, EPI_FORWARD, 2>(p, s, stream) : launch_split<false, EPI_FORWARD, 2>(p, s, stream);
 }
 
 }  // namespace mc2

@@ -114,6 +114,21 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of a cluster barrier, for work in between.  The arrival publishes
+// nothing (no fence): what the others are to see needs one of its own, as
+// fence_mbar_init for barriers just initialised.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Bulk copy from this CTA's shared memory to a CTA of its cluster (16-byte aligned
+// addresses, bytes a multiple of 16); completion is signalled on `bar` there. `dst` and
+// `bar` are shared::cluster addresses.
+__device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // Cluster launch control: ask to cancel the launch of a cluster of this grid
 // that has not started; the 16-byte answer goes to `resp` in every CTA of this
 // cluster and completes 16 transaction bytes on `bar` in each.
@@ -233,6 +248,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
         : "memory");
 }
 
+// Fetch a box of a tensor map into L2 (no data reaches this CTA).
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *m, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
+
 // 2-D tiled store shared -> global (bulk async-group completion).
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, int32_t c0, int32_t c1, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -334,6 +356,16 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
                 bar),
             "h"(static_cast<uint16_t>(3))
             : "memory");
+}
+
+// The same for a CTA pair inside a larger cluster: `mask` has the bits of the pair's two ranks.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            bar),
+        "h"(mask)
+        : "memory");
 }
 
 // Arrive on this CTA's own `bar` once all previously issued tcgen05 ops of
