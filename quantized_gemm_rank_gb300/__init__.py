@@ -1,8 +1,9 @@
 """GB300 (sm_103a) MC2 fused linears: Python binding of the C ABI in
 ``include/mc2_gb300.h``.
 
-Argument marshalling only: every step of both operations runs in the CUDA
-library ``libmc2_gb300.so`` (built in-tree by :mod:`.build`).  PyTorch
+Argument marshalling only: every step of the operations runs in the CUDA
+library ``libmc2_gb300.so`` (built in-tree by :mod:`.build`).  The calls around
+the linears marshal their regular case in an extension module, ``_native.so``.  PyTorch
 provides device memory and streams.  There is no CPU fallback: if the library
 cannot be built or loaded, importing the functions raises.
 
@@ -23,6 +24,8 @@ and, around the linears:
 from __future__ import annotations
 
 import ctypes
+import functools
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -112,6 +115,22 @@ def lib() -> ctypes.CDLL:
         L.mc2_test_expire_next_flag_waits.restype = _INT
         _lib = L
     return _lib
+
+
+_native_module = None
+
+
+def _native():
+    """The extension module of the binding (built first if its source changed)."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        path = _build.build_native()
+        spec = importlib.util.spec_from_file_location(__name__ + "._native", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native_module = module
+    return _native_module
 
 
 def library_path() -> str:
@@ -498,6 +517,14 @@ def _opt_rows(t: Optional[torch.Tensor], shape, dtype, what: str, cur: int):
     return (None, 0) if t is None else _rows(t, shape, dtype, what, cur)
 
 
+_contiguous = torch.contiguous_format
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A new contiguous tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=_contiguous)
+
+
 def _leading(t: torch.Tensor, what: str) -> int:
     """The number of rows of a tensor of two or more dimensions."""
     if t.dim() == 2:
@@ -530,6 +557,13 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optiona
     ``residual`` (None without a residual); outputs not asked for are None.
     """
     cur = _current_device()
+    if cur >= 0:
+        r = (_native_module or _native()).add_rms_norm(x, weight, residual, eps, quant_mode, q_dtype, with_out, with_rstd,
+                                                       out, residual_out, rstd, q, scale, cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
     shape, dt, dev = x.shape, x.dtype, x.device
     m, h = _leading(x, "x"), shape[-1]
     xp, ldx = _rows(x, shape, dt, "x", cur)
@@ -546,7 +580,7 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optiona
     if residual_out is not None:
         rop, ldro = _rows(residual_out, shape, dt, "residual_out", cur)
     elif residual is not None:
-        residual_out = torch.empty(shape, dtype=dt, device=dev)
+        residual_out = _like(x)
         rop, ldro = residual_out.data_ptr(), h
     sp = None
     if rstd is not None or with_rstd:
@@ -581,6 +615,7 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optiona
     return {"out": out if op is not None else None, "residual": residual_out, "rstd": rstd, "q": q, "scale": scale}
 
 
+@functools.lru_cache(maxsize=1024)
 def mc2_rms_norm_grad_workspace(m: int, h: int) -> int:
     nbytes = ctypes.c_size_t(0)
     _check(lib().mc2_rms_norm_grad_workspace(m, h, ctypes.byref(nbytes)))
@@ -599,6 +634,13 @@ def mc2_rms_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, r
     residual, dw of the weight (None without ``with_weight``).
     """
     cur = _current_device()
+    if cur >= 0:
+        r = (_native_module or _native()).rms_norm_grad(dy, x, weight, rstd, dres, with_weight, dx, dw, workspace, cur,
+                                                        _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
     shape, dt, dev = x.shape, x.dtype, x.device
     m, h = _leading(x, "x"), shape[-1]
     xp, ldx = _rows(x, shape, dt, "x", cur)
@@ -608,14 +650,14 @@ def mc2_rms_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, r
     sp = _arg(rstd, shape[:-1], torch.float32, "rstd", cur)
     drp, lddr = _opt_rows(dres, shape, dt, "dres", cur)
     if dx is None:
-        dx = torch.empty(shape, dtype=dt, device=dev)
+        dx = _like(x)
         dxp, lddx = dx.data_ptr(), h
     else:
         dxp, lddx = _rows(dx, shape, dt, "dx", cur)
     dwp, wsp, nbytes = None, None, 0
     if with_weight or dw is not None:
         if dw is None:
-            dw = torch.empty((h,), dtype=wt, device=dev)
+            dw = _like(weight)
             dwp = dw.data_ptr()
         else:
             dwp = _arg(dw, (h,), wt, "dw", cur)
@@ -655,6 +697,13 @@ def mc2_matmul_bias_act(x: torch.Tensor, w: torch.Tensor, *, w_is_nk: bool = Tru
     """
     cur = _current_device()
     act = _activation(activation)
+    if cur >= 0:
+        r = (_native_module or _native()).matmul_bias_act(x, w, w_is_nk, bias, act, residual, with_preact, out, preact,
+                                                          cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
     dt, dev = x.dtype, x.device
     m, k = _leading(x, "x"), x.shape[-1]
     if w.dim() != 2:
@@ -691,6 +740,12 @@ def mc2_matmul_act_grad(dy: torch.Tensor, w: torch.Tensor, z: torch.Tensor, *, a
     """
     cur = _current_device()
     act = _activation(activation)
+    if cur >= 0:
+        r = (_native_module or _native()).matmul_act_grad(dy, w, z, act, w_is_nk, dz, cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
     dt = dy.dtype
     m, n = _leading(dy, "dy"), dy.shape[-1]
     if w.dim() != 2:
@@ -717,6 +772,12 @@ def mc2_act_grad(dy: torch.Tensor, z: torch.Tensor, *, activation: str, dz: Opti
     ``preact`` for a gradient ``dy`` of its ``out``."""
     cur = _current_device()
     act = _activation(activation)
+    if cur >= 0:
+        r = (_native_module or _native()).act_grad(dy, z, act, dz, cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
     shape, dt = dy.shape, dy.dtype
     m = _leading(dy, "dy")
     dyp, lddy = _rows(dy, shape, dt, "dy", cur)

@@ -1,8 +1,9 @@
 """Build step for the CUDA libraries (nvcc, sm_103a only).
 
 Compiles ``csrc/*.cu`` in parallel into ``_build/`` and links
-``libmc2_gb300.so`` (the operations) next to this file, and ``calib/*.cu``
-into ``libmc2_calib.so`` (a measurement probe that only the benchmark loads).
+``libmc2_gb300.so`` (the operations) next to this file, ``calib/*.cu``
+into ``libmc2_calib.so`` (a measurement probe that only the benchmark loads),
+and ``binding/native.cpp`` into ``_native.so`` (the Python binding's fast calls).
 Rebuilds a library only when one of its sources or the public header is newer
 than it.
 """
@@ -11,6 +12,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,8 @@ CALIB = os.path.join(HERE, "calib")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmc2_gb300.so")
 CALIB_LIB = os.path.join(HERE, "libmc2_calib.so")
+NATIVE_SRC = os.path.join(HERE, "binding", "native.cpp")
+NATIVE_LIB = os.path.join(HERE, "_native.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -66,7 +70,7 @@ def _build_one(lib, src_dir, force, verbose, extra_flags):
     with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         objs = list(ex.map(compile_one, srcs))
     tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
+    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", f"-soname={os.path.basename(lib)}", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
@@ -79,6 +83,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     return _build_one(LIB, CSRC, force, verbose, extra_flags)
 
 
+def build_native(force: bool = False, verbose: bool = False) -> str:
+    """Build the binding's extension module (and return its path)."""
+    deps = [NATIVE_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    if not force and os.path.exists(NATIVE_LIB) and all(os.path.getmtime(d) <= os.path.getmtime(NATIVE_LIB) for d in deps):
+        return NATIVE_LIB
+    import torch
+    t = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           os.path.join(ROOT, "include")]
+    lib = os.path.join(t, "lib")
+    tmp = NATIVE_LIB + f".tmp{os.getpid()}"
+    # the library of the operations by its name, found beside the module; torch's by theirs
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{i}" for i in inc], NATIVE_SRC, "-o", tmp, f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+           f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {os.path.basename(NATIVE_SRC)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE_LIB)
+    return NATIVE_LIB
+
+
 def build_calib(force: bool = False, verbose: bool = False) -> str:
     """Build the benchmark's calibration probe library (and return its path)."""
     return _build_one(CALIB_LIB, CALIB, force, verbose, ())
@@ -87,4 +116,5 @@ def build_calib(force: bool = False, verbose: bool = False) -> str:
 if __name__ == "__main__":
     import sys
     print(build(force="--force" in sys.argv, verbose=True))
+    print(build_native(force="--force" in sys.argv, verbose=True))
     print(build_calib(force="--force" in sys.argv, verbose=True))

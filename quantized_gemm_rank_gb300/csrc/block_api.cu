@@ -93,9 +93,9 @@ int mc2_add_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t l
                      void *residual_out, int64_t ldro, float *rstd_out, int quant_mode, int q_dtype, void *q_out,
                      void *scale_out, void *stream) {
     clear_error();
-    if (!x || !weight) return fail(MC2_ERR_NULL, "x and weight are required");
     if (int st = check_norm_types(dtype, weight_dtype)) return st;
     if (int st = check_norm_sizes(m, h)) return st;
+    if (!x || !weight) return fail(MC2_ERR_NULL, "x and weight are required");
     if (!(eps >= 0.0f) || std::isinf(eps)) return fail(MC2_ERR_SHAPE, "eps must be finite and at least 0");
     int qmode = mc2::QM_NONE;
     switch (quant_mode) {
@@ -163,10 +163,10 @@ int mc2_rms_norm_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, 
                       const float *rstd, const void *dres, int64_t lddres, int64_t m, int64_t h, int dtype, void *dx,
                       int64_t lddx, void *dw, void *workspace, size_t workspace_bytes, void *stream) {
     clear_error();
-    if (!dy || !x || !weight || !rstd || !dx) return fail(MC2_ERR_NULL, "dy, x, weight, rstd and dx are required");
     if (int st = check_norm_types(dtype, weight_dtype)) return st;
     size_t need = 0;
     if (int st = mc2_rms_norm_grad_workspace(m, h, &need)) return st;
+    if (!dy || !x || !weight || !rstd || !dx) return fail(MC2_ERR_NULL, "dy, x, weight, rstd and dx are required");
     const size_t es = elem_size(dtype);
     if (int st = check_rows("dy", dy, lddy, m, h, es)) return st;
     if (int st = check_rows("x", x, ldx, m, h, es)) return st;
@@ -208,8 +208,8 @@ int mc2_matmul_bias_act(const void *x, int64_t ldx, const void *w, int64_t ldw, 
                         int64_t k, const void *bias, int act, const void *residual, int64_t ldr, int dtype, void *out,
                         int64_t ldo, void *preact, int64_t ldp, void *stream) {
     clear_error();
-    if (!x || !w || !out) return fail(MC2_ERR_NULL, "x, w and out are required");
     if (int st = check_product(m, n, k, act, dtype)) return st;
+    if (!x || !w || !out) return fail(MC2_ERR_NULL, "x, w and out are required");
     if (int st = check_rows("x", x, ldx, m, k, 2)) return st;
     if (int st = check_rows("w", w, ldw, w_is_nk ? n : k, w_is_nk ? k : n, 2)) return st;
     if (int st = check_rows("out", out, ldo, m, n, 2)) return st;
@@ -236,8 +236,8 @@ int mc2_matmul_act_grad(const void *dy, int64_t lddy, const void *w, int64_t ldw
                         int64_t ldz, int act, int64_t m, int64_t n, int64_t k, int dtype, void *dz, int64_t lddz,
                         void *stream) {
     clear_error();
-    if (!dy || !w || !z || !dz) return fail(MC2_ERR_NULL, "dy, w, z and dz are required");
     if (int st = check_product(m, n, k, act, dtype)) return st;
+    if (!dy || !w || !z || !dz) return fail(MC2_ERR_NULL, "dy, w, z and dz are required");
     if (int st = check_rows("dy", dy, lddy, m, n, 2)) return st;
     if (int st = check_rows("w", w, ldw, w_is_nk ? n : k, w_is_nk ? k : n, 2)) return st;
     if (int st = check_rows("z", z, ldz, m, k, 2)) return st;
@@ -257,8 +257,8 @@ int mc2_matmul_act_grad(const void *dy, int64_t lddy, const void *w, int64_t ldw
 int mc2_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int act, int64_t m, int64_t n, int dtype,
                  void *dz, int64_t lddz, void *stream) {
     clear_error();
-    if (!dy || !z || !dz) return fail(MC2_ERR_NULL, "dy, z and dz are required");
     if (int st = check_product(m, n, 1, act, dtype)) return st;
+    if (!dy || !z || !dz) return fail(MC2_ERR_NULL, "dy, z and dz are required");
     if (int st = check_rows("dy", dy, lddy, m, n, 2)) return st;
     if (int st = check_rows("z", z, ldz, m, n, 2)) return st;
     if (int st = check_rows("dz", dz, lddz, m, n, 2)) return st;
