@@ -89,6 +89,7 @@ constexpr int kGroupMNarrow = 2;                 // ... and on the float path wh
 // 64-column 16-bit slab (128-byte rows, 128-byte swizzle).
 constexpr uint32_t kEpiSlabBytes = 32 * 128;
 constexpr uint32_t kEpiStageBytes = kNumEpiWarps * kEpiSlabBytes;
+constexpr uint32_t kEpiPieceBytes = 32 * 64;   // a slab as two buffers of 32 rows x 32 columns (kEpi)
 
 // kTmaOut: reserve the epilogue's shared staging slabs (8 x 4 KiB) after the
 // stage ring; every instantiation of the GEMM stores its outputs through them.
@@ -158,8 +159,9 @@ struct GemmParams {
     CUtensorMap out_rank_maps[kMaxAMaps];
     int rs_tma;
     // fused-epilogue instantiations only (kEpi): see epilogue.cuh
-    CUtensorMap aux_map;   // the second matrix the epilogue reads, box and swizzle as out_map
-    CUtensorMap pre_map;   // the pre-activation output, the same
+    // (out_map too: boxes of 32 rows x 32 columns, 64-byte swizzle)
+    CUtensorMap aux_map;   // the second matrix the epilogue reads
+    CUtensorMap pre_map;   // the pre-activation output
     int has_aux, has_pre;
     Activation act;
 };
@@ -399,6 +401,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
     uint64_t *walk_resp = bars + 3 * S + 14;  // kDyn: two 16-byte answers (16-byte aligned)
     uint64_t *walk_full = bars + 3 * S + 18;  // kDyn: answer landed (this CTA)
     uint64_t *walk_free = bars + 3 * S + 20;  // kDyn: answer read by every role (the leader's counts both CTAs)
+    uint64_t *aux_bar = bars + 3 * S + 24;    // kEpi: per epilogue warp and buffer: its piece of the second matrix landed
     // the epilogue's output slabs, after the 1 KiB barrier area (1024-byte aligned)
     uint8_t *epi_stage = smem + S * Cfg::kStageBytes + 1024;
     __shared__ int abort_flag_s;
@@ -443,6 +446,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
         }
         ptx::mbar_init(ptx::smem_u32(drain_bar), 1);
         for (int e = 0; e < kNumEpiWarps; ++e) ptx::mbar_init(ptx::smem_u32(&skr_bar[e]), 1);
+        if constexpr (kEpi != EPI_PLAIN)
+            for (int e = 0; e < 2 * kNumEpiWarps; ++e) ptx::mbar_init(ptx::smem_u32(&aux_bar[e]), 1);
         if constexpr (kDyn) {
             // releases per answer: per CTA the producer, the epilogue warps and the
             // gathered-store lane, plus the leader's MMA warp
@@ -851,13 +856,9 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
         const int half = (warp - 4) >> 2;     // which 128 of the 256 columns
         const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
         uint32_t acc_iter = 0;
-        uint32_t skr_phase = 0;   // phase of this warp's stream-K partial barrier (kEpi: of its aux barrier)
-        // one lane asks for 32 rows x 64 columns of the second matrix, into the warp's slab
-        auto load_aux = [&](int e, int col, int row0) {
-            const uint32_t bar = ptx::smem_u32(&skr_bar[e]);
-            ptx::mbar_arrive_expect_tx(bar, kEpiSlabBytes);
-            ptx::tma_load_2d(ptx::smem_u32(epi_stage) + e * kEpiSlabBytes, &p.aux_map, col, row0, bar);
-        };
+        uint32_t skr_phase = 0;   // phase of this warp's stream-K partial barrier
+        uint32_t aux_phase = 0;   // kEpi: bit i, the phase of aux_bar of buffer i
+        (void)aux_phase;
         TileWalk<kDyn> walk = walk0;
         Work w;
         while (walk.template next<kPair>(w, p, abort_flag)) {
@@ -872,108 +873,147 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 // unrolled code past the instruction cache's size: an (8192, 8192) output with
                 // k = 1024 and gelu took 159 us that way and takes 123 this way, with k = 7168, a
                 // bias and the pre-activation 816 and 588).
+                // The warp's 128 columns go in four pieces of 32, through two buffers of 32
+                // rows x 64 bytes (64-byte swizzle: chunk j of row r at chunk j ^ (r / 2 % 4)), so
+                // that a piece's store is read while the next piece is worked on.
                 const int row0 = mb * Cfg::kTileM + kBM * static_cast<int>(cr) + 32 * q;
-                uint8_t *const slab = epi_stage + (warp - 4) * kEpiSlabBytes;
-                uint8_t *const mine = slab + lane * 128;
-                const uint32_t bar = ptx::smem_u32(&skr_bar[warp - 4]);
-                const bool some = colh < p.n;
-                // The first slab of the second matrix comes in while the MMAs run; it is
-                // free once the previous tile's stores have read it.  With a
-                // pre-activation output the slab is needed for that first.
-                const bool early = p.has_aux && !p.has_pre && some;
-                if (early && lane == 0) {
+                const uint32_t buf0 = ptx::smem_u32(epi_stage) + static_cast<uint32_t>(warp - 4) * kEpiSlabBytes;
+                uint8_t *const mine = epi_stage + (warp - 4) * kEpiSlabBytes + lane * 64;
+                const int flip = (lane >> 1) & 3;
+                const int pieces = min(4, (p.n - colh + 31) / 32);   // (none if colh >= n)
+                auto load_aux = [&](int c) {
+                    const uint32_t bar = ptx::smem_u32(&aux_bar[2 * (warp - 4) + (c & 1)]);
+                    ptx::mbar_arrive_expect_tx(bar, kEpiPieceBytes);
+                    ptx::tma_load_2d(buf0 + (c & 1) * kEpiPieceBytes, &p.aux_map, colh + 32 * c, row0, bar);
+                };
+                // the second matrix's first pieces come in while the MMAs run (the buffers are
+                // free once the last tile's stores have read them)
+                const int early = p.has_aux && !p.has_pre ? min(pieces, 2) : 0;
+                if (lane == 0 && early > 0) {
                     ptx::bulk_wait_group_read<0>();
-                    load_aux(warp - 4, colh, row0);
+                    for (int c = 0; c < early; ++c) load_aux(c);
                 }
                 const uint32_t b = acc_iter & 1u;
                 const bool got = wait_or_abort<kPair>(ptx::smem_u32(&tfull_bar[b]), (acc_iter >> 1) & 1u, p, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) {
-                    // a copy asked for above lands before the CTA can exit
-                    if (early) (void)ptx::mbar_wait(bar, skr_phase, p.wait_limit_ns);
+                    // copies asked for above land before the CTA can exit
+                    for (int c = 0; c < early; ++c)
+                        (void)ptx::mbar_wait(ptx::smem_u32(&aux_bar[2 * (warp - 4) + c]), (aux_phase >> c) & 1u, p.wait_limit_ns);
                     break;
                 }
                 ptx::tc_fence_after();
                 const uint32_t acc = tmem_base + lane_addr + b * kBN + half * 128;
-                // kCols sums of this lane's row with their bias
-                constexpr int kCols = 32;
-                auto sums = [&](int c, float (&v)[kCols]) {
-                    uint32_t r[kCols];
-                    ptx::tmem_ld_32x32b_x32(acc + c, r);
-                    ptx::tmem_ld_wait32(r);
+                const bool bias_whole = p.bias16 != nullptr && colh + 128 <= p.n && (reinterpret_cast<uintptr_t>(p.bias16) & 15u) == 0;
+                // 32 outputs of this lane's row, rounded, to buffer i
+                auto put = [&](int i, const float (&v)[32]) {
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) v[i] = __uint_as_float(r[i]);
-                    if (p.bias16 != nullptr) {
-#pragma unroll
-                        for (int j = 0; j < kCols / 8; ++j) {
-                            float b8[8];
-                            load_bias8<kBF16>(p.bias16, colh + c + 8 * j, p.n, b8);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[8 * j + i] = __fadd_rn(v[8 * j + i], b8[i]);
-                        }
-                    }
-                };
-                // ... rounded, to their place in the slab (vectors j0, j0 + 1, ...)
-                auto put = [&](int j0, const float (&v)[kCols]) {
-#pragma unroll
-                    for (int j = 0; j < kCols / 8; ++j)
-                        *reinterpret_cast<uint4 *>(mine + (((j0 + j) ^ (lane & 7)) << 4)) =
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4 *>(mine + i * kEpiPieceBytes + ((j ^ flip) << 4)) =
                             make_uint4(pack2<kBF16>(v[8 * j], v[8 * j + 1]), pack2<kBF16>(v[8 * j + 2], v[8 * j + 3]),
                                        pack2<kBF16>(v[8 * j + 4], v[8 * j + 5]), pack2<kBF16>(v[8 * j + 6], v[8 * j + 7]));
                 };
-                for (int sl = 0; sl < 2 && ok; ++sl) {
-                    const int scol = colh + sl * 64;
-                    if (scol >= p.n) break;
-                    // the slab leaves once every lane has written it
-                    auto send = [&](const CUtensorMap *map) {
-                        ptx::fence_proxy_async_smem();
+                // buffer i leaves for piece c's place once every lane has written it
+                auto send = [&](const CUtensorMap *map, int i, int c) {
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_2d(map, colh + 32 * c, row0, buf0 + i * kEpiPieceBytes);
+                        ptx::bulk_commit_group();
+                    }
+                };
+                // the buffer written next is free: all stores but the latest have been read
+                auto reuse = [&]() {
+                    if (lane == 0) ptx::bulk_wait_group_read<1>();
+                    __syncwarp();
+                };
+#pragma unroll 1
+                for (int c = 0; c < pieces; ++c) {
+                    float v[32];
+                    {
+                        uint32_t r[32];
+                        ptx::tmem_ld_32x32b_x32(acc + 32 * c, r);
+                        ptx::tmem_ld_wait32(r);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                    }
+                    if (c == pieces - 1) {
+                        // every sum has been read: the accumulator is free
+                        ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            ptx::tma_store_2d(map, scol, row0, ptx::smem_u32(slab));
-                            ptx::bulk_commit_group();
-                            // ... and is free again once the copy has read it
-                            ptx::bulk_wait_group_read<0>();
+                            if constexpr (kPair)
+                                ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&tempty_bar[b]), 0));
+                            else
+                                ptx::mbar_arrive(ptx::smem_u32(&tempty_bar[b]));
                         }
-                        __syncwarp();
-                    };
-                    if (p.has_pre) {
-#pragma unroll 1
-                        for (int c = 0; c < 64; c += kCols) {
-                            float v[kCols];
-                            sums(sl * 64 + c, v);
-                            put(c / 8, v);
-                        }
-                        send(&p.pre_map);
                     }
+                    if (bias_whole) {
+                        const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias16) + colh + 32 * c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 t = __ldg(from + j);
+                            const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 f = unpack2<kBF16>(w4[i]);
+                                v[8 * j + 2 * i] = __fadd_rn(v[8 * j + 2 * i], f.x);
+                                v[8 * j + 2 * i + 1] = __fadd_rn(v[8 * j + 2 * i + 1], f.y);
+                            }
+                        }
+                    } else if (p.bias16 != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __fadd_rn(v[i], load16<kBF16>(p.bias16, min(colh + 32 * c + i, p.n - 1)));
+                    }
+                    // with a pre-activation output: that through buffer 0, the output through buffer 1
+                    const int i = p.has_pre ? 1 : c & 1;
+                    if (p.has_pre) {
+                        reuse();
+                        put(0, v);
+                        send(&p.pre_map, 0, c);
+                    }
+                    uint32_t a[16] = {};
                     if (p.has_aux) {
-                        if ((sl != 0 || p.has_pre) && lane == 0) load_aux(warp - 4, scol, row0);
-                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, skr_phase, p.wait_limit_ns))) {
+                        if (p.has_pre) {
+                            // (the output's last store has read buffer 1; the pre-activation's is the latest)
+                            if (lane == 0) {
+                                ptx::bulk_wait_group_read<1>();
+                                const uint32_t bar = ptx::smem_u32(&aux_bar[2 * (warp - 4) + 1]);
+                                ptx::mbar_arrive_expect_tx(bar, kEpiPieceBytes);
+                                ptx::tma_load_2d(buf0 + kEpiPieceBytes, &p.aux_map, colh + 32 * c, row0, bar);
+                            }
+                            __syncwarp();
+                        }
+                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&aux_bar[2 * (warp - 4) + i]),
+                                                                    (aux_phase >> i) & 1u, p.wait_limit_ns))) {
                             *abort_flag = 1;
                             if (p.status && lane == 0) atomicExch(p.status, -7);
+                            ptx::nanosleep(20000);   // a copy still in flight lands before the CTA exits
                             ok = false;
                             break;
                         }
-                        skr_phase ^= 1u;
-                    }
-#pragma unroll 1
-                    for (int c = 0; c < 64; c += kCols) {
-                        float v[kCols];
-                        sums(sl * 64 + c, v);
-                        uint32_t a[kCols / 2];
+                        aux_phase ^= 1u << i;
 #pragma unroll
-                        for (int j = 0; j < kCols / 8; ++j) {
-                            uint4 t = make_uint4(0, 0, 0, 0);
-                            if (p.has_aux) t = *reinterpret_cast<const uint4 *>(mine + (((c / 8 + j) ^ (lane & 7)) << 4));
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 t = *reinterpret_cast<const uint4 *>(mine + i * kEpiPieceBytes + ((j ^ flip) << 4));
                             a[4 * j] = t.x, a[4 * j + 1] = t.y, a[4 * j + 2] = t.z, a[4 * j + 3] = t.w;
                         }
-                        epilogue<kBF16, kEpi>(v, a, p.act, p.has_aux != 0);
-                        put(c / 8, v);
                     }
-                    send(&p.out_map);
+                    epilogue<kBF16, kEpi>(v, a, p.act, p.has_aux != 0);
+                    if (!p.has_aux) {
+                        reuse();
+                    } else if (!p.has_pre && c >= 1 && c + 1 < pieces) {
+                        // the other buffer's store has been read by now: the piece after this one comes in there
+                        if (lane == 0) {
+                            ptx::bulk_wait_group_read<0>();
+                            load_aux(c + 1);
+                        }
+                        __syncwarp();
+                    }
+                    put(i, v);
+                    send(&p.out_map, i, c);
                 }
-                // every sum has been read: the accumulator is free
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
+                if (pieces <= 0 && lane == 0) {
                     if constexpr (kPair)
                         ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&tempty_bar[b]), 0));
                     else

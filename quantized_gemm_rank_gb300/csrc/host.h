@@ -41,7 +41,8 @@ struct DeviceInfo {
 int current_device(DeviceInfo *info);
 
 // 2-D map over a row-major (outer, inner) matrix with 16-bit elements and a
-// 128-byte swizzle; out-of-range box elements read as zero.  pitch: elements
+// swizzle of the box's row, 128 bytes (64 columns) or 64 (32 columns); out-of-range box
+// elements read as zero.  pitch: elements
 // from row to row, 0 for contiguous rows (a multiple of 8 either way).
 bool make_map16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                 uint32_t box_outer, uint64_t pitch = 0);

@@ -57,14 +57,14 @@ cudaError_t launch_linear_tiles(bool bf16, const LinearParams &lp, int num_sms, 
         else
             ok = ok && host::make_map16(&p.b_map, lp.w, n, k, 64, kBK, lp.ldw);
     }
-    ok = ok && host::make_map16(&p.out_map, lp.out, n, m, 64, 32, lp.ldo);
+    ok = ok && host::make_map16(&p.out_map, lp.out, n, m, 32, 32, lp.ldo);
     if (lp.aux_mode != AUX_NONE) {
         p.has_aux = 1;
-        ok = ok && host::make_map16(&p.aux_map, lp.aux, n, m, 64, 32, lp.ldaux);
+        ok = ok && host::make_map16(&p.aux_map, lp.aux, n, m, 32, 32, lp.ldaux);
     }
     if (lp.preact) {
         p.has_pre = 1;
-        ok = ok && host::make_map16(&p.pre_map, lp.preact, n, m, 64, 32, lp.ldp);
+        ok = ok && host::make_map16(&p.pre_map, lp.preact, n, m, 32, 32, lp.ldp);
     }
     if (!ok) return cudaErrorInvalidValue;
     p.num_a_maps = 1;

@@ -104,7 +104,7 @@ static MapCacheSlot &map_slot(const MapKey &k) {
 }
 
 // 2-D map over a row-major (outer, inner) matrix with 16-bit elements and a
-// 128-byte swizzle; out-of-range box elements read as zero.
+// swizzle of the box's row (128 bytes, or 64 for a box 32 wide); out-of-range box elements read as zero.
 bool make_map16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                 uint32_t box_outer, uint64_t pitch) {
     if (pitch == 0) pitch = inner;
@@ -120,8 +120,9 @@ bool make_map16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer
     cuuint64_t strides[1] = {pitch * 2};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
+    const CUtensorMapSwizzle swizzle = box_inner == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return false;
     slot.key = key;

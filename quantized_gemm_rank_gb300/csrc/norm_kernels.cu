@@ -60,10 +60,10 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, float *slots) {
     return s;
 }
 
-__device__ __forceinline__ float weight_at(const NormParams &p, int j, int kT) {
-    if (p.w_f32) return static_cast<const float *>(p.w)[j];
-    if (kT == ELEM_F16) return Elem<ELEM_F16>::load(static_cast<const __half *>(p.w) + j);
-    return Elem<ELEM_BF16>::load(static_cast<const __nv_bfloat16 *>(p.w) + j);
+__device__ __forceinline__ float weight_at(const void *w, int w_f32, int j, int kT) {
+    if (w_f32) return static_cast<const float *>(w)[j];
+    if (kT == ELEM_F16) return Elem<ELEM_F16>::load(static_cast<const __half *>(w) + j);
+    return Elem<ELEM_BF16>::load(static_cast<const __nv_bfloat16 *>(w) + j);
 }
 
 // ------------------------------------------------------------------ rows in registers
@@ -472,6 +472,150 @@ __global__ void __launch_bounds__(1024) norm_grad_row_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------ any layout
+// Rows that are not whole 16-byte vectors: the row in registers too, by element loads.  A
+// warp takes blocks of 128 elements, V of them, lane l elements l, l + 32, l + 64 and
+// l + 96, so a group's largest value is found in one warp.
+template <int kT, int V>
+__global__ void __launch_bounds__(1024, 1) norm_odd_kernel(const __grid_constant__ NormParams p) {
+    using T = typename Elem<kT>::type;
+    __shared__ float sum_slots[32];
+    __shared__ uint32_t max_slots[32];
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int64_t row = blockIdx.x;
+    const T *x = static_cast<const T *>(p.x) + row * p.ldx;
+    const T *res = p.res ? static_cast<const T *>(p.res) + row * p.ldr : nullptr;
+    auto at = [&](int i, int e) { return (warp + i * warps) * 128 + 32 * e + lane; };
+    float s[V][4], w[V][4];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = at(i, e);
+            s[i][e] = w[i][e] = 0.0f;
+            if (j < p.h) {
+                s[i][e] = Elem<kT>::load(x + j);
+                if (res) s[i][e] = __fadd_rn(s[i][e], Elem<kT>::load(res + j));
+                w[i][e] = weight_at(p.w, p.w_f32, j, kT);
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ss = fmaf(s[i][e], s[i][e], ss);
+    const float rstd = rsqrtf(block_sum32(ss, sum_slots) / static_cast<float>(p.h) + p.eps);
+    if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
+    T *out = p.out ? static_cast<T *>(p.out) + row * p.ldo : nullptr;
+    T *ro = p.res_out ? static_cast<T *>(p.res_out) + row * p.ldro : nullptr;
+    float largest = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = at(i, e);
+            if (j < p.h) {
+                if (ro) Elem<kT>::store(ro + j, s[i][e]);
+                s[i][e] = s[i][e] * rstd * w[i][e];
+                if (out) Elem<kT>::store(out + j, s[i][e]);
+                largest = max_abs(largest, s[i][e]);
+            } else {
+                s[i][e] = 0.0f;   // (an infinite rstd times zero)
+            }
+        }
+    if (p.qmode == QM_NONE) return;
+    float token = 0.0f;
+    if (p.qmode == QM_TOKEN) {
+        token = __fdiv_rn(__uint_as_float(block_max32(__float_as_uint(largest), max_slots)), q_max(p.qkind));
+        if (threadIdx.x == 0) static_cast<float *>(p.scale)[row] = token;
+    }
+    uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.h;
+    const int groups = p.qmode == QM_MX ? (p.h + 31) / 32 : (p.h + 127) / 128;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int block = warp + i * warps;
+        if (block * 128 >= p.h) break;   // (the same in the whole warp)
+        float r[4];
+        if (p.qmode == QM_MX) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t code = mx_code(__reduce_max_sync(0xFFFFFFFFu, abs_bits(s[i][e])), p.qkind);
+                if (lane == 0 && block * 4 + e < groups)
+                    static_cast<uint8_t *>(p.scale)[row * groups + block * 4 + e] = static_cast<uint8_t>(code);
+                r[e] = code != 0xFFu ? s[i][e] * mx_inverse(code) : 0.0f;
+            }
+        } else {
+            float step = token;
+            if (p.qmode == QM_GROUP) {
+                uint32_t a = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a = max(a, abs_bits(s[i][e]));
+                step = __fdiv_rn(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, a)), q_max(p.qkind));
+                if (lane == 0) static_cast<float *>(p.scale)[row * groups + block] = step;
+            }
+            quotients(s[i], step, r);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = at(i, e);
+            if (j < p.h) q[j] = static_cast<uint8_t>(encode8(r[e], p.qkind));
+        }
+    }
+}
+
+// Gradient of such rows: block b takes rows b, b + B, ..., its share of dw in registers, E
+// columns a thread; x and dy are read twice (the second time from L1).
+template <int kT, int E>
+__global__ void __launch_bounds__(1024, 1) norm_grad_odd_kernel(const __grid_constant__ NormGradParams p) {
+    using T = typename Elem<kT>::type;
+    __shared__ float slots[2][32];
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    float dw[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) dw[i] = 0.0f;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, turn ^= 1) {
+        const T *dy = static_cast<const T *>(p.dy) + row * p.lddy;
+        const T *x = static_cast<const T *>(p.x) + row * p.ldx;
+        const T *dres = p.dres ? static_cast<const T *>(p.dres) + row * p.lddres : nullptr;
+        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+        const float rstd = p.rstd[row];
+        float c = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (i % 4 == 0) asm volatile("" ::: "memory");   // (four columns' loads at once: more do not fit the registers)
+            const int j = threadIdx.x + i * blockDim.x;
+            if (j < p.h) {
+                const float xhat = Elem<kT>::load(x + j) * rstd, d = Elem<kT>::load(dy + j);
+                dw[i] = fmaf(d, xhat, dw[i]);
+                c = fmaf(d * weight_at(p.w, p.w_f32, j, kT), xhat, c);
+            }
+        }
+        c = block_sum32(c, slots[turn]) / static_cast<float>(p.h);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (i % 4 == 0) asm volatile("" ::: "memory");
+            const int j = threadIdx.x + i * blockDim.x;
+            if (j < p.h) {
+                const float xhat = Elem<kT>::load(x + j) * rstd;
+                const float g = Elem<kT>::load(dy + j) * weight_at(p.w, p.w_f32, j, kT);
+                const float d = g - xhat * c;
+                Elem<kT>::store(dx + j, dres ? fmaf(rstd, d, Elem<kT>::load(dres + j)) : rstd * d);
+            }
+        }
+    }
+    if (p.dw) {
+        float *part = p.parts + static_cast<int64_t>(blockIdx.x) * p.h;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int j = threadIdx.x + i * blockDim.x;
+            if (j < p.h) part[j] = dw[i];
+        }
+    }
+}
+
 // Any sizes, strides and alignments: one block a row, the row re-read for each
 // pass (statistics, largest value, outputs).  A warp takes whole groups of 32 or
 // 128 elements, so that a group's scale is found inside one warp; the thread
@@ -508,7 +652,7 @@ __global__ void __launch_bounds__(kThreads) norm_any_kernel(const __grid_constan
     });
     const float rstd = rsqrtf(block_sum(ss, slots) / static_cast<float>(p.h) + p.eps);
     if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
-    auto y_of = [&](float v, int j) { return v * rstd * weight_at(p, j, kT); };
+    auto y_of = [&](float v, int j) { return v * rstd * weight_at(p.w, p.w_f32, j, kT); };
     float scale = 0.0f;
     if (p.qmode == QM_TOKEN) {
         uint32_t a = 0;
@@ -570,9 +714,6 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const __grid_co
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     float *part = p.dw ? p.parts + static_cast<int64_t>(blockIdx.x) * p.h : nullptr;
-    NormParams wp;
-    wp.w = p.w;
-    wp.w_f32 = p.w_f32;
     bool first = true;
     for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x) {
         const T *dy = static_cast<const T *>(p.dy) + row * p.lddy;
@@ -584,13 +725,13 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const __grid_co
         for (int j = threadIdx.x; j < p.h; j += kThreads) {
             const float xhat = Elem<kT>::load(x + j) * rstd;
             const float d = Elem<kT>::load(dy + j);
-            c = fmaf(d * weight_at(wp, j, kT), xhat, c);
+            c = fmaf(d * weight_at(p.w, p.w_f32, j, kT), xhat, c);
             if (part) part[j] = first ? d * xhat : fmaf(d, xhat, part[j]);
         }
         c = block_sum(c, slots) / static_cast<float>(p.h);
         for (int j = threadIdx.x; j < p.h; j += kThreads) {
             const float xhat = Elem<kT>::load(x + j) * rstd;
-            const float g = Elem<kT>::load(dy + j) * weight_at(wp, j, kT);
+            const float g = Elem<kT>::load(dy + j) * weight_at(p.w, p.w_f32, j, kT);
             float v = rstd * (g - xhat * c);
             if (dres) v += Elem<kT>::load(dres + j);
             Elem<kT>::store(dx + j, v);
@@ -599,25 +740,32 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const __grid_co
     }
 }
 
-// dw from the blocks' shares: a block takes 32 columns, its 32 warps every 32nd
-// share, added in order, and then the warps' sums in order.
+// dw from the blocks' shares: a block takes kCols columns, its 1024 / kCols groups of
+// threads every so many-th share, added in order, and one warp a column the groups' sums, in
+// a fixed tree.
+template <int kCols>
 __global__ void __launch_bounds__(1024) dw_sum_kernel(const float *parts, int count, int h, int w_kind, void *dw) {
-    __shared__ float sums[32][33];
+    constexpr int kGroups = 1024 / kCols;
+    __shared__ float sums[kGroups][kCols + 1];
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int j = blockIdx.x * 32 + lane;
+    const int group = threadIdx.x / kCols, c = threadIdx.x % kCols;
+    const int j0 = blockIdx.x * kCols;
     float s = 0.0f;
-    if (j < h) {
+    if (j0 + c < h) {
 #pragma unroll 10
-        for (int b = warp; b < count; b += 32) s += parts[static_cast<int64_t>(b) * h + j];
+        for (int b = group; b < count; b += kGroups) s += parts[static_cast<int64_t>(b) * h + j0 + c];
     }
-    sums[warp][lane] = s;
+    sums[group][c] = s;
     __syncthreads();
-    if (warp != 0 || j >= h) return;
-    s = sums[0][lane];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = j0 + warp;
+    if (warp >= kCols || j >= h) return;
+    s = 0.0f;
 #pragma unroll
-    for (int w = 1; w < 32; ++w) s += sums[w][lane];
+    for (int g = 0; g < kGroups; g += 32) s += sums[g + lane][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane != 0) return;
     if (w_kind == ELEM_F32)
         static_cast<float *>(dw)[j] = s;
     else if (w_kind == ELEM_F16)
@@ -684,7 +832,12 @@ cudaError_t norm(const NormParams &p, int num_sms, cudaStream_t stream) {
         if (v == 2) return norm_rows<kT, 2>(p, row_threads(nv, 2), stream);
         return norm_rows<kT, 4>(p, row_threads(nv, 4), stream);
     }
-    return launch(norm_any_kernel<kT>, static_cast<unsigned>(p.m), kThreads, 0, stream, p);
+    const unsigned grid = static_cast<unsigned>(p.m);
+    const int blocks = (p.h + 127) / 128;   // a warp's
+    if (blocks <= 32 && p.m <= static_cast<int64_t>(num_sms) * (64 / blocks))
+        return launch(norm_odd_kernel<kT, 1>, grid, 32u * blocks, 0, stream, p);
+    if (blocks <= 4 * 32) return launch(norm_odd_kernel<kT, 4>, grid, 32u * ((blocks + 3) / 4), 0, stream, p);
+    return launch(norm_any_kernel<kT>, grid, kThreads, 0, stream, p);
 }
 
 template <int kT, int V>
@@ -720,7 +873,11 @@ cudaError_t norm_grad(const NormGradParams &p, cudaStream_t stream) {
         vectors(p.dres, p.lddres, p.m, kE) && vectors(p.dx, p.lddx, p.m, kE) &&
         reinterpret_cast<uintptr_t>(p.w) % 16 == 0)
         return nv <= 1024 ? norm_grad_rows<kT, 1>(p, stream) : norm_grad_rows<kT, 2>(p, stream);
-    return launch(norm_grad_any_kernel<kT>, static_cast<unsigned>(norm_grad_parts(p.m, p.h, kE)), kThreads, 0, stream, p);
+    const unsigned grid = static_cast<unsigned>(norm_grad_parts(p.m, p.h, kE));
+    if (p.h <= 4 * 1024) return launch(norm_grad_odd_kernel<kT, 4>, grid, row_threads(p.h, 4), 0, stream, p);
+    if (p.h <= 8 * 1024) return launch(norm_grad_odd_kernel<kT, 8>, grid, row_threads(p.h, 8), 0, stream, p);
+    if (p.h <= 16 * 1024) return launch(norm_grad_odd_kernel<kT, 16>, grid, row_threads(p.h, 16), 0, stream, p);
+    return launch(norm_grad_any_kernel<kT>, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -747,9 +904,12 @@ cudaError_t launch_rms_norm_grad(int kind, const NormGradParams &p, cudaStream_t
 }
 
 cudaError_t launch_rms_norm_dw(int kind, const NormGradParams &p, cudaStream_t stream) {
-    return launch(dw_sum_kernel, static_cast<unsigned>((p.h + 31) / 32), 1024, 0, stream,
-                  static_cast<const float *>(p.parts), norm_grad_parts(p.m, p.h, kind == ELEM_F32 ? 4 : 2), p.h,
-                  p.w_f32 ? int(ELEM_F32) : kind, p.dw);
+    const float *parts = p.parts;
+    const int count = norm_grad_parts(p.m, p.h, kind == ELEM_F32 ? 4 : 2), w_kind = p.w_f32 ? int(ELEM_F32) : kind;
+    // narrow rows have many shares and few columns: 8 a block shortens each thread's sum
+    // (300 x 512: 5.5 -> 4.4 us in all; 333 x 1000 4.4 -> 5.0, one row of 288 2.7 -> 3.3)
+    if (p.h <= 512 && count > 64) return launch(dw_sum_kernel<8>, static_cast<unsigned>((p.h + 7) / 8), 1024, 0, stream, parts, count, p.h, w_kind, p.dw);
+    return launch(dw_sum_kernel<32>, static_cast<unsigned>((p.h + 31) / 32), 1024, 0, stream, parts, count, p.h, w_kind, p.dw);
 }
 
 }  // namespace mc2
