@@ -2,6 +2,8 @@
 // consecutive columns at a time.  All arithmetic is fp32; each output is rounded once.
 #pragma once
 
+#include <type_traits>
+
 #include "num.cuh"
 
 namespace mc2 {
@@ -11,26 +13,6 @@ namespace mc2 {
 //   EPI_FORWARD   z = acc + bias (the optional pre-activation output), out = act(z) (+ aux)
 //   EPI_BACKWARD  out = acc * act'(aux)
 enum EpiMode : int { EPI_PLAIN = 0, EPI_FORWARD = 1, EPI_BACKWARD = 2 };
-
-// An activation as its kernels take it.  silu and the tanh form of gelu are one
-// function, z sigmoid(z (c1 + c2 z^2)), with (1, 0) and 2 sqrt(2/pi) (1, 0.044715):
-// so the epilogues hold four cases and not five.
-enum ActCase : int { CASE_NONE = 0, CASE_RELU = 1, CASE_ERF = 2, CASE_SIGMOID = 3 };
-struct Activation {
-    int form;        // ActCase
-    float c1, c2;    // CASE_SIGMOID
-    float limit;     // CASE_SIGMOID: |z| from which the sigmoid is 0 or 1 in fp32
-};
-
-inline Activation activation_of(int act) {
-    switch (act) {
-        case ACT_RELU: return {CASE_RELU, 0.0f, 0.0f, 0.0f};
-        case ACT_GELU: return {CASE_ERF, 0.0f, 0.0f, 0.0f};
-        case ACT_GELU_TANH: return {CASE_SIGMOID, 2.0f * kSqrt2OverPi, 2.0f * kSqrt2OverPi * kGeluCubic, kTanhLimit};
-        case ACT_SILU: return {CASE_SIGMOID, 1.0f, 0.0f, kSiluLimit};
-        default: return {CASE_NONE, 0.0f, 0.0f, 0.0f};
-    }
-}
 
 template <bool kBF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -86,41 +68,30 @@ __device__ __forceinline__ void load_bias8(const void *bias, int col, int n, flo
 // columns a word.
 template <bool kBF16, int kEpi, int kN>
 __device__ __forceinline__ void epilogue(float (&v)[kN], const uint32_t (&a)[kN / 2], const Activation &act, bool has_aux) {
-    auto aux = [&](auto f) {
+    auto each = [&](auto f) {
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) {
-            const float2 x = unpack2<kBF16>(a[i]);
-            f(v[2 * i], x.x);
-            f(v[2 * i + 1], x.y);
+            const float2 r = f(make_float2(v[2 * i], v[2 * i + 1]), unpack2<kBF16>(a[i]));
+            v[2 * i] = r.x;
+            v[2 * i + 1] = r.y;
         }
     };
-    if constexpr (kEpi == EPI_FORWARD) {
-        switch (act.form) {   // the same in every thread
-            case CASE_RELU:
-#pragma unroll
-                for (int i = 0; i < kN; ++i) v[i] = act_f<ACT_RELU>(v[i]);
-                break;
-            case CASE_ERF:
-#pragma unroll
-                for (int i = 0; i < kN; ++i) v[i] = act_f<ACT_GELU>(v[i]);
-                break;
-            case CASE_SIGMOID:
-#pragma unroll
-                for (int i = 0; i < kN; ++i) v[i] = sigmoid_form(v[i], act.c1, act.c2, act.limit);
-                break;
-            default: break;
-        }
-        if (has_aux) aux([](float &z, float x) { z = __fadd_rn(z, x); });
-    } else {
-        switch (act.form) {
-            case CASE_RELU: aux([](float &z, float x) { z *= act_derivative_f<ACT_RELU>(x); }); break;
-            case CASE_ERF: aux([](float &z, float x) { z *= act_derivative_f<ACT_GELU>(x); }); break;
-            case CASE_SIGMOID:
-                aux([&](float &z, float x) { z *= sigmoid_form_derivative(x, act.c1, act.c2, act.limit); });
-                break;
-            default: break;
-        }
+    // (one loop for each form: the choice is made once for all kN columns)
+    auto apply = [&](auto form) {
+        Activation one = act;
+        one.form = decltype(form)::value;
+        if constexpr (kEpi == EPI_FORWARD)
+            each([&](float2 z, float2) { return act2(z, one); });
+        else
+            each([&](float2 z, float2 x) { return __fmul2_rn(z, act_derivative2(x, one)); });
+    };
+    switch (act.form) {
+        case CASE_RELU: apply(std::integral_constant<int, CASE_RELU>{}); break;
+        case CASE_ERF: apply(std::integral_constant<int, CASE_ERF>{}); break;
+        case CASE_SIGMOID: apply(std::integral_constant<int, CASE_SIGMOID>{}); break;
+        default: break;
     }
+    if (kEpi == EPI_FORWARD && has_aux) each([](float2 z, float2 x) { return __fadd2_rn(z, x); });
 }
 
 }  // namespace mc2

@@ -7,8 +7,6 @@
 // Sums and the epilogue are fp32; each output is rounded once.
 #include "linear.h"
 
-#include <type_traits>
-
 #include "num.cuh"
 #include "sm103_ptx.cuh"
 
@@ -16,19 +14,11 @@ namespace mc2 {
 
 namespace {
 
-// The epilogue of one element: acc with the bias and aux of its place.
-template <int kAct>
-__device__ __forceinline__ float epilogue_one(float z, float aux, int aux_mode) {
-    if (aux_mode == AUX_ACT_GRAD) return z * act_derivative_f<kAct>(aux);
-    const float o = act_f<kAct>(z);
-    return aux_mode == AUX_RESIDUAL ? o + aux : o;
-}
-
 // Any sizes, strides and alignments: a 64 x 64 tile a block, 4 x 4 outputs a
 // thread, the operands staged through shared memory 16 columns at a time with
 // element loads.
-template <int kT, int kAct>
-__global__ void __launch_bounds__(256) linear_any_kernel(const __grid_constant__ LinearParams p) {
+template <int kT>
+__global__ void __launch_bounds__(256) linear_any_kernel(const __grid_constant__ LinearParams p, Activation act) {
     using T = typename Elem<kT>::type;
     __shared__ float xs[16][64 + 4], ws[16][64 + 4];
     ptx::grid_dependency_wait();
@@ -73,12 +63,14 @@ __global__ void __launch_bounds__(256) linear_any_kernel(const __grid_constant__
             if (p.bias) z += Elem<kT>::load(static_cast<const T *>(p.bias) + c);
             if (p.preact) Elem<kT>::store(static_cast<T *>(p.preact) + r * p.ldp + c, z);
             const float aux = p.aux_mode != AUX_NONE ? Elem<kT>::load(static_cast<const T *>(p.aux) + r * p.ldaux + c) : 0.0f;
-            Elem<kT>::store(static_cast<T *>(p.out) + r * p.ldo + c, epilogue_one<kAct>(z, aux, p.aux_mode));
+            const float o = p.aux_mode == AUX_ACT_GRAD ? z * act_derivative2(both(aux), act).x
+                                                       : act2(both(z), act).x + (p.aux_mode == AUX_RESIDUAL ? aux : 0.0f);
+            Elem<kT>::store(static_cast<T *>(p.out) + r * p.ldo + c, o);
         }
 }
 
-template <int kT, int kAct>
-__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradParams p) {
+template <int kT>
+__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradParams p, Activation act) {
     using T = typename Elem<kT>::type;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
@@ -87,7 +79,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
         const int64_t r = e / p.n, c = e - r * p.n;
         const float d = Elem<kT>::load(static_cast<const T *>(p.dy) + r * p.lddy + c);
         const float z = Elem<kT>::load(static_cast<const T *>(p.z) + r * p.ldz + c);
-        Elem<kT>::store(static_cast<T *>(p.dz) + r * p.lddz + c, d * act_derivative_f<kAct>(z));
+        Elem<kT>::store(static_cast<T *>(p.dz) + r * p.lddz + c, d * act_derivative2(both(z), act).x);
     }
 }
 
@@ -106,38 +98,22 @@ cudaError_t launch(K kern, unsigned grid, unsigned block, cudaStream_t stream, c
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// f(std::integral_constant<int, act>) for a run-time activation
-template <class F>
-cudaError_t with_act(int act, F f) {
-    switch (act) {
-        case ACT_RELU: return f(std::integral_constant<int, ACT_RELU>{});
-        case ACT_GELU: return f(std::integral_constant<int, ACT_GELU>{});
-        case ACT_GELU_TANH: return f(std::integral_constant<int, ACT_GELU_TANH>{});
-        case ACT_SILU: return f(std::integral_constant<int, ACT_SILU>{});
-        default: return f(std::integral_constant<int, ACT_NONE>{});
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_linear_any(bool bf16, const LinearParams &p, cudaStream_t stream) {
     const int64_t tiles = ((p.m + 63ll) / 64) * ((p.n + 63ll) / 64);
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    return with_act(p.act, [&](auto a) {
-        constexpr int kAct = decltype(a)::value;
-        return bf16 ? launch(linear_any_kernel<ELEM_BF16, kAct>, static_cast<unsigned>(tiles), 256, stream, p)
-                    : launch(linear_any_kernel<ELEM_F16, kAct>, static_cast<unsigned>(tiles), 256, stream, p);
-    });
+    const Activation act = activation_of(p.act);
+    return bf16 ? launch(linear_any_kernel<ELEM_BF16>, static_cast<unsigned>(tiles), 256, stream, p, act)
+                : launch(linear_any_kernel<ELEM_F16>, static_cast<unsigned>(tiles), 256, stream, p, act);
 }
 
 cudaError_t launch_act_grad(bool bf16, const ActGradParams &p, int num_sms, cudaStream_t stream) {
     const int64_t blocks = (p.m * p.n + 255) / 256;
     const unsigned grid = static_cast<unsigned>(blocks < 64ll * num_sms ? blocks : 64ll * num_sms);
-    return with_act(p.act, [&](auto a) {
-        constexpr int kAct = decltype(a)::value;
-        return bf16 ? launch(act_grad_kernel<ELEM_BF16, kAct>, grid, 256, stream, p)
-                    : launch(act_grad_kernel<ELEM_F16, kAct>, grid, 256, stream, p);
-    });
+    const Activation act = activation_of(p.act);
+    return bf16 ? launch(act_grad_kernel<ELEM_BF16>, grid, 256, stream, p, act)
+                : launch(act_grad_kernel<ELEM_F16>, grid, 256, stream, p, act);
 }
 
 }  // namespace mc2

@@ -39,85 +39,126 @@ struct Elem<ELEM_F32> {
 // ------------------------------------------------------------------ activations
 enum ActKind : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
 
-// 1 / (1 + e^-t).  e^-t overflows to infinity below t = -88 and the quotient is
-// then 0, its limit.
-__device__ __forceinline__ float sigmoid_f(float t) { return __fdividef(1.0f, 1.0f + __expf(-t)); }
+// An activation as its kernels take it.  silu, z / (1 + e^-z), and the tanh form of
+// gelu, z (1 + tanh u) / 2 = z / (1 + e^-2u) with u = sqrt(2/pi) (z + 0.044715 z^3), are one
+// function, z sigmoid(z (c1 + c2 z^2)), with (1, 0) and 2 sqrt(2/pi) (1, 0.044715).
+enum ActCase : int { CASE_NONE = 0, CASE_RELU = 1, CASE_ERF = 2, CASE_SIGMOID = 3 };
+struct Activation {
+    int form;        // ActCase
+    float c1, c2;    // CASE_SIGMOID
+    float limit;     // CASE_SIGMOID: |z| from which the sigmoid is taken to be constant: below 3e-18, or 1
+};
 
+inline Activation activation_of(int act) {
+    constexpr float kSqrt2OverPi = 0.79788456080286536f;
+    switch (act) {
+        case ACT_RELU: return {CASE_RELU, 0.0f, 0.0f, 0.0f};
+        case ACT_GELU: return {CASE_ERF, 0.0f, 0.0f, 0.0f};
+        case ACT_GELU_TANH: return {CASE_SIGMOID, 2.0f * kSqrt2OverPi, 2.0f * kSqrt2OverPi * 0.044715f, 7.4f};
+        case ACT_SILU: return {CASE_SIGMOID, 1.0f, 0.0f, 40.5f};
+        default: return {CASE_NONE, 0.0f, 0.0f, 0.0f};
+    }
+}
+
+// The special function unit takes a warp eight cycles an operation and the rest of an
+// epilogue little more, so the functions below work on pairs: one reciprocal for both
+// (1/a = b r, 1/b = a r with r = 1/(ab)), and packed fp32 arithmetic.
+__device__ __forceinline__ float exp2_f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float2 reciprocals(float2 d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
+    return make_float2(r * d.y, r * d.x);
+}
+
+// z held inside [lo, hi]; a NaN is kept.
+__device__ __forceinline__ float hold(float z, float lo, float hi) {
+    float c;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(z), "f"(lo));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(c), "f"(hi));
+    return c;
+}
+__device__ __forceinline__ float2 hold2(float2 z, float lo, float hi) { return make_float2(hold(z.x, lo, hi), hold(z.y, lo, hi)); }
+// The same where a NaN must not reach a pair's common reciprocal: it becomes lo, and
+// comes back by the factor that z itself is.
+__device__ __forceinline__ float2 inside2(float2 z, float lo, float hi) {
+    return make_float2(fminf(fmaxf(z.x, lo), hi), fminf(fmaxf(z.y, lo), hi));
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSqrtHalf = 0.70710678118654752f;     // 1 / sqrt(2)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;   // 1 / sqrt(2 pi)
-constexpr float kSqrt2OverPi = 0.79788456080286536f;  // sqrt(2 / pi)
-constexpr float kGeluCubic = 0.044715f;
-constexpr float kTanhLimit = 14.0f;    // e^-2u(14) = e^-218 and e^104 are beyond fp32's range
-constexpr float kSiluLimit = 104.0f;
+constexpr float kErfLimit = 14.0f;                    // e^(-14^2 / 2) is below fp32's range
 
-// z sigmoid(t) with t = z (c1 + c2 z^2).  The sigmoid is 0 or 1 in fp32 from |z| =
-// limit on, and is taken at z clamped to that, which keeps t finite (0 times
-// infinity otherwise); a NaN passes the comparisons unchanged.
-__device__ __forceinline__ float sigmoid_form(float z, float c1, float c2, float limit) {
-    const float c = z > limit ? limit : (z < -limit ? -limit : z);
-    return z * sigmoid_f(c * fmaf(c2, c * c, c1));
+// sigmoid(c (c1 + c2 c^2)) for |c| <= limit, where e^-t of two is within fp32's range
+__device__ __forceinline__ float2 sigmoid_form2(float2 c, const Activation &a) {
+    const float2 t = __ffma2_rn(__fmul2_rn(c, c), both(-a.c2 * kLog2e), both(-a.c1 * kLog2e));
+    const float2 x = __fmul2_rn(c, t);
+    return reciprocals(__fadd2_rn(make_float2(exp2_f(x.x), exp2_f(x.y)), both(1.0f)));
 }
 
-// Its derivative, s + z s (1 - s) t'(z), at the same clamped z (see below).
-__device__ __forceinline__ float sigmoid_form_derivative(float z, float c1, float c2, float limit) {
-    const float c = z > limit ? limit : (z < -limit ? -limit : z);
-    const float zz = c * c;
-    const float s = sigmoid_f(c * fmaf(c2, zz, c1));
-    return fmaf(c * s * (1.0f - s), fmaf(3.0f * c2, zz, c1), s);
-}
-
-// The normal distribution at z: Phi(z) = (1 + erf(z / sqrt 2)) / 2 and, for the
+// The normal distribution at |z| <= kErfLimit: Phi(z) = (1 + erf(z / sqrt 2)) / 2 and, for the
 // derivative, e^(-z^2 / 2).  erf by Abramowitz and Stegun, Handbook of Mathematical
 // Functions, 7.1.26: for x >= 0, erf x = 1 - (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x),
 // to 1.5e-7; its exponential is the density's, so the derivative costs little more
-// than the value.  Infinities give the limits (e^-inf = 0, t = 0), a NaN stays one.
-__device__ __forceinline__ float normal_cdf(float z, float &expo) {
-    const float x = fabsf(z) * kSqrtHalf;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    expo = __expf(-x * x);
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float tail = 0.5f * q * t * expo;   // Phi(-|z|)
-    return z < 0.0f ? tail : 1.0f - tail;
+// than the value.
+__device__ __forceinline__ float2 normal_cdf2(float2 z, float2 &expo) {
+    constexpr float kP = 0.3275911f * kSqrtHalf;
+    const float2 t = reciprocals(make_float2(fmaf(fabsf(z.x), kP, 1.0f), fmaf(fabsf(z.y), kP, 1.0f)));
+    const float2 x = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2e));
+    expo = make_float2(exp2_f(x.x), exp2_f(x.y));
+    float2 q = __ffma2_rn(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+    q = __ffma2_rn(q, t, both(0.5f * 1.421413741f));
+    q = __ffma2_rn(q, t, both(0.5f * -0.284496736f));
+    q = __ffma2_rn(q, t, both(0.5f * 0.254829592f));
+    const float2 tail = __fmul2_rn(__fmul2_rn(q, t), expo);   // Phi(-|z|)
+    return make_float2(z.x < 0.0f ? tail.x : 1.0f - tail.x, z.y < 0.0f ? tail.y : 1.0f - tail.y);
 }
 
-// relu  max(z, 0) (a NaN stays a NaN)
-// gelu  z (1 + erf(z / sqrt 2)) / 2
-// gelu_tanh  z (1 + tanh u) / 2 with u = sqrt(2/pi) (z + 0.044715 z^3); as
-//       (1 + tanh u) / 2 = 1 / (1 + e^-2u) it is z sigmoid(2u)
-// silu  z sigmoid(z)
-template <int kAct>
-__device__ __forceinline__ float act_f(float z) {
-    if constexpr (kAct == ACT_RELU) return z < 0.0f ? 0.0f : z;
-    if constexpr (kAct == ACT_GELU) {
-        float e;
-        return z * normal_cdf(z, e);
+// act(z).  Far below zero silu and gelu are taken at their limit's argument (their value
+// there is below 2e-16), so an infinity gives its limit and not infinity times zero.
+__device__ __forceinline__ float2 act2(float2 z, const Activation &a) {
+    switch (a.form) {   // the same in every thread
+        case CASE_RELU: return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);   // (a NaN stays one)
+        case CASE_ERF: {
+            float2 e;
+            const float2 phi = normal_cdf2(inside2(z, -kErfLimit, kErfLimit), e);
+            const float top = __int_as_float(0x7F800000);
+            return __fmul2_rn(hold2(z, -kErfLimit, top), phi);
+        }
+        case CASE_SIGMOID: {
+            const float top = __int_as_float(0x7F800000);
+            return __fmul2_rn(hold2(z, -a.limit, top), sigmoid_form2(inside2(z, -a.limit, a.limit), a));
+        }
+        default: return z;
     }
-    if constexpr (kAct == ACT_GELU_TANH)
-        return sigmoid_form(z, 2.0f * kSqrt2OverPi, 2.0f * kSqrt2OverPi * kGeluCubic, kTanhLimit);
-    if constexpr (kAct == ACT_SILU) return sigmoid_form(z, 1.0f, 0.0f, kSiluLimit);
-    return z;
 }
 
-// The derivatives.  Each is evaluated at z clamped to a range outside which it
-// has reached its limit (0 or 1) in fp32, so that large and infinite z give the
-// limit and not infinity times zero; a NaN passes the comparisons unchanged.
-template <int kAct>
-__device__ __forceinline__ float act_derivative_f(float z) {
-    if constexpr (kAct == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if constexpr (kAct == ACT_GELU) {
-        // Phi(z) + z phi(z)
-        const float c = z > 14.0f ? 14.0f : (z < -14.0f ? -14.0f : z);
-        float e;
-        const float cdf = normal_cdf(c, e);
-        return fmaf(c * kInvSqrt2Pi, e, cdf);
+// act'(z), for z held where it has not yet reached its limit:
+//   relu  1 above 0;  erf form  Phi(z) + z phi(z);  sigmoid form  s + z s (1 - s) (c1 + 3 c2 z^2)
+__device__ __forceinline__ float2 act_derivative2(float2 z, const Activation &a) {
+    switch (a.form) {
+        case CASE_RELU: return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+        case CASE_ERF: {
+            const float2 c = hold2(z, -kErfLimit, kErfLimit);
+            float2 e;
+            const float2 phi = normal_cdf2(inside2(z, -kErfLimit, kErfLimit), e);
+            return __ffma2_rn(__fmul2_rn(c, both(kInvSqrt2Pi)), e, phi);
+        }
+        case CASE_SIGMOID: {
+            const float2 c = hold2(z, -a.limit, a.limit);
+            const float2 s = sigmoid_form2(inside2(z, -a.limit, a.limit), a);
+            const float2 slope = __ffma2_rn(__fmul2_rn(c, c), both(3.0f * a.c2), both(a.c1));
+            const float2 rest = __fmul2_rn(__fmul2_rn(c, s), __ffma2_rn(s, both(-1.0f), both(1.0f)));
+            return __ffma2_rn(rest, slope, s);
+        }
+        default: return both(1.0f);
     }
-    if constexpr (kAct == ACT_GELU_TANH)
-        return sigmoid_form_derivative(z, 2.0f * kSqrt2OverPi, 2.0f * kSqrt2OverPi * kGeluCubic, kTanhLimit);
-    if constexpr (kAct == ACT_SILU) return sigmoid_form_derivative(z, 1.0f, 0.0f, kSiluLimit);
-    return 1.0f;
 }
 
 // ------------------------------------------------------------------ 8-bit codes

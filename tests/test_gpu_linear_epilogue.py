@@ -207,6 +207,34 @@ def test_nan_and_infinity_stay_in_their_rows():
         assert relu[2].isnan().all()
 
 
+@pytest.mark.parametrize("m", [3, 90, 700])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_a_nan_or_infinity_stays_in_its_element(m, act):
+    """One column of the bias, one element of z: the columns beside it are as without it."""
+    x, w, bias, _ = make(m, 136, 64, BF16, seed=2)
+    clean, _ = mc2.mc2_matmul_bias_act(x, w, bias=bias, activation=act)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        b = bias.clone()
+        b[17] = bad
+        got, _ = mc2.mc2_matmul_bias_act(x, w, bias=b, activation=act)
+        keep = [i for i in range(136) if i != 17]
+        assert torch.equal(got[:, keep], clean[:, keep])
+        if bad != bad:
+            assert got[:, 17].isnan().all()
+        elif bad > 0:
+            assert (got[:, 17] == bad).all()
+        else:
+            assert (got[:, 17].abs() < 1e-15).all()   # the limit, 0
+    z = (3 * torch.randn(m, 64, generator=torch.Generator().manual_seed(m))).to(BF16).cuda()
+    dy = torch.randn(m, 136, generator=torch.Generator().manual_seed(m + 1)).to(BF16).cuda()
+    clean = mc2.mc2_matmul_act_grad(dy, w, z, activation=act)
+    z[m // 2, 8] = float("nan")
+    got = mc2.mc2_matmul_act_grad(dy, w, z, activation=act)
+    assert got[m // 2, 8].isnan()
+    got[m // 2, 8] = clean[m // 2, 8]
+    assert torch.equal(got, clean)
+
+
 def test_same_bits_every_time():
     for m, n, k in ((1, 4096, 4096), (40, 1024, 8192), (333, 1000, 2056)):
         x, w, bias, res = make(m, n, k, BF16, seed=7)
