@@ -385,9 +385,11 @@ struct SplitShape {
 };
 
 // Fetching the weight's first stages into L2 ahead of the stream's previous kernel's end
-// pays where two CTAs share each SM (one token, 4096 x 4096: 8.7 -> 7.8 us), and costs
-// where the loads follow at once (1024 x 8192, 64 CTAs: 7.2 -> 7.9).
-bool prefetch_pays(const SplitShape &s, int num_sms) { return s.group == 1 && s.tiles * s.split > num_sms; }
+// pays where two CTAs share most SMs (one token, 4096 x 4096, 256 CTAs: 8.7 -> 7.8 us), and
+// costs where the loads follow at once (1024 x 8192, 64 CTAs: 7.2 -> 7.9).
+bool prefetch_pays(const SplitShape &s, int num_sms) {
+    return s.group == 1 && s.per_sm == 2 && s.tiles * s.split * 8 >= num_sms * 13ll;
+}
 
 // Shared memory and TMEM of a launch whose tiles and split are chosen.
 void fit_split(SplitShape &s, int steps, int num_sms) {
@@ -421,17 +423,16 @@ void fit_split(SplitShape &s, int steps, int num_sms) {
     s.prefetch = prefetch_pays(s, num_sms);
 }
 
-// Clusters of `ctas` CTAs, `per_sm` an SM, that the device runs at once.  A cluster stays
-// inside one GPC, so fewer than the SMs would hold; asked once for each kind.
-int64_t clusters_at_once(int ctas, int per_sm, int num_sms) {
-    if (ctas == 1) return static_cast<int64_t>(num_sms) * per_sm;
-    static std::atomic<int> known[64][kMaxCluster + 1][2];
+// Clusters of `ctas` CTAs, one an SM, that the device runs at once.  A cluster stays inside
+// one GPC, so they are fewer than the SMs would hold (15 of 8 CTAs, not 19); asked once for each size.
+int clusters_at_once(int ctas, int num_sms) {
+    if (ctas == 1) return num_sms;
+    static std::atomic<int> known[64][kMaxCluster + 1];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return num_sms * per_sm / ctas;
-    std::atomic<int> &slot = known[dev][ctas][per_sm - 1];
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return num_sms / ctas;
+    std::atomic<int> &slot = known[dev][ctas];
     int n = slot.load(std::memory_order_relaxed);
     if (n == 0) {
-        const int smem = per_sm == 2 ? 112 * 1024 : 222 * 1024;
         auto kern = linear_split_kernel<true, EPI_FORWARD, 1>;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -441,13 +442,13 @@ int64_t clusters_at_once(int ctas, int per_sm, int num_sms) {
         attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(ctas * num_sms), 1, 1);
         cfg.blockDim = dim3(kSplitThreads, 1, 1);
-        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cfg.dynamicSmemBytes = 222 * 1024;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - kSmemStatic) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
-            n = num_sms * per_sm / ctas > 0 ? num_sms * per_sm / ctas : 1;
+            n = num_sms / ctas > 0 ? num_sms / ctas : 1;
         }
         slot.store(n, std::memory_order_relaxed);
     }
@@ -457,23 +458,25 @@ int64_t clusters_at_once(int ctas, int per_sm, int num_sms) {
 // What a shape takes, in us, fitted to measurements on GB300: launch, set-up and the cluster's
 // barriers; the stages, at the 110 bytes a ns that an SM receives and the rate of device
 // memory, which reads the weight once (the root of the squares' sum, since the two do
-// not overlap wholly); and per token of the tile the way from TMEM to the output, and to
+// not overlap wholly); another set-up for each further wave; and per token of the tile the way from TMEM to the output, and to
 // the other CTAs.  Over 50 shapes (1 to 1274 tokens, 64 to 16384 columns and depth) the
 // shape it chose took at most 8% more than the best one, but for three.
 float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sms) {
-    const int64_t clusters = clusters_at_once(s.group * s.split, s.per_sm, num_sms);
+    const int beside = s.smem <= kSmemPerSm / 2 - kSmemOverhead ? 2 : 1;   // CTAs that fit an SM
+    const int64_t clusters = static_cast<int64_t>(clusters_at_once(s.group * s.split, num_sms)) * beside;
     const int64_t units = s.tiles;   // a cluster each
-    const float waves = static_cast<float>((units + clusters - 1) / clusters);
-    const int64_t resident = (units < clusters ? units : clusters) * s.group * s.split;
-    const float beside = resident > num_sms ? static_cast<float>(resident) / num_sms : 1.0f;
+    // (with two CTAs an SM about a tenth more fit: 32 clusters of 8 run at once)
+    const int64_t slots = beside == 2 ? clusters * 11 / 10 : clusters;
+    const float waves = static_cast<float>((units + slots - 1) / slots);
+    const float share = (units < clusters ? units : clusters) * s.group * s.split > num_sms ? 2.0f : 1.0f;
     const float stage = static_cast<float>(kWBytes) + static_cast<float>(s.rows / s.group) * kDepth * 2;
-    const float stages = waves * (static_cast<float>(steps) / s.split) * stage * beside / 110e3f;
+    const float stages = waves * (static_cast<float>(steps) / s.split) * stage * share / 110e3f;
     const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 2.0f / 6.9e6f;
     const float stream = sqrtf(stages * stages + read * read);
     float join = 0.012f * s.rows;
     if (s.split > 1) join += 0.5f + 0.016f * s.rows * (s.split - 1) / s.split + (s.rows > 128 ? 1.5f : 0.0f);
     const float ahead = prefetch_pays(s, num_sms) ? 0.8f : 0.0f;
-    return 3.3f + (s.group == 2 ? 0.6f : 0.0f) + stream + waves * join - ahead;
+    return 3.3f + (s.group == 2 ? 0.6f : 0.0f) + stream + waves * join + 3.0f * (waves - 1.0f) - ahead;
 }
 
 SplitShape best_split(const LinearParams &p, int num_sms) {
@@ -494,11 +497,11 @@ SplitShape best_split(const LinearParams &p, int num_sms) {
         // 64 tokens: 11.3 against 9.9
         s.per_sm = f.group == 1 && s.rows <= 32 ? 2 : 1;
         for (s.split = 1; s.split <= kMaxCluster / f.group && s.split <= steps; ++s.split) {
+            fit_split(s, steps, num_sms);
             s.us = split_us(s, p, steps, num_sms);
             if (best.group == 0 || s.us < best.us) best = s;
         }
     }
-    fit_split(best, steps, num_sms);
     return best;
 }
 
