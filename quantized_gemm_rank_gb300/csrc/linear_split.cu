@@ -38,7 +38,8 @@ constexpr int kTileN = 128;      // weight columns a tile (MMA M)
 constexpr int kDepth = 64;       // contraction a stage
 constexpr int kMaxStages = 16;
 constexpr int kMaxCluster = 8;
-constexpr int kSplitThreads = 256;
+// Threads a CTA: the pairs' tiles have more to bring out of TMEM and one CTA an SM.
+__host__ __device__ constexpr int split_threads(int group) { return group == 1 ? 256 : 512; }
 constexpr int kBlockSteps = 1024 / kDepth;   // stages of one accumulator
 constexpr uint32_t kWBytes = kTileN * kDepth * 2;
 constexpr uint32_t kSmemPerSm = 228 * 1024;
@@ -90,7 +91,7 @@ __device__ __forceinline__ void load4(const uint16_t *p, int n, uint32_t *w) {
 
 // The tokens first + warp * kT, ... < last of a tile (kT a warp at a time, four columns a
 // lane): the partial sums in rank order, the epilogue, the outputs.
-template <bool kBF16, int kEpi, int kT>
+template <bool kBF16, int kEpi, int kT, int kThreads>
 __device__ __forceinline__ void finish(const SplitParams &p, int m0, int first, int last, int rank, int col, const float4 *own,
                                        const float4 *recv) {
     const int warp = threadIdx.x >> 5;
@@ -103,7 +104,7 @@ __device__ __forceinline__ void finish(const SplitParams &p, int m0, int first, 
             if (i < n) b4[i] = load16<kBF16>(p.bias, col + i);
     }
 #pragma unroll 1
-    for (int t = first + warp * kT; t < last; t += kSplitThreads / 32 * kT) {
+    for (int t = first + warp * kT; t < last; t += kThreads / 32 * kT) {
         const int64_t row = m0 + t;
         const int count = last - t;   // tokens left: those past the last repeat it and are not stored
         uint32_t aux[2 * kT] = {};
@@ -143,7 +144,8 @@ __device__ __forceinline__ void finish(const SplitParams &p, int m0, int first, 
 }
 
 template <bool kBF16, int kEpi, int kG>
-__global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __grid_constant__ SplitParams p) {
+__global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(const __grid_constant__ SplitParams p) {
+    constexpr int kThreads = split_threads(kG);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, recv_bar;
@@ -187,11 +189,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __
     }
     ptx::tc_fence_before();
     __syncthreads();
-    // the barriers of the cluster are ready (one CTA a share: when its sums are sent)
-    if constexpr (kG == 2)
-        ptx::cluster_sync();
-    else if (ctas > 1)
-        ptx::cluster_arrive_relaxed();
+    // the barriers of the cluster are ready (one CTA a share: needed when its sums are sent)
+    if (ctas > 1) ptx::cluster_arrive_relaxed();
+    if constexpr (kG == 2) ptx::cluster_wait();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     if (warp == 0 && lane == 0) {
@@ -301,53 +301,65 @@ __global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __
     __syncthreads();
     bool ok = failed == 0;
     if (kG == 1 && ctas > 1) ptx::cluster_wait();
-    if (p.late) ptx::cluster_sync();
+    if (p.late) {
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    }
     float *part = reinterpret_cast<float *>(smem);   // [rows][128], over the ring
-    if (ok) {
-        // warp w reads TMEM lanes 32 (w % 4) on, every other 16 tokens, two loads at a time
-        ptx::tc_fence_after();
-        const int q = warp & 3;
+    // The sums leave TMEM a chunk of tokens at a time, four warps (one for each 32 columns) at a
+    // chunk: first the chunks with tokens that another CTA finishes, which are sent to it, to
+    // its slot of this rank among the ranks without its own; then, while those are on their
+    // way, this CTA's own.
+    {
+        constexpr int kChunk = kG == 1 ? 16 : 32;
+        const int group = warp >> 2, q = warp & 3;
         const int used = min(p.accs, (count + kBlockSteps - 1) / kBlockSteps);
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
-        for (int c = 16 * (warp >> 2); c < p.rows; c += 64) {
-            const bool two = c + 32 < p.rows;
-            float sum[2][16];
+        // chunks [own0, own1) hold own tokens only; the others come in the order own1, ..., then 0, ...
+        const int chunks = (live + kChunk - 1) / kChunk;
+        const int own0 = min((t0 + kChunk - 1) / kChunk, chunks), own1 = max(own0, t1 == live ? chunks : t1 / kChunk);
+        ptx::tc_fence_after();
+        auto bring = [&](int c) {
+            float sum[kChunk];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[0][i] = sum[1][i] = 0.0f;
+            for (int e = 0; e < kChunk; ++e) sum[e] = 0.0f;
             for (int a = 0; a < used; ++a) {
-                uint32_t r0[16], r1[16];
-                ptx::tmem_ld_32x32b_x16(lanes + a * p.rows + c, r0);
-                ptx::tmem_ld_32x32b_x16(lanes + a * p.rows + (two ? c + 32 : c), r1);
-                ptx::tmem_ld_wait16(r0);
-                ptx::tmem_ld_wait16(r1);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    sum[0][i] = __fadd_rn(sum[0][i], __uint_as_float(r0[i]));
-                    sum[1][i] = __fadd_rn(sum[1][i], __uint_as_float(r1[i]));
+                uint32_t r[kChunk];
+                if constexpr (kChunk == 32) {
+                    ptx::tmem_ld_32x32b_x32(lanes + a * p.rows + c, r);
+                    ptx::tmem_ld_wait32(r);
+                } else {
+                    ptx::tmem_ld_32x32b_x16(lanes + a * p.rows + c, r);
+                    ptx::tmem_ld_wait16(r);
                 }
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) sum[e] = __fadd_rn(sum[e], __uint_as_float(r[e]));
             }
             float *to = part + c * kTileN + 32 * q + lane;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                to[i * kTileN] = sum[0][i];
-                if (two) to[(i + 32) * kTileN] = sum[1][i];
+            for (int e = 0; e < kChunk; ++e) to[e * kTileN] = sum[e];
+        };
+        const int others = chunks - (own1 - own0);
+        if (p.split > 1) {
+            for (int i = group; i < others && ok; i += kThreads / 128) bring((i < chunks - own1 ? own1 + i : i - (chunks - own1)) * kChunk);
+            ptx::fence_proxy_async_smem();
+            __syncthreads();
+            if (threadIdx.x < p.split && static_cast<int>(threadIdx.x) != rank) {
+                const int r = threadIdx.x, first = live * r / p.split, n = live * (r + 1) / p.split - first;
+                const uint32_t bytes = static_cast<uint32_t>(n) * (kTileN * 4);
+                if (bytes)
+                    ptx::bulk_copy_to_cta(
+                        ptx::mapa(ptx::smem_u32(smem) + p.recv_off + (rank < r ? rank : rank - 1) * bytes, r * kG + half),
+                        ptx::smem_u32(part) + static_cast<uint32_t>(first) * (kTileN * 4), bytes,
+                        ptx::mapa(ptx::smem_u32(&recv_bar), r * kG + half));
             }
+            __syncwarp();
         }
+        for (int i = own0 + group; i < own1 && ok; i += kThreads / 128) bring(i * kChunk);
         ptx::tc_fence_before();
     }
-    ptx::fence_proxy_async_smem();
     __syncthreads();
     if (p.split > 1) {
-        // each other CTA's share of the tokens goes to it: its slot of this rank, among the
-        // ranks without its own
-        if (threadIdx.x < p.split && static_cast<int>(threadIdx.x) != rank) {
-            const int r = threadIdx.x, first = live * r / p.split, n = live * (r + 1) / p.split - first;
-            const uint32_t bytes = static_cast<uint32_t>(n) * (kTileN * 4);
-            if (bytes)
-                ptx::bulk_copy_to_cta(ptx::mapa(ptx::smem_u32(smem) + p.recv_off + (rank < r ? rank : rank - 1) * bytes, r * kG + half),
-                                      ptx::smem_u32(part) + static_cast<uint32_t>(first) * (kTileN * 4), bytes,
-                                      ptx::mapa(ptx::smem_u32(&recv_bar), r * kG + half));
-        }
         if (recv_bytes && !ptx::mbar_wait(ptx::smem_u32(&recv_bar), 0u, p.wait_limit_ns)) ok = false;
         __syncwarp();
         ptx::cluster_arrive_relaxed();   // (what this CTA was sent is here)
@@ -358,10 +370,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1) linear_split_kernel(const __
         const float4 *own = reinterpret_cast<const float4 *>(part) + lane;
         const float4 *recv = reinterpret_cast<const float4 *>(smem + p.recv_off) + lane;
         // four tokens at a time hide one another's latency, where there are that many
-        if (t1 - t0 <= kSplitThreads / 32)
-            finish<kBF16, kEpi, 1>(p, m0, t0, t1, rank, col, own, recv);
+        if (t1 - t0 <= kThreads / 32)
+            finish<kBF16, kEpi, 1, kThreads>(p, m0, t0, t1, rank, col, own, recv);
         else
-            finish<kBF16, kEpi, 4>(p, m0, t0, t1, rank, col, own, recv);
+            finish<kBF16, kEpi, 4, kThreads>(p, m0, t0, t1, rank, col, own, recv);
     }
     // no CTA leaves while its sums are on their way to another, nor half a pair before its MMAs' other half
     __syncwarp();
@@ -398,12 +410,15 @@ void fit_split(SplitShape &s, int steps, int num_sms) {
     const uint32_t room = s.per_sm == 2 ? 110u * 1024u : 220u * 1024u;
     const uint32_t sums = static_cast<uint32_t>(s.rows) * kTileN * 4;   // this CTA's, over the ring
     const uint32_t recv = static_cast<uint32_t>((s.split - 1) * ((s.rows + s.split - 1) / s.split)) * kTileN * 4;
-    // the others' sums beside the ring where that leaves it four stages, over it otherwise
+    int full = static_cast<int>(room / stage);
+    if (full > kMaxStages) full = kMaxStages;
+    if (full > most) full = most;
+    // the others' sums beside the ring, or, where that would shorten it, over it: what is in
+    // flight sets a pair's rate (512 tokens, 4096 x 4096, 128 of the 192 KiB that fit: 0.42 us
+    // a stage instead of 0.28)
     s.stages = static_cast<int>((room - recv) / stage);
-    s.late = s.stages < 4 && s.stages < most;
-    if (s.late) s.stages = static_cast<int>(room / stage);
-    if (s.stages > kMaxStages) s.stages = kMaxStages;
-    if (s.stages > most) s.stages = most;
+    s.late = s.stages < full && s.group == 2;
+    if (s.late || s.stages > full) s.stages = full;
     const uint32_t ring = s.stages * stage;
     s.recv_off = s.late || ring < sums ? sums : ring;
     const uint32_t bytes = ring > s.recv_off + recv ? ring : s.recv_off + recv;
@@ -441,7 +456,7 @@ int clusters_at_once(int ctas, int num_sms) {
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(ctas * num_sms), 1, 1);
-        cfg.blockDim = dim3(kSplitThreads, 1, 1);
+        cfg.blockDim = dim3(split_threads(1), 1, 1);
         cfg.dynamicSmemBytes = 222 * 1024;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -473,8 +488,8 @@ float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sm
     const float stages = waves * (static_cast<float>(steps) / s.split) * stage * share / 110e3f;
     const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 2.0f / 6.9e6f;
     const float stream = sqrtf(stages * stages + read * read);
-    float join = 0.012f * s.rows;
-    if (s.split > 1) join += 0.5f + 0.016f * s.rows * (s.split - 1) / s.split + (s.rows > 128 ? 1.5f : 0.0f);
+    float join = 0.008f * s.rows;
+    if (s.split > 1) join += 0.3f + 0.010f * s.rows * (s.split - 1) / s.split;
     const float ahead = prefetch_pays(s, num_sms) ? 0.8f : 0.0f;
     return 3.3f + (s.group == 2 ? 0.6f : 0.0f) + stream + waves * join + 3.0f * (waves - 1.0f) - ahead;
 }
@@ -525,7 +540,7 @@ cudaError_t launch_split(const SplitParams &p, const SplitShape &s, cudaStream_t
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(s.tiles * s.split * kG), 1, 1);
-    cfg.blockDim = dim3(kSplitThreads, 1, 1);
+    cfg.blockDim = dim3(split_threads(kG), 1, 1);
     cfg.dynamicSmemBytes = s.smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -550,7 +565,7 @@ bool linear_prefers_split(const LinearParams &p, int num_sms) {
     if (p.m <= 64) return true;
     // the 256 x 256 tiles: 5.7 us and 0.28 a 64-deep stage for each wave of them (4096 deep, 1,
     // 3 and 4 waves: 23.2, 60.9 and 79.0 us; 100 deep: 6.3).  Where the two cross, at (m, 4096) with k = 4096:
-    // 384 tokens 16.8 us split against 23.3, 512 tokens 21.2 against 23.4, 777 24.8 against 24.5.
+    // 384 tokens 15.6 us split against 24.4, 512 tokens 18.2 against 24.5, 777 24.8 against 24.5.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256), pairs = num_sms / 2;
     const float us = 5.7f + 0.28f * static_cast<float>((tiles + pairs - 1) / pairs) * ((p.k + kDepth - 1) / kDepth);
     return best_split(p, num_sms).us < us;
