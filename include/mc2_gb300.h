@@ -304,7 +304,9 @@ int mc2_alltoall_quant_mm_no_alloc(const void *const *chunks, int rank_size, int
  * the same in every row), so a slice of a wider tensor is passed as it is.
  * They take any sizes from 1 and any alignment that suits the element type;
  * sizes and layouts that the fast kernels cannot take run on a plain kernel,
- * which each call's comment names.
+ * which each call's comment names.  An output overlaps no other tensor of the
+ * call, but where its comment says that it may be an input itself.  A call's
+ * first use of a kernel on a device loads it: make it before a stream capture.
  */
 
 /*

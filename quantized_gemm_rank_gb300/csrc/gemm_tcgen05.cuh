@@ -871,8 +871,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 // The tile is one K block: its sums are read from TMEM where they are used, in
                 // a short loop (kept in registers, 128 of them could only be indexed by
                 // unrolled code past the instruction cache's size: an (8192, 8192) output with
-                // k = 1024 and gelu took 159 us that way and takes 123 this way, with k = 7168, a
-                // bias and the pre-activation 816 and 588).
+                // k = 1024 and gelu took 159 us that way and takes 107 this way, with k = 7168, a
+                // bias and the pre-activation 816 and 573).
                 // The warp's 128 columns go in four pieces of 32, through two buffers of 32
                 // rows x 64 bytes (64-byte swizzle: chunk j of row r at chunk j ^ (r / 2 % 4)), so
                 // that a piece's store is read while the next piece is worked on.

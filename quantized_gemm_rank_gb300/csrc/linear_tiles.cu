@@ -1,6 +1,9 @@
 // linear_tiles.cu -- the fused-epilogue matrix product of many rows: the GEMM of
 // gemm_tcgen05.cuh with its tiles taken at run time and the epilogue forms of
-// epilogue.cuh.
+// epilogue.cuh.  A tile's sum stays in one fp32 accumulator, so the epilogue can read
+// it from TMEM where it uses it (the all-gather GEMM adds blocks of 1024 in registers).
+// The tensor pipe bounds it: 8192 x 8192 x 7168 with bias, gelu and the
+// pre-activation 520 us, 1852 TFLOP/s; without an epilogue 480 to 490.
 #include "gemm_tcgen05.cuh"
 #include "host.h"
 #include "internal.h"

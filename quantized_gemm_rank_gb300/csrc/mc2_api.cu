@@ -277,7 +277,7 @@ int mc2_device_status(void) {
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "cudaDeviceSynchronize: %s", cudaGetErrorString(e));
     int st = 0;
     if (mc2::read_and_clear_gemm_status(&st) != 0) return fail(MC2_ERR_CUDA, "reading the device status word failed");
-    if (st != 0) return fail(MC2_ERR_TIMEOUT, "a bounded wait inside the GEMM kernel gave up");
+    if (st != 0) return fail(MC2_ERR_TIMEOUT, "a bounded wait inside a kernel gave up");
     return MC2_OK;
 }
 
