@@ -406,8 +406,9 @@ typedef enum {
  *   out       (m, n), rows ldo apart; may be residual itself (same stride)
  *   preact    NULL or (m, n), rows ldp apart (what mc2_matmul_act_grad and
  *             mc2_act_grad take)
- *   Where a matrix is not 16-byte aligned or its stride is not a multiple of 8
- *   elements, a plain kernel without tensor cores does the work.
+ *   Where a matrix is not 16-byte aligned, its stride is not a multiple of 8
+ *   elements or is 2^39 or more, or a size is within 512 of INT32_MAX, a plain
+ *   kernel without tensor cores does the work.
  *
  * Returns MC2_OK or a negative mc2_status; nothing is launched on error.
  */

@@ -29,7 +29,8 @@ struct LinearParams {
 cudaError_t launch_linear_any(bool bf16, const LinearParams &p, cudaStream_t stream);
 
 // The tensor-core kernels take 16-byte aligned matrices whose strides are multiples
-// of 8 elements (the tensor copies' rule); the strides of single rows are set here.
+// of 8 elements and below 2^39 (the tensor copies' rule), and sizes that leave a tile
+// of room in 32 bits; the strides of single rows are set by the caller.
 bool linear_layout_fits(const LinearParams &p);
 // A CTA pair per 256 x 256 tile: products of many rows.
 cudaError_t launch_linear_tiles(bool bf16, const LinearParams &p, int num_sms, cudaStream_t stream);

@@ -24,11 +24,11 @@ __global__ void __launch_bounds__(256) linear_any_kernel(const __grid_constant__
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int64_t n_tiles = (p.n + 63) / 64;
+    const int64_t n_tiles = (p.n + 63ll) / 64;
     const int m0 = static_cast<int>(blockIdx.x / n_tiles) * 64, n0 = static_cast<int>(blockIdx.x % n_tiles) * 64;
     const T *x = static_cast<const T *>(p.x), *w = static_cast<const T *>(p.w);
     float acc[4][4] = {};
-    for (int k0 = 0; k0 < p.k; k0 += 16) {
+    for (int64_t k0 = 0; k0 < p.k; k0 += 16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = tid + 256 * i, r = e >> 4, c = e & 15;

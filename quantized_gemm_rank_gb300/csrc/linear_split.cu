@@ -549,13 +549,17 @@ cudaError_t launch_split(const SplitParams &p, const SplitShape &s, cudaStream_t
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-bool rows_aligned(const void *p, int64_t ld) { return !p || (host::aligned16(p) && ld % 8 == 0); }
+// what a tensor map takes: 16-byte units, and rows less than 2^40 bytes apart
+bool rows_fit(const void *p, int64_t ld) { return !p || (host::aligned16(p) && ld % 8 == 0 && ld < (1ll << 39)); }
 
 }  // namespace
 
 bool linear_layout_fits(const LinearParams &p) {
-    return rows_aligned(p.x, p.ldx) && rows_aligned(p.w, p.ldw) && rows_aligned(p.out, p.ldo) &&
-           rows_aligned(p.preact, p.ldp) && rows_aligned(p.aux, p.ldaux);
+    // the kernels count rows, columns and stages in 32 bits, up to a tile past the end
+    constexpr int kMost = INT32_MAX - 512;
+    if (p.m > kMost || p.n > kMost || p.k > kMost) return false;
+    return rows_fit(p.x, p.ldx) && rows_fit(p.w, p.ldw) && rows_fit(p.out, p.ldo) && rows_fit(p.preact, p.ldp) &&
+           rows_fit(p.aux, p.ldaux);
 }
 
 bool linear_prefers_split(const LinearParams &p, int num_sms) {

@@ -101,7 +101,7 @@ SIZES = [(1, 8, 8), (1, 1, 1), (1, 4096, 4096), (2, 136, 64), (7, 128, 72), (15,
          (65, 200, 320), (100, 5000, 96), (127, 136, 1000), (128, 256, 2048), (129, 512, 512), (200, 1000, 4096),
          (255, 384, 640), (256, 256, 1024), (257, 264, 136), (300, 2048, 8), (520, 1000, 264), (777, 1000, 2056),
          (1100, 1104, 1032), (2100, 96, 128), (1500, 2600, 64), (4096, 512, 256), (128, 10000, 4160),
-         (250, 5000, 4096), (60, 40000, 5000)]
+         (250, 5000, 4096), (60, 40000, 5000), (700, 512, 16384), (2000, 1024, 24576)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
