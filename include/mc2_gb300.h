@@ -382,7 +382,7 @@ int mc2_rms_norm_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, 
 /* Activations of the fused-epilogue products. */
 typedef enum {
     MC2_ACT_NONE = 0,
-    MC2_ACT_RELU = 1,      /* max(z, 0) */
+    MC2_ACT_RELU = 1,      /* max(z, 0); its derivative is 1 above 0, and 0 elsewhere: at 0, too */
     MC2_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
     MC2_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
     MC2_ACT_SILU = 4       /* z / (1 + e^-z) */

@@ -35,6 +35,8 @@ def plain_act(z, act):
 
 
 def plain_derivative(z, act):
+    if act == "relu":   # (clamp's own gradient is 1 at the bound itself; relu's is 0 at 0)
+        return (z > 0).double()
     z = z.double().clone().requires_grad_()
     plain_act(z, act).sum().backward()
     return z.grad
@@ -295,6 +297,23 @@ def test_derivative_at_its_limits(act):
     dy = torch.full_like(z, 2.0)
     got = mc2.mc2_act_grad(dy, z, activation=act)[0].tolist()
     assert got[:3] == [0, 0, 0] and got[3:6] == [2, 2, 2] and got[6] != got[6] and got[7] == 1.0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_relu_derivative_at_zero(dtype):
+    """1 above zero down to the least number of the type, 0 at both zeros and below, in each form of the call."""
+    tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    row = torch.tensor([0.0, -0.0, tiny, -tiny, 1.0, -1.0, float("inf"), -float("inf")], dtype=dtype)
+    want = [0, 0, 1, 0, 1, 0, 1, 0]
+    for m in (2, 300, 2000):
+        z = row.repeat(m, 1).cuda()
+        one = torch.ones(m, 8, dtype=dtype, device="cuda")
+        w = torch.full((8, 8), 0.125, dtype=dtype, device="cuda")   # one @ w is 1 everywhere
+        wide = torch.zeros(m, 9, dtype=dtype, device="cuda")       # rows that the plain kernels take
+        wide[:, :8] = z
+        for at in (z, wide[:, :8]):
+            assert mc2.mc2_act_grad(one, at, activation="relu")[m - 1].tolist() == want
+            assert mc2.mc2_matmul_act_grad(one, w, at, activation="relu")[m - 1].tolist() == want
 
 
 def test_derivatives_against_differences():
