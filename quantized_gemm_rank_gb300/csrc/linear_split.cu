@@ -38,6 +38,7 @@ constexpr int kTileN = 128;      // weight columns a tile (MMA M)
 constexpr int kDepth = 64;       // contraction a stage
 constexpr int kMaxStages = 16;
 constexpr int kMaxCluster = 8;
+constexpr int kProducers = 4;
 // Threads a CTA: the pairs' tiles have more to bring out of TMEM and one CTA an SM.
 __host__ __device__ constexpr int split_threads(int group) { return group == 1 ? 256 : 512; }
 constexpr int kBlockSteps = 1024 / kDepth;   // stages of one accumulator
@@ -89,58 +90,106 @@ __device__ __forceinline__ void load4(const uint16_t *p, int n, uint32_t *w) {
     }
 }
 
-// The tokens first + warp * kT, ... < last of a tile (kT a warp at a time, four columns a
-// lane): the partial sums in rank order, the epilogue, the outputs.
-template <bool kBF16, int kEpi, int kT, int kThreads>
-__device__ __forceinline__ void finish(const SplitParams &p, int m0, int first, int last, int rank, int col, const float4 *own,
-                                       const float4 *recv) {
-    const int warp = threadIdx.x >> 5;
-    const int n = p.n - col;   // columns from here on, > 0
-    const int slot = (last - first) * (kTileN / 4);
-    float b4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+// kT tokens of a tile from token t on, four columns a lane: the partial sums in rank order, the
+// epilogue, the outputs.  kWhole: all four columns are in the row.  `from`: the token's sums from rank 0 on, `slot`
+// apart but for this CTA's own (rank `rank`), which are at `own`.
+template <bool kBF16, int kEpi, int kT, bool kWhole>
+__device__ __forceinline__ void finish_tokens(const SplitParams &p, const float4 *own, const float4 *from, int slot, int rank, const float *b4,
+                                              const uint16_t *aux_row, uint16_t *pre_row, uint16_t *out_row, int n) {
+    if constexpr (kWhole) n = 4;
+    uint32_t aux[2 * kT] = {};
+    if (aux_row) {
+#pragma unroll
+        for (int u = 0; u < kT; ++u) load4(aux_row + u * p.ldaux, n, &aux[2 * u]);
+    }
+    float v[4 * kT];
+    auto source = [&](int r) {
+        const float4 *at = r == rank ? own : from;
+        if (r != rank) from += slot;
+        return at;
+    };
+    const float4 *at = source(0);
+#pragma unroll
+    for (int u = 0; u < kT; ++u) {
+        const float4 s = at[u * (kTileN / 4)];
+        v[4 * u] = s.x, v[4 * u + 1] = s.y, v[4 * u + 2] = s.z, v[4 * u + 3] = s.w;
+    }
+#pragma unroll 1
+    for (int r = 1; r < p.split; ++r) {
+        at = source(r);
+#pragma unroll
+        for (int u = 0; u < kT; ++u) {
+            const float4 s = at[u * (kTileN / 4)];
+            v[4 * u] = __fadd_rn(v[4 * u], s.x), v[4 * u + 1] = __fadd_rn(v[4 * u + 1], s.y);
+            v[4 * u + 2] = __fadd_rn(v[4 * u + 2], s.z), v[4 * u + 3] = __fadd_rn(v[4 * u + 3], s.w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * kT; ++i) v[i] = __fadd_rn(v[i], b4[i & 3]);
+    if (pre_row) {
+#pragma unroll
+        for (int u = 0; u < kT; ++u) store4<kBF16>(pre_row + u * p.ldp, n, &v[4 * u]);
+    }
+    epilogue<kBF16, kEpi>(v, aux, p.act, aux_row != nullptr);
+#pragma unroll
+    for (int u = 0; u < kT; ++u) store4<kBF16>(out_row + u * p.ldo, n, &v[4 * u]);
+}
+
+// Where a lane's four columns of the tokens from `first` on are.
+struct Place {
+    const uint16_t *aux;
+    uint16_t *pre, *out;
+    int n;          // columns from the lane's first on; none: 0 or less
+    float b4[4];    // their biases
+};
+
+template <bool kBF16>
+__device__ __forceinline__ Place place(const SplitParams &p, int64_t row, int col) {
+    Place at = {};
+    at.n = p.n - col;
+    if (p.aux) at.aux = static_cast<const uint16_t *>(p.aux) + row * p.ldaux + col;
+    if (p.preact) at.pre = static_cast<uint16_t *>(p.preact) + row * p.ldp + col;
+    at.out = static_cast<uint16_t *>(p.out) + row * p.ldo + col;
     if (p.bias) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (i < n) b4[i] = load16<kBF16>(p.bias, col + i);
+            if (i < at.n) at.b4[i] = load16<kBF16>(p.bias, col + i);
     }
+    return at;
+}
+
+// The tokens [first, last) of a tile, over the CTA's warps.
+template <bool kBF16, int kEpi, int kThreads>
+__device__ __forceinline__ void finish(const SplitParams &p, const Place &at, int first, int last, int rank, const float4 *own,
+                                       const float4 *recv) {
+    constexpr int kWarps = kThreads / 32;
+    const int warp = threadIdx.x >> 5;
+    const int slot = (last - first) * (kTileN / 4);
+    own += first * (kTileN / 4);
+    const int count = last - first;
+    int t = 0;   // from `first` on
+    // four tokens at a time hide one another's latency, where there are that many
+    if (count > kWarps) {
+        for (t = 4 * warp; t + 4 <= count; t += 4 * kWarps) {
+            const float4 *o = own + t * (kTileN / 4), *r = recv + t * (kTileN / 4);
+            if (at.n >= 4) {
+                finish_tokens<kBF16, kEpi, 4, true>(p, o, r, slot, rank, at.b4, at.aux ? at.aux + t * p.ldaux : nullptr,
+                                                    at.pre ? at.pre + t * p.ldp : nullptr, at.out + t * p.ldo, 4);
+            } else {
 #pragma unroll 1
-    for (int t = first + warp * kT; t < last; t += kThreads / 32 * kT) {
-        const int64_t row = m0 + t;
-        const int count = last - t;   // tokens left: those past the last repeat it and are not stored
-        uint32_t aux[2 * kT] = {};
-        if (p.aux) {
-            const uint16_t *from = static_cast<const uint16_t *>(p.aux) + row * p.ldaux + col;
-#pragma unroll
-            for (int u = 0; u < kT; ++u) load4(from + (u < count ? u : 0) * p.ldaux, n, &aux[2 * u]);
-        }
-        float v[4 * kT];
-#pragma unroll
-        for (int i = 0; i < 4 * kT; ++i) v[i] = 0.0f;
-        const float4 *at = recv + (t - first) * (kTileN / 4);
-        for (int r = 0; r < p.split; ++r) {
-            const float4 *from = r == rank ? own + t * (kTileN / 4) : at;
-            if (r != rank) at += slot;
-#pragma unroll
-            for (int u = 0; u < kT; ++u) {
-                const float4 s = from[(u < count ? u : 0) * (kTileN / 4)];
-                v[4 * u] = __fadd_rn(v[4 * u], s.x), v[4 * u + 1] = __fadd_rn(v[4 * u + 1], s.y);
-                v[4 * u + 2] = __fadd_rn(v[4 * u + 2], s.z), v[4 * u + 3] = __fadd_rn(v[4 * u + 3], s.w);
+                for (int u = 0; u < 4; ++u)
+                    finish_tokens<kBF16, kEpi, 1, false>(p, o + u * (kTileN / 4), r + u * (kTileN / 4), slot, rank, at.b4,
+                                                         at.aux ? at.aux + (t + u) * p.ldaux : nullptr,
+                                                         at.pre ? at.pre + (t + u) * p.ldp : nullptr, at.out + (t + u) * p.ldo, at.n);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4 * kT; ++i) v[i] = __fadd_rn(v[i], b4[i & 3]);
-        if (p.preact) {
-            uint16_t *to = static_cast<uint16_t *>(p.preact) + row * p.ldp + col;
-#pragma unroll
-            for (int u = 0; u < kT; ++u)
-                if (u < count) store4<kBF16>(to + u * p.ldp, n, &v[4 * u]);
-        }
-        epilogue<kBF16, kEpi>(v, aux, p.act, p.aux != nullptr);
-        uint16_t *to = static_cast<uint16_t *>(p.out) + row * p.ldo + col;
-#pragma unroll
-        for (int u = 0; u < kT; ++u)
-            if (u < count) store4<kBF16>(to + u * p.ldo, n, &v[4 * u]);
+        t = count & ~3;   // the rest, fewer than four
     }
+#pragma unroll 1
+    for (t += warp; t < count; t += kWarps)
+        finish_tokens<kBF16, kEpi, 1, false>(p, own + t * (kTileN / 4), recv + t * (kTileN / 4), slot, rank, at.b4,
+                                             at.aux ? at.aux + t * p.ldaux : nullptr, at.pre ? at.pre + t * p.ldp : nullptr,
+                                             at.out + t * p.ldo, at.n);
 }
 
 template <bool kBF16, int kEpi, int kG>
@@ -152,10 +201,29 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (broadcast from a lane: what the compiler knows to be the same in a warp it keeps in uniform registers, where the MMA
+    // and copy instructions take their operands)
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int S = p.stages;
+    // (first what takes longest)
+    if (warp == 1) {
+        ptx::tmem_alloc<kG>(ptx::smem_u32(&tmem_slot), static_cast<uint32_t>(p.tmem_cols));
+        ptx::tmem_relinquish<kG>();
+    } else if (warp == 0) {
+        if (lane < S) {
+            ptx::mbar_init(ptx::smem_u32(&full_bar[lane]), 1);
+            ptx::mbar_init(ptx::smem_u32(&empty_bar[lane]), 1);
+        }
+        if (lane == 0) {
+            failed = 0;
+            ptx::mbar_init(ptx::smem_u32(&done_bar), 1);
+            ptx::mbar_init(ptx::smem_u32(&recv_bar), 1);
+        }
+        ptx::fence_mbar_init();
+        __syncwarp();
+    }
     const int ctas = p.split * kG;                       // of the cluster
-    const int crank = ctas > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    const int crank = ctas > 1 ? __shfl_sync(0xffffffffu, static_cast<int>(ptx::cluster_ctarank()), 0) : 0;
     const int half = kG == 2 ? crank & 1 : 0;            // of the pair
     const int rank = crank / kG;                         // share of the contraction
     const int x_rows = p.rows / kG;                      // tokens this CTA loads
@@ -164,42 +232,33 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     // clusters next to one another share the weight's tile
     const int n0 = (tile / p.m_tiles * kG + half) * kTileN;
     const int m0 = tile % p.m_tiles * p.rows;
-    const int step0 = static_cast<int>(static_cast<int64_t>(p.steps) * rank / p.split);
-    const int count = static_cast<int>(static_cast<int64_t>(p.steps) * (rank + 1) / p.split) - step0;
+    // (at most 2^25 steps and 8 ranks)
+    const int step0 = p.steps * rank / p.split;
+    const int count = p.steps * (rank + 1) / p.split - step0;
 
     // the tile's tokens, and this CTA's share of them to finish
     const int live = min(p.rows, p.m - m0);
     const int t0 = live * rank / p.split, t1 = live * (rank + 1) / p.split;
     const uint32_t recv_bytes = static_cast<uint32_t>((p.split - 1) * (t1 - t0)) * (kTileN * 4);
 
-    if (threadIdx.x == 0) {
-        failed = 0;
-        for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(ptx::smem_u32(&full_bar[s]), 1);
-            ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
-        }
-        ptx::mbar_init(ptx::smem_u32(&done_bar), 1);
-        ptx::mbar_init(ptx::smem_u32(&recv_bar), 1);
-        ptx::fence_mbar_init();
-        if (recv_bytes) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&recv_bar), recv_bytes);
-    }
-    if (warp == 1) {
-        ptx::tmem_alloc<kG>(ptx::smem_u32(&tmem_slot), static_cast<uint32_t>(p.tmem_cols));
-        ptx::tmem_relinquish<kG>();
-    }
+    if (threadIdx.x == 0 && recv_bytes) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&recv_bar), recv_bytes);
     ptx::tc_fence_before();
     __syncthreads();
     // the barriers of the cluster are ready (one CTA a share: needed when its sums are sent)
     if (ctas > 1) ptx::cluster_arrive_relaxed();
     if constexpr (kG == 2) ptx::cluster_wait();
     ptx::tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    if (warp == 0 && lane == 0) {
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+    // A producer's wait for a stage tells the stage's last use from the one before only while
+    // the ring is at least as long as there are producers: it has issued the step
+    // `producers` back, so what the ring held before that one is consumed.
+    const int producers = min(kProducers, S), producer = warp == 0 ? 0 : warp - 1;   // (warp 1 issues the MMAs)
+    if (warp != 1 && producer < producers && lane == 0) {
         ptx::prefetch_tmap(&p.w_map);
         ptx::prefetch_tmap(&p.x_map);
         // The weight's first stages into L2 while the stream's previous kernel ends.  Nothing is
         // read by this: were that kernel to write the weight, L2 would hold what it wrote.
-        for (int i = 0; i < min(count, S) && p.prefetch; ++i) {
+        for (int i = producer; i < min(count, S) && p.prefetch; i += producers) {
             const int k0 = (step0 + i) * kDepth;
             if (p.w_kn) {
                 ptx::tma_prefetch_2d(&p.w_map, n0, k0);
@@ -212,9 +271,11 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
 
-    if (warp == 0 && lane == 0) {
-        int stage = 0, issued = 0;
+    if (warp != 1 && producer < producers) {
+        // stages producer, producer + producers, ...; the warp stays converged, an elected lane issues
+        int i = producer, stage = producer;
         uint32_t phase = 1;
+        while (stage >= S) stage -= S, phase ^= 1u;
         bool ok = true;
         auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
             if constexpr (kG == 2)
@@ -222,8 +283,9 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
             else
                 ptx::tma_load_2d(dst, m, c0, c1, bar);
         };
-        for (int i = 0; i < count; ++i) {
-            if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), phase, p.wait_limit_ns)) {
+        for (; i < count; i += producers) {
+            const bool got = ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), phase, p.wait_limit_ns);
+            if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 break;
             }
@@ -231,23 +293,26 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
             const uint32_t full = kG == 2 && half ? ptx::mapa(mine, crank - 1) : mine;
             const uint32_t sw = ptx::smem_u32(smem) + stage * stage_bytes;
             const int k0 = (step0 + i) * kDepth;
-            // (the pair's first CTA counts the bytes of both)
-            if (!half) ptx::mbar_arrive_expect_tx(mine, stage_bytes * kG);
-            if (p.w_kn) {
-                load(sw, &p.w_map, n0, k0, full);
-                load(sw + kWBytes / 2, &p.w_map, n0 + 64, k0, full);
-            } else {
-                load(sw, &p.w_map, k0, n0, full);
+            if (ptx::elect_one()) {
+                // (the pair's first CTA counts the bytes of both)
+                if (!half) ptx::mbar_arrive_expect_tx(mine, stage_bytes * kG);
+                if (p.w_kn) {
+                    load(sw, &p.w_map, n0, k0, full);
+                    load(sw + kWBytes / 2, &p.w_map, n0 + 64, k0, full);
+                } else {
+                    load(sw, &p.w_map, k0, n0, full);
+                }
+                load(sw + kWBytes, &p.x_map, k0, m0 + half * x_rows, full);
             }
-            load(sw + kWBytes, &p.x_map, k0, m0 + half * x_rows, full);
-            ++issued;
-            if (++stage == S) stage = 0, phase ^= 1u;
+            __syncwarp();
+            stage += producers;
+            while (stage >= S) stage -= S, phase ^= 1u;
         }
-        if (!ok) {
+        if (!ok && lane == 0) {
             atomicExch(&failed, 1);
-            // the copies in flight land before the CTA can exit
-            for (int back = 1; back <= S && back <= issued && !half; ++back) {
-                const int i = issued - back;
+            // the copies in flight, among this warp's last ones, land before the CTA can exit
+            for (int back = 0; back <= S && i - producers >= 0 && !half; back += producers) {
+                i -= producers;
                 (void)ptx::mbar_wait(ptx::smem_u32(&full_bar[i % S]), static_cast<uint32_t>((i / S) & 1), p.wait_limit_ns);
             }
             ptx::nanosleep(20000);
@@ -255,47 +320,58 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     } else if (warp == 1 && !half) {
         const uint32_t idesc = ptx::idesc_f16(kBF16, false, kTileN * kG, p.rows, p.w_kn != 0);
         const uint32_t s0 = ptx::smem_u32(smem);
-        const uint64_t w_desc0 = p.w_kn ? ptx::smem_desc_sw128(s0, kDepth * 128, 1024) : ptx::smem_desc_sw128(s0, 16, 1024);
-        const uint64_t x_desc0 = ptx::smem_desc_sw128(s0 + kWBytes, 16, 1024);
+        const uint64_t w_desc = p.w_kn ? ptx::smem_desc_sw128(s0, kDepth * 128, 1024) : ptx::smem_desc_sw128(s0, 16, 1024);
+        const uint64_t x_desc = ptx::smem_desc_sw128(s0 + kWBytes, 16, 1024);
+        // (a stage's addresses stay within the descriptors' low words)
+        const uint32_t w_hi = static_cast<uint32_t>(w_desc >> 32), w_lo0 = static_cast<uint32_t>(w_desc);
+        const uint32_t x_hi = static_cast<uint32_t>(x_desc >> 32), x_lo0 = static_cast<uint32_t>(x_desc);
         const uint32_t w_kk = p.w_kn ? (2048u >> 4) : (32u >> 4);
         const uint32_t x_kk = 32u >> 4;
+        const uint32_t full0 = ptx::smem_u32(&full_bar[0]), to_empty = ptx::smem_u32(&empty_bar[0]) - full0;
+        const uint32_t full_end = full0 + 8u * static_cast<uint32_t>(S), advance = stage_bytes >> 4;
         const uint16_t pair = static_cast<uint16_t>(3u << crank);
-        auto commit = [&](uint64_t *bar) {
-            if constexpr (kG == 2)
-                ptx::mma_commit_pair(ptx::smem_u32(bar), pair);
-            else
-                ptx::mma_commit<1>(ptx::smem_u32(bar));
-        };
-        int stage = 0, in_block = 0, acc = 0, blocks = 0;
-        uint32_t phase = 0;
+        uint32_t full = full0, off = 0, phase = 0;
         bool ok = true;
-        for (int i = 0; i < count; ++i) {
-            const bool got = ptx::mbar_wait(ptx::smem_u32(&full_bar[stage]), phase, p.wait_limit_ns);
-            if (!__all_sync(0xffffffffu, got)) {
-                ok = false;
-                break;
-            }
-            ptx::tc_fence_after();
-            const uint64_t off = static_cast<uint64_t>(stage) * (stage_bytes >> 4);
+        bool ready = ptx::mbar_test(full, 0);
+        for (int done = 0, block = 0, acc = 0; done < count && ok; ++block) {
             const uint32_t d = tmem + static_cast<uint32_t>(acc * p.rows);
-            // an accumulator's first stage starts it from zero
-            ptx::mma_f16_ss<kG>(d, w_desc0 + off, x_desc0 + off, idesc, in_block > 0 || blocks >= p.accs ? 1u : 0u);
-#pragma unroll
-            for (int kk = 1; kk < kDepth / 16; ++kk)
-                ptx::mma_f16_ss<kG>(d, w_desc0 + off + kk * w_kk, x_desc0 + off + kk * x_kk, idesc, 1u);
-            commit(&empty_bar[stage]);
-            if (++stage == S) stage = 0, phase ^= 1u;
-            if (++in_block == kBlockSteps) {
-                in_block = 0;
-                ++blocks;
-                if (++acc == p.accs) acc = 0;
+            uint32_t add = block >= p.accs ? 1u : 0u;   // an accumulator's first stage starts it from zero
+            const int end = min(done + kBlockSteps, count);
+            for (; done < end; ++done) {
+                if (!__all_sync(0xffffffffu, ready)) {
+                    ready = ptx::mbar_wait(full, phase, p.wait_limit_ns);
+                    if (!__all_sync(0xffffffffu, ready)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                ptx::tc_fence_after();
+                const uint32_t bar = full + to_empty, w_lo = w_lo0 + off, x_lo = x_lo0 + off;
+                // the next stage's barrier is asked before this stage's MMAs are issued
+                full += 8;
+                off += advance;
+                if (full == full_end) full = full0, off = 0, phase ^= 1u;
+                ready = ptx::mbar_test(full, phase);
+                ptx::mma_stage_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add, bar, pair);
+                add = 1;
             }
+            if (++acc == p.accs) acc = 0;
         }
         if (!ok && lane == 0) atomicExch(&failed, 1);
         // (also after giving up: the MMAs issued so far complete before TMEM is freed)
-        commit(&done_bar);
+        if constexpr (kG == 2)
+            ptx::mma_commit_pair(ptx::smem_u32(&done_bar), pair);
+        else
+            ptx::mma_commit<1>(ptx::smem_u32(&done_bar));
+    } else if (warp > kProducers && p.aux) {
+        // the other warps: the part of aux that this CTA will need, into L1
+        constexpr int kIdle = kThreads / 32 - kProducers - 1;
+        const uint16_t *aux = static_cast<const uint16_t *>(p.aux) + (static_cast<int64_t>(m0) + t0) * p.ldaux + n0;
+        for (int e = (warp - kProducers - 1) * 32 + lane; e < 2 * (t1 - t0); e += 32 * kIdle)
+            if (n0 + (e & 1) * 64 < p.n) ptx::prefetch_l1(aux + (e >> 1) * p.ldaux + (e & 1) * 64);
     }
     __syncwarp();
+    const Place at = place<kBF16>(p, static_cast<int64_t>(m0) + t0, n0 + 4 * lane);
     // every thread waits (bounded) for the MMAs: from here on the ring is idle
     if (!ptx::mbar_wait(ptx::smem_u32(&done_bar), 0u, p.wait_limit_ns)) atomicExch(&failed, 1);
     __syncthreads();
@@ -365,22 +441,16 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
         ptx::cluster_arrive_relaxed();   // (what this CTA was sent is here)
     }
     if (!ok && p.status) atomicExch(p.status, -7);
-    const int col = n0 + 4 * lane;
-    if (ok && col < p.n) {
+    if (ok && at.n > 0) {
         const float4 *own = reinterpret_cast<const float4 *>(part) + lane;
         const float4 *recv = reinterpret_cast<const float4 *>(smem + p.recv_off) + lane;
-        // four tokens at a time hide one another's latency, where there are that many
-        if (t1 - t0 <= kThreads / 32)
-            finish<kBF16, kEpi, 1, kThreads>(p, m0, t0, t1, rank, col, own, recv);
-        else
-            finish<kBF16, kEpi, 4, kThreads>(p, m0, t0, t1, rank, col, own, recv);
+        finish<kBF16, kEpi, kThreads>(p, at, t0, t1, rank, own, recv);
     }
     // no CTA leaves while its sums are on their way to another, nor half a pair before its MMAs' other half
+    // (nothing is published by this: an arrival with release would wait for the outputs' stores, 0.9 us)
     __syncwarp();
-    if (p.split > 1)
-        ptx::cluster_wait();
-    else if constexpr (kG == 2)
-        ptx::cluster_sync();
+    if (kG == 2 && p.split == 1) ptx::cluster_arrive_relaxed();
+    if (ctas > 1) ptx::cluster_wait();
     __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();

@@ -52,6 +52,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// The same without waiting (try_wait may suspend the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait: spins on try_wait and gives up after `limit_ns` of wall time
 // (checked every 256 polls).  Returns false on timeout.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
@@ -154,6 +167,13 @@ __device__ __forceinline__ bool clc_query(uint32_t resp, uint32_t &first_ctaid_x
         : "memory");
     first_ctaid_x = x;
     return ok != 0;
+}
+
+// One lane of a full, converged warp (the same one at every call): true there.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
 // Named barrier `id` over `count` threads (a multiple of 32) with an AND
@@ -341,6 +361,50 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uin
             "setp.ne.b32 p, %4, 0;\n\t"
             "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// The four MMAs of a 64-deep stage (descriptors of the words lo and hi, and lo + step, ...)
+// and the commit that frees it, under one election.  kG = 2: the commit arrives in the CTAs of `mask`.
+template <int kG>
+__device__ __forceinline__ void mma_stage_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t a_step, uint32_t b_lo,
+                                                 uint32_t b_hi, uint32_t b_step, uint32_t idesc, uint32_t accumulate, uint32_t bar,
+                                                 uint16_t mask) {
+    if constexpr (kG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t.reg .b32 al, bl;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+            "setp.eq.b32 p, %6, %6;\n\t"
+            "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%9];\n\t}" ::"r"(d_tmem),
+            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t.reg .b32 al, bl;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
+            "setp.eq.b32 p, %6, %6;\n\t"
+            "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
+            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
+            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%9], %10;\n\t}" ::"r"(d_tmem),
+            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step), "r"(bar), "h"(mask)
             : "memory");
 }
 
