@@ -10,12 +10,16 @@
 //   kG = 1  up to 64 tokens: a CTA takes 128 columns, M = 128
 //   kG = 2  more tokens: a CTA pair takes 256 columns, M = 256; each CTA loads 128
 //           columns of the weight and half the tokens, which halves what the
-//           tokens cost in L2 reads (at 256 tokens and one CTA per 128 columns
-//           those reads, 48 KiB a 64-deep stage, set the time)
-//   warp 0      TMA producer (one lane)
+//           tokens cost in L2 reads
 //   warp 1      TMEM allocation, MMA issue (the pair's first CTA)
+//   warps 0, 2, 3, 4   TMA producers: each takes every fourth stage
+//   the others  bring what the epilogue will read into L1
 //   all warps   then: partial sums from TMEM to shared memory, the sum over the
 //               cluster, and the epilogue, four columns a thread
+// Next to that, a stage's time was its issue: one lane took 460 clocks for a stage's two copies
+// (a wait, the count of bytes, 170 clocks a copy), four warps hide it; five elections and 64-bit
+// offsets took 360 clocks for its MMAs, which take 128 to 512 (now 220 to 255 where the MMAs are shorter).
+// 512 tokens, 4096 x 4096: 18.2 -> 15.5 us, 128 tokens 11.8 -> 10.4, 512 x 1024 x 8192 17.1 -> 12.5.
 // (Reading the other CTAs' sums with loads ran at 9 bytes a clock: 7.3 us for a pair's
 // 256 x 256 sums, the longest part of the call.)
 // The tensor core adds at the size of its running sum, so each 1024-deep part of
@@ -467,8 +471,8 @@ struct SplitShape {
 };
 
 // Fetching the weight's first stages into L2 ahead of the stream's previous kernel's end
-// pays where two CTAs share most SMs (one token, 4096 x 4096, 256 CTAs: 8.7 -> 7.8 us), and
-// costs where the loads follow at once (1024 x 8192, 64 CTAs: 7.2 -> 7.9).
+// pays where two CTAs share most SMs (one token, 4096 x 4096, 256 CTAs: 8.6 -> 7.7 us), and
+// costs where the loads follow at once (32 tokens, 1024 x 8192, 64 CTAs: 6.9 -> 7.5).
 bool prefetch_pays(const SplitShape &s, int num_sms) {
     return s.group == 1 && s.per_sm == 2 && s.tiles * s.split * 8 >= num_sms * 13ll;
 }
@@ -483,9 +487,8 @@ void fit_split(SplitShape &s, int steps, int num_sms) {
     int full = static_cast<int>(room / stage);
     if (full > kMaxStages) full = kMaxStages;
     if (full > most) full = most;
-    // the others' sums beside the ring, or, where that would shorten it, over it: what is in
-    // flight sets a pair's rate (512 tokens, 4096 x 4096, 128 of the 192 KiB that fit: 0.42 us
-    // a stage instead of 0.28)
+    // the others' sums beside the ring, or, where that would shorten it, over it (256 tokens,
+    // 4096 x 4096, split in two: 12.1 us against 12.7 with a shorter ring)
     s.stages = static_cast<int>((room - recv) / stage);
     s.late = s.stages < full && s.group == 2;
     if (s.late || s.stages > full) s.stages = full;
@@ -540,12 +543,15 @@ int clusters_at_once(int ctas, int num_sms) {
     return n;
 }
 
-// What a shape takes, in us, fitted to measurements on GB300: launch, set-up and the cluster's
-// barriers; the stages, at the 110 bytes a ns that an SM receives and the rate of device
-// memory, which reads the weight once (the root of the squares' sum, since the two do
-// not overlap wholly); another set-up for each further wave; and per token of the tile the way from TMEM to the output, and to
-// the other CTAs.  Over 50 shapes (1 to 1274 tokens, 64 to 16384 columns and depth) the
-// shape it chose took at most 8% more than the best one, but for three.
+// What a shape takes, in us, fitted to 1440 measurements on GB300: launch and set-up; the stages,
+// each bound by its MMAs or by the 175 bytes a ns that an SM receives, and the rate of device memory,
+// which reads the weight once (the root of the squares' sum, since the two do not overlap
+// wholly); another set-up for each further wave; per token of the tile the way from
+// TMEM to the output, and to the other CTAs; less what an early prefetch saves.  Rows that are not a multiple of 128 bytes
+// apart take more of the SM's port: a stage's 128 bytes of each lie in two lines (judged by the
+// sizes: a result does not depend on the strides).
+// Over 117 products (1 to 1536 tokens, 256 to 14336 columns, 1024 to 8192 deep) the
+// shape it chose took 1% more than the best one on average, and at most 13%.
 float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sms) {
     const int beside = s.smem <= kSmemPerSm / 2 - kSmemOverhead ? 2 : 1;   // CTAs that fit an SM
     const int64_t clusters = static_cast<int64_t>(clusters_at_once(s.group * s.split, num_sms)) * beside;
@@ -554,14 +560,14 @@ float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sm
     const int64_t slots = beside == 2 ? clusters * 11 / 10 : clusters;
     const float waves = static_cast<float>((units + slots - 1) / slots);
     const float share = (units < clusters ? units : clusters) * s.group * s.split > num_sms ? 2.0f : 1.0f;
-    const float stage = static_cast<float>(kWBytes) + static_cast<float>(s.rows / s.group) * kDepth * 2;
-    const float stages = waves * (static_cast<float>(steps) / s.split) * stage * share / 110e3f;
-    const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 2.0f / 6.9e6f;
+    const float bytes = static_cast<float>(kWBytes) + static_cast<float>(s.rows / s.group) * kDepth * 2;
+    const float port = (p.k % 64 != 0 || (!p.w_nk && p.n % 64 != 0) ? 1.87f : 1.0f) * share * bytes / 175e3f;
+    const float stages = waves * ((steps + s.split - 1) / s.split) * fmaxf(0.00102f * s.rows, port);
+    const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 2.0f / 7.0e6f;
     const float stream = sqrtf(stages * stages + read * read);
-    float join = 0.008f * s.rows;
-    if (s.split > 1) join += 0.3f + 0.010f * s.rows * (s.split - 1) / s.split;
-    const float ahead = prefetch_pays(s, num_sms) ? 0.8f : 0.0f;
-    return 3.3f + (s.group == 2 ? 0.6f : 0.0f) + stream + waves * join + 3.0f * (waves - 1.0f) - ahead;
+    float join = 0.017f * s.rows;
+    if (s.split > 1) join += 0.14f + 0.063f * s.split + 0.0116f * s.rows * (s.split - 1) / s.split;
+    return 2.1f + (s.group == 2 ? 0.17f : 0.0f) + stream + waves * join + 2.0f * (waves - 1.0f) - (s.prefetch ? fminf(0.5f, 0.1f * read) : 0.0f);
 }
 
 SplitShape best_split(const LinearParams &p, int num_sms) {
@@ -578,10 +584,10 @@ SplitShape best_split(const LinearParams &p, int num_sms) {
         s.m_tiles = (p.m + f.most - 1) / f.most;
         s.rows = ((p.m + s.m_tiles - 1) / s.m_tiles + unit - 1) / unit * unit;
         s.tiles = static_cast<int64_t>(s.m_tiles) * ((p.n + cols - 1) / cols);
-        // two CTAs an SM where their stages are short: 32 tokens, 4096 x 4096, 9.2 us against 9.3;
-        // 64 tokens: 11.3 against 9.9
-        s.per_sm = f.group == 1 && s.rows <= 32 ? 2 : 1;
         for (s.split = 1; s.split <= kMaxCluster / f.group && s.split <= steps; ++s.split) {
+            // two CTAs an SM where there are more than SMs and their stages are short: one token, 4096 x 4096, 7.7 us
+            // against 7.9; but 32 tokens, 1024 x 8192, 64 CTAs, 8.6 against 6.9
+            s.per_sm = f.group == 1 && s.rows <= 32 && s.tiles > clusters_at_once(s.split, num_sms) ? 2 : 1;
             fit_split(s, steps, num_sms);
             s.us = split_us(s, p, steps, num_sms);
             if (best.group == 0 || s.us < best.us) best = s;
@@ -639,7 +645,7 @@ bool linear_prefers_split(const LinearParams &p, int num_sms) {
     if (p.m <= 64) return true;
     // the 256 x 256 tiles: 5.7 us and 0.28 a 64-deep stage for each wave of them (4096 deep, 1,
     // 3 and 4 waves: 23.2, 60.9 and 79.0 us; 100 deep: 6.3).  Where the two cross, at (m, 4096) with k = 4096:
-    // 384 tokens 15.6 us split against 24.4, 512 tokens 18.2 against 24.5, 777 24.8 against 24.5.
+    // 512 tokens 15.5 us split against 24.4, 777 22.1 against 25.1, 1024 24.7 against 25.6, 1536 43.8 against 42.7.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256), pairs = num_sms / 2;
     const float us = 5.7f + 0.28f * static_cast<float>((tiles + pairs - 1) / pairs) * ((p.k + kDepth - 1) / kDepth);
     return best_split(p, num_sms).us < us;
