@@ -12,12 +12,12 @@
 //           columns of the weight and half the tokens, which halves what the
 //           tokens cost in L2 reads
 //   warp 1      TMEM allocation, MMA issue (the pair's first CTA)
-//   warps 0, 2, 3, 4   TMA producers: each takes every fourth stage
+//   warps 0, 2  TMA producers, every other stage each
 //   the others  bring what the epilogue will read into L1
 //   all warps   then: partial sums from TMEM to shared memory, the sum over the
 //               cluster, and the epilogue, four columns a thread
 // Next to that, a stage's time was its issue: one lane took 460 clocks for a stage's two copies
-// (a wait, the count of bytes, 170 clocks a copy), four warps hide it; five elections and 64-bit
+// (a wait, the count of bytes, 170 clocks a copy), two warps hide it; five elections and 64-bit
 // offsets took 360 clocks for its MMAs, which take 128 to 512 (now 220 to 255 where the MMAs are shorter).
 // 512 tokens, 4096 x 4096: 18.2 -> 15.5 us, 128 tokens 11.8 -> 10.4, 512 x 1024 x 8192 17.1 -> 12.5.
 // (Reading the other CTAs' sums with loads ran at 9 bytes a clock: 7.3 us for a pair's
@@ -42,7 +42,7 @@ constexpr int kTileN = 128;      // weight columns a tile (MMA M)
 constexpr int kDepth = 64;       // contraction a stage
 constexpr int kMaxStages = 16;
 constexpr int kMaxCluster = 8;
-constexpr int kProducers = 4;
+constexpr int kProducers = 2;
 // Threads a CTA: the pairs' tiles have more to bring out of TMEM and one CTA an SM.
 __host__ __device__ constexpr int split_threads(int group) { return group == 1 ? 256 : 512; }
 constexpr int kBlockSteps = 1024 / kDepth;   // stages of one accumulator
@@ -56,7 +56,10 @@ struct SplitParams {
     const void *bias, *aux;
     void *out, *preact;
     int64_t ldaux, ldo, ldp;
-    int m, n, steps;          // steps: 64-deep stages of the whole contraction
+    int m, n;
+    int steps, more;          // 64-deep stages of a rank; the first `more` ranks have one more
+    int share;                // tokens of a tile that a rank finishes (the last ones' may be fewer, or none)
+    uint64_t m_tiles_inv;     // 2^64 / m_tiles, rounded up
     int w_kn;                 // the weight is (k, n): read M-major
     int rows;                 // tokens a tile (MMA N), a multiple of 16
     int m_tiles, split;       // token tiles; CTAs (or pairs) that share a tile's contraction
@@ -209,7 +212,29 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     // and copy instructions take their operands)
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int S = p.stages;
-    // (first what takes longest)
+    const int ctas = p.split * kG;                       // of the cluster
+    const int crank = ctas > 1 ? __shfl_sync(0xffffffffu, static_cast<int>(ptx::cluster_ctarank()), 0) : 0;
+    const int half = kG == 2 ? crank & 1 : 0;            // of the pair
+    const int rank = crank / kG;                         // share of the contraction
+    const int x_rows = p.rows / kG;                      // tokens this CTA loads
+    const uint32_t stage_bytes = kWBytes + static_cast<uint32_t>(x_rows) * kDepth * 2;
+    // (no divisions: seven of them, one after another, took 0.5 us of each call.  A quotient of 32-bit numbers is the
+    // high word of the product with the reciprocal rounded up to 64 bits: its error, below 2^-64 x tile, does not
+    // reach the next integer.)
+    const uint32_t tile = ctas > 1 ? ptx::cluster_id() : blockIdx.x;
+    const uint32_t n_tile = p.m_tiles == 1 ? tile : static_cast<uint32_t>(__umul64hi(tile, p.m_tiles_inv));
+    // clusters next to one another share the weight's tile
+    const int n0 = static_cast<int>(n_tile * kG + half) * kTileN;
+    const int m0 = static_cast<int>(tile - n_tile * p.m_tiles) * p.rows;
+    const int step0 = p.steps * rank + min(rank, p.more);
+    const int count = p.steps + (rank < p.more ? 1 : 0);
+
+    // the tile's tokens, and this CTA's share of them to finish
+    const int live = min(p.rows, p.m - m0);
+    const auto share_from = [&](int r) { return min(live, r * p.share); };
+    const int t0 = share_from(rank), t1 = share_from(rank + 1);
+    const uint32_t recv_bytes = static_cast<uint32_t>((p.split - 1) * (t1 - t0)) * (kTileN * 4);
+
     if (warp == 1) {
         ptx::tmem_alloc<kG>(ptx::smem_u32(&tmem_slot), static_cast<uint32_t>(p.tmem_cols));
         ptx::tmem_relinquish<kG>();
@@ -226,25 +251,6 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
         ptx::fence_mbar_init();
         __syncwarp();
     }
-    const int ctas = p.split * kG;                       // of the cluster
-    const int crank = ctas > 1 ? __shfl_sync(0xffffffffu, static_cast<int>(ptx::cluster_ctarank()), 0) : 0;
-    const int half = kG == 2 ? crank & 1 : 0;            // of the pair
-    const int rank = crank / kG;                         // share of the contraction
-    const int x_rows = p.rows / kG;                      // tokens this CTA loads
-    const uint32_t stage_bytes = kWBytes + static_cast<uint32_t>(x_rows) * kDepth * 2;
-    const int tile = blockIdx.x / ctas;
-    // clusters next to one another share the weight's tile
-    const int n0 = (tile / p.m_tiles * kG + half) * kTileN;
-    const int m0 = tile % p.m_tiles * p.rows;
-    // (at most 2^25 steps and 8 ranks)
-    const int step0 = p.steps * rank / p.split;
-    const int count = p.steps * (rank + 1) / p.split - step0;
-
-    // the tile's tokens, and this CTA's share of them to finish
-    const int live = min(p.rows, p.m - m0);
-    const int t0 = live * rank / p.split, t1 = live * (rank + 1) / p.split;
-    const uint32_t recv_bytes = static_cast<uint32_t>((p.split - 1) * (t1 - t0)) * (kTileN * 4);
-
     if (threadIdx.x == 0 && recv_bytes) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&recv_bar), recv_bytes);
     ptx::tc_fence_before();
     __syncthreads();
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
             ptx::fence_proxy_async_smem();
             __syncthreads();
             if (threadIdx.x < p.split && static_cast<int>(threadIdx.x) != rank) {
-                const int r = threadIdx.x, first = live * r / p.split, n = live * (r + 1) / p.split - first;
+                const int r = threadIdx.x, first = share_from(r), n = share_from(r + 1) - first;
                 const uint32_t bytes = static_cast<uint32_t>(n) * (kTileN * 4);
                 if (bytes)
                     ptx::bulk_copy_to_cta(
@@ -663,7 +669,10 @@ cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, 
     p.bias = lp.bias, p.aux = lp.aux_mode == AUX_NONE ? nullptr : lp.aux, p.out = lp.out, p.preact = lp.preact;
     p.ldaux = lp.ldaux, p.ldo = lp.ldo, p.ldp = lp.ldp;
     p.m = lp.m, p.n = lp.n;
-    p.steps = (lp.k + kDepth - 1) / kDepth;
+    const int steps = (lp.k + kDepth - 1) / kDepth;
+    p.steps = steps / s.split, p.more = steps % s.split;
+    p.share = ((lp.m < s.rows ? lp.m : s.rows) + s.split - 1) / s.split;
+    p.m_tiles_inv = UINT64_MAX / static_cast<uint64_t>(s.m_tiles) + 1;   // (0 for one tile: not used)
     p.w_kn = !lp.w_nk;
     p.rows = s.rows, p.m_tiles = s.m_tiles, p.split = s.split;
     p.stages = s.stages, p.accs = s.accs, p.tmem_cols = s.tmem_cols;

@@ -106,6 +106,13 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
+// Index of this cluster in a grid whose clusters lie along x.
+__device__ __forceinline__ uint32_t cluster_id() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+
 // Shared::cluster address of the variable at local shared address `a` in CTA `rank`.
 __device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank) {
     uint32_t r;
