@@ -19,7 +19,7 @@
 // Next to that, a stage's time was its issue: one lane took 460 clocks for a stage's two copies
 // (a wait, the count of bytes, 170 clocks a copy), two warps hide it; five elections and 64-bit
 // offsets took 360 clocks for its MMAs, which take 128 to 512 (now 220 to 255 where the MMAs are shorter).
-// 512 tokens, 4096 x 4096: 18.2 -> 15.5 us, 128 tokens 11.8 -> 10.4, 512 x 1024 x 8192 17.1 -> 12.5.
+// With set-up free of divisions 512 tokens, 4096 x 4096: 18.2 -> 15.2 us, 128 tokens 11.8 -> 10.0, 512 x 1024 x 8192 17.1 -> 12.2.
 // (Reading the other CTAs' sums with loads ran at 9 bytes a clock: 7.3 us for a pair's
 // 256 x 256 sums, the longest part of the call.)
 // The tensor core adds at the size of its running sum, so each 1024-deep part of
@@ -649,11 +649,12 @@ bool linear_prefers_split(const LinearParams &p, int num_sms) {
     // that ends inside one would have up to 7 elements past its end overwritten
     if (p.n % 8 != 0) return true;
     if (p.m <= 64) return true;
-    // the 256 x 256 tiles: 5.7 us and 0.28 a 64-deep stage for each wave of them (4096 deep, 1,
-    // 3 and 4 waves: 23.2, 60.9 and 79.0 us; 100 deep: 6.3).  Where the two cross, at (m, 4096) with k = 4096:
-    // 512 tokens 15.5 us split against 24.4, 777 22.1 against 25.1, 1024 24.7 against 25.6, 1536 43.8 against 42.7.
+    // the 256 x 256 tiles: 6.3 us and 0.29 a 64-deep stage for each wave of them (1024 deep 10.6 to
+    // 12.5 us, 4096 deep 24.0 to 25.6, 8192 deep 40.5 to 43.5, two waves 42.7 to 45).  Where the two cross, at
+    // (m, 4096) with k = 4096: 512 tokens 15.1 us split against 24.4, 777 21.6 against 25.0, 1024 24.0 against
+    // 25.5, 1536 43.8 against 42.7.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256), pairs = num_sms / 2;
-    const float us = 5.7f + 0.28f * static_cast<float>((tiles + pairs - 1) / pairs) * ((p.k + kDepth - 1) / kDepth);
+    const float us = 6.3f + 0.29f * static_cast<float>((tiles + pairs - 1) / pairs) * ((p.k + kDepth - 1) / kDepth);
     return best_split(p, num_sms).us < us;
 }
 
