@@ -550,11 +550,11 @@ int clusters_at_once(int ctas, int num_sms) {
 }
 
 // What a shape takes, in us, fitted to 1440 measurements on GB300: launch and set-up; the stages,
-// each bound by its MMAs or by the 175 bytes a ns that an SM receives, and the rate of device memory,
+// each bound by its MMAs or by its bytes at 175 a ns (fitted), and the rate of device memory,
 // which reads the weight once (the root of the squares' sum, since the two do not overlap
 // wholly); another set-up for each further wave; per token of the tile the way from
 // TMEM to the output, and to the other CTAs; less what an early prefetch saves.  Rows that are not a multiple of 128 bytes
-// apart take more of the SM's port: a stage's 128 bytes of each lie in two lines (judged by the
+// apart take longer to receive: a stage's 128 bytes of each lie in two lines (judged by the
 // sizes: a result does not depend on the strides).
 // Over 117 products (1 to 1536 tokens, 256 to 14336 columns, 1024 to 8192 deep) the
 // shape it chose took 1% more than the best one on average, and at most 13%.
@@ -567,8 +567,8 @@ float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sm
     const float waves = static_cast<float>((units + slots - 1) / slots);
     const float share = (units < clusters ? units : clusters) * s.group * s.split > num_sms ? 2.0f : 1.0f;
     const float bytes = static_cast<float>(kWBytes) + static_cast<float>(s.rows / s.group) * kDepth * 2;
-    const float port = (p.k % 64 != 0 || (!p.w_nk && p.n % 64 != 0) ? 1.87f : 1.0f) * share * bytes / 175e3f;
-    const float stages = waves * ((steps + s.split - 1) / s.split) * fmaxf(0.00102f * s.rows, port);
+    const float receive = (p.k % 64 != 0 || (!p.w_nk && p.n % 64 != 0) ? 1.87f : 1.0f) * share * bytes / 175e3f;
+    const float stages = waves * ((steps + s.split - 1) / s.split) * fmaxf(0.00102f * s.rows, receive);
     const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 2.0f / 7.0e6f;
     const float stream = sqrtf(stages * stages + read * read);
     float join = 0.017f * s.rows;
