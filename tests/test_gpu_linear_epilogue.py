@@ -245,6 +245,25 @@ def test_same_bits_every_time():
         assert torch.equal(a, b)
 
 
+def test_launches_beside_one_another():
+    """Shapes with one and two CTAs an SM, pairs and clusters, on streams of their own: the bits of a call by itself."""
+    cases = []
+    for i, (m, n, k) in enumerate(((1, 4096, 4096), (16, 1000, 2056), (32, 1024, 8192), (64, 4096, 512), (128, 1024, 4096),
+                                   (300, 4096, 1024), (512, 1000, 2056), (777, 2048, 512))):
+        x, w, bias, res = make(m, n, k, BF16 if i % 2 else F16, seed=i)
+        cases.append((x, w, bias, res, mc2.mc2_matmul_bias_act(x, w, bias=bias, activation="silu", residual=res)[0]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for i in range(240):
+        x, w, bias, res, want = cases[(5 * i + i // 8) % 8]
+        with torch.cuda.stream(streams[i % 4]):
+            got.append((mc2.mc2_matmul_bias_act(x, w, bias=bias, activation="silu", residual=res)[0], want))
+    torch.cuda.synchronize()
+    assert mc2.mc2_device_status() == mc2.MC2_OK
+    assert all(torch.equal(o, want) for o, want in got)
+
+
 # ------------------------------------------------------------------ gradients
 
 def check_act_grad(m, n, k, dtype, act, w_is_nk, wide=0, seed=0, in_place=False):
