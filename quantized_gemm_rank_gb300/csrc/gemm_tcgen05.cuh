@@ -868,11 +868,10 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
             const int colh = nb * kBN + half * 128;
             bool ok = true;
             if constexpr (kEpi != EPI_PLAIN) {
-                // The tile is one K block: its sums are read from TMEM where they are used, in
-                // a short loop (kept in registers, 128 of them could only be indexed by
-                // unrolled code past the instruction cache's size: an (8192, 8192) output with
-                // k = 1024 and gelu took 159 us that way and takes 107 this way, with k = 7168, a
-                // bias and the pre-activation 816 and 573).
+                // The tile's sums are read from TMEM where they are used, in a short loop (kept
+                // in registers, 128 of them could only be indexed by unrolled code past the
+                // instruction cache's size: an (8192, 8192) output with k = 1024 and gelu took 159 us
+                // that way and 107 this way).
                 // The warp's 128 columns go in four pieces of 32, through two buffers of 32
                 // rows x 64 bytes (64-byte swizzle: chunk j of row r at chunk j ^ (r / 2 % 4)), so
                 // that a piece's store is read while the next piece is worked on.
@@ -893,15 +892,69 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     ptx::bulk_wait_group_read<0>();
                     for (int c = 0; c < early; ++c) load_aux(c);
                 }
-                const uint32_t b = acc_iter & 1u;
-                const bool got = wait_or_abort<kPair>(ptx::smem_u32(&tfull_bar[b]), (acc_iter >> 1) & 1u, p, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
+                auto release = [&](uint32_t buf) {   // of this warp's part of an accumulator that it has read
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kPair)
+                            ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&tempty_bar[buf]), 0));
+                        else
+                            ptx::mbar_arrive(ptx::smem_u32(&tempty_bar[buf]));
+                    }
+                };
+                auto arrived = [&]() {   // the next accumulator, in all lanes
+                    const bool got = wait_or_abort<kPair>(ptx::smem_u32(&tfull_bar[acc_iter & 1u]), (acc_iter >> 1) & 1u, p, abort_flag);
+                    return __all_sync(0xffffffffu, got) != 0;
+                };
+                if (w.kb1 - w.kb0 > 1) {
+                    // a deep contraction: the K blocks' sums are added in registers, and the total
+                    // goes back to the last block's accumulator, from where the loop below takes it
+                    float sum[128];
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+                    for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                        if (!arrived()) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        if (pieces > 0) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t r[16];
+                                ptx::tmem_ld_32x32b_x16(tmem_base + lane_addr + (acc_iter & 1u) * kBN + half * 128 + c * 16, r);
+                                ptx::tmem_ld_wait16(r);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) sum[c * 16 + i] = __fadd_rn(sum[c * 16 + i], __uint_as_float(r[i]));
+                            }
+                        }
+                        if (kb + 1 < w.kb1) {
+                            release(acc_iter & 1u);
+                            ++acc_iter;
+                        }
+                    }
+                    if (ok && pieces > 0) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t r[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(sum[c * 16 + i]);
+                            ptx::tmem_st_32x32b_x16(tmem_base + lane_addr + (acc_iter & 1u) * kBN + half * 128 + c * 16, r);
+                        }
+                        ptx::tmem_st_wait();
+                    }
+                } else {
+                    ok = arrived();
+                    ptx::tc_fence_after();
+                }
+                if (!ok) {
                     // copies asked for above land before the CTA can exit
                     for (int c = 0; c < early; ++c)
                         (void)ptx::mbar_wait(ptx::smem_u32(&aux_bar[2 * (warp - 4) + c]), (aux_phase >> c) & 1u, p.wait_limit_ns);
                     break;
                 }
-                ptx::tc_fence_after();
+                const uint32_t b = acc_iter & 1u;
                 const uint32_t acc = tmem_base + lane_addr + b * kBN + half * 128;
                 const bool bias_whole = p.bias16 != nullptr && colh + 128 <= p.n && (reinterpret_cast<uintptr_t>(p.bias16) & 15u) == 0;
                 // 32 outputs of this lane's row, rounded, to buffer i
@@ -936,17 +989,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
                     }
-                    if (c == pieces - 1) {
-                        // every sum has been read: the accumulator is free
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (kPair)
-                                ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&tempty_bar[b]), 0));
-                            else
-                                ptx::mbar_arrive(ptx::smem_u32(&tempty_bar[b]));
-                        }
-                    }
+                    if (c == pieces - 1) release(b);   // every sum has been read: the accumulator is free
                     if (bias_whole) {
                         const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias16) + colh + 32 * c);
 #pragma unroll
@@ -1013,12 +1056,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     put(i, v);
                     send(&p.out_map, i, c);
                 }
-                if (pieces <= 0 && lane == 0) {
-                    if constexpr (kPair)
-                        ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&tempty_bar[b]), 0));
-                    else
-                        ptx::mbar_arrive(ptx::smem_u32(&tempty_bar[b]));
-                }
+                if (pieces <= 0) release(b);
                 ++acc_iter;
                 if (!ok) break;
                 continue;

@@ -654,8 +654,12 @@ bool linear_prefers_split(const LinearParams &p, int num_sms) {
     // (m, 4096) with k = 4096: 512 tokens 15.1 us split against 24.4, 777 21.6 against 25.0, 1024 24.0 against
     // 25.5, 1536 43.8 against 42.7.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256), pairs = num_sms / 2;
-    const float us = 6.3f + 0.29f * static_cast<float>((tiles + pairs - 1) / pairs) * ((p.k + kDepth - 1) / kDepth);
-    return best_split(p, num_sms).us < us;
+    const SplitShape s = best_split(p, num_sms);
+    const int steps = (p.k + kDepth - 1) / kDepth, blocks = ((steps + s.split - 1) / s.split + kBlockSteps - 1) / kBlockSteps;
+    // where the tiles fill the device, no sum is left deeper in one accumulator than it would be in theirs
+    if (tiles >= pairs && (blocks + s.accs - 1) / s.accs * kBlockSteps > linear_tiles_block(p.k)) return false;
+    const float us = 6.3f + 0.29f * static_cast<float>((tiles + pairs - 1) / pairs) * steps;
+    return s.us < us;
 }
 
 cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, cudaStream_t stream) {
