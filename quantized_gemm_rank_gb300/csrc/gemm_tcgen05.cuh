@@ -974,9 +974,15 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                         ptx::bulk_commit_group();
                     }
                 };
-                // the buffer written next is free: all stores but the latest have been read
-                auto reuse = [&]() {
-                    if (lane == 0) ptx::bulk_wait_group_read<1>();
+                // the buffer written next is free: all stores but the latest have been read (at a tile's first
+                // piece all of them: a last tile of one or three pieces ended with that buffer)
+                auto reuse = [&](int c) {
+                    if (lane == 0) {
+                        if (c == 0)
+                            ptx::bulk_wait_group_read<0>();
+                        else
+                            ptx::bulk_wait_group_read<1>();
+                    }
                     __syncwarp();
                 };
 #pragma unroll 1
@@ -1011,7 +1017,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     // with a pre-activation output: that through buffer 0, the output through buffer 1
                     const int i = p.has_pre ? 1 : c & 1;
                     if (p.has_pre) {
-                        reuse();
+                        reuse(c);
                         put(0, v);
                         send(&p.pre_map, 0, c);
                     }
@@ -1044,7 +1050,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     }
                     epilogue<kBF16, kEpi>(v, a, p.act, p.has_aux != 0);
                     if (!p.has_aux) {
-                        reuse();
+                        reuse(p.has_pre ? 1 : c);
                     } else if (!p.has_pre && c >= 1 && c + 1 < pieces) {
                         // the other buffer's store has been read by now: the piece after this one comes in there
                         if (lane == 0) {
