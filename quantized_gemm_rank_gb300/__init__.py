@@ -237,6 +237,39 @@ def _stream(stream, cur: int) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _on_stream(f, args: dict):
+    """A call with ``stream=``: f under that stream, whose pool its workspace and new outputs come from.
+
+    (Memory of the current stream's pool could still be in use there, and a
+    workspace would go back to it, for the next tensor made, while the launched kernels
+    use it.)  The new outputs may be used on the caller's stream, once that waits for the
+    given one, and freed like any tensor of its own: their memory is kept until it is done with them.
+    (This takes some 20 us of host time; a call within ``torch.cuda.stream(stream)`` takes none of it.)
+    """
+    stream = args.pop("stream")
+    cur = _current_device()
+    if cur < 0:
+        return f(**args)   # (refuses, in its own words)
+    if stream.device_index != cur:
+        raise ValueError(f"stream must belong to the current device (cuda:{cur})")
+    if _raw_current_stream is not None and stream.cuda_stream == _raw_current_stream(cur):
+        return f(**args)
+    home = torch.cuda.current_stream()
+    torch.cuda.set_stream(stream)   # (the context manager takes 5 us of host time more)
+    try:
+        r = f(**args)
+    finally:
+        torch.cuda.set_stream(home)
+    given = set()
+    for v in args.values():
+        given.update(map(id, v) if isinstance(v, (list, tuple)) else (id(v),))
+    made = r.values() if isinstance(r, dict) else r if isinstance(r, (list, tuple)) else (r,)
+    for t in made:
+        if t is not None and id(t) not in given:
+            t.record_stream(home)
+    return r
+
+
 def mc2_all_gather_mm(x_chunks: Sequence[torch.Tensor], x2: torch.Tensor, *, x2_is_nk: bool = False,
                       bias: Optional[torch.Tensor] = None, gather_output: bool = True,
                       out: Optional[torch.Tensor] = None, gathered: Optional[torch.Tensor] = None,
@@ -246,6 +279,8 @@ def mc2_all_gather_mm(x_chunks: Sequence[torch.Tensor], x2: torch.Tensor, *, x2_
     x_chunks: world_size tensors (m_local, k); x2 (k, n), or w (n, k) with
     ``x2_is_nk``.  Returns (out (m, n), gathered (m, k) or None).
     """
+    if stream is not None:
+        return _on_stream(mc2_all_gather_mm, locals())
     cur = _current_device()
     R = len(x_chunks)
     m_local, k = x_chunks[0].shape
@@ -278,6 +313,8 @@ def mc2_matmul_reduce_scatter(x_chunks: Sequence[torch.Tensor], w_chunks: Sequen
     (n, k_local) (or (k_local, n) with ``w_is_nk=False``).  Returns the list of
     the ranks' outputs, each (m / world_size, n).
     """
+    if stream is not None:
+        return _on_stream(mc2_matmul_reduce_scatter, locals())
     cur = _current_device()
     R = len(x_chunks)
     m, k_local = x_chunks[0].shape
@@ -307,6 +344,8 @@ def mc2_matmul_weight_grad(dy: torch.Tensor, x: torch.Tensor, *, with_bias: bool
     dy (m, n) and x (m, k) of one 16-bit type on this GPU (for the all-gather
     layer, x is the ``gathered`` output of its forward call).  Returns (dw, db).
     """
+    if stream is not None:
+        return _on_stream(mc2_matmul_weight_grad, locals())
     cur = _current_device()
     m, n = dy.shape
     k = x.shape[1]
@@ -342,6 +381,8 @@ def mc2_quant_all_reduce(x_chunks: Sequence[torch.Tensor], scale_chunks: Sequenc
     codes (bs, h/64, 2) as uint8 (mx).  Returns out of the same leading shape
     as x in ``out_dtype`` (fp32, fp16 or bf16).
     """
+    if stream is not None:
+        return _on_stream(mc2_quant_all_reduce, locals())
     cur = _current_device()
     x0 = x_chunks[0]
     if x_kind is None:
@@ -425,6 +466,8 @@ def mc2_alltoall_quant_mm(chunks: Sequence[torch.Tensor], x2: torch.Tensor, x2_s
     Returns dict(out, q, x1_scale, acc, alltoall_out) with the optional outputs
     that were given.
     """
+    if stream is not None:
+        return _on_stream(mc2_alltoall_quant_mm, locals())
     cur = _current_device()
     R = len(chunks)
     bs_local, h = chunks[0].shape
@@ -556,6 +599,8 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optiona
     Returns dict(out, residual, rstd, q, scale): the sum that was normalised is
     ``residual`` (None without a residual); outputs not asked for are None.
     """
+    if stream is not None:
+        return _on_stream(mc2_add_rms_norm, locals())
     cur = _current_device()
     if cur >= 0:
         r = (_native_module or _native()).add_rms_norm(x, weight, residual, eps, quant_mode, q_dtype, with_out, with_rstd,
@@ -633,6 +678,8 @@ def mc2_rms_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, r
     ``residual`` output.  Returns (dx, dw): dx is the gradient of both x and the
     residual, dw of the weight (None without ``with_weight``).
     """
+    if stream is not None:
+        return _on_stream(mc2_rms_norm_grad, locals())
     cur = _current_device()
     if cur >= 0:
         r = (_native_module or _native()).rms_norm_grad(dy, x, weight, rstd, dres, with_weight, dx, dw, workspace, cur,
@@ -695,6 +742,8 @@ def mc2_matmul_bias_act(x: torch.Tensor, w: torch.Tensor, *, w_is_nk: bool = Tru
     "gelu_tanh" or "silu".  Returns (out, preact): preact = x @ w^T + bias, with
     ``with_preact`` or when given, is what the gradients take.
     """
+    if stream is not None:
+        return _on_stream(mc2_matmul_bias_act, locals())
     cur = _current_device()
     act = _activation(activation)
     if cur >= 0:
@@ -738,6 +787,8 @@ def mc2_matmul_act_grad(dy: torch.Tensor, w: torch.Tensor, z: torch.Tensor, *, a
     dy (..., n); w (n, k), or (k, n) with ``w_is_nk=False``; z (..., k), the forward
     call's ``preact``.  The layer's dW and dB are mc2_matmul_weight_grad(dy, act(z)).
     """
+    if stream is not None:
+        return _on_stream(mc2_matmul_act_grad, locals())
     cur = _current_device()
     act = _activation(activation)
     if cur >= 0:
@@ -770,6 +821,8 @@ def mc2_act_grad(dy: torch.Tensor, z: torch.Tensor, *, activation: str, dz: Opti
                  stream=None) -> torch.Tensor:
     """dz = dy * act'(z), elementwise: the gradient of mc2_matmul_bias_act's
     ``preact`` for a gradient ``dy`` of its ``out``."""
+    if stream is not None:
+        return _on_stream(mc2_act_grad, locals())
     cur = _current_device()
     act = _activation(activation)
     if cur >= 0:
