@@ -3,7 +3,7 @@
 
 Argument marshalling only: every step of the operations runs in the CUDA
 library ``libmc2_gb300.so`` (built in-tree by :mod:`.build`).  The calls around
-the linears marshal their regular case in an extension module, ``_native.so``.  PyTorch
+the linears marshal their regular case in an extension module (``binding/native.cpp``).  PyTorch
 provides device memory and streams.  There is no CPU fallback: if the library
 cannot be built or loaded, importing the functions raises.
 

@@ -3,7 +3,7 @@
 Compiles ``csrc/*.cu`` in parallel into ``_build/`` and links
 ``libmc2_gb300.so`` (the operations) next to this file, ``calib/*.cu``
 into ``libmc2_calib.so`` (a measurement probe that only the benchmark loads),
-and ``binding/native.cpp`` into ``_native.so`` (the Python binding's fast calls).
+and ``binding/native.cpp`` into ``_native.<python>-torch<version>.so`` (the Python binding's fast calls).
 Rebuilds a library only when one of its sources or the public header is newer
 than it.
 """
@@ -23,7 +23,6 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmc2_gb300.so")
 CALIB_LIB = os.path.join(HERE, "libmc2_calib.so")
 NATIVE_SRC = os.path.join(HERE, "binding", "native.cpp")
-NATIVE_LIB = os.path.join(HERE, "_native.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -83,18 +82,26 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     return _build_one(LIB, CSRC, force, verbose, extra_flags)
 
 
+def native_lib() -> str:
+    """Where the binding's extension module is.  It is bound to one Python and one torch, so its name says
+    which: after an upgrade of either the old one is not loaded."""
+    import torch
+    return os.path.join(HERE, f"_native.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}.so")
+
+
 def build_native(force: bool = False, verbose: bool = False) -> str:
     """Build the binding's extension module (and return its path)."""
+    module = native_lib()
     deps = [NATIVE_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(ROOT, "include", "*.h"))
-    if not force and os.path.exists(NATIVE_LIB) and all(os.path.getmtime(d) <= os.path.getmtime(NATIVE_LIB) for d in deps):
-        return NATIVE_LIB
+    if not force and os.path.exists(module) and all(os.path.getmtime(d) <= os.path.getmtime(module) for d in deps):
+        return module
     import torch
     t = os.path.dirname(os.path.abspath(torch.__file__))
     inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
            os.path.join(ROOT, "include")]
     lib = os.path.join(t, "lib")
-    tmp = NATIVE_LIB + f".tmp{os.getpid()}"
+    tmp = module + f".tmp{os.getpid()}"
     # the library of the operations by its name, found beside the module; torch's by theirs
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-I{i}" for i in inc], NATIVE_SRC, "-o", tmp, f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
@@ -104,8 +111,8 @@ def build_native(force: bool = False, verbose: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {os.path.basename(NATIVE_SRC)}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, NATIVE_LIB)
-    return NATIVE_LIB
+    os.replace(tmp, module)
+    return module
 
 
 def build_calib(force: bool = False, verbose: bool = False) -> str:
