@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(1024) norm_grad_row_kernel(const __grid_consta
             for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
         } else {
             any = __any_sync(0xFFFFFFFFu, failed);
+            __syncwarp();   // (a vote orders no memory: the lanes' reads of the row before, ahead of the copy that replaces it)
         }
         if (any) {
             // a copy did not arrive in time: the launch is given up, once those in flight have had time to land
