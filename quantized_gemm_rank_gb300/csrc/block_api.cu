@@ -78,7 +78,7 @@ int product(const char *what, bool bf16, mc2::LinearParams &p, void *stream) {
     cudaError_t e = !mc2::linear_layout_fits(p) ? mc2::launch_linear_any(bf16, p, s)
                     : mc2::linear_prefers_split(p, dev.num_sms)
                         ? mc2::launch_linear_split(bf16, p, dev.num_sms, s)
-                        : mc2::launch_linear_tiles(bf16, p, dev.num_sms, s);
+                        : mc2::launch_linear_tiles(bf16, p, s);
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
     marks.launched();
     return MC2_OK;

@@ -45,25 +45,6 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     }
 }
 
-// The biases of columns col .. col + 7, zero from column n on.
-template <bool kBF16>
-__device__ __forceinline__ void load_bias8(const void *bias, int col, int n, float (&b)[8]) {
-    const uint16_t *p = static_cast<const uint16_t *>(bias) + col;
-    if (col + 8 <= n && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2<kBF16>(w[i]);
-            b[2 * i] = f.x;
-            b[2 * i + 1] = f.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = col + i < n ? load16<kBF16>(bias, col + i) : 0.0f;
-    }
-}
-
 // v: z of kN columns (EPI_FORWARD), or the product (EPI_BACKWARD); a: their aux, two
 // columns a word.
 template <bool kBF16, int kEpi, int kN>

@@ -44,7 +44,7 @@ inline int linear_tiles_block(int k) {
     return even > 32 || blocks <= 1 ? even : 32;
 }
 // A CTA pair per 256 x 256 tile: products of many rows.
-cudaError_t launch_linear_tiles(bool bf16, const LinearParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_linear_tiles(bool bf16, const LinearParams &p, cudaStream_t stream);
 // The weight's columns as the tile's rows, the contraction split over a cluster:
 // products whose tiles would not fill the device.
 cudaError_t launch_linear_split(bool bf16, const LinearParams &p, int num_sms, cudaStream_t stream);

@@ -47,8 +47,7 @@ cudaError_t launch_tiles(GemmParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_linear_tiles(bool bf16, const LinearParams &lp, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
+cudaError_t launch_linear_tiles(bool bf16, const LinearParams &lp, cudaStream_t stream) {
     GemmParams p = {};
     const uint64_t m = lp.m, n = lp.n, k = lp.k;
     bool ok = host::make_map16(&p.a_maps[0], lp.x, k, m, kBK, kBM, lp.ldx);

@@ -832,7 +832,8 @@ cudaError_t norm(const NormParams &p, int num_sms, cudaStream_t stream) {
         else if (nv <= 2048 && p.qmode == QM_NONE)
             v = 2;
         if (v == 1) return norm_rows<kT, 1>(p, t1, stream);
-        if (v == 2) return norm_rows<kT, 2>(p, row_threads(nv, 2), stream);
+        if (v == 2)   // (without codes)
+            return launch(norm_row_kernel<kT, 2, QM_NONE>, static_cast<unsigned>(p.m), row_threads(nv, 2), 0, stream, p);
         return norm_rows<kT, 4>(p, row_threads(nv, 4), stream);
     }
     const unsigned grid = static_cast<unsigned>(p.m);
@@ -893,6 +894,7 @@ cudaError_t launch_add_rms_norm(int kind, const NormParams &p, int num_sms, cuda
     }
 }
 
+// (GB300's 152 SMs written out: the workspace's size is asked without a device.)
 int norm_grad_parts(int64_t m, int64_t h, int elem_size) {
     const int64_t most = 152ll * norm_grad_blocks_per_sm(h, elem_size);
     return static_cast<int>(m < most ? m : most);

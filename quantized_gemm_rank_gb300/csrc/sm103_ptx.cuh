@@ -196,11 +196,6 @@ __device__ __forceinline__ bool bar_red_and(uint32_t id, uint32_t count, bool pr
     return r != 0;
 }
 
-// Named barrier `id` over `count` threads (a multiple of 32).
-__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
 __device__ __forceinline__ void nanosleep(uint32_t ns) { asm volatile("nanosleep.u32 %0;" ::"r"(ns)); }
 
 // Fetch the line holding `p` into L1 (no register result).
