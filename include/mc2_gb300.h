@@ -330,7 +330,7 @@ int mc2_alltoall_quant_mm_no_alloc(const void *const *chunks, int rank_size, int
  *   not above zero or not finite (a zero row, a scale that underflows, a NaN) the
  *   codes are 0; a row or group that holds a NaN has a NaN scale.
  *
- *   All arithmetic is fp32 (the mean of squares must be within its range).
+ *   All arithmetic is fp32 (a row's sum of squares must be within its range).
  *
  *   x             (m, h) of dtype, rows ldx apart
  *   residual      NULL or (m, h), rows ldr apart
@@ -362,8 +362,8 @@ int mc2_add_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t l
  *   x is the tensor that was normalised: residual_out of the forward call (x
  *   itself without a residual).  dx is the gradient of both the forward call's
  *   x and its residual; dres is the gradient that arrives at residual_out.
- *   Sums are fp32, in an order that only m and h set; dx and dw are
- *   rounded once, dw to weight_dtype.
+ *   Sums are fp32; dx and dw are rounded once, dw to weight_dtype.  Calls of the same
+ *   sizes, types, strides and alignment add in the same order and give the same bits.
  *
  *   dy, x         (m, h) of dtype;  rstd fp32 (m);  weight (h) of weight_dtype
  *   dres          NULL or (m, h)
@@ -395,7 +395,8 @@ typedef enum {
  *   out = act(z) (+ residual),  preact = z
  *
  *   Sums are fp32; z is rounded once where it is stored, and out once (from
- *   the unrounded z).
+ *   the unrounded z).  Calls of the same sizes, types, weight layout, strides and
+ *   alignment add in the same order and give the same bits on devices alike.
  *
  *   x         (m, k), rows ldx apart
  *   w         (n, k) (the nn.Linear layout) or (k, n), rows ldw apart

@@ -19,12 +19,14 @@
 // Next to that, a stage's time was its issue: one lane took 460 clocks for a stage's two copies
 // (a wait, the count of bytes, 170 clocks a copy), two warps hide it; five elections and 64-bit
 // offsets took 360 clocks for its MMAs, which take 128 to 512 (now 220 to 255 where the MMAs are shorter).
-// With set-up free of divisions 512 tokens, 4096 x 4096: 18.2 -> 15.2 us, 128 tokens 11.8 -> 10.0, 512 x 1024 x 8192 17.1 -> 12.2.
+// That and a set-up free of divisions took 16% off 512 tokens, 4096 x 4096 (now 14.2 us), 15% off 128 tokens (9.5) and 29% off
+// 512 x 1024 x 8192 (11.4).
 // (Reading the other CTAs' sums with loads ran at 9 bytes a clock: 7.3 us for a pair's
 // 256 x 256 sums, the longest part of the call.)
 // The tensor core adds at the size of its running sum, so each 1024-deep part of
 // the contraction goes to an accumulator of its own while TMEM has room, and
-// these are added in fp32 with round-to-nearest.
+// these are added in fp32 with round-to-nearest.  Beyond that they are used again (two for 256
+// tokens: 6144 deep each for 2000 x 1024 x 24576, split in two).
 #include <atomic>
 #include <cmath>
 
@@ -477,8 +479,8 @@ struct SplitShape {
 };
 
 // Fetching the weight's first stages into L2 ahead of the stream's previous kernel's end
-// pays where two CTAs share most SMs (one token, 4096 x 4096, 256 CTAs: 8.6 -> 7.7 us), and
-// costs where the loads follow at once (32 tokens, 1024 x 8192, 64 CTAs: 6.9 -> 7.5).
+// pays where two CTAs share most SMs (one token, 4096 x 4096, 256 CTAs: 0.9 us less), and
+// costs where the loads follow at once (32 tokens, 1024 x 8192, 64 CTAs: 0.6 us more).
 bool prefetch_pays(const SplitShape &s, int num_sms) {
     return s.group == 1 && s.per_sm == 2 && s.tiles * s.split * 8 >= num_sms * 13ll;
 }
@@ -494,7 +496,7 @@ void fit_split(SplitShape &s, int steps, int num_sms) {
     if (full > kMaxStages) full = kMaxStages;
     if (full > most) full = most;
     // the others' sums beside the ring, or, where that would shorten it, over it (256 tokens,
-    // 4096 x 4096, split in two: 12.1 us against 12.7 with a shorter ring)
+    // 4096 x 4096, split in two: 0.6 us less than with a shorter ring)
     s.stages = static_cast<int>((room - recv) / stage);
     s.late = s.stages < full && s.group == 2;
     if (s.late || s.stages > full) s.stages = full;
@@ -591,8 +593,8 @@ SplitShape best_split(const LinearParams &p, int num_sms) {
         s.rows = ((p.m + s.m_tiles - 1) / s.m_tiles + unit - 1) / unit * unit;
         s.tiles = static_cast<int64_t>(s.m_tiles) * ((p.n + cols - 1) / cols);
         for (s.split = 1; s.split <= kMaxCluster / f.group && s.split <= steps; ++s.split) {
-            // two CTAs an SM where there are more than SMs and their stages are short: one token, 4096 x 4096, 7.7 us
-            // against 7.9; but 32 tokens, 1024 x 8192, 64 CTAs, 8.6 against 6.9
+            // two CTAs an SM where there are more than SMs and their stages are short: 0.2 us less for one token, 4096 x 4096;
+            // but 1.7 us more for 32 tokens, 1024 x 8192, 64 CTAs
             s.per_sm = f.group == 1 && s.rows <= 32 && s.tiles > clusters_at_once(s.split, num_sms) ? 2 : 1;
             fit_split(s, steps, num_sms);
             s.us = split_us(s, p, steps, num_sms);
@@ -651,8 +653,8 @@ bool linear_prefers_split(const LinearParams &p, int num_sms) {
     if (p.m <= 64) return true;
     // the 256 x 256 tiles: 6.3 us and 0.29 a 64-deep stage for each wave of them (1024 deep 10.6 to
     // 12.5 us, 4096 deep 24.0 to 25.6, 8192 deep 40.5 to 43.5, two waves 42.7 to 45).  Where the two cross, at
-    // (m, 4096) with k = 4096: 512 tokens 15.1 us split against 24.4, 777 21.6 against 25.0, 1024 24.0 against
-    // 25.5, 1536 43.8 against 42.7.
+    // (m, 4096) with k = 4096, both in one run: 512 tokens 15.1 us split against 24.4, 777 21.6 against 25.0, 1024
+    // 24.0 against 25.5, 1536 43.8 against 42.7.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256), pairs = num_sms / 2;
     const SplitShape s = best_split(p, num_sms);
     const int steps = (p.k + kDepth - 1) / kDepth, blocks = ((steps + s.split - 1) / s.split + kBlockSteps - 1) / kBlockSteps;
