@@ -289,7 +289,7 @@ def _exact_values(q, scale, quant):
     size = {"token": h, "group": 128, "mx": 32}[quant]
     full = torch.zeros(m, -(-h // size) * size, dtype=torch.float64, device=q.device)
     full[:, :h] = q.double()
-    step = torch.exp2(scale.double() - 127.0) if quant == "mx" else scale.double()
+    step = torch.ldexp(torch.ones_like(scale, dtype=torch.float64), scale.int() - 127) if quant == "mx" else scale.double()
     return (full.view(m, -1, size) * step.reshape(m, -1, 1)).reshape(m, -1)[:, :h]
 
 
@@ -310,7 +310,10 @@ def exact(case, seed):
         full[:, :h] = y
         full = full.view(m, -1, size)
         top = full.abs().max(2, keepdim=True).values
-        step = torch.exp2(torch.floor(torch.log2(top)) - EMAX[c["q"]]) if c["quant"] == "mx" else top / QMAX[c["q"]]
+        if c["quant"] == "mx":   # (a logarithm's floor may miss a power of two)
+            step = torch.ldexp(torch.ones_like(top), torch.frexp(top).exponent - 1 - EMAX[c["q"]])
+        else:
+            step = top / QMAX[c["q"]]
         codes = _round8(torch.where(top > 0, full / step, 0.0), c["q"])
         if c["quant"] == "token" and c["q"] != "int8":
             return {"q": codes.reshape(m, -1)[:, :h], "scale": step.reshape(m)}
