@@ -447,6 +447,101 @@ int mc2_matmul_act_grad(const void *dy, int64_t lddy, const void *w, int64_t ldw
 int mc2_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int act, int64_t m, int64_t n, int dtype,
                  void *dz, int64_t lddz, void *stream);
 
+/*
+ * The 8-bit path of a linear: an activation's codes with their scales, as
+ * mc2_add_rms_norm and mc2_act_quant make them, multiplied by an int8 weight, or
+ * kept for the backward pass (a byte an element instead of two or four).
+ * Where a call takes quant_mode and q_dtype, they say what the codes are:
+ *     MC2_QUANT_PERTOKEN_DYNAMIC   scale fp32 (m)
+ *     MC2_QUANT_PERGROUP           scale fp32 (m, ceil(h / 128)), one for each 128 columns
+ *     MC2_QUANT_MX                 scale e8m0 codes (m, ceil(h / 32)); fp8 codes only
+ * and q (m, h) of MC2_I8, MC2_F8E4M3 or MC2_F8E5M2 and scale are contiguous.  A
+ * code stands for q times its scale in fp32 (a scale that is a NaN or infinite makes
+ * its zeros NaN, so that what could not be held is not lost).
+ * Sizes are at most 2^30.  A call's tensors may have any alignment that suits their
+ * elements, and its matrices any row stride.
+ */
+
+/*
+ * Matrix product of int8 codes with scales per token and per channel, with bias,
+ * activation and residual in its epilogue.
+ *
+ *   acc = x @ w^T, exact           (w_is_nk != 0; x @ w otherwise)
+ *   z   = (float(acc) * x_scale[t]) * w_scale[j] (+ bias[j])
+ *   out = act(z) (+ residual)
+ *
+ *   The sums are exact integers, so an output depends on its row and its column alone: not on
+ *   the other tokens of the call, on strides or alignment.  The rest is fp32; out is rounded once.
+ *
+ *   x          (m, k) int8, rows ldx apart;  x_scale fp32 (m)
+ *   w          (n, k) (the nn.Linear layout) or (k, n) int8, rows ldw apart;  w_scale fp32 (n)
+ *   k          1 to 131071 (so that int32 holds any sum, of codes -128 to 127)
+ *   bias       NULL or (n) of bias_dtype: dtype or MC2_F32
+ *   act        an mc2_activation
+ *   residual   NULL or (m, n) of dtype, rows ldr apart
+ *   dtype      MC2_F16 or MC2_BF16;  out (m, n), rows ldo apart; may be residual itself (same stride)
+ *   workspace  device scratch of at least the bytes the query returns for the same matrices
+ *              (0 where the product of few tokens reads its operands as they are: NULL is then fine), 16-byte
+ *              aligned, no initialisation; reusable by calls ordered on one stream
+ *
+ * Returns MC2_OK or a negative mc2_status; nothing is launched on error.
+ */
+int mc2_quant_matmul_workspace(const int8_t *x, int64_t ldx, const int8_t *w, int64_t ldw, int w_is_nk, int64_t m,
+                               int64_t n, int64_t k, size_t *bytes);
+int mc2_quant_matmul(const int8_t *x, int64_t ldx, const float *x_scale, const int8_t *w, int64_t ldw, int w_is_nk,
+                     const float *w_scale, int64_t m, int64_t n, int64_t k, const void *bias, int bias_dtype, int act,
+                     const void *residual, int64_t ldr, int dtype, void *out, int64_t ldo, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * An activation in 8 bits: the codes of act(z), as mc2_add_rms_norm makes them but for the last bit
+ * of an fp32 scale: max|act(z)| of the row or group times 1 / Q, 1 / Q rounded to fp32 first.  Codes are
+ * act(z) / scale to nearest-even, saturated; mx scales are powers of two; codes of a scale that is zero or
+ * not finite are 0.  With MC2_ACT_NONE z itself is kept; with an activation the codes are the
+ * next linear's input.
+ *
+ *   z          (m, h) of dtype (MC2_F16, MC2_BF16 or MC2_F32), rows ldz apart
+ *   q, scale   out, as quant_mode and q_dtype say
+ */
+int mc2_act_quant(const void *z, int64_t ldz, int64_t m, int64_t h, int act, int dtype, int quant_mode, int q_dtype,
+                  void *q, void *scale, void *stream);
+
+/*
+ * The values of codes: out = act(q * scale), rounded once to dtype (MC2_F16, MC2_BF16
+ * or MC2_F32); out (m, h), rows ldo apart.
+ */
+int mc2_act_dequant(const void *q, const void *scale, int64_t m, int64_t h, int act, int quant_mode, int q_dtype,
+                    int dtype, void *out, int64_t ldo, void *stream);
+
+/*
+ * Gradient through an activation whose pre-activation was kept in 8 bits:
+ * dz = dy * act'(q * scale), elementwise over (m, h); rows of dy and dz lddy and
+ * lddz apart; dz may be dy itself (same stride).  dtype MC2_F16 or MC2_BF16.
+ */
+int mc2_act_grad_quant(const void *dy, int64_t lddy, const void *q, const void *scale, int64_t m, int64_t h, int act,
+                       int quant_mode, int q_dtype, int dtype, void *dz, int64_t lddz, void *stream);
+
+/*
+ * Weight and bias gradients of a linear whose input was kept in 8 bits (as the forward product's
+ * codes, or as the pre-activation of the activation that made it):
+ *
+ *   dw[i, j] = sum_t dy[t, i] * act(q[t, j] * scale)       (n, k)
+ *   db[i]    = sum_t dy[t, i]                              (n)
+ *
+ *   act(q * scale) is rounded to dtype, the tensor cores' operand type; sums are fp32, and
+ *   dw and db rounded once.  Calls of the same sizes, types and layouts add in the same order.
+ *
+ *   dy         (m, n), rows lddy apart;  q (m, k) with its scales
+ *   dw         (n, k);  db NULL or (n);  dtype MC2_F16 or MC2_BF16 for dy, dw and db
+ *   workspace  device scratch of at least the bytes the query returns for the same dy and dw,
+ *              16-byte aligned, no initialisation; reusable by calls ordered on one stream
+ */
+int mc2_matmul_weight_grad_quant_workspace(const void *dy, int64_t lddy, const void *dw, int64_t m, int64_t n,
+                                           int64_t k, size_t *bytes);
+int mc2_matmul_weight_grad_quant(const void *dy, int64_t lddy, const void *q, const void *scale, int64_t m, int64_t n,
+                                 int64_t k, int act, int quant_mode, int q_dtype, int dtype, void *dw, void *db,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
 /* Name of a status code (static string). */
 const char *mc2_status_str(int status);
 

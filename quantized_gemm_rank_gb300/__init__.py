@@ -20,6 +20,14 @@ and, around the linears:
   mc2_matmul_bias_act      out = act(x @ w^T + bias) + residual
   mc2_matmul_act_grad      dz = (dy @ w) * act'(z)
   mc2_act_grad             dz = dy * act'(z)
+
+and on 8-bit codes with their scales:
+
+  mc2_quant_matmul         out = act(x @ w^T * x_scale * w_scale + bias) + residual, int8 by int8
+  mc2_act_quant            the codes of act(z)
+  mc2_act_dequant          act of what codes stand for
+  mc2_act_grad_quant       dz = dy * act'(z), z kept in 8 bits
+  mc2_matmul_weight_grad_quant  dw = dy^T @ act(x), db = dy.sum(0), x kept in 8 bits
 """
 from __future__ import annotations
 
@@ -103,6 +111,23 @@ def lib() -> ctypes.CDLL:
         L.mc2_matmul_act_grad.restype = _INT
         L.mc2_act_grad.argtypes = [_P, _I64, _P, _I64, _INT, _I64, _I64, _INT, _P, _I64, _P]
         L.mc2_act_grad.restype = _INT
+        L.mc2_quant_matmul_workspace.argtypes = [_P, _I64, _P, _I64, _INT, _I64, _I64, _I64,
+                                                 ctypes.POINTER(ctypes.c_size_t)]
+        L.mc2_quant_matmul_workspace.restype = _INT
+        L.mc2_quant_matmul.argtypes = [_P, _I64, _P, _P, _I64, _INT, _P, _I64, _I64, _I64, _P, _INT, _INT, _P, _I64, _INT,
+                                       _P, _I64, _P, ctypes.c_size_t, _P]
+        L.mc2_quant_matmul.restype = _INT
+        L.mc2_act_quant.argtypes = [_P, _I64, _I64, _I64, _INT, _INT, _INT, _INT, _P, _P, _P]
+        L.mc2_act_quant.restype = _INT
+        L.mc2_act_dequant.argtypes = [_P, _P, _I64, _I64, _INT, _INT, _INT, _INT, _P, _I64, _P]
+        L.mc2_act_dequant.restype = _INT
+        L.mc2_act_grad_quant.argtypes = [_P, _I64, _P, _P, _I64, _I64, _INT, _INT, _INT, _INT, _P, _I64, _P]
+        L.mc2_act_grad_quant.restype = _INT
+        L.mc2_matmul_weight_grad_quant_workspace.argtypes = [_P, _I64, _P, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)]
+        L.mc2_matmul_weight_grad_quant_workspace.restype = _INT
+        L.mc2_matmul_weight_grad_quant.argtypes = [_P, _I64, _P, _P, _I64, _I64, _I64, _INT, _INT, _INT, _INT, _P, _P, _P,
+                                                   ctypes.c_size_t, _P]
+        L.mc2_matmul_weight_grad_quant.restype = _INT
         L.mc2_status_str.argtypes = [_INT]
         L.mc2_status_str.restype = ctypes.c_char_p
         L.mc2_last_error.argtypes = []
@@ -846,6 +871,250 @@ def mc2_act_grad(dy: torch.Tensor, z: torch.Tensor, *, activation: str, dz: Opti
     return dz
 
 
+# ------------------------------------------------------------------ the 8-bit path of a linear
+
+def _kept(q: torch.Tensor, scale: torch.Tensor, cur: int):
+    """The pointers, quant mode and code type of codes (..., h) and their scales, whose type and shape say
+    what they are scales of: fp32 (...) of rows, fp32 (..., ceil(h / 128)) or uint8 (..., ceil(h / 32)) of groups."""
+    if q.dtype not in _QNORM:
+        raise ValueError(f"q must be of dtype int8, float8_e4m3fn or float8_e5m2, got {q.dtype}")
+    _leading(q, "q")
+    shape, h = q.shape[:-1], q.shape[-1]
+    sdt, mode = torch.float32, QUANT_PERTOKEN_DYNAMIC
+    if scale.dtype == torch.uint8:
+        shape, sdt, mode = (*shape, -(-h // 32)), torch.uint8, QUANT_MX
+    elif scale.dim() == q.dim():
+        shape, mode = (*shape, -(-h // 128)), QUANT_PERGROUP
+    return _arg(q, q.shape, q.dtype, "q", cur), _arg(scale, shape, sdt, "scale", cur), mode, _QNORM[q.dtype]
+
+
+def _workspace(given: Optional[torch.Tensor], nbytes: int, device, cur: int):
+    """A workspace's tensor, pointer and size: the one given, or one of nbytes."""
+    if given is None:
+        given = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return given, _arg(given, given.shape, given.dtype, "workspace", cur), given.numel() * given.element_size()
+
+
+def mc2_quant_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
+                     w_is_nk: bool = True, bias: Optional[torch.Tensor] = None, activation: str = "none",
+                     residual: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """out = act((x @ w^T) * x_scale * w_scale + bias) + residual: int8 codes, exact integer sums.
+
+    x (..., k) int8 with x_scale (...) fp32, one per row (mc2_add_rms_norm's or mc2_act_quant's codes and scales with
+    QUANT_PERTOKEN_DYNAMIC); w (n, k) int8, or (k, n) with ``w_is_nk=False``, with w_scale (n) fp32; bias (n) of the
+    output's type or fp32; residual (..., n).  dtype: the output's, float16 or bfloat16 (by default out's or residual's,
+    else bfloat16).  k is at most 131071.  ``workspace``, if given, holds mc2_quant_matmul_workspace(...) bytes.
+    """
+    if stream is not None:
+        return _on_stream(mc2_quant_matmul, locals())
+    cur = _current_device()
+    act = _activation(activation)
+    dt = dtype if dtype is not None else out.dtype if out is not None else residual.dtype if residual is not None else torch.bfloat16
+    if cur >= 0:
+        r = (_native_module or _native()).quant_matmul(x, x_scale, w, w_scale, w_is_nk, bias, act, residual, dt, out, workspace,
+                                                       cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
+    m, k = _leading(x, "x"), x.shape[-1]
+    if w.dim() != 2:
+        raise ValueError(f"w must have 2 dimensions, got {w.dim()}")
+    n = w.shape[0] if w_is_nk else w.shape[1]
+    xp, ldx = _rows(x, x.shape, torch.int8, "x", cur)
+    xsp = _arg(x_scale, x.shape[:-1], torch.float32, "x_scale", cur)
+    wp, ldw = _rows(w, (n, k) if w_is_nk else (k, n), torch.int8, "w", cur)
+    wsp = _arg(w_scale, (n,), torch.float32, "w_scale", cur)
+    bp, bdt = None, dt
+    if bias is not None:
+        bdt = torch.float32 if bias.dtype == torch.float32 else dt
+        bp = _arg(bias, (n,), bdt, "bias", cur)
+    oshape = (*x.shape[:-1], n)
+    rp, ldr = _opt_rows(residual, oshape, dt, "residual", cur)
+    _dtype_code(dt)
+    if out is None:
+        out = torch.empty(oshape, dtype=dt, device=x.device)
+        op, ldo = out.data_ptr(), n
+    else:
+        op, ldo = _rows(out, oshape, dt, "out", cur)
+    _need_device(cur)
+    nbytes = ctypes.c_size_t(0)
+    if workspace is None:
+        _check(lib().mc2_quant_matmul_workspace(xp, ldx, wp, ldw, w_is_nk, m, n, k, ctypes.byref(nbytes)))
+    workspace, ws, size = _workspace(workspace, nbytes.value, x.device, cur)
+    _check(lib().mc2_quant_matmul(xp, ldx, xsp, wp, ldw, w_is_nk, wsp, m, n, k, bp, _dtype_code(bdt), act, rp, ldr, _dtype_code(dt),
+                                  op, ldo, ws, size, _stream(stream, cur)))
+    return out
+
+
+def mc2_quant_matmul_workspace(x: torch.Tensor, w: torch.Tensor, *, w_is_nk: bool = True) -> int:
+    """Bytes of workspace that mc2_quant_matmul needs for these matrices (0 for few tokens in aligned rows)."""
+    cur = _current_device()
+    m, k = _leading(x, "x"), x.shape[-1]
+    n = w.shape[0] if w_is_nk else w.shape[1]
+    xp, ldx = _rows(x, x.shape, torch.int8, "x", cur)
+    wp, ldw = _rows(w, (n, k) if w_is_nk else (k, n), torch.int8, "w", cur)
+    nbytes = ctypes.c_size_t(0)
+    _check(lib().mc2_quant_matmul_workspace(xp, ldx, wp, ldw, w_is_nk, m, n, k, ctypes.byref(nbytes)))
+    return int(nbytes.value)
+
+
+def mc2_act_quant(z: torch.Tensor, *, activation: str = "none", quant_mode: int = QUANT_PERTOKEN_DYNAMIC,
+                  q_dtype: torch.dtype = torch.int8, q: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None, stream=None):
+    """The 8-bit codes of act(z) and their scales: (q, scale).
+
+    z (..., h) of fp16, bf16 or fp32.  quant_mode and q_dtype, and the scales they give, as in mc2_add_rms_norm:
+    QUANT_PERTOKEN_DYNAMIC, QUANT_PERGROUP or QUANT_MX; int8, float8_e4m3fn or float8_e5m2.  Without an activation z
+    itself is kept in 8 bits (for mc2_act_grad_quant and mc2_matmul_weight_grad_quant); with one, the codes
+    are the next linear's input (int8 per token: mc2_quant_matmul's x).
+    """
+    if stream is not None:
+        return _on_stream(mc2_act_quant, locals())
+    cur = _current_device()
+    act = _activation(activation)
+    if cur >= 0:
+        r = (_native_module or _native()).act_quant(z, act, quant_mode, q_dtype, q, scale, cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
+    shape, dev = z.shape, z.device
+    m, h = _leading(z, "z"), shape[-1]
+    zp, ldz = _rows(z, shape, z.dtype, "z", cur)
+    if q_dtype not in _QNORM:
+        raise ValueError(f"q_dtype must be int8, float8_e4m3fn or float8_e5m2, got {q_dtype}")
+    sshape, sdt = shape[:-1], torch.float32
+    if quant_mode == QUANT_PERGROUP:
+        sshape = (*sshape, -(-h // 128))
+    elif quant_mode == QUANT_MX:
+        sshape, sdt = (*sshape, -(-h // 32)), torch.uint8
+    if q is None:
+        q = torch.empty(shape, dtype=q_dtype, device=dev)
+    qp = _arg(q, shape, q_dtype, "q", cur)
+    if scale is None:
+        scale = torch.empty(sshape, dtype=sdt, device=dev)
+    sp = _arg(scale, sshape, sdt, "scale", cur)
+    _need_device(cur)
+    _check(lib().mc2_act_quant(zp, ldz, m, h, act, _dtype_code(z.dtype), quant_mode, _QNORM[q_dtype], qp, sp, _stream(stream, cur)))
+    return q, scale
+
+
+def mc2_act_dequant(q: torch.Tensor, scale: torch.Tensor, *, activation: str = "none", dtype: Optional[torch.dtype] = None,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """act(q * scale), rounded once to ``dtype`` (float16, bfloat16 or float32; by default out's, else bfloat16).
+
+    q (..., h) int8, float8_e4m3fn or float8_e5m2; scale as mc2_act_quant and mc2_add_rms_norm make it: fp32 (...) per
+    token, fp32 (..., ceil(h / 128)) per 128 columns or uint8 (..., ceil(h / 32)) e8m0 codes.
+    """
+    if stream is not None:
+        return _on_stream(mc2_act_dequant, locals())
+    cur = _current_device()
+    act = _activation(activation)
+    dt = dtype if dtype is not None else out.dtype if out is not None else torch.bfloat16
+    if cur >= 0:
+        r = (_native_module or _native()).act_dequant(q, scale, act, dt, out, cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
+    qp, sp, mode, qd = _kept(q, scale, cur)
+    m, h = _leading(q, "q"), q.shape[-1]
+    _dtype_code(dt)
+    if out is None:
+        out = torch.empty(q.shape, dtype=dt, device=q.device)
+        op, ldo = out.data_ptr(), h
+    else:
+        op, ldo = _rows(out, q.shape, dt, "out", cur)
+    _need_device(cur)
+    _check(lib().mc2_act_dequant(qp, sp, m, h, act, mode, qd, _dtype_code(dt), op, ldo, _stream(stream, cur)))
+    return out
+
+
+def mc2_act_grad_quant(dy: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *, activation: str,
+                       dz: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dz = dy * act'(q * scale), elementwise: mc2_act_grad for a pre-activation kept in 8 bits (``dz`` may be dy)."""
+    if stream is not None:
+        return _on_stream(mc2_act_grad_quant, locals())
+    cur = _current_device()
+    act = _activation(activation)
+    if cur >= 0:
+        r = (_native_module or _native()).act_grad_quant(dy, q, scale, act, dz, cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
+    qp, sp, mode, qd = _kept(q, scale, cur)
+    shape, dt = q.shape, dy.dtype
+    m, h = _leading(q, "q"), shape[-1]
+    dyp, lddy = _rows(dy, shape, dt, "dy", cur)
+    if dz is None:
+        dz = torch.empty(shape, dtype=dt, device=dy.device)
+        dzp, lddz = dz.data_ptr(), h
+    else:
+        dzp, lddz = _rows(dz, shape, dt, "dz", cur)
+    _need_device(cur)
+    _check(lib().mc2_act_grad_quant(dyp, lddy, qp, sp, m, h, act, mode, qd, _dtype_code(dt), dzp, lddz, _stream(stream, cur)))
+    return dz
+
+
+def mc2_matmul_weight_grad_quant(dy: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *, activation: str = "none",
+                                 with_bias: bool = True, dw: Optional[torch.Tensor] = None,
+                                 db: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """dw = dy^T @ act(q * scale) (n, k) and, with ``with_bias``, db = dy.sum(0) (n): (dw, db).
+
+    mc2_matmul_weight_grad for an input kept in 8 bits: dy (..., n) of float16 or bfloat16, q (..., k) with its scales as
+    in mc2_act_dequant.  With an activation, q is the pre-activation that the linear's input came from.
+    ``workspace``, if given, holds mc2_matmul_weight_grad_quant_workspace(...) bytes.
+    """
+    if stream is not None:
+        return _on_stream(mc2_matmul_weight_grad_quant, locals())
+    cur = _current_device()
+    act = _activation(activation)
+    if cur >= 0:
+        r = (_native_module or _native()).weight_grad_quant(dy, q, scale, act, with_bias, dw, db, workspace, cur, _stream(stream, cur))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
+    qp, sp, mode, qd = _kept(q, scale, cur)
+    m, k, dt = _leading(q, "q"), q.shape[-1], dy.dtype
+    _leading(dy, "dy")
+    n = dy.shape[-1]
+    dyp, lddy = _rows(dy, (*q.shape[:-1], n), dt, "dy", cur)
+    if dw is None:
+        dw = torch.empty((n, k), dtype=dt, device=dy.device)
+    dwp = _arg(dw, (n, k), dt, "dw", cur)
+    dbp = None
+    if with_bias or db is not None:
+        if db is None:
+            db = torch.empty((n,), dtype=dt, device=dy.device)
+        dbp = _arg(db, (n,), dt, "db", cur)
+    _need_device(cur)
+    nbytes = ctypes.c_size_t(0)
+    if workspace is None:
+        _check(lib().mc2_matmul_weight_grad_quant_workspace(dyp, lddy, dwp, m, n, k, ctypes.byref(nbytes)))
+    workspace, ws, size = _workspace(workspace, nbytes.value, dy.device, cur)
+    _check(lib().mc2_matmul_weight_grad_quant(dyp, lddy, qp, sp, m, n, k, act, mode, qd, _dtype_code(dt), dwp, dbp, ws, size,
+                                              _stream(stream, cur)))
+    return dw, db
+
+
+def mc2_matmul_weight_grad_quant_workspace(dy: torch.Tensor, k: int, *, dw: Optional[torch.Tensor] = None) -> int:
+    """Bytes of workspace that mc2_matmul_weight_grad_quant needs for this dy (..., n) and k columns of codes.
+
+    For a ``dw`` of one's own that may not be 16-byte aligned, that too."""
+    cur = _current_device()
+    m, n = _leading(dy, "dy"), dy.shape[-1]
+    dyp, lddy = _rows(dy, dy.shape, dy.dtype, "dy", cur)
+    dwp = 16 if dw is None else _arg(dw, (n, k), dy.dtype, "dw", cur)
+    nbytes = ctypes.c_size_t(0)
+    _check(lib().mc2_matmul_weight_grad_quant_workspace(dyp, lddy, dwp, m, n, k, ctypes.byref(nbytes)))
+    return int(nbytes.value)
+
+
 def mc2_device_status() -> int:
     """Synchronise and return (and clear) the kernels' bounded-wait status."""
     return int(lib().mc2_device_status())
@@ -879,6 +1148,8 @@ __all__ = [
     "mc2_alltoall_quant_mm_no_alloc",
     "mc2_add_rms_norm", "mc2_rms_norm_grad_workspace", "mc2_rms_norm_grad", "mc2_matmul_bias_act",
     "mc2_matmul_act_grad", "mc2_act_grad",
+    "mc2_quant_matmul_workspace", "mc2_quant_matmul", "mc2_act_quant", "mc2_act_dequant", "mc2_act_grad_quant",
+    "mc2_matmul_weight_grad_quant_workspace", "mc2_matmul_weight_grad_quant",
     "NO_ALLOC_SCRATCH_BYTES", "mc2_device_status", "mc2_set_launch_events", "mc2_test_expire_next_flag_waits",
     "MC2_OK", "MC2_ERR_NULL", "MC2_ERR_SHAPE", "MC2_ERR_DTYPE", "MC2_ERR_UNSUPPORTED", "MC2_ERR_WORKSPACE",
     "MC2_ERR_CUDA", "MC2_ERR_TIMEOUT", "MC2_F16", "MC2_BF16", "MC2_F32", "MC2_I8",

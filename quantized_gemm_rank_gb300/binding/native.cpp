@@ -373,8 +373,209 @@ PyObject *act_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// Codes and their scales: what the scales' type and shape say.
+struct Codes {
+    void *q = nullptr, *scale = nullptr;
+    int64_t m = 0, h = 0;
+    int mode = 0, kind = 0;
+    at::IntArrayRef shape;
+};
+
+bool codes(PyObject *q, PyObject *scale, int64_t cur, Codes &c) {
+    if (!is_tensor(q) || !is_tensor(scale)) return false;
+    const at::Tensor &t = THPVariable_Unpack(q), &s = THPVariable_Unpack(scale);
+    c.shape = t.sizes();
+    c.kind = code_kind(t.scalar_type());
+    if (!c.kind || c.shape.size() < 2) return false;
+    c.h = c.shape.back(), c.m = row_count(c.shape);
+    c10::SmallVector<int64_t, 5> ss(c.shape.begin(), c.shape.end() - 1);
+    c.mode = MC2_QUANT_PERTOKEN_DYNAMIC;
+    if (s.scalar_type() == at::kByte) {
+        ss.push_back((c.h + 31) / 32);
+        c.mode = MC2_QUANT_MX;
+    } else if (s.dim() == t.dim()) {
+        ss.push_back((c.h + 127) / 128);
+        c.mode = MC2_QUANT_PERGROUP;
+    }
+    return dense(q, c.shape, t.scalar_type(), cur, c.q) && dense(scale, ss, c.mode == MC2_QUANT_MX ? at::kByte : at::kFloat, cur, c.scale);
+}
+
+// A workspace of `need` bytes: the tensor given, or a new one (`own`).
+bool workspace(PyObject *given, size_t need, const at::Tensor &like, int64_t cur, at::Tensor &own, void *&p, size_t &bytes) {
+    if (given != Py_None) {
+        if (!is_tensor(given)) return false;
+        const at::Tensor &t = THPVariable_Unpack(given);
+        if (!on(t, cur) || !t.is_contiguous()) return false;
+        p = t.data_ptr(), bytes = t.nbytes();
+    } else if (need) {
+        const int64_t size = static_cast<int64_t>(need);
+        own = make(at::IntArrayRef(size), like, at::kByte);
+        p = own.data_ptr(), bytes = need;
+    }
+    return true;
+}
+
+// quant_matmul(x, x_scale, w, w_scale, w_is_nk, bias, activation, residual, dtype, out, workspace, device, stream)
+PyObject *quant_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        if (n != 13 || !is_tensor(a[0]) || !THPDtype_Check(a[8])) return irregular();
+        const at::Tensor &x = THPVariable_Unpack(a[0]);
+        const int64_t cur = PyLong_AsLongLong(a[11]);
+        const int act = static_cast<int>(PyLong_AsLong(a[6]));
+        const int nk = PyObject_IsTrue(a[4]);
+        const at::ScalarType dt = reinterpret_cast<THPDtype *>(a[8])->scalar_type;
+        const at::IntArrayRef shape = x.sizes();
+        if (shape.size() < 2 || !dtype_code(dt)) return irregular();
+        const int64_t k = shape.back(), m = row_count(shape);
+        const at::IntArrayRef lead = shape.slice(0, shape.size() - 1);
+        Rows xr, wr, rr, outr;
+        int64_t w0 = 0, w1 = 0;
+        void *xs = nullptr, *ws = nullptr, *bp = nullptr, *wk = nullptr;
+        Owned out;
+        if (!rows(a[0], shape, at::kChar, cur, xr) || !dense(a[1], lead, at::kFloat, cur, xs) ||
+            !matrix(a[2], at::kChar, cur, wr, w0, w1) || (nk ? w1 : w0) != k)
+            return irregular();
+        const int64_t cols = nk ? w0 : w1;
+        if (!dense(a[3], at::IntArrayRef(cols), at::kFloat, cur, ws)) return irregular();
+        int bias_type = 0;
+        if (a[5] != Py_None) {
+            if (!is_tensor(a[5])) return irregular();
+            const at::ScalarType bt = THPVariable_Unpack(a[5]).scalar_type();
+            if ((bt != dt && bt != at::kFloat) || !dense(a[5], at::IntArrayRef(cols), bt, cur, bp)) return irregular();
+            bias_type = dtype_code(bt);
+        }
+        c10::SmallVector<int64_t, 5> os(shape.begin(), shape.end());
+        os.back() = cols;
+        if (a[7] != Py_None && !rows(a[7], os, dt, cur, rr)) return irregular();
+        if (!output(a[9], os, x, dt, cur, outr, out.o)) return irregular();
+        size_t need = 0, bytes = 0;
+        const int8_t *xp = static_cast<int8_t *>(xr.p), *wp = static_cast<int8_t *>(wr.p);
+        at::Tensor own;
+        if (a[10] == Py_None && mc2_quant_matmul_workspace(xp, xr.ld, wp, wr.ld, nk, m, cols, k, &need) != MC2_OK) return irregular();
+        if (!workspace(a[10], need, x, cur, own, wk, bytes)) return irregular();
+        void *stream = handle(a[12]);
+        const int st = unlocked([&] {
+            return mc2_quant_matmul(xp, xr.ld, static_cast<float *>(xs), wp, wr.ld, nk, static_cast<float *>(ws), m, cols, k, bp,
+                                    bias_type, act, rr.p, rr.ld, dtype_code(dt), outr.p, outr.ld, wk, bytes, stream);
+        });
+        return st != MC2_OK ? PyLong_FromLong(st) : out.take();
+    });
+}
+
+// act_quant(z, activation, quant_mode, q_dtype, q, scale, device, stream)
+PyObject *act_quant(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        if (n != 8 || !is_tensor(a[0]) || !THPDtype_Check(a[3])) return irregular();
+        const at::Tensor &z = THPVariable_Unpack(a[0]);
+        const int64_t cur = PyLong_AsLongLong(a[6]);
+        const int act = static_cast<int>(PyLong_AsLong(a[1]));
+        const long mode = PyLong_AsLong(a[2]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return irregular();
+        }
+        const at::ScalarType dt = z.scalar_type(), qt = reinterpret_cast<THPDtype *>(a[3])->scalar_type;
+        const at::IntArrayRef shape = z.sizes();
+        const int qd = code_kind(qt);
+        if (shape.size() < 2 || !dtype_code(dt) || !qd ||
+            (mode != MC2_QUANT_PERTOKEN_DYNAMIC && mode != MC2_QUANT_PERGROUP && mode != MC2_QUANT_MX))
+            return irregular();
+        const int64_t h = shape.back(), m = row_count(shape);
+        Rows zr;
+        void *qp = nullptr, *sp = nullptr;
+        Owned q, scale;
+        c10::SmallVector<int64_t, 5> ss(shape.begin(), shape.end() - 1);
+        if (mode == MC2_QUANT_PERGROUP) ss.push_back((h + 127) / 128);
+        if (mode == MC2_QUANT_MX) ss.push_back((h + 31) / 32);
+        if (!rows(a[0], shape, dt, cur, zr) || !output_dense(a[4], shape, z, qt, cur, qp, q.o) ||
+            !output_dense(a[5], ss, z, mode == MC2_QUANT_MX ? at::kByte : at::kFloat, cur, sp, scale.o))
+            return irregular();
+        void *stream = handle(a[7]);
+        const int st = unlocked([&] {
+            return mc2_act_quant(zr.p, zr.ld, m, h, act, dtype_code(dt), static_cast<int>(mode), qd, qp, sp, stream);
+        });
+        return st != MC2_OK ? PyLong_FromLong(st) : pair(q, scale);
+    });
+}
+
+// act_dequant(q, scale, activation, dtype, out, device, stream)
+PyObject *act_dequant(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        if (n != 7 || !THPDtype_Check(a[3])) return irregular();
+        const int64_t cur = PyLong_AsLongLong(a[5]);
+        const int act = static_cast<int>(PyLong_AsLong(a[2]));
+        const at::ScalarType dt = reinterpret_cast<THPDtype *>(a[3])->scalar_type;
+        Codes c;
+        Rows outr;
+        Owned out;
+        if (!dtype_code(dt) || !codes(a[0], a[1], cur, c) || !output(a[4], c.shape, THPVariable_Unpack(a[0]), dt, cur, outr, out.o))
+            return irregular();
+        void *stream = handle(a[6]);
+        const int st = unlocked([&] {
+            return mc2_act_dequant(c.q, c.scale, c.m, c.h, act, c.mode, c.kind, dtype_code(dt), outr.p, outr.ld, stream);
+        });
+        return st != MC2_OK ? PyLong_FromLong(st) : out.take();
+    });
+}
+
+// act_grad_quant(dy, q, scale, activation, dz, device, stream)
+PyObject *act_grad_quant(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        if (n != 7 || !is_tensor(a[0])) return irregular();
+        const at::Tensor &dy = THPVariable_Unpack(a[0]);
+        const int64_t cur = PyLong_AsLongLong(a[5]);
+        const int act = static_cast<int>(PyLong_AsLong(a[3]));
+        const at::ScalarType dt = dy.scalar_type();
+        Codes c;
+        Rows dyr, dzr;
+        Owned dz;
+        if (!dtype_code(dt) || !codes(a[1], a[2], cur, c) || !rows(a[0], c.shape, dt, cur, dyr) ||
+            !output(a[4], c.shape, dy, dt, cur, dzr, dz.o))
+            return irregular();
+        void *stream = handle(a[6]);
+        const int st = unlocked([&] {
+            return mc2_act_grad_quant(dyr.p, dyr.ld, c.q, c.scale, c.m, c.h, act, c.mode, c.kind, dtype_code(dt), dzr.p, dzr.ld, stream);
+        });
+        return st != MC2_OK ? PyLong_FromLong(st) : dz.take();
+    });
+}
+
+// weight_grad_quant(dy, q, scale, activation, with_bias, dw, db, workspace, device, stream)
+PyObject *weight_grad_quant(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        if (n != 10 || !is_tensor(a[0])) return irregular();
+        const at::Tensor &dy = THPVariable_Unpack(a[0]);
+        const int64_t cur = PyLong_AsLongLong(a[8]);
+        const int act = static_cast<int>(PyLong_AsLong(a[3]));
+        const at::ScalarType dt = dy.scalar_type();
+        Codes c;
+        Rows dyr;
+        void *dwp = nullptr, *dbp = nullptr, *wk = nullptr;
+        Owned dw, db;
+        if (!dtype_code(dt) || dy.dim() < 2 || !codes(a[1], a[2], cur, c)) return irregular();
+        const int64_t cols = dy.sizes().back();
+        c10::SmallVector<int64_t, 5> ds(c.shape.begin(), c.shape.end());
+        ds.back() = cols;
+        const int64_t ws[2] = {cols, c.h};
+        if (!rows(a[0], ds, dt, cur, dyr) || !output_dense(a[5], at::IntArrayRef(ws, 2), dy, dt, cur, dwp, dw.o)) return irregular();
+        if ((a[6] != Py_None || PyObject_IsTrue(a[4]) == 1) && !output_dense(a[6], at::IntArrayRef(cols), dy, dt, cur, dbp, db.o))
+            return irregular();
+        size_t need = 0, bytes = 0;
+        at::Tensor own;
+        if (a[7] == Py_None && mc2_matmul_weight_grad_quant_workspace(dyr.p, dyr.ld, dwp, c.m, cols, c.h, &need) != MC2_OK) return irregular();
+        if (!workspace(a[7], need, dy, cur, own, wk, bytes)) return irregular();
+        void *stream = handle(a[9]);
+        const int st = unlocked([&] {
+            return mc2_matmul_weight_grad_quant(dyr.p, dyr.ld, c.q, c.scale, c.m, cols, c.h, act, c.mode, c.kind, dtype_code(dt), dwp,
+                                                dbp, wk, bytes, stream);
+        });
+        return st != MC2_OK ? PyLong_FromLong(st) : pair(dw, db);
+    });
+}
+
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FAST(add_rms_norm), FAST(rms_norm_grad), FAST(matmul_bias_act), FAST(matmul_act_grad), FAST(act_grad),
+                          FAST(quant_matmul), FAST(act_quant), FAST(act_dequant), FAST(act_grad_quant), FAST(weight_grad_quant),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

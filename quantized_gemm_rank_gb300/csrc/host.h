@@ -7,6 +7,9 @@
 
 #include <cstdint>
 
+#include "mc2_gb300.h"
+#include "num.cuh"
+
 namespace mc2 {
 namespace host {
 
@@ -15,6 +18,25 @@ __attribute__((format(printf, 2, 3))) int fail(int status, const char *fmt, ...)
 void clear_error();
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline size_t elem_size(int dtype) { return dtype == MC2_F32 ? 4 : 2; }
+
+inline int elem_kind(int dtype) {
+    return dtype == MC2_F16 ? mc2::ELEM_F16 : (dtype == MC2_BF16 ? mc2::ELEM_BF16 : mc2::ELEM_F32);
+}
+
+// A matrix argument: its rows must not overlap and its elements must be aligned
+// to their own size.  Optional ones are passed only when given.
+inline int check_rows(const char *what, const void *p, int64_t ld, int64_t m, int64_t cols, size_t size) {
+    if (ld < cols && m > 1)
+        return fail(MC2_ERR_SHAPE, "%s: rows of %lld elements cannot be %lld elements apart", what, (long long)cols,
+                    (long long)ld);
+    if (ld > INT64_MAX / 4 / (m > 1 ? m : 1))
+        return fail(MC2_ERR_SHAPE, "%s: a row stride of %lld elements is too large", what, (long long)ld);
+    if (reinterpret_cast<uintptr_t>(p) % size != 0)
+        return fail(MC2_ERR_UNSUPPORTED, "%s is not aligned to its %zu-byte elements", what, size);
+    return MC2_OK;
+}
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per bounded device-side wait
 

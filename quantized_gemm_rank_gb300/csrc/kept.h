@@ -1,0 +1,52 @@
+// kept.h -- an activation kept in 8 bits, and its uses: the kernels, as the C entry points call them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace mc2 {
+
+// Codes (m, h) without gaps, and their scales: fp32 per row (QM_TOKEN) or per 128 columns (QM_GROUP), or e8m0 codes
+// per 32 columns (QM_MX).
+struct Kept {
+    void *q, *scale;
+    int64_t m;
+    int h;
+    int qmode, qkind;
+};
+
+// codes of act(z); z of elem kind (rows ldz apart)
+cudaError_t launch_act_quant(int kind, const void *z, int64_t ldz, const Kept &to, int act, int num_sms, cudaStream_t stream);
+// out = act(q scale), of elem kind
+cudaError_t launch_act_dequant(int kind, const Kept &from, int act, void *out, int64_t ldo, int num_sms, cudaStream_t stream);
+// dz = dy act'(q scale), 16-bit
+cudaError_t launch_act_grad_quant(bool bf16, const void *dy, int64_t lddy, const Kept &z, int act, void *dz, int64_t lddz,
+                                  int num_sms, cudaStream_t stream);
+
+// out (m, n) = act(float(x w^T) x_scale w_scale + bias) + residual; x (m, k) and w int8, w (n, k) or (k, n) (w_nk == 0)
+struct QuantProduct {
+    const int8_t *x, *w;
+    const float *x_scale, *w_scale;
+    const void *bias, *residual;
+    void *out;
+    int64_t ldx, ldw, ldr, ldo;
+    int m, n, k;
+    int w_nk;
+    int act;
+    int bias_f32;   // (otherwise of out's type)
+};
+cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, cudaStream_t stream);
+
+// dw (n, k) = dy^T act(q scale), db (n) = column sums of dy; x is (m, k)
+struct QuantWeightGrad {
+    const void *dy;
+    void *dw, *db;
+    Kept x;
+    int64_t lddy;
+    int m, n, k;
+    int act;
+};
+cudaError_t launch_quant_weight_grad(bool bf16, const QuantWeightGrad &p, cudaStream_t stream);
+
+}  // namespace mc2

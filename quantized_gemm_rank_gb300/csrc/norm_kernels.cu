@@ -14,6 +14,7 @@
 //   dw[j]    = sum_t dy[t, j] xhat[t, j]
 #include "norm.h"
 
+#include "codes.cuh"
 #include "host.h"
 #include "internal.h"
 #include "num.cuh"
@@ -73,56 +74,6 @@ __device__ __forceinline__ float weight_at(const void *w, int w_f32, int j, int 
 // vectors t, t + T, ..., V of them, so neighbouring lanes hold neighbouring
 // vectors and a group of 32 or 128 elements is 4 to 32 consecutive lanes.
 
-template <int kT>
-struct Vec {
-    static constexpr int kW = kT == ELEM_F32 ? 4 : 8;   // elements of 16 bytes
-};
-
-template <int kT>
-__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[Vec<kT>::kW]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (kT == ELEM_F32) {
-            f[i] = __uint_as_float(w[i]);
-        } else if constexpr (kT == ELEM_BF16) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        } else {
-            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            f[2 * i] = h.x;
-            f[2 * i + 1] = h.y;
-        }
-    }
-}
-
-template <int kT>
-__device__ __forceinline__ uint4 pack(const float (&f)[Vec<kT>::kW]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (kT == ELEM_F32) {
-            w[i] = __float_as_uint(f[i]);
-        } else if constexpr (kT == ELEM_BF16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&b);
-        } else {
-            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// 16 bytes that are read once: not kept in L1.
-__device__ __forceinline__ uint4 load_once(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(reinterpret_cast<uint64_t>(p)));
-    return v;
-}
-
 // The weights of vector c, of x's type or fp32.
 template <int kT>
 __device__ __forceinline__ void load_weights(const void *w, int w_f32, int c, float (&f)[Vec<kT>::kW]) {
@@ -137,15 +88,8 @@ __device__ __forceinline__ void load_weights(const void *w, int w_f32, int c, fl
     }
 }
 
-// The larger of a and |b|; a NaN is kept.
-__device__ __forceinline__ float max_abs(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
-    return d;
-}
-
-// Sum and largest value over the block: one barrier each, the warps' values in
-// slots of their own, and the same tree in every warp (so every thread has the same bits).
+// Sum over the block: one barrier, the warps' values in slots of their own, and
+// the same tree in every warp (so every thread has the same bits).
 __device__ __forceinline__ float block_sum32(float v, float *slots) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -157,68 +101,6 @@ __device__ __forceinline__ float block_sum32(float v, float *slots) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
-}
-
-__device__ __forceinline__ uint32_t block_max32(uint32_t v, uint32_t *slots) {
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    if (blockDim.x == 32) return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) slots[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return __reduce_max_sync(0xFFFFFFFFu, lane < (blockDim.x >> 5) ? slots[lane] : 0u);
-}
-
-// A scale that codes can be made with; the others give zeros.
-__device__ __forceinline__ bool usable(float step) { return step > 0.0f && step < __int_as_float(0x7F800000); }
-
-// The quotients y / step of a vector by one reciprocal for all of them and
-// Markstein's correction (IBM J. Res. Dev. 34, 1990): with inv the rounded
-// reciprocal, r = y inv is corrected by its exact remainder, r + (y - r step) inv.
-// The result is the rounded quotient, but for quotients within 2^-46 of the middle
-// of two floats, where it may be the other one.  Three operations an element: the
-// IEEE division of every element set the kernel's time (4096 x 8192 to int8: 51.7 us
-// against 40.9 with this).  The remainder must not underflow, so steps below 2^-80 and
-// above 1e30 are divided by; a step that is zero, infinite or a NaN gives zeros.
-template <int kN>
-__device__ __forceinline__ void quotients(const float (&y)[kN], float step, float (&r)[kN]) {
-    if (step > 8.2718061e-25f && step < 1e30f) {
-        const float inv = __frcp_rn(step);
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            const float q = __fmul_rn(y[e], inv);
-            r[e] = __fmaf_rn(__fmaf_rn(-q, step, y[e]), inv, q);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < kN; ++e) r[e] = usable(step) ? __fdiv_rn(y[e], step) : 0.0f;
-    }
-}
-
-// The codes of one vector, in one store.
-template <int kN>
-__device__ __forceinline__ void store_codes(void *q, int64_t at, const float (&r)[kN], int kind) {
-    uint32_t w[kN / 4];
-#pragma unroll
-    for (int i = 0; i < kN / 4; ++i) {
-        if (kind == Q_I8) {
-            // |r| is clamped to 127 and 1.5 * 2^23 added: the sum rounds r to an integer, to
-            // nearest-even, whose two's complement is its low byte
-            uint32_t b[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                b[e] = __float_as_uint(fminf(fmaxf(r[4 * i + e], -127.0f), 127.0f) + 12582912.0f);
-            w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-        } else {
-            const __nv_fp8_interpretation_t t = kind == Q_E4M3 ? __NV_E4M3 : __NV_E5M2;
-            w[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(r[4 * i], r[4 * i + 1]), __NV_SATFINITE, t)) |
-                   static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(r[4 * i + 2], r[4 * i + 3]), __NV_SATFINITE, t))
-                       << 16;
-        }
-    }
-    if constexpr (kN == 8)
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(q) + at) = make_uint2(w[0], w[1]);
-    else
-        *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(q) + at) = w[0];
 }
 
 // One row a block, V vectors a thread.
