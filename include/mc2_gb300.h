@@ -487,7 +487,8 @@ int mc2_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int a
  * Returns MC2_OK or a negative mc2_status; nothing is launched on error.
  */
 int mc2_quant_matmul_workspace(const int8_t *x, int64_t ldx, const int8_t *w, int64_t ldw, int w_is_nk, int64_t m,
-                               int64_t n, int64_t k, size_t *bytes);
+                               int64_t n, int64_t k, const void *residual, int64_t ldr, const void *out, int64_t ldo,
+                               size_t *bytes);
 int mc2_quant_matmul(const int8_t *x, int64_t ldx, const float *x_scale, const int8_t *w, int64_t ldw, int w_is_nk,
                      const float *w_scale, int64_t m, int64_t n, int64_t k, const void *bias, int bias_dtype, int act,
                      const void *residual, int64_t ldr, int dtype, void *out, int64_t ldo, void *workspace,

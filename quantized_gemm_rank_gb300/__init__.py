@@ -111,7 +111,7 @@ def lib() -> ctypes.CDLL:
         L.mc2_matmul_act_grad.restype = _INT
         L.mc2_act_grad.argtypes = [_P, _I64, _P, _I64, _INT, _I64, _I64, _INT, _P, _I64, _P]
         L.mc2_act_grad.restype = _INT
-        L.mc2_quant_matmul_workspace.argtypes = [_P, _I64, _P, _I64, _INT, _I64, _I64, _I64,
+        L.mc2_quant_matmul_workspace.argtypes = [_P, _I64, _P, _I64, _INT, _I64, _I64, _I64, _P, _I64, _P, _I64,
                                                  ctypes.POINTER(ctypes.c_size_t)]
         L.mc2_quant_matmul_workspace.restype = _INT
         L.mc2_quant_matmul.argtypes = [_P, _I64, _P, _P, _I64, _INT, _P, _I64, _I64, _I64, _P, _INT, _INT, _P, _I64, _INT,
@@ -942,22 +942,26 @@ def mc2_quant_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_
     _need_device(cur)
     nbytes = ctypes.c_size_t(0)
     if workspace is None:
-        _check(lib().mc2_quant_matmul_workspace(xp, ldx, wp, ldw, w_is_nk, m, n, k, ctypes.byref(nbytes)))
+        _check(lib().mc2_quant_matmul_workspace(xp, ldx, wp, ldw, w_is_nk, m, n, k, rp, ldr, op, ldo,
+                                                ctypes.byref(nbytes)))
     workspace, ws, size = _workspace(workspace, nbytes.value, x.device, cur)
     _check(lib().mc2_quant_matmul(xp, ldx, xsp, wp, ldw, w_is_nk, wsp, m, n, k, bp, _dtype_code(bdt), act, rp, ldr, _dtype_code(dt),
                                   op, ldo, ws, size, _stream(stream, cur)))
     return out
 
 
-def mc2_quant_matmul_workspace(x: torch.Tensor, w: torch.Tensor, *, w_is_nk: bool = True) -> int:
-    """Bytes of workspace that mc2_quant_matmul needs for these matrices (0 for few tokens in aligned rows)."""
+def mc2_quant_matmul_workspace(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, *, w_is_nk: bool = True,
+                               residual: Optional[torch.Tensor] = None) -> int:
+    """Bytes of workspace that mc2_quant_matmul needs for these matrices."""
     cur = _current_device()
     m, k = _leading(x, "x"), x.shape[-1]
     n = w.shape[0] if w_is_nk else w.shape[1]
     xp, ldx = _rows(x, x.shape, torch.int8, "x", cur)
     wp, ldw = _rows(w, (n, k) if w_is_nk else (k, n), torch.int8, "w", cur)
+    op, ldo = _rows(out, (*x.shape[:-1], n), out.dtype, "out", cur)
+    rp, ldr = _opt_rows(residual, (*x.shape[:-1], n), out.dtype, "residual", cur)
     nbytes = ctypes.c_size_t(0)
-    _check(lib().mc2_quant_matmul_workspace(xp, ldx, wp, ldw, w_is_nk, m, n, k, ctypes.byref(nbytes)))
+    _check(lib().mc2_quant_matmul_workspace(xp, ldx, wp, ldw, w_is_nk, m, n, k, rp, ldr, op, ldo, ctypes.byref(nbytes)))
     return int(nbytes.value)
 
 

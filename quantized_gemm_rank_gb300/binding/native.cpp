@@ -451,7 +451,8 @@ PyObject *quant_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
         size_t need = 0, bytes = 0;
         const int8_t *xp = static_cast<int8_t *>(xr.p), *wp = static_cast<int8_t *>(wr.p);
         at::Tensor own;
-        if (a[10] == Py_None && mc2_quant_matmul_workspace(xp, xr.ld, wp, wr.ld, nk, m, cols, k, &need) != MC2_OK) return irregular();
+        if (a[10] == Py_None && mc2_quant_matmul_workspace(xp, xr.ld, wp, wr.ld, nk, m, cols, k, rr.p, rr.ld, outr.p, outr.ld, &need) != MC2_OK)
+            return irregular();
         if (!workspace(a[10], need, x, cur, own, wk, bytes)) return irregular();
         void *stream = handle(a[12]);
         const int st = unlocked([&] {

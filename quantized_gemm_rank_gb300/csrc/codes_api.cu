@@ -66,24 +66,51 @@ int check_workspace(const void *workspace, size_t given, size_t need) {
     return MC2_OK;
 }
 
-int check_product(int64_t ldx, int64_t ldw, int w_is_nk, int64_t m, int64_t n, int64_t k) {
+// The matrices of an int8 product.
+int check_product(const int8_t *x, int64_t ldx, const int8_t *w, int64_t ldw, int w_is_nk, int64_t m, int64_t n, int64_t k,
+                  const void *residual, int64_t ldr, const void *out, int64_t ldo, mc2::QuantProduct *p) {
     if (int st = check_sizes(m, n, k)) return st;
     if (k > kMostDepth) return fail(MC2_ERR_SHAPE, "k must be at most %lld, so that int32 holds any sum", (long long)kMostDepth);
-    if (int st = check_rows("x", nullptr, ldx, m, k, 1)) return st;
-    return check_rows("w", nullptr, ldw, w_is_nk ? n : k, w_is_nk ? k : n, 1);
+    if (!x || !w || !out) return fail(MC2_ERR_NULL, "x, w and out are required");
+    if (int st = check_rows("x", x, ldx, m, k, 1)) return st;
+    if (int st = check_rows("w", w, ldw, w_is_nk ? n : k, w_is_nk ? k : n, 1)) return st;
+    if (int st = check_rows("out", out, ldo, m, n, 2)) return st;
+    if (residual) {
+        if (int st = check_rows("residual", residual, ldr, m, n, 2)) return st;
+        if (residual == out && m > 1 && ldr != ldo)
+            return fail(MC2_ERR_SHAPE, "residual and out in one buffer need the same row stride");
+    }
+    p->x = x, p->w = w, p->residual = residual, p->out = const_cast<void *>(out);
+    p->ldx = ldx, p->ldw = ldw, p->ldr = ldr, p->ldo = ldo;
+    p->m = static_cast<int>(m), p->n = static_cast<int>(n), p->k = static_cast<int>(k);
+    p->w_nk = w_is_nk != 0;
+    return MC2_OK;
 }
+
+int check_weight_grad(const void *dy, int64_t lddy, const void *dw, int64_t m, int64_t n, int64_t k, mc2::QuantWeightGrad *p) {
+    if (int st = check_sizes(m, n, k)) return st;
+    if (!dy || !dw) return fail(MC2_ERR_NULL, "dy and dw are required");
+    if (int st = check_rows("dy", dy, lddy, m, n, 2)) return st;
+    if (int st = check_rows("dw", dw, k, n, k, 2)) return st;
+    p->dy = dy, p->dw = const_cast<void *>(dw), p->lddy = lddy;
+    p->m = static_cast<int>(m), p->n = static_cast<int>(n), p->k = static_cast<int>(k);
+    return MC2_OK;
+}
+
+// Each kernel of a call of several is marked as it is launched.
+void mark(void *marks) { static_cast<LaunchMarks *>(marks)->launched(); }
 
 }  // namespace
 
 extern "C" {
 
 int mc2_quant_matmul_workspace(const int8_t *x, int64_t ldx, const int8_t *w, int64_t ldw, int w_is_nk, int64_t m, int64_t n,
-                               int64_t k, size_t *bytes) {
+                               int64_t k, const void *residual, int64_t ldr, const void *out, int64_t ldo, size_t *bytes) {
     clear_error();
     if (!bytes) return fail(MC2_ERR_NULL, "bytes is NULL");
-    if (!x || !w) return fail(MC2_ERR_NULL, "x and w are required");
-    if (int st = check_product(ldx, ldw, w_is_nk, m, n, k)) return st;
-    *bytes = 0;
+    mc2::QuantProduct p = {};
+    if (int st = check_product(x, ldx, w, ldw, w_is_nk, m, n, k, residual, ldr, out, ldo, &p)) return st;
+    *bytes = mc2::quant_product_workspace(p);
     return MC2_OK;
 }
 
@@ -94,39 +121,27 @@ int mc2_quant_matmul(const int8_t *x, int64_t ldx, const float *x_scale, const i
     clear_error();
     if (int st = check_16bit(dtype)) return st;
     if (int st = check_act(act)) return st;
-    if (int st = check_product(ldx, ldw, w_is_nk, m, n, k)) return st;
-    if (!x || !x_scale || !w || !w_scale || !out) return fail(MC2_ERR_NULL, "x, x_scale, w, w_scale and out are required");
+    mc2::QuantProduct p = {};
+    if (int st = check_product(x, ldx, w, ldw, w_is_nk, m, n, k, residual, ldr, out, ldo, &p)) return st;
+    if (!x_scale || !w_scale) return fail(MC2_ERR_NULL, "x_scale and w_scale are required");
     if (int st = check_rows("x_scale", x_scale, m, 1, m, 4)) return st;
     if (int st = check_rows("w_scale", w_scale, n, 1, n, 4)) return st;
-    if (int st = check_rows("out", out, ldo, m, n, 2)) return st;
     if (bias) {
         if (bias_dtype != dtype && bias_dtype != MC2_F32)
             return fail(MC2_ERR_DTYPE, "the bias must be of the type of out or MC2_F32 (got %d)", bias_dtype);
         if (int st = check_rows("bias", bias, n, 1, n, elem_size(bias_dtype))) return st;
     }
-    if (residual) {
-        if (int st = check_rows("residual", residual, ldr, m, n, 2)) return st;
-        if (residual == out && m > 1 && ldr != ldo)
-            return fail(MC2_ERR_SHAPE, "residual and out in one buffer need the same row stride");
-    }
-    size_t need = 0;
-    if (int st = mc2_quant_matmul_workspace(x, ldx, w, ldw, w_is_nk, m, n, k, &need)) return st;
-    if (int st = check_workspace(workspace, workspace_bytes, need)) return st;
-
+    if (int st = check_workspace(workspace, workspace_bytes, mc2::quant_product_workspace(p))) return st;
     DeviceInfo dev;
     if (int st = current_device(&dev)) return st;
-    mc2::QuantProduct p = {};
-    p.x = x, p.w = w, p.x_scale = x_scale, p.w_scale = w_scale, p.bias = bias, p.residual = residual, p.out = out;
-    p.ldx = ldx, p.ldw = ldw, p.ldr = ldr, p.ldo = ldo;
-    p.m = static_cast<int>(m), p.n = static_cast<int>(n), p.k = static_cast<int>(k);
-    p.w_nk = w_is_nk != 0;
+    p.x_scale = x_scale, p.w_scale = w_scale, p.bias = bias;
     p.act = act;
     p.bias_f32 = bias_dtype == MC2_F32;
+    p.workspace = workspace;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     LaunchMarks marks(s);
-    cudaError_t e = mc2::launch_quant_product(dtype == MC2_BF16, p, s);
+    cudaError_t e = mc2::launch_quant_product(dtype == MC2_BF16, p, dev.num_sms, s, mark, &marks);
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "quant_matmul launch: %s", cudaGetErrorString(e));
-    marks.launched();
     return MC2_OK;
 }
 
@@ -193,11 +208,9 @@ int mc2_matmul_weight_grad_quant_workspace(const void *dy, int64_t lddy, const v
                                            size_t *bytes) {
     clear_error();
     if (!bytes) return fail(MC2_ERR_NULL, "bytes is NULL");
-    if (int st = check_sizes(m, n, k)) return st;
-    if (!dy || !dw) return fail(MC2_ERR_NULL, "dy and dw are required");
-    if (int st = check_rows("dy", dy, lddy, m, n, 2)) return st;
-    if (int st = check_rows("dw", dw, k, n, k, 2)) return st;
-    *bytes = 0;
+    mc2::QuantWeightGrad p = {};
+    if (int st = check_weight_grad(dy, lddy, dw, m, n, k, &p)) return st;
+    *bytes = mc2::quant_weight_grad_workspace(p);
     return MC2_OK;
 }
 
@@ -207,26 +220,19 @@ int mc2_matmul_weight_grad_quant(const void *dy, int64_t lddy, const void *q, co
     clear_error();
     if (int st = check_16bit(dtype)) return st;
     if (int st = check_act(act)) return st;
-    if (int st = check_sizes(m, n, k)) return st;
     mc2::QuantWeightGrad p = {};
+    if (int st = check_weight_grad(dy, lddy, dw, m, n, k, &p)) return st;
     if (int st = check_kept(q, scale, m, k, quant_mode, q_dtype, &p.x)) return st;
-    if (!dy || !dw) return fail(MC2_ERR_NULL, "dy and dw are required");
     if (db)
         if (int st = check_rows("db", db, n, 1, n, 2)) return st;
-    size_t need = 0;
-    if (int st = mc2_matmul_weight_grad_quant_workspace(dy, lddy, dw, m, n, k, &need)) return st;
-    if (int st = check_workspace(workspace, workspace_bytes, need)) return st;
-
+    if (int st = check_workspace(workspace, workspace_bytes, mc2::quant_weight_grad_workspace(p))) return st;
     DeviceInfo dev;
     if (int st = current_device(&dev)) return st;
-    p.dy = dy, p.dw = dw, p.db = db, p.lddy = lddy;
-    p.m = static_cast<int>(m), p.n = static_cast<int>(n), p.k = static_cast<int>(k);
-    p.act = act;
+    p.db = db, p.act = act, p.workspace = workspace;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     LaunchMarks marks(s);
-    cudaError_t e = mc2::launch_quant_weight_grad(dtype == MC2_BF16, p, s);
+    cudaError_t e = mc2::launch_quant_weight_grad(dtype == MC2_BF16, p, dev.num_sms, s, mark, &marks);
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "matmul_weight_grad_quant launch: %s", cudaGetErrorString(e));
-    marks.launched();
     return MC2_OK;
 }
 

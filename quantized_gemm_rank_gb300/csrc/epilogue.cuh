@@ -12,7 +12,10 @@ namespace mc2 {
 //   EPI_PLAIN     out = acc + bias
 //   EPI_FORWARD   z = acc + bias (the optional pre-activation output), out = act(z) (+ aux)
 //   EPI_BACKWARD  out = acc * act'(aux)
-enum EpiMode : int { EPI_PLAIN = 0, EPI_FORWARD = 1, EPI_BACKWARD = 2 };
+//   EPI_SCALED    z = float(acc) * scale of the row * scale of the column + bias, acc an exact
+//                 integer sum of 8-bit codes (held as fp16), out = act(z) (+ aux)
+//   EPI_SUMS      acc itself, in 32 bits: a part of a split contraction
+enum EpiMode : int { EPI_PLAIN = 0, EPI_FORWARD = 1, EPI_BACKWARD = 2, EPI_SCALED = 3, EPI_SUMS = 4 };
 
 template <bool kBF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -45,7 +48,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     }
 }
 
-// v: z of kN columns (EPI_FORWARD), or the product (EPI_BACKWARD); a: their aux, two
+// v: z of kN columns (EPI_FORWARD, EPI_SCALED), or the product (EPI_BACKWARD); a: their aux, two
 // columns a word.
 template <bool kBF16, int kEpi, int kN>
 __device__ __forceinline__ void epilogue(float (&v)[kN], const uint32_t (&a)[kN / 2], const Activation &act, bool has_aux) {
@@ -61,7 +64,7 @@ __device__ __forceinline__ void epilogue(float (&v)[kN], const uint32_t (&a)[kN 
     auto apply = [&](auto form) {
         Activation one = act;
         one.form = decltype(form)::value;
-        if constexpr (kEpi == EPI_FORWARD)
+        if constexpr (kEpi != EPI_BACKWARD)
             each([&](float2 z, float2) { return act2(z, one); });
         else
             each([&](float2 z, float2 x) { return __fmul2_rn(z, act_derivative2(x, one)); });
@@ -72,7 +75,7 @@ __device__ __forceinline__ void epilogue(float (&v)[kN], const uint32_t (&a)[kN 
         case CASE_SIGMOID: apply(std::integral_constant<int, CASE_SIGMOID>{}); break;
         default: break;
     }
-    if (kEpi == EPI_FORWARD && has_aux) each([](float2 z, float2 x) { return __fadd2_rn(z, x); });
+    if (kEpi != EPI_BACKWARD && has_aux) each([](float2 z, float2 x) { return __fadd2_rn(z, x); });
 }
 
 }  // namespace mc2

@@ -2,7 +2,9 @@
 #include <atomic>
 #include <chrono>
 #include "gemm_tcgen05.cuh"
+#include "host.h"
 #include "internal.h"
+#include "linear.h"
 
 namespace mc2 {
 
@@ -185,6 +187,31 @@ cudaError_t launch_gemm(GemmKind kind, int group, const GemmParams &p, int num_s
         }
     }
     return cudaErrorInvalidValue;
+}
+
+// dW (n, k) = dY^T @ X: A = dY^T read M-major from dY (m, n), B = X (m, k) N-major,
+// the contraction runs down the m rows of both; the same launch sums A's rows
+// over the contraction (the column sums of dY) into db
+cudaError_t launch_weight_grad_tiles(bool bf16, const void *dy, int64_t lddy, const void *x, int64_t ldx, int m, int n, int k, void *dw,
+                                     void *db, int num_sms, cudaStream_t stream) {
+    GemmParams p = {};
+    const int group = gemm_group_for(n);
+    bool ok = host::make_map16(&p.a_maps[0], dy, n, m, 64, kBK, lddy);
+    if (host::make_map16_nmajor3d(&p.b_map, x, k, m, kBK, (kBN / group) / 64, ldx))
+        p.b_3d = 1;
+    else
+        ok = ok && host::make_map16(&p.b_map, x, k, m, 64, kBK, ldx);
+    ok = ok && host::make_map16(&p.out_map, dw, k, n, 64, 32);
+    if (!ok) return cudaErrorInvalidValue;
+    p.num_a_maps = 1;
+    p.a_mode = A_SINGLE_MN;
+    p.b_mn_major = 1;
+    p.m = n, p.n = k, p.k = m;
+    p.kblock_tiles = 1024 / kBK;
+    p.out = dw;
+    p.colsum_out = db;
+    p.wait_limit_ns = host::kWaitLimitNs;
+    return launch_gemm(bf16 ? GEMM_BF16 : GEMM_F16, group, p, num_sms, stream);
 }
 
 int *device_status_word() {

@@ -164,6 +164,10 @@ struct GemmParams {
     CUtensorMap pre_map;   // the pre-activation output
     int has_aux, has_pre;
     Activation act;
+    const float *bias_f32;   // EPI_SCALED: (n), instead of bias16
+    // EPI_SUMS: the contraction in `splits` parts of split_blocks K blocks, each with a launch id of its own (part by
+    // part); out_map: fp32 [part][m][n], boxes of 32 x 32, 128-byte swizzle; colsum_out: fp32 [part][m]
+    int splits, split_blocks;
 };
 
 // ---------------------------------------------------------------------------
@@ -181,6 +185,7 @@ enum WorkKind : int { WORK_FULL = 0, WORK_WRITE = 1, WORK_FINISH = 2 };
 
 struct Work {
     int tile, kb0, kb1, kind;
+    int split = 0;   // EPI_SUMS: the part of the contraction
 };
 
 struct Schedule {
@@ -317,7 +322,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, con
 // answer lands in a two-slot ring in both CTAs, and every role of both CTAs
 // reads it there when it finishes that tile, then releases the slot on the
 // leader's barrier (one release per role).
-template <bool kDyn>
+template <bool kDyn, bool kSplit>
 struct TileWalk {
     const Schedule *sched;
     int wi;            // static: next schedule index
@@ -329,6 +334,18 @@ struct TileWalk {
     uint32_t full0;    // dynamic: the ring's arrival barriers (this CTA)
     uint32_t free0;    // dynamic: the ring's release barriers (the leader's, cluster address)
     bool releaser;     // this thread releases the slot for its role
+    int tiles;         // kSplit: tiles of a part of the contraction
+
+    // dynamic: the work of launch id `id`
+    __device__ __forceinline__ Work at(int id, const GemmParams &p) const {
+        const int blocks = (num_k + p.kblock_tiles - 1) / p.kblock_tiles;
+        if constexpr (kSplit) {
+            const int part = id / tiles;
+            return Work{id - part * tiles, part * p.split_blocks, min(blocks, (part + 1) * p.split_blocks), WORK_FULL, part};
+        } else {
+            return Work{id, 0, blocks, WORK_FULL};
+        }
+    }
 
     template <bool kPair>
     __device__ __forceinline__ bool next(Work &w, const GemmParams &p, volatile int *abort_flag) {
@@ -339,7 +356,7 @@ struct TileWalk {
         } else {
             if (tile < 0) {
                 tile = first_tile;
-                w = Work{tile, 0, (num_k + p.kblock_tiles - 1) / p.kblock_tiles, WORK_FULL};
+                w = at(tile, p);
                 return true;
             }
             const int j = reads & 1;
@@ -352,7 +369,7 @@ struct TileWalk {
             ++reads;
             if (!more) return false;
             tile = static_cast<int>(x) / (kPair ? 2 : 1);
-            w = Work{tile, 0, (num_k + p.kblock_tiles - 1) / p.kblock_tiles, WORK_FULL};
+            w = at(tile, p);
             return true;
         }
     }
@@ -373,7 +390,7 @@ __device__ __forceinline__ void store_row32_16(uint16_t *row_ptr, int n, int col
     }
 }
 
-// kDyn: one CTA pair launched per tile, balanced at run time by cluster launch
+// kDyn: one CTA pair launched per tile (and part, EPI_SUMS), balanced at run time by cluster launch
 // control (float path only: no stream-K tail).  kNarrow: see TileCfg (float
 // path, one CTA per tile, n <= 64).  kEpi: the epilogue's form (EpiMode); other
 // than EPI_PLAIN a float-path form.
@@ -421,7 +438,9 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
     Schedule sched;
     sched.init(cluster_id, num_clusters, num_tiles, p.sk_tiles, nkb);
     // every role walks its own copy
-    TileWalk<kDyn> walk0;
+    using Walk = TileWalk<kDyn, kEpi == EPI_SUMS>;
+    Walk walk0;
+    walk0.tiles = num_tiles;
     walk0.sched = &sched;
     walk0.wi = 0;
     walk0.tile = -1;
@@ -574,7 +593,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 if (++stage == S) stage = 0, phase ^= 1u;
             }
         };
-        TileWalk<kDyn> walk = walk0;
+        Walk walk = walk0;
         int asked = 0;   // kDyn: answers asked for (one per tile started)
         Work w;
         while (ok && walk.template next<kPair>(w, p, abort_flag)) {
@@ -648,7 +667,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
     } else if (warp == 1 && leader) {
         // ------------------------------------------------------------ MMA issuer
         const bool a_mn = p.a_mode == A_SINGLE_MN;
-        const uint32_t idesc = ptx::idesc_f16(kBF16 && !kIntPath, p.b_mn_major != 0, Cfg::kTileM, Cfg::kMmaN, a_mn);
+        const uint32_t idesc = ptx::idesc_f16(kBF16 && !kIntPath && kEpi != EPI_SCALED, p.b_mn_major != 0, Cfg::kTileM, Cfg::kMmaN, a_mn);
         // descriptors of stage 0, k-slice 0; later ones add to the address field
         // (>> 4 units): per 16-wide k-slice +2 (K-major: 32 bytes into the
         // swizzled row) or +128 (MN-major: 16 rows of 128 bytes), +stage bytes per stage
@@ -668,7 +687,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
         bool ok = true;
         uint32_t d_tmem = tmem_base;
         const uint32_t consumed0 = ptx::smem_u32(&consumed_bar[0]);
-        TileWalk<kDyn> walk = walk0;
+        Walk walk = walk0;
         Work w;
         while (ok && walk.template next<kPair>(w, p, abort_flag)) {
             const int kt_begin = w.kb0 * kblock, kt_end = min(num_k, w.kb1 * kblock);
@@ -742,7 +761,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
         int stage = 0;
         uint32_t consumed_parity = 0;  // bit s: parity of the next consumed_bar[s] phase
         bool ok = true;
-        TileWalk<kDyn> walk = walk0;
+        Walk walk = walk0;
         Work w;
         while (ok) {
             // the two warps take each tile together: with tiles obtained at run time
@@ -804,12 +823,23 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
             }
             const int col = mb * Cfg::kTileM + kBM * static_cast<int>(cr) + 64 * slab + 8 * c;
             if (g == 0 && col < p.m) {
-                uint4 o;
-                o.x = pack2<kBF16>(acc[0], acc[1]);
-                o.y = pack2<kBF16>(acc[2], acc[3]);
-                o.z = pack2<kBF16>(acc[4], acc[5]);
-                o.w = pack2<kBF16>(acc[6], acc[7]);
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.colsum_out) + col) = o;
+                if constexpr (kEpi == EPI_SUMS) {
+                    float *to = static_cast<float *>(p.colsum_out) + static_cast<int64_t>(w.split) * p.m + col;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (col + e < p.m) to[e] = acc[e];
+                } else {
+                    uint16_t *to = static_cast<uint16_t *>(p.colsum_out) + col;
+                    const uint32_t o[4] = {pack2<kBF16>(acc[0], acc[1]), pack2<kBF16>(acc[2], acc[3]), pack2<kBF16>(acc[4], acc[5]),
+                                           pack2<kBF16>(acc[6], acc[7])};
+                    if (col + 8 <= p.m && (reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (col + e < p.m) to[e] = static_cast<uint16_t>(o[e >> 1] >> ((e & 1) * 16));
+                    }
+                }
             }
         }
     } else if (warp == 2 && lane == 0 && p.gather) {
@@ -819,7 +849,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
         uint32_t consumed_parity = 0;  // bit s: parity of the next consumed_bar[s] phase
         int pending_stage = -1;        // stage whose store may still be reading shared memory
         bool ok = true;
-        TileWalk<kDyn> walk = walk0;
+        Walk walk = walk0;
         Work w;
         while (ok && walk.template next<kPair>(w, p, abort_flag)) {
             const int kt_begin = w.kb0 * p.kblock_tiles, kt_end = min(num_k, w.kb1 * p.kblock_tiles);
@@ -859,7 +889,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
         uint32_t skr_phase = 0;   // phase of this warp's stream-K partial barrier
         uint32_t aux_phase = 0;   // kEpi: bit i, the phase of aux_bar of buffer i
         (void)aux_phase;
-        TileWalk<kDyn> walk = walk0;
+        Walk walk = walk0;
         Work w;
         while (walk.template next<kPair>(w, p, abort_flag)) {
             int mb, nb;
@@ -909,9 +939,10 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 if (w.kb1 - w.kb0 > 1) {
                     // a deep contraction: the K blocks' sums are added in registers, and the total
                     // goes back to the last block's accumulator, from where the loop below takes it
-                    float sum[128];
+                    using sum_t = typename std::conditional<kEpi == EPI_SCALED, int32_t, float>::type;
+                    sum_t sum[128];
 #pragma unroll
-                    for (int i = 0; i < 128; ++i) sum[i] = 0.0f;
+                    for (int i = 0; i < 128; ++i) sum[i] = sum_t(0);
 #pragma unroll 1
                     for (int kb = w.kb0; kb < w.kb1; ++kb) {
                         if (!arrived()) {
@@ -926,7 +957,12 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                                 ptx::tmem_ld_32x32b_x16(tmem_base + lane_addr + (acc_iter & 1u) * kBN + half * 128 + c * 16, r);
                                 ptx::tmem_ld_wait16(r);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[c * 16 + i] = __fadd_rn(sum[c * 16 + i], __uint_as_float(r[i]));
+                                for (int i = 0; i < 16; ++i) {
+                                    if constexpr (kEpi == EPI_SCALED)
+                                        sum[c * 16 + i] += __float2int_rn(__uint_as_float(r[i]));
+                                    else
+                                        sum[c * 16 + i] = __fadd_rn(sum[c * 16 + i], __uint_as_float(r[i]));
+                                }
                             }
                         }
                         if (kb + 1 < w.kb1) {
@@ -939,7 +975,12 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                         for (int c = 0; c < 8; ++c) {
                             uint32_t r[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(sum[c * 16 + i]);
+                            for (int i = 0; i < 16; ++i) {
+                                if constexpr (kEpi == EPI_SCALED)
+                                    r[i] = __float_as_uint(__int2float_rn(sum[c * 16 + i]));
+                                else
+                                    r[i] = __float_as_uint(sum[c * 16 + i]);
+                            }
                             ptx::tmem_st_32x32b_x16(tmem_base + lane_addr + (acc_iter & 1u) * kBN + half * 128 + c * 16, r);
                         }
                         ptx::tmem_st_wait();
@@ -956,6 +997,33 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 }
                 const uint32_t b = acc_iter & 1u;
                 const uint32_t acc = tmem_base + lane_addr + b * kBN + half * 128;
+                if constexpr (kEpi == EPI_SUMS) {
+                    // 32 rows x 128 bytes a piece, through the warp's whole slab (128-byte swizzle), to this part's sums
+#pragma unroll 1
+                    for (int c = 0; c < pieces; ++c) {
+                        uint32_t r[32];
+                        ptx::tmem_ld_32x32b_x32(acc + 32 * c, r);
+                        ptx::tmem_ld_wait32(r);
+                        if (c == pieces - 1) release(b);
+                        if (lane == 0) ptx::bulk_wait_group_read<0>();
+                        __syncwarp();
+                        uint8_t *const to = epi_stage + (warp - 4) * kEpiSlabBytes + lane * 128;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4 *>(to + ((j ^ (lane & 7)) << 4)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_3d(&p.out_map, colh + 32 * c, row0, w.split, buf0);
+                            ptx::bulk_commit_group();
+                        }
+                    }
+                    if (pieces <= 0) release(b);
+                    ++acc_iter;
+                    continue;
+                }
+                const float row_scale = kEpi == EPI_SCALED && row < p.m ? p.x1_scale[row] : 0.0f;
+                const bool scales_whole = kEpi == EPI_SCALED && colh + 128 <= p.n && (reinterpret_cast<uintptr_t>(p.x2_scale) & 15u) == 0;
                 const bool bias_whole = p.bias16 != nullptr && colh + 128 <= p.n && (reinterpret_cast<uintptr_t>(p.bias16) & 15u) == 0;
                 // 32 outputs of this lane's row, rounded, to buffer i
                 auto put = [&](int i, const float (&v)[32]) {
@@ -996,6 +1064,26 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
                     }
                     if (c == pieces - 1) release(b);   // every sum has been read: the accumulator is free
+                    if constexpr (kEpi == EPI_SCALED) {
+                        const float *from = p.x2_scale + colh + 32 * c;
+                        if (scales_whole) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 t = __ldg(reinterpret_cast<const float4 *>(from) + j);
+                                const float t4[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) v[4 * j + i] = __fmul_rn(__fmul_rn(v[4 * j + i], row_scale), t4[i]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __fmul_rn(__fmul_rn(v[i], row_scale), __ldg(p.x2_scale + min(colh + 32 * c + i, p.n - 1)));
+                        }
+                        if (p.bias_f32 != nullptr) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __fadd_rn(v[i], __ldg(p.bias_f32 + min(colh + 32 * c + i, p.n - 1)));
+                        }
+                    }
                     if (bias_whole) {
                         const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias16) + colh + 32 * c);
 #pragma unroll

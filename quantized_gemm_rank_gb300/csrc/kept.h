@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 namespace mc2 {
@@ -35,10 +36,14 @@ struct QuantProduct {
     int w_nk;
     int act;
     int bias_f32;   // (otherwise of out's type)
+    void *workspace;
 };
-cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, cudaStream_t stream);
+size_t quant_product_workspace(const QuantProduct &p);
+// Kernels of a call, each followed by mark(ctx)
+using Mark = void (*)(void *ctx);
+cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, cudaStream_t stream, Mark mark, void *ctx);
 
-// dw (n, k) = dy^T act(q scale), db (n) = column sums of dy; x is (m, k)
+// dw (n, k) = dy^T act(q scale), db (n) = column sums of dy (or none); x is (m, k)
 struct QuantWeightGrad {
     const void *dy;
     void *dw, *db;
@@ -46,7 +51,9 @@ struct QuantWeightGrad {
     int64_t lddy;
     int m, n, k;
     int act;
+    void *workspace;
 };
-cudaError_t launch_quant_weight_grad(bool bf16, const QuantWeightGrad &p, cudaStream_t stream);
+size_t quant_weight_grad_workspace(const QuantWeightGrad &p);
+cudaError_t launch_quant_weight_grad(bool bf16, const QuantWeightGrad &p, int num_sms, cudaStream_t stream, Mark mark, void *ctx);
 
 }  // namespace mc2

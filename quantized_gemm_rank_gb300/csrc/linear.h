@@ -23,6 +23,10 @@ struct LinearParams {
     int w_nk;
     int act;        // ActKind
     int aux_mode;   // AuxMode
+    // a product of int8 codes: x and w are fp16 that hold them, out, aux and a 16-bit bias of the given type, and
+    // z = float(acc) x_scale w_scale + bias (the tiles only)
+    const float *x_scale, *w_scale;   // (m), (n)
+    int bias_f32;
 };
 
 // Any sizes and layouts, without tensor cores.
@@ -50,6 +54,21 @@ cudaError_t launch_linear_tiles(bool bf16, const LinearParams &p, cudaStream_t s
 cudaError_t launch_linear_split(bool bf16, const LinearParams &p, int num_sms, cudaStream_t stream);
 // Which of the two is expected to be faster for these sizes.
 bool linear_prefers_split(const LinearParams &p, int num_sms);
+
+// The sums of dy^T x, (n, k), over parts of the m rows, each to a matrix of its own in `parts` (fp32, rows ldp apart), and
+// dy's column sums to col_parts (splits, n) if given.  A part is split_blocks blocks of block_tiles 64-row stages; a
+// block's sum stays in one accumulator, blocks are added in fp32 to nearest.
+struct WeightGradParts {
+    const void *dy, *x;
+    float *parts, *col_parts;
+    int64_t lddy, ldx, ldp;
+    int m, n, k;
+    int splits, split_blocks, block_tiles;
+};
+cudaError_t launch_weight_grad_parts(bool bf16, const WeightGradParts &w, cudaStream_t stream);
+// The whole of it in 16 bits: dw (n, k) with rows of a multiple of 8 elements, dw 16-byte aligned; db (n) or none.
+cudaError_t launch_weight_grad_tiles(bool bf16, const void *dy, int64_t lddy, const void *x, int64_t ldx, int m, int n, int k, void *dw,
+                                     void *db, int num_sms, cudaStream_t stream);
 
 // dz = dy * act'(z), (m, n)
 struct ActGradParams {

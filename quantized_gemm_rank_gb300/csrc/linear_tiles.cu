@@ -26,7 +26,7 @@ cudaError_t launch_tiles(GemmParams &p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         ready_ctx = ctx;
     }
-    const int64_t tiles = ((p.m + Cfg::kTileM - 1ll) / Cfg::kTileM) * ((p.n + kBN - 1ll) / kBN);
+    const int64_t tiles = ((p.m + Cfg::kTileM - 1ll) / Cfg::kTileM) * ((p.n + kBN - 1ll) / kBN) * (kEpi == EPI_SUMS ? p.splits : 1);
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -74,15 +74,45 @@ cudaError_t launch_linear_tiles(bool bf16, const LinearParams &lp, cudaStream_t 
     p.num_a_maps = 1;
     p.a_mode = A_SINGLE;
     p.m = lp.m, p.n = lp.n, p.k = lp.k;
-    p.kblock_tiles = linear_tiles_block(lp.k);
     p.out = lp.out;
-    p.bias16 = lp.bias;
     p.act = activation_of(lp.act);
     p.wait_limit_ns = host::kWaitLimitNs;
     p.status = device_status_word();
+    if (lp.x_scale) {
+        p.kblock_tiles = 1024 / kBK;   // (an fp32 accumulator holds the sum of 1024 products of two int8 exactly)
+        p.x1_scale = lp.x_scale, p.x2_scale = lp.w_scale;
+        if (lp.bias_f32)
+            p.bias_f32 = static_cast<const float *>(lp.bias);
+        else
+            p.bias16 = lp.bias;
+        return bf16 ? launch_tiles<true, EPI_SCALED>(p, stream) : launch_tiles<false, EPI_SCALED>(p, stream);
+    }
+    p.kblock_tiles = linear_tiles_block(lp.k);
+    p.bias16 = lp.bias;
     if (lp.aux_mode == AUX_ACT_GRAD)
         return bf16 ? launch_tiles<true, EPI_BACKWARD>(p, stream) : launch_tiles<false, EPI_BACKWARD>(p, stream);
     return bf16 ? launch_tiles<true, EPI_FORWARD>(p, stream) : launch_tiles<false, EPI_FORWARD>(p, stream);
+}
+
+cudaError_t launch_weight_grad_parts(bool bf16, const WeightGradParts &w, cudaStream_t stream) {
+    GemmParams p = {};
+    bool ok = host::make_map16(&p.a_maps[0], w.dy, w.n, w.m, 64, kBK, w.lddy);
+    if (host::make_map16_nmajor3d(&p.b_map, w.x, w.k, w.m, kBK, kBN / 2 / 64, w.ldx))
+        p.b_3d = 1;
+    else
+        ok = ok && host::make_map16(&p.b_map, w.x, w.k, w.m, 64, kBK, w.ldx);
+    ok = ok && host::make_map32_parts(&p.out_map, w.parts, w.k, w.n, w.splits, w.ldp);
+    if (!ok) return cudaErrorInvalidValue;
+    p.num_a_maps = 1;
+    p.a_mode = A_SINGLE_MN;
+    p.b_mn_major = 1;
+    p.m = w.n, p.n = w.k, p.k = w.m;
+    p.kblock_tiles = w.block_tiles;
+    p.splits = w.splits, p.split_blocks = w.split_blocks;
+    p.colsum_out = w.col_parts;
+    p.wait_limit_ns = host::kWaitLimitNs;
+    p.status = device_status_word();
+    return bf16 ? launch_tiles<true, EPI_SUMS>(p, stream) : launch_tiles<false, EPI_SUMS>(p, stream);
 }
 
 }  // namespace mc2

@@ -13,6 +13,7 @@
 #include "gemm_tcgen05.cuh"
 #include "host.h"
 #include "internal.h"
+#include "linear.h"
 #include "mc2_gb300.h"
 
 namespace {
@@ -160,6 +161,17 @@ bool make_map16_nmajor3d(CUtensorMap *m, const void *base, uint64_t inner, uint6
     slot.map = *m;
     slot.used = true;
     return true;
+}
+
+bool make_map32_parts(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t parts, uint64_t pitch) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {inner, outer, parts};
+    cuuint64_t strides[2] = {pitch * 4, pitch * outer * 4};
+    cuuint32_t box[3] = {32, 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int current_device(DeviceInfo *info) {
@@ -497,31 +509,8 @@ int mc2_matmul_weight_grad(const void *dy, int64_t m, int64_t n, const void *x, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     LaunchMarks marks(s);
-    // dW (n, k) = dY^T @ X: A = dY^T read M-major from dY (m, n), B = X (m, k) N-major,
-    // the contraction runs down the m rows of both; the same launch sums A's rows
-    // over the contraction (the column sums of dY) into db
-    mc2::GemmParams p;
-    memset(&p, 0, sizeof(p));
-    if (!make_map16(&p.a_maps[0], dy, n, m, 64, mc2::kBK)) return fail(MC2_ERR_CUDA, "cuTensorMapEncodeTiled failed for dy");
-    const int wgroup = mc2::gemm_group_for(static_cast<int>(n));
-    if (make_map16_nmajor3d(&p.b_map, x, k, m, mc2::kBK, (mc2::kBN / wgroup) / 64))
-        p.b_3d = 1;
-    else if (!make_map16(&p.b_map, x, k, m, 64, mc2::kBK))
-        return fail(MC2_ERR_CUDA, "cuTensorMapEncodeTiled failed for x");
-    p.num_a_maps = 1;
-    p.a_mode = mc2::A_SINGLE_MN;
-    p.b_mn_major = 1;
-    p.m = static_cast<int>(n);
-    p.n = static_cast<int>(k);
-    p.k = static_cast<int>(m);
-    p.kblock_tiles = kKBlockTiles;
-    p.out = dw;
-    if (!make_map16(&p.out_map, p.out, static_cast<uint64_t>(p.n), static_cast<uint64_t>(p.m), 64, 32))
-        return fail(MC2_ERR_CUDA, "cuTensorMapEncodeTiled failed for the output");
-    p.colsum_out = db;
-    p.wait_limit_ns = kWaitLimitNs;
-    const int group = mc2::gemm_group_for(static_cast<int>(n));
-    e = mc2::launch_gemm(dtype == MC2_BF16 ? mc2::GEMM_BF16 : mc2::GEMM_F16, group, p, dev.num_sms, s);
+    e = mc2::launch_weight_grad_tiles(dtype == MC2_BF16, dy, n, x, k, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), dw, db,
+                                      dev.num_sms, s);
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "GEMM launch: %s", cudaGetErrorString(e));
     marks.launched();
     return MC2_OK;

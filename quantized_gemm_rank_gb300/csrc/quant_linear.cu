@@ -3,132 +3,323 @@
 //
 //   out[t, j] = act(float(sum_l x[t, l] W[l, j]) x_scale[t] w_scale[j] + bias[j]) + residual[t, j]
 //   dw[i, j]  = sum_t dy[t, i] act(q[t, j] scale),  db[i] = sum_t dy[t, i]
+//
+// The tensor cores take 16-bit operands (their int8 rate is a tenth of it here).  int8 codes are exact in fp16, and so are
+// the fp32 sums of 1024 of their products; act(q scale) is rounded to dy's type.  The operands of many rows are
+// brought to 16 bits in the workspace, each element once, and multiplied by the GEMM of gemm_tcgen05.cuh; matrices that the
+// tensor copies cannot take go through the workspace, too.
 #include "kept.h"
 
 #include "codes.cuh"
+#include "host.h"
+#include "linear.h"
 #include "sm103_ptx.cuh"
 
 namespace mc2 {
 
 namespace {
 
-// Any sizes, strides and alignments: a 64 x 64 tile a block, 4 x 4 outputs a thread, exact int32 sums.
-template <int kT>
-__global__ void __launch_bounds__(256) quant_product_any_kernel(const __grid_constant__ QuantProduct p, Activation act) {
-    using T = typename Elem<kT>::type;
-    __shared__ int xs[16][64 + 4], ws[16][64 + 4];
+constexpr int kThreads = 256;
+constexpr int kPairs = 76;   // CTA pairs of a GB300 (the plans, and so the workspace queries, ask no device)
+
+// A matrix of int8 and where it goes as fp16, in rows `pitch` apart (a multiple of 8).
+struct Widened {
+    const int8_t *src;
+    __half *dst;
+    int64_t ld, pitch, rows;
+    int64_t cols;
+    int64_t vectors;   // 16 columns each
+};
+
+// Four codes, as a word, to four halves: 0x6400 + u is the half 1024 + u, so with u = q + 128 it is 1152 too large.
+__device__ __forceinline__ uint2 widen4(uint32_t q) {
+    const uint32_t u = q ^ 0x80808080u;
+    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __half2half2(__ushort_as_half(0x6480));
+    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), k), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), k);
+    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+
+// Both operands of a product in one launch: blocks [0, first) widen a, the others b, 16 codes a thread at a time.
+__global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ Widened a, const __grid_constant__ Widened b, int first) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int n_tiles = (p.n + 63) / 64;
-    const int m0 = static_cast<int>(blockIdx.x / n_tiles) * 64, n0 = static_cast<int>(blockIdx.x % n_tiles) * 64;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < p.k; k0 += 16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = tid + 256 * i, r = e >> 4, c = e & 15;
-            xs[c][r] = (m0 + r < p.m && k0 + c < p.k) ? p.x[(m0 + r) * p.ldx + k0 + c] : 0;
-            if (p.w_nk) {
-                ws[c][r] = (n0 + r < p.n && k0 + c < p.k) ? p.w[(n0 + r) * p.ldw + k0 + c] : 0;
+    const bool is_a = static_cast<int>(blockIdx.x) < first;
+    const Widened &t = is_a ? a : b;
+    const int64_t block = is_a ? blockIdx.x : blockIdx.x - first, blocks = is_a ? first : gridDim.x - first;
+    const int64_t total = t.rows * t.vectors;
+    for (int64_t e = block * kThreads + threadIdx.x; e < total; e += blocks * kThreads) {
+        int64_t r = 0, v = e;
+        if (t.rows > 1) {
+            if (total <= UINT32_MAX) {
+                r = static_cast<uint32_t>(e) / static_cast<uint32_t>(t.vectors);
             } else {
-                const int kr = e >> 6, nc = e & 63;
-                ws[kr][nc] = (n0 + nc < p.n && k0 + kr < p.k) ? p.w[(k0 + kr) * p.ldw + n0 + nc] : 0;
+                r = e / t.vectors;
+            }
+            v = e - r * t.vectors;
+        }
+        const int8_t *from = t.src + r * t.ld + v * 16;
+        const int64_t left = t.cols - v * 16;
+        uint32_t q[4];
+        if (left >= 16 && (reinterpret_cast<uintptr_t>(from) & 15u) == 0) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(from));
+            q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                q[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * i + j < left) q[i] |= static_cast<uint32_t>(static_cast<uint8_t>(from[4 * i + j])) << (8 * j);
             }
         }
-        __syncthreads();
+        uint4 *to = reinterpret_cast<uint4 *>(t.dst + r * t.pitch + v * 16);
 #pragma unroll
-        for (int l = 0; l < 16; ++l)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += xs[l][ty * 4 + i] * ws[l][tx * 4 + j];
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
-            if (r >= p.m || c >= p.n) continue;
-            float z = __fmul_rn(__fmul_rn(__int2float_rn(acc[i][j]), p.x_scale[r]), p.w_scale[c]);
-            if (p.bias) z = __fadd_rn(z, p.bias_f32 ? static_cast<const float *>(p.bias)[c] : Elem<kT>::load(static_cast<const T *>(p.bias) + c));
-            float o = act2(both(z), act).x;
-            if (p.residual) o = __fadd_rn(o, Elem<kT>::load(static_cast<const T *>(p.residual) + r * p.ldr + c));
-            Elem<kT>::store(static_cast<T *>(p.out) + r * p.ldo + c, o);
+        for (int i = 0; i < 2; ++i) {
+            const uint2 lo = widen4(q[2 * i]), hi = widen4(q[2 * i + 1]);
+            if (8 * i < left) to[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);   // (a row ends inside its pitch, a multiple of 8)
         }
+    }
 }
 
-// The same for the weight gradient; the blocks of the first column of tiles sum dy.
-template <int kT>
-__global__ void __launch_bounds__(256) quant_weight_grad_any_kernel(const __grid_constant__ QuantWeightGrad p, Activation act) {
-    using T = typename Elem<kT>::type;
-    __shared__ float ds[16][64 + 4], xs[16][64 + 4];
+// Rows of 16-bit elements from one layout to another, element by element.
+__global__ void __launch_bounds__(kThreads) copy_rows_kernel(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd, int64_t rows, int cols) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int k_tiles = (p.k + 63) / 64;
-    const int i0 = static_cast<int>(blockIdx.x / k_tiles) * 64, j0 = static_cast<int>(blockIdx.x % k_tiles) * 64;
-    float acc[4][4] = {}, sum = 0.0f;
-    for (int t0 = 0; t0 < p.m; t0 += 16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = tid + 256 * i, t = e >> 6, c = e & 63;
-            const int64_t row = t0 + t;
-            ds[t][c] = (row < p.m && i0 + c < p.n) ? Elem<kT>::load(static_cast<const T *>(p.dy) + row * p.lddy + i0 + c) : 0.0f;
-            float v = 0.0f;
-            if (row < p.m && j0 + c < p.k)
-                v = act2(both(decode8(static_cast<const uint8_t *>(p.x.q)[row * p.k + j0 + c], p.x.qkind) *
-                              scale_at(p.x.scale, p.x.qmode, row, p.k, j0 + c)), act).x;
-            xs[t][c] = v;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int l = 0; l < 16; ++l) {
-            if (tid < 64) sum += ds[l][tid];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ds[l][ty * 4 + i], xs[l][tx * 4 + j], acc[i][j]);
-        }
-        __syncthreads();
-    }
-    if (p.db && j0 == 0 && tid < 64 && i0 + tid < p.n) Elem<kT>::store(static_cast<T *>(p.db) + i0 + tid, sum);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = i0 + ty * 4 + i, c = j0 + tx * 4 + j;
-            if (r < p.n && c < p.k) Elem<kT>::store(static_cast<T *>(p.dw) + r * p.k + c, acc[i][j]);
-        }
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int c = threadIdx.x; c < cols; c += kThreads) dst[r * ldd + c] = src[r * lds + c];
 }
 
-template <class P>
-cudaError_t launch(void (*kern)(P, Activation), int64_t tiles, const P &p, int act, cudaStream_t stream) {
-    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+// dw and db from the parts' sums, added in order.  Four columns a thread; rows of dw are k elements, of a part ldp.
+template <bool kBF16>
+__global__ void __launch_bounds__(kThreads) add_parts_kernel(const float *parts, int64_t ldp, int splits, int n, int k, void *dw,
+                                                             const float *col_parts, void *db, int dw_blocks) {
+    using T = typename Elem<kBF16 ? ELEM_BF16 : ELEM_F16>::type;
+    using E = Elem<kBF16 ? ELEM_BF16 : ELEM_F16>;
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    if (static_cast<int>(blockIdx.x) >= dw_blocks) {
+        for (int i = (blockIdx.x - dw_blocks) * kThreads + threadIdx.x; i < n; i += (gridDim.x - dw_blocks) * kThreads) {
+            float s = 0.0f;
+            for (int p = 0; p < splits; ++p) s = __fadd_rn(s, col_parts[static_cast<int64_t>(p) * n + i]);
+            E::store(static_cast<T *>(db) + i, s);
+        }
+        return;
+    }
+    const int64_t quads = (k + 3) / 4, total = quads * n, part = ldp * n;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; e < total; e += static_cast<int64_t>(dw_blocks) * kThreads) {
+        const int64_t r = e / quads;
+        const int c = static_cast<int>(e - r * quads) * 4;
+        const float4 *from = reinterpret_cast<const float4 *>(parts + r * ldp + c);
+        float4 s = *from;
+        for (int p = 1; p < splits; ++p) {
+            const float4 t = from[p * (part / 4)];
+            s.x = __fadd_rn(s.x, t.x), s.y = __fadd_rn(s.y, t.y), s.z = __fadd_rn(s.z, t.z), s.w = __fadd_rn(s.w, t.w);
+        }
+        T *to = static_cast<T *>(dw) + r * k + c;
+        const float v[4] = {s.x, s.y, s.z, s.w};
+        if (c + 4 <= k && (reinterpret_cast<uintptr_t>(to) & 7u) == 0) {
+            T o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) E::store(&o[i], v[i]);
+            *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c + i < k) E::store(to + i, v[i]);
+        }
+    }
+}
+
+template <class... A>
+cudaError_t launch(void (*kern)(A...), int64_t grid, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles), 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, activation_of(act));
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-int64_t tiles64(int a, int b) { return ((a + 63ll) / 64) * ((b + 63ll) / 64); }
+int64_t blocks_for(int64_t items, int num_sms) {
+    const int64_t blocks = (items + kThreads - 1) / kThreads, most = 32ll * num_sms;
+    return blocks < 1 ? 1 : (blocks < most ? blocks : most);
+}
+
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// What the tensor copies take: 16-byte aligned, rows a multiple of 16 bytes (and less than 2^40) apart; writes go in units of
+// 16 bytes, so an output's rows are whole units.
+bool copies_read16(const void *p, int64_t ld, int64_t rows) {
+    return host::aligned16(p) && (rows == 1 || (ld % 8 == 0 && ld < (1ll << 39)));
+}
+bool copies_write16(const void *p, int64_t ld, int64_t rows, int64_t cols) { return copies_read16(p, ld, rows) && cols % 8 == 0; }
+
+// Pieces of a workspace, 256-byte aligned to one another.
+struct Pieces {
+    size_t total = 0;
+    size_t take(int64_t elems, size_t size) {
+        const size_t at = total;
+        total += (static_cast<size_t>(elems) * size + 255) / 256 * 256;
+        return at;
+    }
+};
+
+struct ProductPlan {
+    size_t x = 0, w = 0, out = 0, total = 0;
+    bool out_apart = false;    // the output goes through the workspace
+    bool residual_in = false;  // the residual is copied to where the output will be
+};
+
+ProductPlan plan_product(const QuantProduct &p) {
+    ProductPlan at;
+    Pieces ws;
+    at.x = ws.take(p.m * up8(p.k), 2);
+    at.w = p.w_nk ? ws.take(p.n * up8(p.k), 2) : ws.take(p.k * up8(p.n), 2);
+    at.out_apart = !copies_write16(p.out, p.ldo, p.m, p.n);
+    at.residual_in = p.residual && (at.out_apart || !copies_read16(p.residual, p.ldr, p.m));
+    if (at.out_apart) at.out = ws.take(p.m * up8(p.n), 2);
+    at.total = ws.total;
+    return at;
+}
+
+// A contraction over m rows for few outputs is split: parts of it on CTA pairs that would have no tile, and their sums added by
+// a kernel of their own.  In us: 6.3 and 0.29 a 64-row stage for each wave of tiles (as in linear_prefers_split), and for the parts their
+// bytes, written and read, at 5000 a ns, and a launch.
+struct WeightPlan {
+    size_t x = 0, dy = 0, parts = 0, col_parts = 0, total = 0;
+    bool dy_apart = false, in_parts = false;
+    int splits = 1, split_blocks = 1, block_tiles = 16;
+};
+
+WeightPlan plan_weight_grad(const QuantWeightGrad &p) {
+    WeightPlan at;
+    const int64_t tiles = ((p.n + 255ll) / 256) * ((p.k + 255ll) / 256);
+    const int steps = (p.m + 63) / 64;
+    const bool whole = copies_write16(p.dw, p.k, p.n, p.k);
+    float best = 0.0f;
+    for (int s = 1; s <= 32 && s <= steps; ++s) {
+        const float waves = static_cast<float>((tiles * s + kPairs - 1) / kPairs);
+        float us = 6.3f + 0.29f * waves * static_cast<float>((steps + s - 1) / s);
+        if (s > 1 || !whole) us += 3.0f + static_cast<float>(s) * static_cast<float>(p.n) * static_cast<float>(p.k) * 8.0f / 5.0e6f;
+        if (s == 1 || us < best) best = us, at.splits = s;
+    }
+    at.in_parts = at.splits > 1 || !whole;
+    if (at.in_parts) {
+        // equal blocks of at most 1024 rows, a whole number of them a part
+        const int each = (steps + at.splits - 1) / at.splits;
+        at.split_blocks = (each + 15) / 16;
+        at.block_tiles = (each + at.split_blocks - 1) / at.split_blocks;
+        const int blocks = (steps + at.block_tiles - 1) / at.block_tiles;
+        at.splits = (blocks + at.split_blocks - 1) / at.split_blocks;
+    }
+    Pieces ws;
+    at.x = ws.take(p.m * up8(p.k), 2);
+    at.dy_apart = !copies_read16(p.dy, p.lddy, p.m);
+    if (at.dy_apart) at.dy = ws.take(p.m * up8(p.n), 2);
+    if (at.in_parts) {
+        at.parts = ws.take(static_cast<int64_t>(at.splits) * p.n * ((p.k + 3ll) / 4 * 4), 4);
+        at.col_parts = ws.take(static_cast<int64_t>(at.splits) * p.n, 4);
+    }
+    at.total = ws.total;
+    return at;
+}
 
 }  // namespace
 
-cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, cudaStream_t stream) {
-    return launch(bf16 ? quant_product_any_kernel<ELEM_BF16> : quant_product_any_kernel<ELEM_F16>, tiles64(p.m, p.n), p, p.act, stream);
+size_t quant_product_workspace(const QuantProduct &p) { return plan_product(p).total; }
+
+cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, cudaStream_t stream, Mark mark, void *ctx) {
+    const ProductPlan at = plan_product(p);
+    char *ws = static_cast<char *>(p.workspace);
+    __half *xh = reinterpret_cast<__half *>(ws + at.x), *wh = reinterpret_cast<__half *>(ws + at.w);
+    const auto widened = [](const int8_t *src, int64_t ld, __half *dst, int64_t rows, int64_t cols) {
+        Widened t = {src, dst, ld, up8(cols), rows, cols, (cols + 15) / 16};
+        // matrices without gaps are one row
+        if (rows > 1 && ld == cols && cols % 8 == 0) t.cols = rows * cols, t.rows = 1, t.vectors = (t.cols + 15) / 16;
+        return t;
+    };
+    const Widened a = widened(p.x, p.ldx, xh, p.m, p.k);
+    const Widened b = p.w_nk ? widened(p.w, p.ldw, wh, p.n, p.k) : widened(p.w, p.ldw, wh, p.k, p.n);
+    // blocks in proportion to the elements
+    const int64_t na = a.rows * a.vectors, nb = b.rows * b.vectors, blocks = blocks_for(na + nb, num_sms) + 1;
+    int64_t first = static_cast<int64_t>(static_cast<double>(blocks) * na / (na + nb) + 0.5);
+    first = first < 1 ? 1 : (first > blocks - 1 ? blocks - 1 : first);
+    cudaError_t e = launch(widen_kernel, blocks, stream, a, b, static_cast<int>(first));
+    if (e != cudaSuccess) return e;
+    mark(ctx);
+    void *out = at.out_apart ? static_cast<void *>(ws + at.out) : p.out;
+    const int64_t ldo = at.out_apart || p.m == 1 ? up8(p.n) : p.ldo;
+    if (at.residual_in) {
+        e = launch(copy_rows_kernel, p.m < 4096 ? p.m : 4096, stream, static_cast<const uint16_t *>(p.residual), p.ldr,
+                   static_cast<uint16_t *>(out), ldo, static_cast<int64_t>(p.m), p.n);
+        if (e != cudaSuccess) return e;
+        mark(ctx);
+    }
+    LinearParams l = {};
+    l.x = xh, l.w = wh, l.bias = p.bias, l.out = out;
+    l.aux = at.residual_in ? out : p.residual;
+    l.ldx = up8(p.k), l.ldw = p.w_nk ? up8(p.k) : up8(p.n), l.ldo = ldo;
+    l.ldaux = at.residual_in ? ldo : (p.m == 1 ? up8(p.n) : p.ldr);
+    l.m = p.m, l.n = p.n, l.k = p.k;
+    l.w_nk = p.w_nk;
+    l.act = p.act;
+    l.aux_mode = p.residual ? AUX_RESIDUAL : AUX_NONE;
+    l.x_scale = p.x_scale, l.w_scale = p.w_scale, l.bias_f32 = p.bias_f32;
+    e = launch_linear_tiles(bf16, l, stream);
+    if (e != cudaSuccess) return e;
+    mark(ctx);
+    if (at.out_apart) {
+        e = launch(copy_rows_kernel, p.m < 4096 ? p.m : 4096, stream, static_cast<const uint16_t *>(out), ldo, static_cast<uint16_t *>(p.out),
+                   p.ldo, static_cast<int64_t>(p.m), p.n);
+        if (e != cudaSuccess) return e;
+        mark(ctx);
+    }
+    return cudaSuccess;
 }
 
-cudaError_t launch_quant_weight_grad(bool bf16, const QuantWeightGrad &p, cudaStream_t stream) {
-    return launch(bf16 ? quant_weight_grad_any_kernel<ELEM_BF16> : quant_weight_grad_any_kernel<ELEM_F16>, tiles64(p.n, p.k), p, p.act,
-                  stream);
+size_t quant_weight_grad_workspace(const QuantWeightGrad &p) { return plan_weight_grad(p).total; }
+
+cudaError_t launch_quant_weight_grad(bool bf16, const QuantWeightGrad &p, int num_sms, cudaStream_t stream, Mark mark, void *ctx) {
+    const WeightPlan at = plan_weight_grad(p);
+    char *ws = static_cast<char *>(p.workspace);
+    const int64_t ldx = up8(p.k);
+    cudaError_t e = launch_act_dequant(bf16 ? ELEM_BF16 : ELEM_F16, p.x, p.act, ws + at.x, ldx, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    mark(ctx);
+    const void *dy = p.dy;
+    int64_t lddy = p.m == 1 ? up8(p.n) : p.lddy;
+    if (at.dy_apart) {
+        dy = ws + at.dy, lddy = up8(p.n);
+        e = launch(copy_rows_kernel, p.m < 4096 ? p.m : 4096, stream, static_cast<const uint16_t *>(p.dy), p.lddy,
+                   reinterpret_cast<uint16_t *>(ws + at.dy), lddy, static_cast<int64_t>(p.m), p.n);
+        if (e != cudaSuccess) return e;
+        mark(ctx);
+    }
+    if (!at.in_parts) {
+        e = launch_weight_grad_tiles(bf16, dy, lddy, ws + at.x, ldx, p.m, p.n, p.k, p.dw, p.db, num_sms, stream);
+        if (e == cudaSuccess) mark(ctx);
+        return e;
+    }
+    WeightGradParts w = {};
+    w.dy = dy, w.x = ws + at.x, w.parts = reinterpret_cast<float *>(ws + at.parts);
+    w.col_parts = p.db ? reinterpret_cast<float *>(ws + at.col_parts) : nullptr;
+    w.lddy = lddy, w.ldx = ldx, w.ldp = (p.k + 3ll) / 4 * 4;
+    w.m = p.m, w.n = p.n, w.k = p.k;
+    w.splits = at.splits, w.split_blocks = at.split_blocks, w.block_tiles = at.block_tiles;
+    e = launch_weight_grad_parts(bf16, w, stream);
+    if (e != cudaSuccess) return e;
+    mark(ctx);
+    const int64_t dw_blocks = blocks_for(p.n * ((p.k + 3ll) / 4), num_sms), db_blocks = p.db ? (p.n + kThreads - 1) / kThreads : 0;
+    e = launch(bf16 ? add_parts_kernel<true> : add_parts_kernel<false>, dw_blocks + db_blocks, stream, static_cast<const float *>(w.parts), w.ldp,
+               at.splits, p.n, p.k, p.dw, static_cast<const float *>(w.col_parts), p.db, static_cast<int>(dw_blocks));
+    if (e == cudaSuccess) mark(ctx);
+    return e;
 }
 
 }  // namespace mc2

@@ -290,6 +290,14 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, int32_t c0, i
                  : "memory");
 }
 
+// The same of three coordinates.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int32_t c0, int32_t c1, int32_t c2, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 template <int N>

@@ -86,16 +86,25 @@ def test_each_call_rejects(call, kw, status):
 def test_workspace_queries():
     L, n = mc2.lib(), ctypes.c_size_t(1)
     ref = ctypes.byref(n)
-    assert L.mc2_quant_matmul_workspace(FAKE, 64, FAKE, 64, 1, 4, 32, 64, ref) == mc2.MC2_OK
-    for a, status in (((None, 64, FAKE, 64, 1, 4, 32, 64, ref), mc2.MC2_ERR_NULL), ((FAKE, 64, FAKE, 64, 1, 4, 32, 64, None), mc2.MC2_ERR_NULL),
-                      ((FAKE, 64, FAKE, 64, 1, 0, 32, 64, ref), mc2.MC2_ERR_SHAPE), ((FAKE, 8, FAKE, 64, 1, 4, 32, 64, ref), mc2.MC2_ERR_SHAPE)):
-        assert L.mc2_quant_matmul_workspace(*a) == status
+    f = L.mc2_quant_matmul_workspace
+    good = (FAKE, 64, FAKE, 64, 1, 400, 32, 64, None, 0, FAKE, 32, ref)
+    assert f(*good) == mc2.MC2_OK and n.value > 0
+    for at, value, status in ((0, None, mc2.MC2_ERR_NULL), (2, None, mc2.MC2_ERR_NULL), (10, None, mc2.MC2_ERR_NULL), (12, None, mc2.MC2_ERR_NULL),
+                              (5, 0, mc2.MC2_ERR_SHAPE), (1, 8, mc2.MC2_ERR_SHAPE), (11, 31, mc2.MC2_ERR_SHAPE)):
+        assert f(*good[:at], value, *good[at + 1:]) == status
     f = L.mc2_matmul_weight_grad_quant_workspace
-    assert f(FAKE, 32, FAKE, 4, 32, 64, ref) == mc2.MC2_OK
-    for a, status in (((None, 32, FAKE, 4, 32, 64, ref), mc2.MC2_ERR_NULL), ((FAKE, 32, None, 4, 32, 64, ref), mc2.MC2_ERR_NULL),
-                      ((FAKE, 32, FAKE, 4, 32, 64, None), mc2.MC2_ERR_NULL), ((FAKE, 32, FAKE, 4, 32, 0, ref), mc2.MC2_ERR_SHAPE),
-                      ((FAKE, 31, FAKE, 4, 32, 64, ref), mc2.MC2_ERR_SHAPE)):
-        assert f(*a) == status
+    good = (FAKE, 32, FAKE, 4, 32, 64, ref)
+    assert f(*good) == mc2.MC2_OK and n.value > 0
+    for at, value, status in ((0, None, mc2.MC2_ERR_NULL), (2, None, mc2.MC2_ERR_NULL), (6, None, mc2.MC2_ERR_NULL), (5, 0, mc2.MC2_ERR_SHAPE),
+                              (1, 31, mc2.MC2_ERR_SHAPE)):
+        assert f(*good[:at], value, *good[at + 1:]) == status
+
+
+@pytest.mark.parametrize("kw", [dict(wk=None), dict(nbytes=64)])
+def test_a_workspace_that_is_missing_or_small(kw):
+    assert product(**kw) == mc2.MC2_ERR_WORKSPACE
+    assert weight(**kw) == mc2.MC2_ERR_WORKSPACE
+    assert product(wk=FAKE + 8) == mc2.MC2_ERR_UNSUPPORTED and weight(wk=FAKE + 8) == mc2.MC2_ERR_UNSUPPORTED
 
 
 def refuses(match, f, *a, **kw):
