@@ -143,10 +143,41 @@ __device__ __forceinline__ float mx_value(uint32_t code) {
     return code == 0xFFu ? __int_as_float(0x7FC00000) : __uint_as_float(code == 0 ? 0x00400000u : code << 23);
 }
 
-// The scale of column j of a row of h codes, by quant mode.
-__device__ __forceinline__ float scale_at(const void *scale, int qmode, int64_t row, int h, int j) {
-    if (qmode == QM_TOKEN) return static_cast<const float *>(scale)[row];
-    if (qmode == QM_GROUP) return static_cast<const float *>(scale)[row * ((h + 127) / 128) + j / 128];
+// Eight codes, of two words, to their values.
+__device__ __forceinline__ void decode_codes(uint2 w, int kind, float (&v)[8]) {
+    const uint32_t words[2] = {w.x, w.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (kind == Q_I8) {
+            // 0x4B000000 + u is the float 2^23 + u: with u = q + 128 it is 2^23 + 128 too large
+            const uint32_t u = words[i] ^ 0x80808080u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * i + e] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540 + e)) - 8388736.0f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float2 f;
+                if (kind == Q_E5M2) {   // the upper byte of a half
+                    const uint32_t h = __byte_perm(words[i], 0, e ? 0x3424 : 0x1404);
+                    f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                } else {
+                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(words[i] >> (16 * e)), __NV_E4M3);
+                    f = __half22float2(__half2(h));
+                }
+                v[4 * i + 2 * e] = f.x, v[4 * i + 2 * e + 1] = f.y;
+            }
+        }
+    }
+}
+
+// Columns of a group that share a scale.
+__host__ __device__ __forceinline__ int group_size(int qmode) { return qmode == QM_MX ? 32 : 128; }
+
+// The scale of column j of a row of h codes.
+template <int kQM>
+__device__ __forceinline__ float scale_at(const void *scale, int64_t row, int h, int j) {
+    if constexpr (kQM == QM_TOKEN) return static_cast<const float *>(scale)[row];
+    if constexpr (kQM == QM_GROUP) return static_cast<const float *>(scale)[row * ((h + 127) / 128) + j / 128];
     return mx_value(static_cast<const uint8_t *>(scale)[row * ((h + 31) / 32) + j / 32]);
 }
 

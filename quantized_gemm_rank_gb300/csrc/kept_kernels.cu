@@ -3,7 +3,8 @@
 //   y = act(z),  scale = max|y| (1 / Q) over a row or a group,  q = y / scale to nearest-even    (act_quant)
 //   out = act(q scale)                                                                           (act_dequant)
 //   dz = dy act'(q scale)                                                                        (act_grad_quant)
-// Arithmetic is fp32; codes and outputs are rounded once.
+// Arithmetic is fp32; codes and outputs are rounded once.  All of them are bound by memory: each element is read once, eight
+// at a time (16 bytes of a 16-bit matrix, 8 of codes).
 #include "kept.h"
 
 #include "codes.cuh"
@@ -15,6 +16,315 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 8;   // elements a thread takes at a time
+
+// f(activation with its form a constant): the choice is made once for all of a thread's elements.
+template <class F>
+__device__ __forceinline__ void with_form(const Activation &act, F f) {
+    Activation one = act;
+    switch (act.form) {   // the same in every thread
+        case CASE_RELU: one.form = CASE_RELU; f(one); break;
+        case CASE_ERF: one.form = CASE_ERF; f(one); break;
+        case CASE_SIGMOID: one.form = CASE_SIGMOID; f(one); break;
+        default: one.form = CASE_NONE; f(one); break;
+    }
+}
+
+__device__ __forceinline__ void apply_act(float (&y)[kChunk], const Activation &act) {
+    with_form(act, [&](const Activation &one) {
+#pragma unroll
+        for (int e = 0; e < kChunk; e += 2) {
+            const float2 v = act2(make_float2(y[e], y[e + 1]), one);
+            y[e] = v.x, y[e + 1] = v.y;
+        }
+    });
+}
+
+__device__ __forceinline__ void times_derivative(float (&d)[kChunk], const float (&z)[kChunk], const Activation &act) {
+    with_form(act, [&](const Activation &one) {
+#pragma unroll
+        for (int e = 0; e < kChunk; e += 2) {
+            const float2 v = __fmul2_rn(make_float2(d[e], d[e + 1]), act_derivative2(make_float2(z[e], z[e + 1]), one));
+            d[e] = v.x, d[e + 1] = v.y;
+        }
+    });
+}
+
+// Eight elements, as the 16-byte words they are in memory.
+template <int kT>
+struct Raw {
+    uint4 v[kT == ELEM_F32 ? 2 : 1];
+};
+
+template <int kT>
+__device__ __forceinline__ Raw<kT> load_raw(const void *p) {
+    Raw<kT> r;
+    r.v[0] = load_once(p);
+    if constexpr (kT == ELEM_F32) r.v[1] = load_once(static_cast<const char *>(p) + 16);
+    return r;
+}
+
+template <int kT>
+__device__ __forceinline__ void values(const Raw<kT> &r, float (&f)[kChunk]) {
+    if constexpr (kT == ELEM_F32) {
+        float a[4], b[4];
+        unpack<kT>(r.v[0], a);
+        unpack<kT>(r.v[1], b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+    } else {
+        unpack<kT>(r.v[0], f);
+    }
+}
+
+template <int kT>
+__device__ __forceinline__ void store_values(void *p, const float (&f)[kChunk]) {
+    uint4 *to = static_cast<uint4 *>(p);
+    if constexpr (kT == ELEM_F32) {
+        const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
+        to[0] = pack<kT>(a), to[1] = pack<kT>(b);
+    } else {
+        to[0] = pack<kT>(f);
+    }
+}
+
+__device__ __forceinline__ uint2 load_codes(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(reinterpret_cast<uint64_t>(p)));
+    return v;
+}
+
+// How a launch covers a matrix: a thread keeps one chunk of columns and goes down the rows; a row takes `lanes` threads of
+// a block (a power of two), a block kThreads / lanes rows at a time.
+struct Cover {
+    int lanes_log2;
+    int chunks;   // of a row
+};
+
+// ------------------------------------------------------------------ from codes
+// Rows of whole chunks: every access is a whole one.  kRows rows of a thread are on their way at once.
+template <int kT, bool kGrad, int kQM, int kRows>
+__global__ void __launch_bounds__(kThreads) from_kept_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p, Activation act,
+                                                             void *out, int64_t ldo, Cover cover) {
+    constexpr int kE = kT == ELEM_F32 ? 4 : 2;
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    const int lanes = 1 << cover.lanes_log2, per_block = kThreads >> cover.lanes_log2;
+    const int c = blockIdx.x * lanes + (threadIdx.x & (lanes - 1));
+    if (c >= cover.chunks) return;
+    const int j = c * kChunk;
+    const int64_t step = static_cast<int64_t>(gridDim.y) * per_block;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * per_block + (threadIdx.x >> cover.lanes_log2); r0 < p.m; r0 += kRows * step) {
+        uint2 q[kRows];
+        Raw<kT> d[kRows];
+        float scale[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + i * step;
+            if (r < p.m) {
+                q[i] = load_codes(static_cast<const uint8_t *>(p.q) + r * p.h + j);
+                if constexpr (kGrad) d[i] = load_raw<kT>(static_cast<const char *>(dy) + (r * lddy + j) * kE);
+                scale[i] = scale_at<kQM>(p.scale, r, p.h, j);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + i * step;
+            if (r < p.m) {
+                float z[kChunk];
+                decode_codes(q[i], p.qkind, z);
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) z[e] = __fmul_rn(z[e], scale[i]);
+                char *to = static_cast<char *>(out) + (r * ldo + j) * kE;
+                if constexpr (kGrad) {
+                    float g[kChunk];
+                    values<kT>(d[i], g);
+                    times_derivative(g, z, act);
+                    store_values<kT>(to, g);
+                } else {
+                    apply_act(z, act);
+                    store_values<kT>(to, z);
+                }
+            }
+        }
+    }
+}
+
+// Eight bytes from any address, by the aligned words that hold them.
+__device__ __forceinline__ uint2 load_bytes8(const uint8_t *p) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~uintptr_t(3));
+    const uint32_t shift = static_cast<uint32_t>(a & 3) * 8;
+    const uint32_t w0 = __ldg(w), w1 = __ldg(w + 1);
+    if (shift == 0) return make_uint2(w0, w1);
+    const uint32_t w2 = __ldg(w + 2);
+    return make_uint2(__funnelshift_r(w0, w1, shift), __funnelshift_r(w1, w2, shift));
+}
+
+// Rows of any width and alignment: the chunks are those of the output's aligned 16-byte units, the first and the
+// last of a row partial; codes come from any address, dy in whole chunks where it is aligned as dz is.
+template <int kT, bool kGrad, int kQM>
+__global__ void __launch_bounds__(kThreads) from_kept_any_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p, Activation act,
+                                                                 void *out, int64_t ldo, Cover cover) {
+    using T = typename Elem<kT>::type;
+    constexpr int kE = kT == ELEM_F32 ? 4 : 2;
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    const int lanes = 1 << cover.lanes_log2, per_block = kThreads >> cover.lanes_log2;
+    const int c = blockIdx.x * lanes + (threadIdx.x & (lanes - 1));
+    const int64_t step = static_cast<int64_t>(gridDim.y) * per_block;
+    for (int64_t r = static_cast<int64_t>(blockIdx.y) * per_block + (threadIdx.x >> cover.lanes_log2); r < p.m; r += step) {
+        T *to = static_cast<T *>(out) + r * ldo;
+        const T *from = kGrad ? static_cast<const T *>(dy) + r * lddy : nullptr;
+        const uint8_t *q = static_cast<const uint8_t *>(p.q) + r * p.h;
+        const int j0 = c * kChunk - static_cast<int>(reinterpret_cast<uintptr_t>(to) / kE % kChunk);
+        const int lo = max(j0, 0), hi = min(j0 + kChunk, p.h);
+        if (lo >= hi) continue;
+        const bool whole = hi - lo == kChunk;
+        float z[kChunk], g[kChunk];
+        if (whole) {
+            decode_codes(load_bytes8(q + j0), p.qkind, z);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e) z[e] = j0 + e >= lo && j0 + e < hi ? decode8(q[j0 + e], p.qkind) : 0.0f;
+        }
+        // a chunk reaches into two groups at most
+        const float first = scale_at<kQM>(p.scale, r, p.h, lo), last = scale_at<kQM>(p.scale, r, p.h, hi - 1);
+        const int border = (lo / group_size(kQM) + 1) * group_size(kQM);
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) z[e] = __fmul_rn(z[e], kQM == QM_TOKEN || j0 + e < border ? first : last);
+        if constexpr (kGrad) {
+            if (whole && ((reinterpret_cast<uintptr_t>(from) ^ reinterpret_cast<uintptr_t>(to)) & 15u) == 0) {
+                values<kT>(load_raw<kT>(from + j0), g);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) g[e] = j0 + e >= lo && j0 + e < hi ? Elem<kT>::load(from + j0 + e) : 0.0f;
+            }
+            times_derivative(g, z, act);
+        } else {
+            apply_act(z, act);
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e) g[e] = z[e];
+        }
+        if (whole) {
+            store_values<kT>(to + j0, g);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e)
+                if (j0 + e >= lo && j0 + e < hi) Elem<kT>::store(to + j0 + e, g[e]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ to codes
+// The scale of a group and the codes of a thread's chunk of it, from the group's largest value (as bits).
+template <int kQM>
+__device__ __forceinline__ void encode_chunk(const Kept &p, const float (&y)[kChunk], uint32_t top, int64_t scale_index, bool writes_scale,
+                                             float (&r)[kChunk]) {
+    if constexpr (kQM == QM_MX) {
+        const uint32_t code = mx_code(top, p.qkind);
+        if (writes_scale) static_cast<uint8_t *>(p.scale)[scale_index] = static_cast<uint8_t>(code);
+        const float inverse = mx_inverse(code);
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) r[e] = code != 0xFFu ? y[e] * inverse : 0.0f;
+    } else {
+        const float step = __fmul_rn(__uint_as_float(top), q_inverse(p.qkind));
+        if (writes_scale) static_cast<float *>(p.scale)[scale_index] = step;
+        quotients(y, step, r);
+    }
+}
+
+__device__ __forceinline__ uint32_t largest_of(const float (&y)[kChunk]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) top = max_abs(top, y[e]);
+    return __float_as_uint(top);   // of non-negative values: ordered like them
+}
+
+// Rows of whole chunks with scales of groups (16 or 4 neighbouring threads), or with one scale a row of at most 32
+// chunks (`lanes` threads): covered like from_kept_kernel.
+template <int kT, int kQM, int kRows>
+__global__ void __launch_bounds__(kThreads) act_quant_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act, Cover cover) {
+    constexpr int kE = kT == ELEM_F32 ? 4 : 2;
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    const int lanes = 1 << cover.lanes_log2, per_block = kThreads >> cover.lanes_log2;
+    const int c = blockIdx.x * lanes + (threadIdx.x & (lanes - 1));
+    const bool live = c < cover.chunks;
+    const int j = c * kChunk;
+    const int group = kQM == QM_TOKEN ? lanes : group_size(kQM) / kChunk;   // threads that share a scale
+    const int groups = kQM == QM_TOKEN ? 1 : (p.h + group_size(kQM) - 1) / group_size(kQM);
+    const int64_t step = static_cast<int64_t>(gridDim.y) * per_block;
+    // (all threads of a block take as many turns, so that the groups' exchanges are whole)
+    for (int64_t first = static_cast<int64_t>(blockIdx.y) * per_block; first < p.m; first += kRows * step) {
+        const int64_t r0 = first + (threadIdx.x >> cover.lanes_log2);
+        Raw<kT> raw[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + i * step;
+            if (live && r < p.m) raw[i] = load_raw<kT>(static_cast<const char *>(z) + (r * ldz + j) * kE);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + i * step;
+            const bool here = live && r < p.m;
+            float y[kChunk];
+            if (here) {
+                values<kT>(raw[i], y);
+                apply_act(y, act);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) y[e] = 0.0f;
+            }
+            uint32_t top = largest_of(y);
+            for (int o = group / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            if (here) {
+                float code[kChunk];
+                encode_chunk<kQM>(p, y, top, r * groups + (kQM == QM_TOKEN ? 0 : c / group), (threadIdx.x & (group - 1)) == 0, code);
+                store_codes(p.q, r * p.h + j, code, p.qkind);
+            }
+        }
+    }
+}
+
+// One scale a row, rows of whole chunks, one a block: V chunks a thread, kept between the row's largest value and its codes.
+template <int kT, int V>
+__global__ void __launch_bounds__(1024) act_quant_row_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act) {
+    constexpr int kE = kT == ELEM_F32 ? 4 : 2;
+    __shared__ uint32_t slots[32];
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    const int64_t row = blockIdx.x;
+    const int T = blockDim.x, chunks = p.h / kChunk;
+    const char *from = static_cast<const char *>(z) + row * ldz * kE;
+    Raw<kT> raw[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * T;
+        if (c < chunks) raw[i] = load_raw<kT>(from + static_cast<int64_t>(c) * (kChunk * kE));
+    }
+    float y[V][kChunk];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (threadIdx.x + i * T < chunks) {
+            values<kT>(raw[i], y[i]);
+            apply_act(y[i], act);
+            top = max(top, largest_of(y[i]));
+        }
+    }
+    const float step = __fmul_rn(__uint_as_float(block_max32(top, slots)), q_inverse(p.qkind));
+    if (threadIdx.x == 0) static_cast<float *>(p.scale)[row] = step;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * T;
+        if (c < chunks) {
+            float code[kChunk];
+            quotients(y[i], step, code);
+            store_codes(p.q, row * p.h + static_cast<int64_t>(c) * kChunk, code, p.qkind);
+        }
+    }
+}
 
 // Any sizes, strides and alignments: one block a row, read once for its largest value and once for its codes.  A warp
 // takes whole groups of 32 or 128 elements, so that a group's scale is found inside one warp.
@@ -36,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) act_quant_any_kernel(const void *z, 
         token = __fmul_rn(__uint_as_float(block_max32(__float_as_uint(top), slots)), q_inverse(p.qkind));
         if (threadIdx.x == 0) static_cast<float *>(p.scale)[row] = token;
     }
-    const int group = p.qmode == QM_MX ? 32 : 128, groups = (p.h + group - 1) / group;
+    const int group = group_size(p.qmode), groups = (p.h + group - 1) / group;
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.h;
     for (int g = warp; g < groups; g += kWarps) {
         float y[4];
@@ -69,32 +379,14 @@ __global__ void __launch_bounds__(kThreads) act_quant_any_kernel(const void *z, 
     }
 }
 
-// Element by element.
-template <int kT, bool kGrad>
-__global__ void __launch_bounds__(kThreads) from_kept_any_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p,
-                                                                 Activation act, void *out, int64_t ldo) {
-    using T = typename Elem<kT>::type;
-    ptx::grid_dependency_wait();
-    ptx::allow_dependent_launch();
-    const int64_t total = p.m * p.h, step = static_cast<int64_t>(gridDim.x) * kThreads;
-    for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; e < total; e += step) {
-        const int64_t r = e / p.h;
-        const int c = static_cast<int>(e - r * p.h);
-        const float z = decode8(static_cast<const uint8_t *>(p.q)[e], p.qkind) * scale_at(p.scale, p.qmode, r, p.h, c);
-        const float v = kGrad ? Elem<kT>::load(static_cast<const T *>(dy) + r * lddy + c) * act_derivative2(both(z), act).x
-                              : act2(both(z), act).x;
-        Elem<kT>::store(static_cast<T *>(out) + r * ldo + c, v);
-    }
-}
-
-template <class K, class... A>
-cudaError_t launch(K kern, unsigned grid, cudaStream_t stream, const A &...args) {
+template <class... P, class... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int block, cudaStream_t stream, const A &...args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block, 1, 1);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -102,42 +394,96 @@ cudaError_t launch(K kern, unsigned grid, cudaStream_t stream, const A &...args)
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-unsigned elementwise_grid(int64_t items, int num_sms) {
-    const int64_t blocks = (items + kThreads - 1) / kThreads, most = 64ll * num_sms;
-    return static_cast<unsigned>(blocks < most ? blocks : most);
+// The cover of rows of `chunks` chunks, at least `least` threads a row, and the grid for it: as many blocks as the device
+// holds, of `resident` an SM, each with several rows where there are more.
+dim3 cover_rows(int chunks, int least, int64_t m, int num_sms, int resident, Cover *cover) {
+    cover->chunks = chunks;
+    cover->lanes_log2 = 0;
+    while ((1 << cover->lanes_log2) < kThreads && (1 << cover->lanes_log2) < (chunks > least ? chunks : least)) ++cover->lanes_log2;
+    const int lanes = 1 << cover->lanes_log2;
+    const int64_t across = (chunks + lanes - 1) / lanes, per_block = kThreads / lanes, down = (m + per_block - 1) / per_block;
+    int64_t rows = (static_cast<int64_t>(num_sms) * resident + across - 1) / across;
+    if (rows > down) rows = down;
+    if (rows > 65535) rows = 65535;
+    return dim3(static_cast<unsigned>(across), static_cast<unsigned>(rows), 1);
+}
+
+bool whole_chunks(const void *p, int64_t ld, int64_t m, size_t size) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (m == 1 || ld * static_cast<int64_t>(size) % 16 == 0);
+}
+
+template <int kT, bool kGrad, int kQM>
+cudaError_t launch_from(const void *dy, int64_t lddy, const Kept &p, int act, void *out, int64_t ldo, int num_sms, cudaStream_t stream) {
+    const Activation a = activation_of(act);
+    constexpr size_t kE = kT == ELEM_F32 ? 4 : 2;
+    Cover cover;
+    if (p.h % kChunk == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && whole_chunks(out, ldo, p.m, kE) && (!kGrad || whole_chunks(dy, lddy, p.m, kE))) {
+        const dim3 grid = cover_rows(p.h / kChunk, 1, p.m, num_sms, 8, &cover);
+        return launch(from_kept_kernel<kT, kGrad, kQM, 4>, grid, kThreads, stream, dy, lddy, p, a, out, ldo, cover);
+    }
+    // (a row may begin inside its first chunk)
+    const dim3 grid = cover_rows((p.h + 2 * kChunk - 2) / kChunk, 1, p.m, num_sms, 32, &cover);
+    return launch(from_kept_any_kernel<kT, kGrad, kQM>, grid, kThreads, stream, dy, lddy, p, a, out, ldo, cover);
+}
+
+template <int kT, bool kGrad>
+cudaError_t launch_from(const void *dy, int64_t lddy, const Kept &p, int act, void *out, int64_t ldo, int num_sms, cudaStream_t stream) {
+    switch (p.qmode) {
+        case QM_TOKEN: return launch_from<kT, kGrad, QM_TOKEN>(dy, lddy, p, act, out, ldo, num_sms, stream);
+        case QM_GROUP: return launch_from<kT, kGrad, QM_GROUP>(dy, lddy, p, act, out, ldo, num_sms, stream);
+        default: return launch_from<kT, kGrad, QM_MX>(dy, lddy, p, act, out, ldo, num_sms, stream);
+    }
+}
+
+template <int kT>
+cudaError_t launch_to(const void *z, int64_t ldz, const Kept &p, int act, int num_sms, cudaStream_t stream) {
+    const Activation a = activation_of(act);
+    constexpr size_t kE = kT == ELEM_F32 ? 4 : 2;
+    const int chunks = p.h / kChunk;
+    if (p.h % kChunk == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && whole_chunks(z, ldz, p.m, kE) &&
+        (p.qmode != QM_TOKEN || chunks <= 4 * 1024)) {
+        Cover cover;
+        if (p.qmode == QM_GROUP)
+            return launch(act_quant_kernel<kT, QM_GROUP, 4>, cover_rows(chunks, 16, p.m, num_sms, 8, &cover), kThreads, stream, z, ldz, p, a, cover);
+        if (p.qmode == QM_MX)
+            return launch(act_quant_kernel<kT, QM_MX, 4>, cover_rows(chunks, 4, p.m, num_sms, 8, &cover), kThreads, stream, z, ldz, p, a, cover);
+        if (chunks <= 32)
+            return launch(act_quant_kernel<kT, QM_TOKEN, 4>, cover_rows(chunks, 1, p.m, num_sms, 8, &cover), kThreads, stream, z, ldz, p, a, cover);
+        // few rows: more threads a row; many: more chunks a thread
+        const int v = p.m > 2 * num_sms || chunks > 2048 ? 4 : (chunks > 1024 ? 2 : 1);
+        const int threads = ((chunks + v - 1) / v + 31) / 32 * 32;
+        const dim3 grid(static_cast<unsigned>(p.m), 1, 1);
+        switch (v) {
+            case 1: return launch(act_quant_row_kernel<kT, 1>, grid, threads, stream, z, ldz, p, a);
+            case 2: return launch(act_quant_row_kernel<kT, 2>, grid, threads, stream, z, ldz, p, a);
+            default: return launch(act_quant_row_kernel<kT, 4>, grid, threads, stream, z, ldz, p, a);
+        }
+    }
+    return launch(act_quant_any_kernel<kT>, dim3(static_cast<unsigned>(p.m), 1, 1), kThreads, stream, z, ldz, p, a);
 }
 
 }  // namespace
 
 cudaError_t launch_act_quant(int kind, const void *z, int64_t ldz, const Kept &to, int act, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    const Activation a = activation_of(act);
-    const unsigned grid = static_cast<unsigned>(to.m);
     switch (kind) {
-        case ELEM_F16: return launch(act_quant_any_kernel<ELEM_F16>, grid, stream, z, ldz, to, a);
-        case ELEM_BF16: return launch(act_quant_any_kernel<ELEM_BF16>, grid, stream, z, ldz, to, a);
-        default: return launch(act_quant_any_kernel<ELEM_F32>, grid, stream, z, ldz, to, a);
+        case ELEM_F16: return launch_to<ELEM_F16>(z, ldz, to, act, num_sms, stream);
+        case ELEM_BF16: return launch_to<ELEM_BF16>(z, ldz, to, act, num_sms, stream);
+        default: return launch_to<ELEM_F32>(z, ldz, to, act, num_sms, stream);
     }
 }
 
 cudaError_t launch_act_dequant(int kind, const Kept &from, int act, void *out, int64_t ldo, int num_sms, cudaStream_t stream) {
-    const Activation a = activation_of(act);
-    const unsigned grid = elementwise_grid(from.m * from.h, num_sms);
-    const void *none = nullptr;
-    const int64_t zero = 0;
     switch (kind) {
-        case ELEM_F16: return launch(from_kept_any_kernel<ELEM_F16, false>, grid, stream, none, zero, from, a, out, ldo);
-        case ELEM_BF16: return launch(from_kept_any_kernel<ELEM_BF16, false>, grid, stream, none, zero, from, a, out, ldo);
-        default: return launch(from_kept_any_kernel<ELEM_F32, false>, grid, stream, none, zero, from, a, out, ldo);
+        case ELEM_F16: return launch_from<ELEM_F16, false>(nullptr, 0, from, act, out, ldo, num_sms, stream);
+        case ELEM_BF16: return launch_from<ELEM_BF16, false>(nullptr, 0, from, act, out, ldo, num_sms, stream);
+        default: return launch_from<ELEM_F32, false>(nullptr, 0, from, act, out, ldo, num_sms, stream);
     }
 }
 
 cudaError_t launch_act_grad_quant(bool bf16, const void *dy, int64_t lddy, const Kept &z, int act, void *dz, int64_t lddz,
                                   int num_sms, cudaStream_t stream) {
-    const Activation a = activation_of(act);
-    const unsigned grid = elementwise_grid(z.m * z.h, num_sms);
-    return bf16 ? launch(from_kept_any_kernel<ELEM_BF16, true>, grid, stream, dy, lddy, z, a, dz, lddz)
-                : launch(from_kept_any_kernel<ELEM_F16, true>, grid, stream, dy, lddy, z, a, dz, lddz);
+    return bf16 ? launch_from<ELEM_BF16, true>(dy, lddy, z, act, dz, lddz, num_sms, stream)
+                : launch_from<ELEM_F16, true>(dy, lddy, z, act, dz, lddz, num_sms, stream);
 }
 
 }  // namespace mc2
