@@ -16,7 +16,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 8;   // elements a thread takes at a time
+constexpr int kChunk = 8;      // elements a thread takes at a time
+constexpr int kResident = 4;   // blocks of the covering kernels an SM holds
 
 // f(activation with its form a constant): the choice is made once for all of a thread's elements.
 template <class F>
@@ -104,7 +105,7 @@ struct Cover {
 // ------------------------------------------------------------------ from codes
 // Rows of whole chunks: every access is a whole one.  kRows rows of a thread are on their way at once.
 template <int kT, bool kGrad, int kQM, int kRows>
-__global__ void __launch_bounds__(kThreads) from_kept_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p, Activation act,
+__global__ void __launch_bounds__(kThreads, kResident) from_kept_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p, Activation act,
                                                              void *out, int64_t ldo, Cover cover) {
     constexpr int kE = kT == ELEM_F32 ? 4 : 2;
     ptx::grid_dependency_wait();
@@ -217,20 +218,56 @@ __global__ void __launch_bounds__(kThreads) from_kept_any_kernel(const void *dy,
 }
 
 // ------------------------------------------------------------------ to codes
+// The codes of a thread's chunk, y / step to nearest-even, in one store.  The quotients are those of quotients() in codes.cuh,
+// two at a time; |y| is at most the value that the step was made from, so that they need no clamp but where the step lost
+// bits to fp32's lower end (there, as at steps that are zero or not finite, quotients() takes over).
+__device__ __forceinline__ void store_quotients(void *q, int64_t at, const float (&y)[kChunk], float step, int kind) {
+    if (step > 8.2718061e-25f && step < 1e30f) {
+        const float2 inv = both(__frcp_rn(step)), minus = both(-step);
+        float2 r[kChunk / 2];
+#pragma unroll
+        for (int e = 0; e < kChunk / 2; ++e) {
+            const float2 v = make_float2(y[2 * e], y[2 * e + 1]);
+            const float2 t = __fmul2_rn(v, inv);
+            r[e] = __ffma2_rn(__ffma2_rn(t, minus, v), inv, t);
+        }
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (kind == Q_I8) {   // (as in store_codes)
+                const float2 a = __fadd2_rn(r[2 * i], both(12582912.0f)), b = __fadd2_rn(r[2 * i + 1], both(12582912.0f));
+                w[i] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                                   __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+            } else {
+                const __nv_fp8_interpretation_t t = kind == Q_E4M3 ? __NV_E4M3 : __NV_E5M2;
+                w[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(r[2 * i], __NV_SATFINITE, t)) |
+                       static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(r[2 * i + 1], __NV_SATFINITE, t)) << 16;
+            }
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(q) + at) = make_uint2(w[0], w[1]);
+    } else {
+        float r[kChunk];
+        quotients(y, step, r);
+        store_codes(q, at, r, kind);
+    }
+}
+
 // The scale of a group and the codes of a thread's chunk of it, from the group's largest value (as bits).
 template <int kQM>
 __device__ __forceinline__ void encode_chunk(const Kept &p, const float (&y)[kChunk], uint32_t top, int64_t scale_index, bool writes_scale,
-                                             float (&r)[kChunk]) {
+                                             int64_t at) {
     if constexpr (kQM == QM_MX) {
         const uint32_t code = mx_code(top, p.qkind);
         if (writes_scale) static_cast<uint8_t *>(p.scale)[scale_index] = static_cast<uint8_t>(code);
         const float inverse = mx_inverse(code);
+        float r[kChunk];
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) r[e] = code != 0xFFu ? y[e] * inverse : 0.0f;
+        store_codes(p.q, at, r, p.qkind);
     } else {
         const float step = __fmul_rn(__uint_as_float(top), q_inverse(p.qkind));
         if (writes_scale) static_cast<float *>(p.scale)[scale_index] = step;
-        quotients(y, step, r);
+        store_quotients(p.q, at, y, step, p.qkind);
     }
 }
 
@@ -244,7 +281,7 @@ __device__ __forceinline__ uint32_t largest_of(const float (&y)[kChunk]) {
 // Rows of whole chunks with scales of groups (16 or 4 neighbouring threads), or with one scale a row of at most 32
 // chunks (`lanes` threads): covered like from_kept_kernel.
 template <int kT, int kQM, int kRows>
-__global__ void __launch_bounds__(kThreads) act_quant_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act, Cover cover) {
+__global__ void __launch_bounds__(kThreads, kResident) act_quant_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act, Cover cover) {
     constexpr int kE = kT == ELEM_F32 ? 4 : 2;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
@@ -279,50 +316,47 @@ __global__ void __launch_bounds__(kThreads) act_quant_kernel(const void *z, int6
             uint32_t top = largest_of(y);
             for (int o = group / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             if (here) {
-                float code[kChunk];
-                encode_chunk<kQM>(p, y, top, r * groups + (kQM == QM_TOKEN ? 0 : c / group), (threadIdx.x & (group - 1)) == 0, code);
-                store_codes(p.q, r * p.h + j, code, p.qkind);
+                encode_chunk<kQM>(p, y, top, r * groups + (kQM == QM_TOKEN ? 0 : c / group), (threadIdx.x & (group - 1)) == 0, r * p.h + j);
             }
         }
     }
 }
 
-// One scale a row, rows of whole chunks, one a block: V chunks a thread, kept between the row's largest value and its codes.
-template <int kT, int V>
-__global__ void __launch_bounds__(1024) act_quant_row_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act) {
+// One scale a row, rows of whole chunks: V chunks a thread, kept between the row's largest value and its codes.  One row a
+// block, or (kWarpRow) one a warp.
+template <int kT, int V, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? kThreads : 1024) act_quant_row_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act) {
     constexpr int kE = kT == ELEM_F32 ? 4 : 2;
     __shared__ uint32_t slots[32];
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    const int64_t row = blockIdx.x;
-    const int T = blockDim.x, chunks = p.h / kChunk;
+    const int64_t row = kWarpRow ? static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5) : blockIdx.x;
+    if (kWarpRow && row >= p.m) return;
+    const int T = kWarpRow ? 32 : blockDim.x, mine = kWarpRow ? threadIdx.x & 31 : threadIdx.x, chunks = p.h / kChunk;
     const char *from = static_cast<const char *>(z) + row * ldz * kE;
     Raw<kT> raw[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * T;
+        const int c = mine + i * T;
         if (c < chunks) raw[i] = load_raw<kT>(from + static_cast<int64_t>(c) * (kChunk * kE));
     }
     float y[V][kChunk];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if (threadIdx.x + i * T < chunks) {
+        if (mine + i * T < chunks) {
             values<kT>(raw[i], y[i]);
             apply_act(y[i], act);
             top = max(top, largest_of(y[i]));
         }
     }
-    const float step = __fmul_rn(__uint_as_float(block_max32(top, slots)), q_inverse(p.qkind));
-    if (threadIdx.x == 0) static_cast<float *>(p.scale)[row] = step;
+    top = kWarpRow ? __reduce_max_sync(0xFFFFFFFFu, top) : block_max32(top, slots);
+    const float step = __fmul_rn(__uint_as_float(top), q_inverse(p.qkind));
+    if (mine == 0) static_cast<float *>(p.scale)[row] = step;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * T;
-        if (c < chunks) {
-            float code[kChunk];
-            quotients(y[i], step, code);
-            store_codes(p.q, row * p.h + static_cast<int64_t>(c) * kChunk, code, p.qkind);
-        }
+        const int c = mine + i * T;
+        if (c < chunks) store_quotients(p.q, row * p.h + static_cast<int64_t>(c) * kChunk, y[i], step, p.qkind);
     }
 }
 
@@ -418,8 +452,8 @@ cudaError_t launch_from(const void *dy, int64_t lddy, const Kept &p, int act, vo
     constexpr size_t kE = kT == ELEM_F32 ? 4 : 2;
     Cover cover;
     if (p.h % kChunk == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && whole_chunks(out, ldo, p.m, kE) && (!kGrad || whole_chunks(dy, lddy, p.m, kE))) {
-        const dim3 grid = cover_rows(p.h / kChunk, 1, p.m, num_sms, 8, &cover);
-        return launch(from_kept_kernel<kT, kGrad, kQM, 4>, grid, kThreads, stream, dy, lddy, p, a, out, ldo, cover);
+        const dim3 grid = cover_rows(p.h / kChunk, 1, p.m, num_sms, kResident, &cover);
+        return launch(from_kept_kernel<kT, kGrad, kQM, 2>, grid, kThreads, stream, dy, lddy, p, a, out, ldo, cover);
     }
     // (a row may begin inside its first chunk)
     const dim3 grid = cover_rows((p.h + 2 * kChunk - 2) / kChunk, 1, p.m, num_sms, 32, &cover);
@@ -444,19 +478,21 @@ cudaError_t launch_to(const void *z, int64_t ldz, const Kept &p, int act, int nu
         (p.qmode != QM_TOKEN || chunks <= 4 * 1024)) {
         Cover cover;
         if (p.qmode == QM_GROUP)
-            return launch(act_quant_kernel<kT, QM_GROUP, 4>, cover_rows(chunks, 16, p.m, num_sms, 8, &cover), kThreads, stream, z, ldz, p, a, cover);
+            return launch(act_quant_kernel<kT, QM_GROUP, 2>, cover_rows(chunks, 16, p.m, num_sms, kResident, &cover), kThreads, stream, z, ldz, p, a, cover);
         if (p.qmode == QM_MX)
-            return launch(act_quant_kernel<kT, QM_MX, 4>, cover_rows(chunks, 4, p.m, num_sms, 8, &cover), kThreads, stream, z, ldz, p, a, cover);
+            return launch(act_quant_kernel<kT, QM_MX, 2>, cover_rows(chunks, 4, p.m, num_sms, kResident, &cover), kThreads, stream, z, ldz, p, a, cover);
         if (chunks <= 32)
-            return launch(act_quant_kernel<kT, QM_TOKEN, 4>, cover_rows(chunks, 1, p.m, num_sms, 8, &cover), kThreads, stream, z, ldz, p, a, cover);
+            return launch(act_quant_kernel<kT, QM_TOKEN, 2>, cover_rows(chunks, 1, p.m, num_sms, kResident, &cover), kThreads, stream, z, ldz, p, a, cover);
         // few rows: more threads a row; many: more chunks a thread
         const int v = p.m > 2 * num_sms || chunks > 2048 ? 4 : (chunks > 1024 ? 2 : 1);
         const int threads = ((chunks + v - 1) / v + 31) / 32 * 32;
-        const dim3 grid(static_cast<unsigned>(p.m), 1, 1);
+        const dim3 grid(static_cast<unsigned>(p.m), 1, 1), warps(static_cast<unsigned>((p.m + kWarps - 1) / kWarps), 1, 1);
+        if (v == 4 && chunks <= 64) return launch(act_quant_row_kernel<kT, 2, true>, warps, kThreads, stream, z, ldz, p, a);
+        if (v == 4 && chunks <= 128) return launch(act_quant_row_kernel<kT, 4, true>, warps, kThreads, stream, z, ldz, p, a);
         switch (v) {
-            case 1: return launch(act_quant_row_kernel<kT, 1>, grid, threads, stream, z, ldz, p, a);
-            case 2: return launch(act_quant_row_kernel<kT, 2>, grid, threads, stream, z, ldz, p, a);
-            default: return launch(act_quant_row_kernel<kT, 4>, grid, threads, stream, z, ldz, p, a);
+            case 1: return launch(act_quant_row_kernel<kT, 1, false>, grid, threads, stream, z, ldz, p, a);
+            case 2: return launch(act_quant_row_kernel<kT, 2, false>, grid, threads, stream, z, ldz, p, a);
+            default: return launch(act_quant_row_kernel<kT, 4, false>, grid, threads, stream, z, ldz, p, a);
         }
     }
     return launch(act_quant_any_kernel<kT>, dim3(static_cast<unsigned>(p.m), 1, 1), kThreads, stream, z, ldz, p, a);
