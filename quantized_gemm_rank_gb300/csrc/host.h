@@ -73,6 +73,8 @@ bool make_map16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer
 bool make_map16_nmajor3d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint32_t box_outer,
                          uint32_t groups, uint64_t pitch = 0);
 
+// 2-D map over 8-bit elements: boxes of 128 columns x box_outer rows, 128-byte swizzle; pitch a multiple of 16.
+bool make_map8(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint32_t box_outer, uint64_t pitch);
 // 3-D map over fp32 matrices (parts, outer, inner) with rows `pitch` elements apart (a multiple of 4): boxes of 32 columns x 32
 // rows, 128-byte swizzle.
 bool make_map32_parts(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t parts, uint64_t pitch);

@@ -23,8 +23,8 @@ struct LinearParams {
     int w_nk;
     int act;        // ActKind
     int aux_mode;   // AuxMode
-    // a product of int8 codes: x and w are fp16 that hold them, out, aux and a 16-bit bias of the given type, and
-    // z = float(acc) x_scale w_scale + bias (the tiles only)
+    // a product of int8 codes: out, aux and a 16-bit bias of the given type, z = float(acc) x_scale w_scale + bias.  The split
+    // kernel takes x and w as they are (16-byte aligned, strides a multiple of 16; out and aux of any layout), the tiles as fp16
     const float *x_scale, *w_scale;   // (m), (n)
     int bias_f32;
 };
@@ -52,6 +52,8 @@ cudaError_t launch_linear_tiles(bool bf16, const LinearParams &p, cudaStream_t s
 // The weight's columns as the tile's rows, the contraction split over a cluster:
 // products whose tiles would not fill the device.
 cudaError_t launch_linear_split(bool bf16, const LinearParams &p, int num_sms, cudaStream_t stream);
+// What the split kernel is expected to take for codes, in us; negative where it cannot sum them exactly.
+float linear_split_codes_us(const LinearParams &p, int num_sms);
 // Which of the two is expected to be faster for these sizes.
 bool linear_prefers_split(const LinearParams &p, int num_sms);
 

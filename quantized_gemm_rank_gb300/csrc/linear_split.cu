@@ -42,15 +42,19 @@ namespace {
 
 constexpr int kTileN = 128;      // weight columns a tile (MMA M)
 constexpr int kDepth = 64;       // contraction a stage
+constexpr int kDepth8 = 128;     // ... of int8 codes
 constexpr int kMaxStages = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kProducers = 2;
-// Threads a CTA: the pairs' tiles have more to bring out of TMEM and one CTA an SM.
-__host__ __device__ constexpr int split_threads(int group) { return group == 1 ? 256 : 512; }
-constexpr int kBlockSteps = 1024 / kDepth;   // stages of one accumulator
+// Threads a CTA: the pairs' tiles have more to bring out of TMEM and one CTA an SM; codes have warps that widen them.
+__host__ __device__ constexpr int split_threads(int group, bool codes) { return group == 2 ? 512 : (codes ? 384 : 256); }
+constexpr int kWidenFirst = 4;   // the first of those warps; the others are producers, MMA, and one that is idle
+constexpr int kBlockDepth = 1024;   // of one accumulator
 constexpr uint32_t kWBytes = kTileN * kDepth * 2;
 constexpr uint32_t kSmemPerSm = 228 * 1024;
-constexpr uint32_t kSmemStatic = 288;            // this kernel's static shared memory
+constexpr uint32_t kSmemStatic = 288;            // this kernel's static shared memory ...
+constexpr uint32_t kSmemStaticCodes = 544;       // ... and with the barriers of a ring of codes
+constexpr uint32_t kMostSmem = 227 * 1024 - kSmemStatic, kMostSmemCodes = 227 * 1024 - kSmemStaticCodes;
 constexpr uint32_t kSmemOverhead = 1024 + kSmemStatic;   // with the system's part of each CTA's
 
 struct SplitParams {
@@ -72,46 +76,59 @@ struct SplitParams {
     Activation act;
     int *status;
     uint64_t wait_limit_ns;
+    // int8 codes (EPI_SCALED)
+    const float *x_scale, *w_scale;
+    int bias_f32;
+    int raws;                 // stages of codes, from raw_off on
+    uint32_t raw_off;
+    int words;                // rows of out and aux begin at multiples of 8 bytes
 };
 
-// Four columns of a row, of which the first `n` (4 or more: all) are in it; whole ones in one access.
+// Four columns of a row, of which the first `n` (4 or more: all) are in it; whole ones in one access, where rows allow it (`words`).
 template <bool kBF16>
-__device__ __forceinline__ void store4(uint16_t *p, int n, const float *v) {
+__device__ __forceinline__ void store4(uint16_t *p, int n, const float *v, bool words) {
     const uint32_t pk[2] = {pack2<kBF16>(v[0], v[1]), pack2<kBF16>(v[2], v[3])};
-    if (n >= 4) {
+    if (n >= 4 && words) {
         *reinterpret_cast<uint2 *>(p) = make_uint2(pk[0], pk[1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
+        for (int i = 0; i < 4; ++i)
             if (i < n) p[i] = static_cast<uint16_t>(pk[i >> 1] >> ((i & 1) * 16));
     }
 }
 
-__device__ __forceinline__ void load4(const uint16_t *p, int n, uint32_t *w) {
-    if (n >= 4) {
+__device__ __forceinline__ void load4(const uint16_t *p, int n, uint32_t *w, bool words) {
+    if (n >= 4 && words) {
         const uint2 v = *reinterpret_cast<const uint2 *>(p);
         w[0] = v.x, w[1] = v.y;
     } else {
         w[0] = w[1] = 0;
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
+        for (int i = 0; i < 4; ++i)
             if (i < n) w[i >> 1] |= static_cast<uint32_t>(p[i]) << ((i & 1) * 16);
     }
 }
 
 // kT tokens of a tile from token t on, four columns a lane: the partial sums in rank order, the
 // epilogue, the outputs.  kWhole: all four columns are in the row.  `from`: the token's sums from rank 0 on, `slot`
-// apart but for this CTA's own (rank `rank`), which are at `own`.
+// apart but for this CTA's own (rank `rank`), which are at `own`.  EPI_SCALED: the sums are int32, x_scale that of the tokens.
 template <bool kBF16, int kEpi, int kT, bool kWhole>
 __device__ __forceinline__ void finish_tokens(const SplitParams &p, const float4 *own, const float4 *from, int slot, int rank, const float *b4,
-                                              const uint16_t *aux_row, uint16_t *pre_row, uint16_t *out_row, int n) {
+                                              const float *w4, const float *x_scale, const uint16_t *aux_row, uint16_t *pre_row, uint16_t *out_row,
+                                              int n) {
+    constexpr bool kCodes = kEpi == EPI_SCALED;
     if constexpr (kWhole) n = 4;
+    const bool words = !kCodes || p.words != 0;
     uint32_t aux[2 * kT] = {};
     if (aux_row) {
 #pragma unroll
-        for (int u = 0; u < kT; ++u) load4(aux_row + u * p.ldaux, n, &aux[2 * u]);
+        for (int u = 0; u < kT; ++u) load4(aux_row + u * p.ldaux, n, &aux[2 * u], words);
     }
     float v[4 * kT];
+    const auto add = [](float a, float b) {
+        if constexpr (kCodes) return __int_as_float(__float_as_int(a) + __float_as_int(b));
+        return __fadd_rn(a, b);
+    };
     auto source = [&](int r) {
         const float4 *at = r == rank ? own : from;
         if (r != rank) from += slot;
@@ -129,19 +146,27 @@ __device__ __forceinline__ void finish_tokens(const SplitParams &p, const float4
 #pragma unroll
         for (int u = 0; u < kT; ++u) {
             const float4 s = at[u * (kTileN / 4)];
-            v[4 * u] = __fadd_rn(v[4 * u], s.x), v[4 * u + 1] = __fadd_rn(v[4 * u + 1], s.y);
-            v[4 * u + 2] = __fadd_rn(v[4 * u + 2], s.z), v[4 * u + 3] = __fadd_rn(v[4 * u + 3], s.w);
+            v[4 * u] = add(v[4 * u], s.x), v[4 * u + 1] = add(v[4 * u + 1], s.y);
+            v[4 * u + 2] = add(v[4 * u + 2], s.z), v[4 * u + 3] = add(v[4 * u + 3], s.w);
+        }
+    }
+    if constexpr (kCodes) {
+#pragma unroll
+        for (int u = 0; u < kT; ++u) {
+            const float s = __ldg(x_scale + u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * u + i] = __fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[4 * u + i])), s), w4[i]);
         }
     }
 #pragma unroll
     for (int i = 0; i < 4 * kT; ++i) v[i] = __fadd_rn(v[i], b4[i & 3]);
     if (pre_row) {
 #pragma unroll
-        for (int u = 0; u < kT; ++u) store4<kBF16>(pre_row + u * p.ldp, n, &v[4 * u]);
+        for (int u = 0; u < kT; ++u) store4<kBF16>(pre_row + u * p.ldp, n, &v[4 * u], words);
     }
     epilogue<kBF16, kEpi>(v, aux, p.act, aux_row != nullptr);
 #pragma unroll
-    for (int u = 0; u < kT; ++u) store4<kBF16>(out_row + u * p.ldo, n, &v[4 * u]);
+    for (int u = 0; u < kT; ++u) store4<kBF16>(out_row + u * p.ldo, n, &v[4 * u], words);
 }
 
 // Where a lane's four columns of the tokens from `first` on are.
@@ -150,9 +175,11 @@ struct Place {
     uint16_t *pre, *out;
     int n;          // columns from the lane's first on; none: 0 or less
     float b4[4];    // their biases
+    const float *x_scale;   // EPI_SCALED: the tokens' scales
+    float w4[4];            // and the columns'
 };
 
-template <bool kBF16>
+template <bool kBF16, int kEpi>
 __device__ __forceinline__ Place place(const SplitParams &p, int64_t row, int col) {
     Place at = {};
     at.n = p.n - col;
@@ -162,7 +189,13 @@ __device__ __forceinline__ Place place(const SplitParams &p, int64_t row, int co
     if (p.bias) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (i < at.n) at.b4[i] = load16<kBF16>(p.bias, col + i);
+            if (i < at.n) at.b4[i] = kEpi == EPI_SCALED && p.bias_f32 ? static_cast<const float *>(p.bias)[col + i] : load16<kBF16>(p.bias, col + i);
+    }
+    if constexpr (kEpi == EPI_SCALED) {
+        at.x_scale = p.x_scale + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < at.n) at.w4[i] = p.w_scale[col + i];
     }
     return at;
 }
@@ -182,12 +215,12 @@ __device__ __forceinline__ void finish(const SplitParams &p, const Place &at, in
         for (t = 4 * warp; t + 4 <= count; t += 4 * kWarps) {
             const float4 *o = own + t * (kTileN / 4), *r = recv + t * (kTileN / 4);
             if (at.n >= 4) {
-                finish_tokens<kBF16, kEpi, 4, true>(p, o, r, slot, rank, at.b4, at.aux ? at.aux + t * p.ldaux : nullptr,
+                finish_tokens<kBF16, kEpi, 4, true>(p, o, r, slot, rank, at.b4, at.w4, at.x_scale + t, at.aux ? at.aux + t * p.ldaux : nullptr,
                                                     at.pre ? at.pre + t * p.ldp : nullptr, at.out + t * p.ldo, 4);
             } else {
 #pragma unroll 1
                 for (int u = 0; u < 4; ++u)
-                    finish_tokens<kBF16, kEpi, 1, false>(p, o + u * (kTileN / 4), r + u * (kTileN / 4), slot, rank, at.b4,
+                    finish_tokens<kBF16, kEpi, 1, false>(p, o + u * (kTileN / 4), r + u * (kTileN / 4), slot, rank, at.b4, at.w4, at.x_scale + t + u,
                                                          at.aux ? at.aux + (t + u) * p.ldaux : nullptr,
                                                          at.pre ? at.pre + (t + u) * p.ldp : nullptr, at.out + (t + u) * p.ldo, at.n);
             }
@@ -196,17 +229,21 @@ __device__ __forceinline__ void finish(const SplitParams &p, const Place &at, in
     }
 #pragma unroll 1
     for (t += warp; t < count; t += kWarps)
-        finish_tokens<kBF16, kEpi, 1, false>(p, own + t * (kTileN / 4), recv + t * (kTileN / 4), slot, rank, at.b4,
+        finish_tokens<kBF16, kEpi, 1, false>(p, own + t * (kTileN / 4), recv + t * (kTileN / 4), slot, rank, at.b4, at.w4, at.x_scale + t,
                                              at.aux ? at.aux + t * p.ldaux : nullptr, at.pre ? at.pre + t * p.ldp : nullptr,
                                              at.out + t * p.ldo, at.n);
 }
 
 template <bool kBF16, int kEpi, int kG>
-__global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(const __grid_constant__ SplitParams p) {
-    constexpr int kThreads = split_threads(kG);
+__global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) linear_split_kernel(const __grid_constant__ SplitParams p) {
+    constexpr bool kCodes = kEpi == EPI_SCALED;   // int8 operands
+    constexpr int kThreads = split_threads(kG, kCodes);
+    constexpr int kWiden = kThreads / 32 - kWidenFirst;   // warps that widen codes
+    constexpr int kStep = kCodes ? kDepth8 : kDepth;      // contraction a stage
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, recv_bar;
+    __shared__ __align__(8) uint64_t raw_full[kCodes ? kMaxStages : 1], raw_empty[kCodes ? kMaxStages : 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
 
@@ -219,7 +256,7 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     const int half = kG == 2 ? crank & 1 : 0;            // of the pair
     const int rank = crank / kG;                         // share of the contraction
     const int x_rows = p.rows / kG;                      // tokens this CTA loads
-    const uint32_t stage_bytes = kWBytes + static_cast<uint32_t>(x_rows) * kDepth * 2;
+    const uint32_t stage_bytes = (kTileN + static_cast<uint32_t>(x_rows)) * kStep * 2;
     // (no divisions: seven of them, one after another, took 0.5 us of each call.  A quotient of 32-bit numbers is the
     // high word of the product with the reciprocal rounded up to 64 bits: its error, below 2^-64 x tile, does not
     // reach the next integer.)
@@ -242,8 +279,12 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
         ptx::tmem_relinquish<kG>();
     } else if (warp == 0) {
         if (lane < S) {
-            ptx::mbar_init(ptx::smem_u32(&full_bar[lane]), 1);
+            ptx::mbar_init(ptx::smem_u32(&full_bar[lane]), kCodes ? kWiden * kG : 1);
             ptx::mbar_init(ptx::smem_u32(&empty_bar[lane]), 1);
+        }
+        if (kCodes && lane < p.raws) {
+            ptx::mbar_init(ptx::smem_u32(&raw_full[lane]), 1);
+            ptx::mbar_init(ptx::smem_u32(&raw_empty[lane]), kWiden);
         }
         if (lane == 0) {
             failed = 0;
@@ -264,17 +305,18 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     // A producer's wait for a stage tells the stage's last use from the one before only while
     // the ring is at least as long as there are producers: it has issued the step
     // `producers` back, so what the ring held before that one is consumed.
-    const int producers = min(kProducers, S), producer = warp == 0 ? 0 : warp - 1;   // (warp 1 issues the MMAs)
+    const int ring = kCodes ? p.raws : S;
+    const int producers = min(kProducers, ring), producer = warp == 0 ? 0 : warp - 1;   // (warp 1 issues the MMAs)
     if (warp != 1 && producer < producers && lane == 0) {
         ptx::prefetch_tmap(&p.w_map);
         ptx::prefetch_tmap(&p.x_map);
         // The weight's first stages into L2 while the stream's previous kernel ends.  Nothing is
         // read by this: were that kernel to write the weight, L2 would hold what it wrote.
-        for (int i = producer; i < min(count, S) && p.prefetch; i += producers) {
-            const int k0 = (step0 + i) * kDepth;
+        for (int i = producer; i < min(count, ring) && p.prefetch; i += producers) {
+            const int k0 = (step0 + i) * kStep;
             if (p.w_kn) {
                 ptx::tma_prefetch_2d(&p.w_map, n0, k0);
-                ptx::tma_prefetch_2d(&p.w_map, n0 + 64, k0);
+                if (!kCodes) ptx::tma_prefetch_2d(&p.w_map, n0 + 64, k0);
             } else {
                 ptx::tma_prefetch_2d(&p.w_map, k0, n0);
             }
@@ -283,7 +325,92 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
 
-    if (warp != 1 && producer < producers) {
+    if (kCodes && warp != 1 && producer < producers) {
+        // codes as they are, each CTA its own: 128 columns of the weight and x_rows tokens, 128 deep
+        const uint32_t raw_bytes = stage_bytes / 2;
+        int i = producer, stage = producer;
+        uint32_t phase = 1;
+        while (stage >= ring) stage -= ring, phase ^= 1u;
+        bool ok = true;
+        for (; i < count; i += producers) {
+            const bool got = ptx::mbar_wait(ptx::smem_u32(&raw_empty[stage]), phase, p.wait_limit_ns);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            const uint32_t full = ptx::smem_u32(&raw_full[stage]);
+            const uint32_t sw = ptx::smem_u32(smem) + p.raw_off + stage * raw_bytes;
+            const int k0 = (step0 + i) * kStep;
+            if (ptx::elect_one()) {
+                ptx::mbar_arrive_expect_tx(full, raw_bytes);
+                ptx::tma_load_2d(sw, &p.w_map, p.w_kn ? n0 : k0, p.w_kn ? k0 : n0, full);
+                ptx::tma_load_2d(sw + kTileN * kStep, &p.x_map, k0, m0 + half * x_rows, full);
+            }
+            __syncwarp();
+            stage += producers;
+            while (stage >= ring) stage -= ring, phase ^= 1u;
+        }
+        if (!ok && lane == 0) {
+            atomicExch(&failed, 1);
+            // the copies in flight, among this warp's last ones, land before the CTA can exit
+            for (int back = 0; back <= ring && i - producers >= 0; back += producers) {
+                i -= producers;
+                (void)ptx::mbar_wait(ptx::smem_u32(&raw_full[i % ring]), static_cast<uint32_t>((i / ring) & 1), p.wait_limit_ns);
+            }
+            ptx::nanosleep(20000);
+        }
+    } else if (kCodes && warp >= kWidenFirst) {
+        // Codes to fp16, a stage over all these warps.  A turn takes a warp half of eight rows of 128 bytes: 64 codes of each,
+        // 16 a lane, to the 128-byte row of the operand's 64-deep (K-major) or 64-wide (M-major) half.  Both sides have the
+        // 128-byte swizzle (chunk c of row r at c ^ r % 8), and the lanes' rows in the order 0 5 1 4 2 7 3 6 meet all
+        // banks in eight lanes at a time, in the loads (neighbouring rows differ in bit 2) and in the stores (and in bit 0).
+        const int row_in = (lane >> 3) ^ ((lane >> 2) & 1 ? 5 : 0);
+        const int chunk = lane & 3;
+        const int turns_w = 2 * kTileN / 8, turns = turns_w + 2 * x_rows / 8;
+        const uint8_t *raw0 = smem + p.raw_off;
+        const uint32_t half_w = p.w_kn ? kDepth * 128u : kTileN * 128u;         // to the other half of the weight's rows
+        const uint32_t full0 = ptx::smem_u32(&full_bar[0]);
+        const uint32_t ready0 = kG == 2 ? ptx::mapa(full0, crank - half) : full0;   // (the pair's first CTA counts both)
+        int rs = 0, stage = 0;
+        uint32_t raw_phase = 0, phase = 1;
+        bool ok = true;
+        for (int i = 0; i < count; ++i) {
+            const bool got = ptx::mbar_wait(ptx::smem_u32(&raw_full[rs]), raw_phase, p.wait_limit_ns) &&
+                             ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), phase, p.wait_limit_ns);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            const uint8_t *raw = raw0 + rs * (stage_bytes / 2);
+            uint8_t *to = smem + stage * stage_bytes;
+            for (int t = warp - kWidenFirst; t < turns; t += kWiden) {
+                const bool is_w = t < turns_w;
+                const int u = is_w ? t : t - turns_w, h = u & 1, row = (u >> 1) * 8 + row_in;
+                const uint4 q = *reinterpret_cast<const uint4 *>(raw + (is_w ? 0 : kTileN * kStep) + row * 128 + (((4 * h + chunk) ^ row_in) << 4));
+                // the weight's row r of codes: K-major, row r of both depths; M-major, depth r (64 of them a part) of both slabs
+                uint8_t *dst;
+                if (is_w)
+                    dst = to + (p.w_kn ? (row >> 6) * kWBytes + (row & 63) * 128 : row * 128) + h * half_w;
+                else
+                    dst = to + 2 * kWBytes + h * (x_rows * 128) + row * 128;
+                const uint2 a = widen4(q.x), b = widen4(q.y), c = widen4(q.z), d = widen4(q.w);
+                *reinterpret_cast<uint4 *>(dst + (((2 * chunk) ^ row_in) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<uint4 *>(dst + (((2 * chunk + 1) ^ row_in) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(ptx::smem_u32(&raw_empty[rs]));
+                if (kG == 2)
+                    ptx::mbar_arrive_remote(ready0 + 8u * stage);
+                else
+                    ptx::mbar_arrive(ready0 + 8u * stage);
+            }
+            if (++rs == ring) rs = 0, raw_phase ^= 1u;
+            if (++stage == S) stage = 0, phase ^= 1u;
+        }
+        if (!ok && lane == 0) atomicExch(&failed, 1);
+    } else if (!kCodes && warp != 1 && producer < producers) {
         // stages producer, producer + producers, ...; the warp stays converged, an elected lane issues
         int i = producer, stage = producer;
         uint32_t phase = 1;
@@ -330,10 +457,10 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
             ptx::nanosleep(20000);
         }
     } else if (warp == 1 && !half) {
-        const uint32_t idesc = ptx::idesc_f16(kBF16, false, kTileN * kG, p.rows, p.w_kn != 0);
+        const uint32_t idesc = ptx::idesc_f16(kBF16 && !kCodes, false, kTileN * kG, p.rows, p.w_kn != 0);
         const uint32_t s0 = ptx::smem_u32(smem);
         const uint64_t w_desc = p.w_kn ? ptx::smem_desc_sw128(s0, kDepth * 128, 1024) : ptx::smem_desc_sw128(s0, 16, 1024);
-        const uint64_t x_desc = ptx::smem_desc_sw128(s0 + kWBytes, 16, 1024);
+        const uint64_t x_desc = ptx::smem_desc_sw128(s0 + (kCodes ? 2 : 1) * kWBytes, 16, 1024);
         // (a stage's addresses stay within the descriptors' low words)
         const uint32_t w_hi = static_cast<uint32_t>(w_desc >> 32), w_lo0 = static_cast<uint32_t>(w_desc);
         const uint32_t x_hi = static_cast<uint32_t>(x_desc >> 32), x_lo0 = static_cast<uint32_t>(x_desc);
@@ -348,10 +475,11 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
         for (int done = 0, block = 0, acc = 0; done < count && ok; ++block) {
             const uint32_t d = tmem + static_cast<uint32_t>(acc * p.rows);
             uint32_t add = block >= p.accs ? 1u : 0u;   // an accumulator's first stage starts it from zero
-            const int end = min(done + kBlockSteps, count);
+            const int end = min(done + kBlockDepth / kStep, count);
             for (; done < end; ++done) {
-                if (!__all_sync(0xffffffffu, ready)) {
-                    ready = ptx::mbar_wait(full, phase, p.wait_limit_ns);
+                // (codes: the pair's other CTA arrives here, too)
+                if (kCodes || !__all_sync(0xffffffffu, ready)) {
+                    ready = kCodes && kG == 2 ? ptx::mbar_wait_cluster(full, phase, p.wait_limit_ns) : ptx::mbar_wait(full, phase, p.wait_limit_ns);
                     if (!__all_sync(0xffffffffu, ready)) {
                         ok = false;
                         break;
@@ -363,8 +491,14 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
                 full += 8;
                 off += advance;
                 if (full == full_end) full = full0, off = 0, phase ^= 1u;
-                ready = ptx::mbar_test(full, phase);
-                ptx::mma_stage_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add, bar, pair);
+                if (!kCodes) ready = ptx::mbar_test(full, phase);
+                if constexpr (kCodes) {
+                    ptx::mma_four_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add);
+                    ptx::mma_stage_f16_ss<kG>(d, w_lo + (kWBytes >> 4), w_hi, w_kk, x_lo + static_cast<uint32_t>(x_rows * 128 >> 4), x_hi, x_kk,
+                                              idesc, 1, bar, pair);
+                } else {
+                    ptx::mma_stage_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add, bar, pair);
+                }
                 add = 1;
             }
             if (++acc == p.accs) acc = 0;
@@ -375,7 +509,7 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
             ptx::mma_commit_pair(ptx::smem_u32(&done_bar), pair);
         else
             ptx::mma_commit<1>(ptx::smem_u32(&done_bar));
-    } else if (warp > kProducers && p.aux) {
+    } else if (!kCodes && warp > kProducers && p.aux) {
         // the other warps: the part of aux that this CTA will need, into L1
         constexpr int kIdle = kThreads / 32 - kProducers - 1;
         const uint16_t *aux = static_cast<const uint16_t *>(p.aux) + (static_cast<int64_t>(m0) + t0) * p.ldaux + n0;
@@ -383,7 +517,7 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
             if (n0 + (e & 1) * 64 < p.n) ptx::prefetch_l1(aux + (e >> 1) * p.ldaux + (e & 1) * 64);
     }
     __syncwarp();
-    const Place at = place<kBF16>(p, static_cast<int64_t>(m0) + t0, n0 + 4 * lane);
+    const Place at = place<kBF16, kEpi>(p, static_cast<int64_t>(m0) + t0, n0 + 4 * lane);
     // every thread waits (bounded) for the MMAs: from here on the ring is idle
     if (!ptx::mbar_wait(ptx::smem_u32(&done_bar), 0u, p.wait_limit_ns)) atomicExch(&failed, 1);
     __syncthreads();
@@ -401,7 +535,7 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
     {
         constexpr int kChunk = kG == 1 ? 16 : 32;
         const int group = warp >> 2, q = warp & 3;
-        const int used = min(p.accs, (count + kBlockSteps - 1) / kBlockSteps);
+        const int used = min(p.accs, (count + kBlockDepth / kStep - 1) / (kBlockDepth / kStep));
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
         // chunks [own0, own1) hold own tokens only; the others come in the order own1, ..., then 0, ...
         const int chunks = (live + kChunk - 1) / kChunk;
@@ -421,7 +555,12 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
                     ptx::tmem_ld_wait16(r);
                 }
 #pragma unroll
-                for (int e = 0; e < kChunk; ++e) sum[e] = __fadd_rn(sum[e], __uint_as_float(r[e]));
+                for (int e = 0; e < kChunk; ++e) {
+                    if constexpr (kCodes)   // an int32, as its bits
+                        sum[e] = __int_as_float(__float_as_int(sum[e]) + __float2int_rn(__uint_as_float(r[e])));
+                    else
+                        sum[e] = __fadd_rn(sum[e], __uint_as_float(r[e]));
+                }
             }
             float *to = part + c * kTileN + 32 * q + lane;
 #pragma unroll
@@ -473,7 +612,8 @@ __global__ void __launch_bounds__(split_threads(kG), 1) linear_split_kernel(cons
 // The shape of a launch.
 struct SplitShape {
     int group, rows, m_tiles, split, per_sm, stages, accs, tmem_cols, late, prefetch;
-    uint32_t smem, recv_off;
+    int raws;   // int8 codes: stages of them as they are (0: 16-bit operands)
+    uint32_t smem, recv_off, raw_off;
     int64_t tiles;
     float us;   // what it is expected to take
 };
@@ -485,27 +625,38 @@ bool prefetch_pays(const SplitShape &s, int num_sms) {
     return s.group == 1 && s.per_sm == 2 && s.tiles * s.split * 8 >= num_sms * 13ll;
 }
 
-// Shared memory and TMEM of a launch whose tiles and split are chosen.
-void fit_split(SplitShape &s, int steps, int num_sms) {
+// Shared memory and TMEM of a launch whose tiles and split are chosen; false if it has none.
+bool fit_split(SplitShape &s, int steps, int num_sms, bool codes) {
     const int most = (steps + s.split - 1) / s.split;   // stages of one CTA
-    const uint32_t stage = kWBytes + static_cast<uint32_t>(s.rows / s.group) * kDepth * 2;
+    const int block_steps = kBlockDepth / (codes ? kDepth8 : kDepth);
+    // (the bytes of a 16-bit stage; of codes, those of a stage as it is, half of the widened one)
+    const uint32_t stage = codes ? static_cast<uint32_t>(kTileN + s.rows / s.group) * kDepth8
+                                 : kWBytes + static_cast<uint32_t>(s.rows / s.group) * kDepth * 2;
     const uint32_t room = s.per_sm == 2 ? 110u * 1024u : 220u * 1024u;
     const uint32_t sums = static_cast<uint32_t>(s.rows) * kTileN * 4;   // this CTA's, over the ring
     const uint32_t recv = static_cast<uint32_t>((s.split - 1) * ((s.rows + s.split - 1) / s.split)) * kTileN * 4;
-    int full = static_cast<int>(room / stage);
+    // two widened stages: the MMAs take one while the other is filled
+    const uint32_t before = codes ? 2u * 2u * stage : 0u;
+    int full = static_cast<int>((room - before) / stage);
     if (full > kMaxStages) full = kMaxStages;
     if (full > most) full = most;
     // the others' sums beside the ring, or, where that would shorten it, over it (256 tokens,
     // 4096 x 4096, split in two: 0.6 us less than with a shorter ring)
-    s.stages = static_cast<int>((room - recv) / stage);
-    s.late = s.stages < full && s.group == 2;
-    if (s.late || s.stages > full) s.stages = full;
-    const uint32_t ring = s.stages * stage;
+    int ring_stages = recv + before < room ? static_cast<int>((room - before - recv) / stage) : 0;
+    s.late = ring_stages < full && s.group == 2;
+    if (s.late || ring_stages > full) ring_stages = full;
+    if (ring_stages < 1) return false;
+    const uint32_t ring = before + ring_stages * stage;
+    s.stages = codes ? 2 : ring_stages;
+    s.raws = codes ? ring_stages : 0;
+    s.raw_off = before;
     s.recv_off = s.late || ring < sums ? sums : ring;
     const uint32_t bytes = ring > s.recv_off + recv ? ring : s.recv_off + recv;
     s.smem = bytes + 1024;   // (slack to align the ring)
-    const int blocks = (most + kBlockSteps - 1) / kBlockSteps;
+    const int blocks = (most + block_steps - 1) / block_steps;
     s.accs = (s.per_sm == 2 ? 256 : 512) / s.rows;
+    // (integer sums stay exact in an accumulator of their own for each block)
+    if (codes && s.accs < blocks) return false;
     if (s.accs > blocks) s.accs = blocks;
     s.tmem_cols = 32;
     while (s.tmem_cols < s.accs * s.rows) s.tmem_cols *= 2;
@@ -516,7 +667,9 @@ void fit_split(SplitShape &s, int steps, int num_sms) {
     // CTAs that fit beside one another find their columns free.
     const uint32_t share = static_cast<uint32_t>(s.tmem_cols) * (kSmemPerSm / 512) - kSmemOverhead;
     if (s.smem < share) s.smem = share;
-    s.prefetch = prefetch_pays(s, num_sms);
+    if (codes && s.smem > kMostSmemCodes) return false;
+    s.prefetch = codes || prefetch_pays(s, num_sms);
+    return true;
 }
 
 // Clusters of `ctas` CTAs, one an SM, that the device runs at once.  A cluster stays inside
@@ -537,11 +690,11 @@ int clusters_at_once(int ctas, int num_sms) {
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(ctas * num_sms), 1, 1);
-        cfg.blockDim = dim3(split_threads(1), 1, 1);
+        cfg.blockDim = dim3(split_threads(1, false), 1, 1);
         cfg.dynamicSmemBytes = 222 * 1024;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - kSmemStatic) != cudaSuccess ||
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
             n = num_sms / ctas > 0 ? num_sms / ctas : 1;
@@ -578,8 +731,23 @@ float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sm
     return 2.1f + (s.group == 2 ? 0.17f : 0.0f) + stream + waves * join + 2.0f * (waves - 1.0f) - (s.prefetch ? fminf(0.5f, 0.1f * read) : 0.0f);
 }
 
+// The same for int8 codes: a 128-deep stage is bound by its MMAs, by its bytes, or by the warps that widen it.
+float split_codes_us(const SplitShape &s, const LinearParams &p, int steps, int num_sms) {
+    const int64_t clusters = clusters_at_once(s.group * s.split, num_sms);
+    const float waves = static_cast<float>((s.tiles + clusters - 1) / clusters);
+    const float rows = static_cast<float>(kTileN + s.rows / s.group);
+    const float stage = fmaxf(fmaxf(0.00204f * s.rows, rows * kDepth8 / 90e3f), rows / 4 * (s.group == 2 ? 0.006f : 0.0085f));
+    const float stages = waves * ((steps + s.split - 1) / s.split) * stage;
+    const float read = static_cast<float>(p.n) * static_cast<float>(p.k) / 7.0e6f;
+    const float stream = sqrtf(stages * stages + read * read);
+    float join = 0.017f * s.rows;
+    if (s.split > 1) join += 0.14f + 0.063f * s.split + 0.0116f * s.rows * (s.split - 1) / s.split;
+    return 2.5f + stream + waves * join + 2.0f * (waves - 1.0f);
+}
+
 SplitShape best_split(const LinearParams &p, int num_sms) {
-    const int steps = (p.k + kDepth - 1) / kDepth;
+    const bool codes = p.x_scale != nullptr;
+    const int steps = codes ? (p.k + kDepth8 - 1) / kDepth8 : (p.k + kDepth - 1) / kDepth;
     SplitShape best = {};
     // tiles of at most 64 tokens by single CTAs; of 64, 128 or 256 by pairs
     const struct { int group, most; } forms[4] = {{1, 64}, {2, 64}, {2, 128}, {2, 256}};
@@ -595,9 +763,9 @@ SplitShape best_split(const LinearParams &p, int num_sms) {
         for (s.split = 1; s.split <= kMaxCluster / f.group && s.split <= steps; ++s.split) {
             // two CTAs an SM where there are more than SMs and their stages are short: 0.2 us less for one token, 4096 x 4096;
             // but 1.7 us more for 32 tokens, 1024 x 8192, 64 CTAs
-            s.per_sm = f.group == 1 && s.rows <= 32 && s.tiles > clusters_at_once(s.split, num_sms) ? 2 : 1;
-            fit_split(s, steps, num_sms);
-            s.us = split_us(s, p, steps, num_sms);
+            s.per_sm = !codes && f.group == 1 && s.rows <= 32 && s.tiles > clusters_at_once(s.split, num_sms) ? 2 : 1;
+            if (!fit_split(s, steps, num_sms, codes)) continue;
+            s.us = codes ? split_codes_us(s, p, steps, num_sms) : split_us(s, p, steps, num_sms);
             if (best.group == 0 || s.us < best.us) best = s;
         }
     }
@@ -611,7 +779,7 @@ cudaError_t launch_split(const SplitParams &p, const SplitShape &s, cudaStream_t
     const unsigned long long ctx = current_context_id();
     if (ctx == 0 || ctx != ready_ctx) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             227 * 1024 - kSmemStatic);
+                                             kEpi == EPI_SCALED ? kMostSmemCodes : kMostSmem);
         if (e != cudaSuccess) return e;
         ready_ctx = ctx;
     }
@@ -624,7 +792,7 @@ cudaError_t launch_split(const SplitParams &p, const SplitShape &s, cudaStream_t
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(s.tiles * s.split * kG), 1, 1);
-    cfg.blockDim = dim3(split_threads(kG), 1, 1);
+    cfg.blockDim = dim3(split_threads(kG, kEpi == EPI_SCALED), 1, 1);
     cfg.dynamicSmemBytes = s.smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -657,26 +825,37 @@ bool linear_prefers_split(const LinearParams &p, int num_sms) {
     // 24.0 against 25.5, 1536 43.8 against 42.7.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256), pairs = num_sms / 2;
     const SplitShape s = best_split(p, num_sms);
-    const int steps = (p.k + kDepth - 1) / kDepth, blocks = ((steps + s.split - 1) / s.split + kBlockSteps - 1) / kBlockSteps;
+    const int steps = (p.k + kDepth - 1) / kDepth, blocks = ((steps + s.split - 1) / s.split * kDepth + kBlockDepth - 1) / kBlockDepth;
     // where the tiles fill the device, no sum is left deeper in one accumulator than it would be in theirs
-    if (tiles >= pairs && (blocks + s.accs - 1) / s.accs * kBlockSteps > linear_tiles_block(p.k)) return false;
+    if (tiles >= pairs && (blocks + s.accs - 1) / s.accs * (kBlockDepth / kDepth) > linear_tiles_block(p.k)) return false;
     const float us = 6.3f + 0.29f * static_cast<float>((tiles + pairs - 1) / pairs) * steps;
     return s.us < us;
 }
 
+float linear_split_codes_us(const LinearParams &p, int num_sms) {
+    const SplitShape s = best_split(p, num_sms);
+    return s.group == 0 ? -1.0f : s.us;
+}
+
 cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, cudaStream_t stream) {
     const SplitShape s = best_split(lp, num_sms);
-    if (s.tiles * s.split * s.group > INT32_MAX) return cudaErrorInvalidValue;
+    if (s.group == 0 || s.tiles * s.split * s.group > INT32_MAX) return cudaErrorInvalidValue;
     SplitParams p = {};
     const uint64_t m = lp.m, n = lp.n, k = lp.k;
-    bool ok = host::make_map16(&p.x_map, lp.x, k, m, kDepth, static_cast<uint32_t>(s.rows / s.group), lp.ldx);
-    ok = ok && (lp.w_nk ? host::make_map16(&p.w_map, lp.w, k, n, kDepth, kTileN, lp.ldw)
-                        : host::make_map16(&p.w_map, lp.w, n, k, 64, kDepth, lp.ldw));
+    bool ok;
+    if (lp.x_scale)
+        ok = host::make_map8(&p.x_map, lp.x, k, m, static_cast<uint32_t>(s.rows / s.group), lp.ldx) &&
+             host::make_map8(&p.w_map, lp.w, lp.w_nk ? k : n, lp.w_nk ? n : k, 128, lp.ldw);
+    else
+        ok = host::make_map16(&p.x_map, lp.x, k, m, kDepth, static_cast<uint32_t>(s.rows / s.group), lp.ldx);
+    if (!lp.x_scale)
+        ok = ok && (lp.w_nk ? host::make_map16(&p.w_map, lp.w, k, n, kDepth, kTileN, lp.ldw)
+                            : host::make_map16(&p.w_map, lp.w, n, k, 64, kDepth, lp.ldw));
     if (!ok) return cudaErrorInvalidValue;
     p.bias = lp.bias, p.aux = lp.aux_mode == AUX_NONE ? nullptr : lp.aux, p.out = lp.out, p.preact = lp.preact;
     p.ldaux = lp.ldaux, p.ldo = lp.ldo, p.ldp = lp.ldp;
     p.m = lp.m, p.n = lp.n;
-    const int steps = (lp.k + kDepth - 1) / kDepth;
+    const int steps = lp.x_scale ? (lp.k + kDepth8 - 1) / kDepth8 : (lp.k + kDepth - 1) / kDepth;
     p.steps = steps / s.split, p.more = steps % s.split;
     p.share = ((lp.m < s.rows ? lp.m : s.rows) + s.split - 1) / s.split;
     p.m_tiles_inv = UINT64_MAX / static_cast<uint64_t>(s.m_tiles) + 1;   // (0 for one tile: not used)
@@ -687,6 +866,14 @@ cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, 
     p.act = activation_of(lp.act);
     p.status = device_status_word();
     p.wait_limit_ns = host::kWaitLimitNs;
+    if (lp.x_scale) {
+        p.x_scale = lp.x_scale, p.w_scale = lp.w_scale, p.bias_f32 = lp.bias_f32;
+        p.raws = s.raws, p.raw_off = s.raw_off;
+        const auto words = [](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 8 == 0 && ld % 4 == 0; };
+        p.words = words(lp.out, lp.ldo) && (!p.aux || words(p.aux, lp.ldaux));
+        if (s.group == 1) return bf16 ? launch_split<true, EPI_SCALED, 1>(p, s, stream) : launch_split<false, EPI_SCALED, 1>(p, s, stream);
+        return bf16 ? launch_split<true, EPI_SCALED, 2>(p, s, stream) : launch_split<false, EPI_SCALED, 2>(p, s, stream);
+    }
     const bool back = lp.aux_mode == AUX_ACT_GRAD;
     if (s.group == 1) {
         if (back) return bf16 ? launch_split<true, EPI_BACKWARD, 1>(p, s, stream) : launch_split<false, EPI_BACKWARD, 1>(p, s, stream);

@@ -80,13 +80,14 @@ static EncodeTiledFn encode_fn() {
 struct MapKey {
     const void *base;
     uint64_t inner, outer, pitch;
-    uint32_t box_inner, box_outer, groups;  // groups 0: a 2-D map
+    uint32_t box_inner, box_outer, groups;  // groups 0: a 2-D map, kMap8: one of 8-bit elements
     bool operator==(const MapKey &o) const {
         return base == o.base && inner == o.inner && outer == o.outer && pitch == o.pitch && box_inner == o.box_inner &&
                box_outer == o.box_outer && groups == o.groups;
     }
 };
 
+constexpr uint32_t kMap8 = UINT32_MAX;
 constexpr int kMapCacheSlots = 64;
 struct MapCacheSlot {
     MapKey key;
@@ -157,6 +158,28 @@ bool make_map16_nmajor3d(CUtensorMap *m, const void *base, uint64_t inner, uint6
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return false;
+    slot.key = key;
+    slot.map = *m;
+    slot.used = true;
+    return true;
+}
+
+bool make_map8(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint32_t box_outer, uint64_t pitch) {
+    const MapKey key{base, inner, outer, pitch, 128, box_outer, kMap8};
+    MapCacheSlot &slot = map_slot(key);
+    if (slot.used && slot.key == key) {
+        *m = slot.map;
+        return true;
+    }
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {pitch};
+    cuuint32_t box[2] = {128, box_outer};
+    cuuint32_t estr[2] = {1, 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
     slot.key = key;
     slot.map = *m;
     slot.used = true;

@@ -189,4 +189,13 @@ __device__ __forceinline__ uint32_t mx_code(uint32_t amax, int kind) {
 // 2^-(code - 127), the factor from a value to its code's value (codes of finite groups)
 __device__ __forceinline__ float mx_inverse(uint32_t code) { return __uint_as_float((254u - code) << 23); }
 
+// Four int8 codes, as a word, to four halves (exact): 0x6400 + u is the half 1024 + u, so with u = q + 128 it is 1152 too large.
+__device__ __forceinline__ uint2 widen4(uint32_t q) {
+    const uint32_t u = q ^ 0x80808080u;
+    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __half2half2(__ushort_as_half(0x6480));
+    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), k), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), k);
+    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+
 }  // namespace mc2

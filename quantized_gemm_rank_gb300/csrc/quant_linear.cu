@@ -5,7 +5,8 @@
 //   dw[i, j]  = sum_t dy[t, i] act(q[t, j] scale),  db[i] = sum_t dy[t, i]
 //
 // The tensor cores take 16-bit operands (their int8 rate is a tenth of it here).  int8 codes are exact in fp16, and so are
-// the fp32 sums of 1024 of their products; act(q scale) is rounded to dy's type.  The operands of many rows are
+// the fp32 sums of 1024 of their products; act(q scale) is rounded to dy's type.  The codes of few tokens are widened on
+// their way to the tensor cores (linear_split.cu): the weight is read once, as bytes.  The operands of many rows are
 // brought to 16 bits in the workspace, each element once, and multiplied by the GEMM of gemm_tcgen05.cuh; matrices that the
 // tensor copies cannot take go through the workspace, too.
 #include "kept.h"
@@ -20,27 +21,19 @@ namespace mc2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPairs = 76;   // CTA pairs of a GB300 (the plans, and so the workspace queries, ask no device)
+constexpr int kSms = 152, kPairs = kSms / 2;   // of a GB300 (the plans, and so the workspace queries, ask no device)
 
-// A matrix of int8 and where it goes as fp16, in rows `pitch` apart (a multiple of 8).
+// A matrix of int8 and where it goes, in rows `pitch` apart (a multiple of 16): as fp16, or as it is.
 struct Widened {
     const int8_t *src;
-    __half *dst;
+    void *dst;
     int64_t ld, pitch, rows;
     int64_t cols;
     int64_t vectors;   // 16 columns each
 };
 
-// Four codes, as a word, to four halves: 0x6400 + u is the half 1024 + u, so with u = q + 128 it is 1152 too large.
-__device__ __forceinline__ uint2 widen4(uint32_t q) {
-    const uint32_t u = q ^ 0x80808080u;
-    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 k = __half2half2(__ushort_as_half(0x6480));
-    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), k), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), k);
-    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
-}
-
-// Both operands of a product in one launch: blocks [0, first) widen a, the others b, 16 codes a thread at a time.
+// Both operands of a product in one launch: blocks [0, first) take a, the others b, 16 codes a thread at a time.
+template <bool kWiden>
 __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ Widened a, const __grid_constant__ Widened b, int first) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
@@ -73,11 +66,16 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
                     if (4 * i + j < left) q[i] |= static_cast<uint32_t>(static_cast<uint8_t>(from[4 * i + j])) << (8 * j);
             }
         }
-        uint4 *to = reinterpret_cast<uint4 *>(t.dst + r * t.pitch + v * 16);
+        // (a row's last vector is whole, zeros behind its end)
+        if constexpr (kWiden) {
+            uint4 *to = reinterpret_cast<uint4 *>(static_cast<__half *>(t.dst) + r * t.pitch + v * 16);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint2 lo = widen4(q[2 * i]), hi = widen4(q[2 * i + 1]);
-            if (8 * i < left) to[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);   // (a row ends inside its pitch, a multiple of 8)
+            for (int i = 0; i < 2; ++i) {
+                const uint2 lo = widen4(q[2 * i]), hi = widen4(q[2 * i + 1]);
+                to[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<int8_t *>(t.dst) + r * t.pitch + v * 16) = make_uint4(q[0], q[1], q[2], q[3]);
         }
     }
 }
@@ -152,11 +150,15 @@ int64_t blocks_for(int64_t items, int num_sms) {
 }
 
 int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
 // What the tensor copies take: 16-byte aligned, rows a multiple of 16 bytes (and less than 2^40) apart; writes go in units of
 // 16 bytes, so an output's rows are whole units.
 bool copies_read16(const void *p, int64_t ld, int64_t rows) {
     return host::aligned16(p) && (rows == 1 || (ld % 8 == 0 && ld < (1ll << 39)));
+}
+bool copies_read8(const void *p, int64_t ld, int64_t rows) {
+    return host::aligned16(p) && (rows == 1 || (ld % 16 == 0 && ld < (1ll << 40)));
 }
 bool copies_write16(const void *p, int64_t ld, int64_t rows, int64_t cols) { return copies_read16(p, ld, rows) && cols % 8 == 0; }
 
@@ -172,18 +174,48 @@ struct Pieces {
 
 struct ProductPlan {
     size_t x = 0, w = 0, out = 0, total = 0;
-    bool out_apart = false;    // the output goes through the workspace
+    bool split = false;        // the kernel of few tokens, on int8 operands
+    bool apart = false;        // the operands go through the workspace (the tiles': always)
+    bool out_apart = false;    // the output, too
     bool residual_in = false;  // the residual is copied to where the output will be
 };
 
+// The matrices and sizes as the product kernels take them.
+LinearParams product_of(const QuantProduct &p) {
+    LinearParams l = {};
+    l.m = p.m, l.n = p.n, l.k = p.k;
+    l.w_nk = p.w_nk;
+    l.act = p.act;
+    l.bias = p.bias, l.bias_f32 = p.bias_f32;
+    l.aux_mode = p.residual ? AUX_RESIDUAL : AUX_NONE;
+    l.x_scale = p.x_scale, l.w_scale = p.w_scale;
+    return l;
+}
+
 ProductPlan plan_product(const QuantProduct &p) {
     ProductPlan at;
+    // which kernel, by the sizes alone: the tiles take 6.3 us and 0.3 a 64-deep stage for each wave of them, and widening
+    // three bytes a code at 5500 a ns and a launch
+    const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256);
+    const float steps = static_cast<float>((p.k + 63) / 64);
+    const float tiles_us = 9.3f + 0.3f * static_cast<float>((tiles + kPairs - 1) / kPairs) * steps +
+                           (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 3.0f / 5.5e6f;
+    LinearParams l = product_of(p);
+    l.x_scale = reinterpret_cast<const float *>(p.x);   // (codes; not read)
+    const float split_us = linear_split_codes_us(l, kSms);
+    at.split = split_us >= 0.0f && split_us < tiles_us;
     Pieces ws;
-    at.x = ws.take(p.m * up8(p.k), 2);
-    at.w = p.w_nk ? ws.take(p.n * up8(p.k), 2) : ws.take(p.k * up8(p.n), 2);
-    at.out_apart = !copies_write16(p.out, p.ldo, p.m, p.n);
-    at.residual_in = p.residual && (at.out_apart || !copies_read16(p.residual, p.ldr, p.m));
-    if (at.out_apart) at.out = ws.take(p.m * up8(p.n), 2);
+    const int64_t w_rows = p.w_nk ? p.n : p.k, w_cols = p.w_nk ? p.k : p.n;
+    at.apart = !at.split || !copies_read8(p.x, p.ldx, p.m) || !copies_read8(p.w, p.ldw, w_rows);
+    if (at.apart) {
+        at.x = ws.take(p.m * up16(p.k), at.split ? 1 : 2);
+        at.w = ws.take(w_rows * up16(w_cols), at.split ? 1 : 2);
+    }
+    if (!at.split) {
+        at.out_apart = !copies_write16(p.out, p.ldo, p.m, p.n);
+        at.residual_in = p.residual && (at.out_apart || !copies_read16(p.residual, p.ldr, p.m));
+        if (at.out_apart) at.out = ws.take(p.m * up8(p.n), 2);
+    }
     at.total = ws.total;
     return at;
 }
@@ -237,22 +269,36 @@ size_t quant_product_workspace(const QuantProduct &p) { return plan_product(p).t
 cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, cudaStream_t stream, Mark mark, void *ctx) {
     const ProductPlan at = plan_product(p);
     char *ws = static_cast<char *>(p.workspace);
-    __half *xh = reinterpret_cast<__half *>(ws + at.x), *wh = reinterpret_cast<__half *>(ws + at.w);
-    const auto widened = [](const int8_t *src, int64_t ld, __half *dst, int64_t rows, int64_t cols) {
-        Widened t = {src, dst, ld, up8(cols), rows, cols, (cols + 15) / 16};
-        // matrices without gaps are one row
-        if (rows > 1 && ld == cols && cols % 8 == 0) t.cols = rows * cols, t.rows = 1, t.vectors = (t.cols + 15) / 16;
-        return t;
-    };
-    const Widened a = widened(p.x, p.ldx, xh, p.m, p.k);
-    const Widened b = p.w_nk ? widened(p.w, p.ldw, wh, p.n, p.k) : widened(p.w, p.ldw, wh, p.k, p.n);
-    // blocks in proportion to the elements
-    const int64_t na = a.rows * a.vectors, nb = b.rows * b.vectors, blocks = blocks_for(na + nb, num_sms) + 1;
-    int64_t first = static_cast<int64_t>(static_cast<double>(blocks) * na / (na + nb) + 0.5);
-    first = first < 1 ? 1 : (first > blocks - 1 ? blocks - 1 : first);
-    cudaError_t e = launch(widen_kernel, blocks, stream, a, b, static_cast<int>(first));
-    if (e != cudaSuccess) return e;
-    mark(ctx);
+    LinearParams l = product_of(p);
+    const int64_t w_rows = p.w_nk ? p.n : p.k, w_cols = p.w_nk ? p.k : p.n;
+    cudaError_t e = cudaSuccess;
+    // (the stride of a single row is free: one that the tensor copies take)
+    l.x = p.x, l.ldx = p.m == 1 ? up16(p.k) : p.ldx;
+    l.w = p.w, l.ldw = w_rows == 1 ? up16(w_cols) : p.ldw;
+    if (at.apart) {
+        const auto taken = [&](const int8_t *src, int64_t ld, void *dst, int64_t rows, int64_t cols) {
+            Widened t = {src, dst, ld, up16(cols), rows, cols, (cols + 15) / 16};
+            // matrices without gaps are one row
+            if (rows > 1 && ld == cols && cols % 16 == 0) t.cols = rows * cols, t.rows = 1, t.vectors = t.cols / 16;
+            return t;
+        };
+        const Widened a = taken(p.x, p.ldx, ws + at.x, p.m, p.k), b = taken(p.w, p.ldw, ws + at.w, w_rows, w_cols);
+        // blocks in proportion to the elements
+        const int64_t na = a.rows * a.vectors, nb = b.rows * b.vectors, blocks = blocks_for(na + nb, num_sms) + 1;
+        int64_t first = static_cast<int64_t>(static_cast<double>(blocks) * na / (na + nb) + 0.5);
+        first = first < 1 ? 1 : (first > blocks - 1 ? blocks - 1 : first);
+        e = launch(at.split ? widen_kernel<false> : widen_kernel<true>, blocks, stream, a, b, static_cast<int>(first));
+        if (e != cudaSuccess) return e;
+        mark(ctx);
+        l.x = ws + at.x, l.ldx = up16(p.k);
+        l.w = ws + at.w, l.ldw = up16(w_cols);
+    }
+    if (at.split) {
+        l.out = p.out, l.ldo = p.ldo, l.aux = p.residual, l.ldaux = p.ldr;
+        e = launch_linear_split(bf16, l, kSms, stream);
+        if (e == cudaSuccess) mark(ctx);
+        return e;
+    }
     void *out = at.out_apart ? static_cast<void *>(ws + at.out) : p.out;
     const int64_t ldo = at.out_apart || p.m == 1 ? up8(p.n) : p.ldo;
     if (at.residual_in) {
@@ -261,16 +307,9 @@ cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, 
         if (e != cudaSuccess) return e;
         mark(ctx);
     }
-    LinearParams l = {};
-    l.x = xh, l.w = wh, l.bias = p.bias, l.out = out;
+    l.out = out, l.ldo = ldo;
     l.aux = at.residual_in ? out : p.residual;
-    l.ldx = up8(p.k), l.ldw = p.w_nk ? up8(p.k) : up8(p.n), l.ldo = ldo;
     l.ldaux = at.residual_in ? ldo : (p.m == 1 ? up8(p.n) : p.ldr);
-    l.m = p.m, l.n = p.n, l.k = p.k;
-    l.w_nk = p.w_nk;
-    l.act = p.act;
-    l.aux_mode = p.residual ? AUX_RESIDUAL : AUX_NONE;
-    l.x_scale = p.x_scale, l.w_scale = p.w_scale, l.bias_f32 = p.bias_f32;
     e = launch_linear_tiles(bf16, l, stream);
     if (e != cudaSuccess) return e;
     mark(ctx);

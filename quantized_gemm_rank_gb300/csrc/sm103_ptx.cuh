@@ -418,6 +418,46 @@ __device__ __forceinline__ void mma_stage_f16_ss(uint32_t d_tmem, uint32_t a_lo,
             : "memory");
 }
 
+// The four MMAs alone.
+template <int kG>
+__device__ __forceinline__ void mma_four_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t a_step, uint32_t b_lo,
+                                                uint32_t b_hi, uint32_t b_step, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (kG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t.reg .b32 al, bl;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+            "setp.eq.b32 p, %6, %6;\n\t"
+            "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t.reg .b32 al, bl;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
+            "setp.eq.b32 p, %6, %6;\n\t"
+            "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
+            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
+            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step)
+            : "memory");
+}
+
 // Arrive on `bar` once all previously issued tcgen05 ops of this thread
 // complete; with kG = 2 the arrival goes to the barrier at the same offset in
 // both CTAs of the pair.

@@ -87,8 +87,11 @@ def test_workspace_queries():
     L, n = mc2.lib(), ctypes.c_size_t(1)
     ref = ctypes.byref(n)
     f = L.mc2_quant_matmul_workspace
-    good = (FAKE, 64, FAKE, 64, 1, 400, 32, 64, None, 0, FAKE, 32, ref)
-    assert f(*good) == mc2.MC2_OK and n.value > 0
+    good = (FAKE, 4096, FAKE, 4096, 1, 4096, 4096, 4096, None, 0, FAKE, 4096, ref)
+    assert f(*good) == mc2.MC2_OK and n.value >= 2 * 2 * 4096 * 4096   # both operands in 16 bits
+    few = (*good[:5], 1, *good[6:])
+    assert f(*few) == mc2.MC2_OK and n.value == 0
+    assert f(FAKE + 1, *few[1:]) == mc2.MC2_OK and n.value > 4096 * 4096
     for at, value, status in ((0, None, mc2.MC2_ERR_NULL), (2, None, mc2.MC2_ERR_NULL), (10, None, mc2.MC2_ERR_NULL), (12, None, mc2.MC2_ERR_NULL),
                               (5, 0, mc2.MC2_ERR_SHAPE), (1, 8, mc2.MC2_ERR_SHAPE), (11, 31, mc2.MC2_ERR_SHAPE)):
         assert f(*good[:at], value, *good[at + 1:]) == status
@@ -102,9 +105,10 @@ def test_workspace_queries():
 
 @pytest.mark.parametrize("kw", [dict(wk=None), dict(nbytes=64)])
 def test_a_workspace_that_is_missing_or_small(kw):
-    assert product(**kw) == mc2.MC2_ERR_WORKSPACE
+    many = dict(m=4096, n=4096, k=4096, ldx=4096, ldw=4096, ldo=4096)
+    assert product(**many, **kw) == mc2.MC2_ERR_WORKSPACE
     assert weight(**kw) == mc2.MC2_ERR_WORKSPACE
-    assert product(wk=FAKE + 8) == mc2.MC2_ERR_UNSUPPORTED and weight(wk=FAKE + 8) == mc2.MC2_ERR_UNSUPPORTED
+    assert product(**many, wk=FAKE + 8) == mc2.MC2_ERR_UNSUPPORTED and weight(wk=FAKE + 8) == mc2.MC2_ERR_UNSUPPORTED
 
 
 def refuses(match, f, *a, **kw):
