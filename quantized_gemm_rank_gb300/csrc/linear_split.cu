@@ -29,6 +29,7 @@
 // tokens: 6144 deep each for 2000 x 1024 x 24576, split in two).
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "epilogue.cuh"
 #include "host.h"
@@ -47,8 +48,11 @@ constexpr int kMaxStages = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kProducers = 2;
 // Threads a CTA: the pairs' tiles have more to bring out of TMEM and one CTA an SM; codes have warps that widen them.
-__host__ __device__ constexpr int split_threads(int group, bool codes) { return group == 2 ? 512 : (codes ? 384 : 256); }
+__host__ __device__ constexpr int split_threads(int group, bool codes) { return group == 2 || codes ? 512 : 256; }
 constexpr int kWidenFirst = 4;   // the first of those warps; the others are producers, MMA, and one that is idle
+constexpr int kWidenTeam = 4;    // warps that widen a stage together, one for each quarter of TMEM's lanes
+constexpr int kMaxTeams = 3;
+static_assert(kWidenFirst % 4 == 0 && kWidenFirst + kMaxTeams * kWidenTeam <= split_threads(1, true) / 32, "warps of the teams");
 constexpr int kBlockDepth = 1024;   // of one accumulator
 constexpr uint32_t kWBytes = kTileN * kDepth * 2;
 constexpr uint32_t kSmemPerSm = 228 * 1024;
@@ -79,8 +83,8 @@ struct SplitParams {
     // int8 codes (EPI_SCALED)
     const float *x_scale, *w_scale;
     int bias_f32;
-    int raws;                 // stages of codes, from raw_off on
-    uint32_t raw_off;
+    int raws, teams;          // stages of codes, from raw_off on; teams that widen them
+    uint32_t raw_off, a_cols; // ... and the weight's widened stages in TMEM, from this column on (K-major)
     int words;                // rows of out and aux begin at multiples of 8 bytes
 };
 
@@ -238,7 +242,6 @@ template <bool kBF16, int kEpi, int kG>
 __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) linear_split_kernel(const __grid_constant__ SplitParams p) {
     constexpr bool kCodes = kEpi == EPI_SCALED;   // int8 operands
     constexpr int kThreads = split_threads(kG, kCodes);
-    constexpr int kWiden = kThreads / 32 - kWidenFirst;   // warps that widen codes
     constexpr int kStep = kCodes ? kDepth8 : kDepth;      // contraction a stage
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -256,7 +259,10 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
     const int half = kG == 2 ? crank & 1 : 0;            // of the pair
     const int rank = crank / kG;                         // share of the contraction
     const int x_rows = p.rows / kG;                      // tokens this CTA loads
-    const uint32_t stage_bytes = (kTileN + static_cast<uint32_t>(x_rows)) * kStep * 2;
+    // (codes: of the weight, the widened stages are in TMEM where it is K-major)
+    const uint32_t w_bytes = !kCodes ? kWBytes : (p.w_kn ? 2 * kWBytes : 0);
+    const uint32_t stage_bytes = w_bytes + static_cast<uint32_t>(x_rows) * kStep * 2;
+    const uint32_t raw_bytes = (kTileN + static_cast<uint32_t>(x_rows)) * kDepth8;
     // (no divisions: seven of them, one after another, took 0.5 us of each call.  A quotient of 32-bit numbers is the
     // high word of the product with the reciprocal rounded up to 64 bits: its error, below 2^-64 x tile, does not
     // reach the next integer.)
@@ -279,12 +285,12 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
         ptx::tmem_relinquish<kG>();
     } else if (warp == 0) {
         if (lane < S) {
-            ptx::mbar_init(ptx::smem_u32(&full_bar[lane]), kCodes ? kWiden * kG : 1);
+            ptx::mbar_init(ptx::smem_u32(&full_bar[lane]), kCodes ? kWidenTeam * kG : 1);
             ptx::mbar_init(ptx::smem_u32(&empty_bar[lane]), 1);
         }
         if (kCodes && lane < p.raws) {
             ptx::mbar_init(ptx::smem_u32(&raw_full[lane]), 1);
-            ptx::mbar_init(ptx::smem_u32(&raw_empty[lane]), kWiden);
+            ptx::mbar_init(ptx::smem_u32(&raw_empty[lane]), kWidenTeam);
         }
         if (lane == 0) {
             failed = 0;
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
     // the ring is at least as long as there are producers: it has issued the step
     // `producers` back, so what the ring held before that one is consumed.
     const int ring = kCodes ? p.raws : S;
-    const int producers = min(kProducers, ring), producer = warp == 0 ? 0 : warp - 1;   // (warp 1 issues the MMAs)
+    const int producers = kCodes ? 1 : min(kProducers, ring), producer = warp == 0 ? 0 : warp - 1;   // (warp 1 issues the MMAs)
     if (warp != 1 && producer < producers && lane == 0) {
         ptx::prefetch_tmap(&p.w_map);
         ptx::prefetch_tmap(&p.x_map);
@@ -327,12 +333,10 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
 
     if (kCodes && warp != 1 && producer < producers) {
         // codes as they are, each CTA its own: 128 columns of the weight and x_rows tokens, 128 deep
-        const uint32_t raw_bytes = stage_bytes / 2;
-        int i = producer, stage = producer;
+        int i = 0, stage = 0;
         uint32_t phase = 1;
-        while (stage >= ring) stage -= ring, phase ^= 1u;
         bool ok = true;
-        for (; i < count; i += producers) {
+        for (; i < count; ++i) {
             const bool got = ptx::mbar_wait(ptx::smem_u32(&raw_empty[stage]), phase, p.wait_limit_ns);
             if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
@@ -347,67 +351,107 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
                 ptx::tma_load_2d(sw + kTileN * kStep, &p.x_map, k0, m0 + half * x_rows, full);
             }
             __syncwarp();
-            stage += producers;
-            while (stage >= ring) stage -= ring, phase ^= 1u;
+            if (++stage == ring) stage = 0, phase ^= 1u;
         }
         if (!ok && lane == 0) {
             atomicExch(&failed, 1);
-            // the copies in flight, among this warp's last ones, land before the CTA can exit
-            for (int back = 0; back <= ring && i - producers >= 0; back += producers) {
-                i -= producers;
+            // the copies in flight land before the CTA can exit
+            for (int back = 0; back < ring && i > 0; ++back) {
+                --i;
                 (void)ptx::mbar_wait(ptx::smem_u32(&raw_full[i % ring]), static_cast<uint32_t>((i / ring) & 1), p.wait_limit_ns);
             }
             ptx::nanosleep(20000);
         }
-    } else if (kCodes && warp >= kWidenFirst) {
-        // Codes to fp16, a stage over all these warps.  A turn takes a warp half of eight rows of 128 bytes: 64 codes of each,
-        // 16 a lane, to the 128-byte row of the operand's 64-deep (K-major) or 64-wide (M-major) half.  Both sides have the
+    } else if (kCodes && warp >= kWidenFirst && warp < kWidenFirst + kWidenTeam * p.teams) {
+        // Codes to fp16: a team of four warps takes a 128-deep stage, the teams take turns, so that the latencies of one stage's
+        // loads, stores and fences are hidden by the others' (all warps at one stage after another: 1640 clocks a stage).
+        // A K-major weight goes to TMEM, a row a lane.  (Through shared memory it crosses that four times, 48 KiB in and out
+        // a 64-deep stage, which takes 384 clocks; this way 16.)  An M-major one, whose rows are depth, and the tokens go to shared
+        // memory, half of eight rows of 128 bytes a warp's turn: 64 codes of each, 16 a lane.  Codes and operands have the
         // 128-byte swizzle (chunk c of row r at c ^ r % 8), and the lanes' rows in the order 0 5 1 4 2 7 3 6 meet all
         // banks in eight lanes at a time, in the loads (neighbouring rows differ in bit 2) and in the stores (and in bit 0).
-        const int row_in = (lane >> 3) ^ ((lane >> 2) & 1 ? 5 : 0);
-        const int chunk = lane & 3;
-        const int turns_w = 2 * kTileN / 8, turns = turns_w + 2 * x_rows / 8;
-        const uint8_t *raw0 = smem + p.raw_off;
-        const uint32_t half_w = p.w_kn ? kDepth * 128u : kTileN * 128u;         // to the other half of the weight's rows
+        // (A wait on a barrier's parity tells a phase from the one two before it only if that one cannot still be open.  With at
+        // most as many teams as widened stages, a team at step i has seen the MMAs of the step two turns of them before done;
+        // with a ring that is a multiple of the teams, the last user of a slot was itself.)
+        const int team = (warp - kWidenFirst) / kWidenTeam, member = warp % kWidenTeam;
+        const int row_in = (lane >> 3) ^ ((lane >> 2) & 1 ? 5 : 0), chunk = lane & 3, h = member & 1;
+        const uint32_t rows0 = static_cast<uint32_t>((member >> 1) * 1024 + row_in * 128);   // of the first turn, either side
+        const uint32_t from0 = rows0 + (((4 * h + chunk) ^ row_in) << 4);
+        const uint32_t to0 = rows0 + (((2 * chunk) ^ row_in) << 4), to1 = rows0 + (((2 * chunk + 1) ^ row_in) << 4);
         const uint32_t full0 = ptx::smem_u32(&full_bar[0]);
         const uint32_t ready0 = kG == 2 ? ptx::mapa(full0, crank - half) : full0;   // (the pair's first CTA counts both)
+        // kTurns turns, 16 rows apart; from the fifth on `jump` further
+        const auto widen = [&](const uint8_t *from, uint8_t *to, auto turns, uint32_t jump) {
+            constexpr int kTurns = decltype(turns)::value;
+            uint4 q[kTurns];
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) q[i] = *reinterpret_cast<const uint4 *>(from + i * 2048);
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) {
+                const uint2 a = widen4(q[i].x), b = widen4(q[i].y), c = widen4(q[i].z), d = widen4(q[i].w);
+                uint8_t *at = to + i * 2048 + (i >= 4 ? jump : 0);
+                *reinterpret_cast<uint4 *>(at + to0) = make_uint4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<uint4 *>(at + to1) = make_uint4(c.x, c.y, d.x, d.y);
+            }
+        };
         int rs = 0, stage = 0;
         uint32_t raw_phase = 0, phase = 1;
+        const auto skip = [&](int n) {
+            for (rs += n; rs >= ring; rs -= ring) raw_phase ^= 1u;
+            for (stage += n; stage >= S; stage -= S) phase ^= 1u;
+        };
+        skip(team);
         bool ok = true;
-        for (int i = 0; i < count; ++i) {
+        for (int i = team; i < count; i += p.teams) {
             const bool got = ptx::mbar_wait(ptx::smem_u32(&raw_full[rs]), raw_phase, p.wait_limit_ns) &&
                              ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), phase, p.wait_limit_ns);
             if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 break;
             }
-            const uint8_t *raw = raw0 + rs * (stage_bytes / 2);
+            const uint8_t *raw = smem + p.raw_off + rs * raw_bytes;
             uint8_t *to = smem + stage * stage_bytes;
-            for (int t = warp - kWidenFirst; t < turns; t += kWiden) {
-                const bool is_w = t < turns_w;
-                const int u = is_w ? t : t - turns_w, h = u & 1, row = (u >> 1) * 8 + row_in;
-                const uint4 q = *reinterpret_cast<const uint4 *>(raw + (is_w ? 0 : kTileN * kStep) + row * 128 + (((4 * h + chunk) ^ row_in) << 4));
-                // the weight's row r of codes: K-major, row r of both depths; M-major, depth r (64 of them a part) of both slabs
-                uint8_t *dst;
-                if (is_w)
-                    dst = to + (p.w_kn ? (row >> 6) * kWBytes + (row & 63) * 128 : row * 128) + h * half_w;
-                else
-                    dst = to + 2 * kWBytes + h * (x_rows * 128) + row * 128;
-                const uint2 a = widen4(q.x), b = widen4(q.y), c = widen4(q.z), d = widen4(q.w);
-                *reinterpret_cast<uint4 *>(dst + (((2 * chunk) ^ row_in) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-                *reinterpret_cast<uint4 *>(dst + (((2 * chunk + 1) ^ row_in) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
+            // the tokens' turns, in fours
+            const uint8_t *from = raw + kTileN * kDepth8 + from0;
+            uint8_t *x_to = to + w_bytes + h * x_rows * 128;
+            int left = x_rows / 16;
+            for (; left >= 4; left -= 4, from += 4 * 2048, x_to += 4 * 2048) widen(from, x_to, std::integral_constant<int, 4>{}, 0);
+            for (; left > 0; --left, from += 2048, x_to += 2048) widen(from, x_to, std::integral_constant<int, 1>{}, 0);
+            if (p.w_kn) {
+                // depth 64 on is another 64-deep part, half h a slab 8 KiB on
+                widen(raw + from0, to + h * (kWBytes / 2), std::integral_constant<int, 8>{}, kWBytes / 2);
+            } else {
+                const uint8_t *row = raw + (32 * member + lane) * 128;
+                const uint32_t a = tmem + p.a_cols + static_cast<uint32_t>(stage * (kDepth8 / 2)) + (static_cast<uint32_t>(32 * member) << 16);
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 q = *reinterpret_cast<const uint4 *>(row + (((4 * d + c) ^ (lane & 7)) << 4));
+                        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint2 v = widen4(words[e]);
+                            w[8 * c + 2 * e] = v.x, w[8 * c + 2 * e + 1] = v.y;
+                        }
+                    }
+                    ptx::tmem_st_32x32b_x32(a + 32 * d, w);
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 ptx::mbar_arrive(ptx::smem_u32(&raw_empty[rs]));
                 if (kG == 2)
-                    ptx::mbar_arrive_remote(ready0 + 8u * stage);
+                    ptx::mbar_arrive_remote_cta(ready0 + 8u * stage);
                 else
                     ptx::mbar_arrive(ready0 + 8u * stage);
             }
-            if (++rs == ring) rs = 0, raw_phase ^= 1u;
-            if (++stage == S) stage = 0, phase ^= 1u;
+            skip(p.teams);
         }
         if (!ok && lane == 0) atomicExch(&failed, 1);
     } else if (!kCodes && warp != 1 && producer < producers) {
@@ -460,7 +504,7 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
         const uint32_t idesc = ptx::idesc_f16(kBF16 && !kCodes, false, kTileN * kG, p.rows, p.w_kn != 0);
         const uint32_t s0 = ptx::smem_u32(smem);
         const uint64_t w_desc = p.w_kn ? ptx::smem_desc_sw128(s0, kDepth * 128, 1024) : ptx::smem_desc_sw128(s0, 16, 1024);
-        const uint64_t x_desc = ptx::smem_desc_sw128(s0 + (kCodes ? 2 : 1) * kWBytes, 16, 1024);
+        const uint64_t x_desc = ptx::smem_desc_sw128(s0 + w_bytes, 16, 1024);
         // (a stage's addresses stay within the descriptors' low words)
         const uint32_t w_hi = static_cast<uint32_t>(w_desc >> 32), w_lo0 = static_cast<uint32_t>(w_desc);
         const uint32_t x_hi = static_cast<uint32_t>(x_desc >> 32), x_lo0 = static_cast<uint32_t>(x_desc);
@@ -477,9 +521,8 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
             uint32_t add = block >= p.accs ? 1u : 0u;   // an accumulator's first stage starts it from zero
             const int end = min(done + kBlockDepth / kStep, count);
             for (; done < end; ++done) {
-                // (codes: the pair's other CTA arrives here, too)
-                if (kCodes || !__all_sync(0xffffffffu, ready)) {
-                    ready = kCodes && kG == 2 ? ptx::mbar_wait_cluster(full, phase, p.wait_limit_ns) : ptx::mbar_wait(full, phase, p.wait_limit_ns);
+                if (!__all_sync(0xffffffffu, ready)) {
+                    ready = ptx::mbar_wait(full, phase, p.wait_limit_ns);
                     if (!__all_sync(0xffffffffu, ready)) {
                         ok = false;
                         break;
@@ -491,11 +534,16 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
                 full += 8;
                 off += advance;
                 if (full == full_end) full = full0, off = 0, phase ^= 1u;
-                if (!kCodes) ready = ptx::mbar_test(full, phase);
+                ready = ptx::mbar_test(full, phase);
                 if constexpr (kCodes) {
-                    ptx::mma_four_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add);
-                    ptx::mma_stage_f16_ss<kG>(d, w_lo + (kWBytes >> 4), w_hi, w_kk, x_lo + static_cast<uint32_t>(x_rows * 128 >> 4), x_hi, x_kk,
-                                              idesc, 1, bar, pair);
+                    const uint32_t x_half = static_cast<uint32_t>(x_rows * 128) >> 4;
+                    if (p.w_kn) {
+                        ptx::mma_four_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add);
+                        ptx::mma_stage_f16_ss<kG>(d, w_lo + (kWBytes >> 4), w_hi, w_kk, x_lo + x_half, x_hi, x_kk, idesc, 1, bar, pair);
+                    } else {
+                        ptx::mma_stage_f16_ts<kG>(d, tmem + p.a_cols + static_cast<uint32_t>((bar - to_empty - full0) * (kDepth8 / 16)), x_lo, x_hi, x_kk,
+                                                  x_half, idesc, add, bar, pair);
+                    }
                 } else {
                     ptx::mma_stage_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add, bar, pair);
                 }
@@ -612,7 +660,7 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
 // The shape of a launch.
 struct SplitShape {
     int group, rows, m_tiles, split, per_sm, stages, accs, tmem_cols, late, prefetch;
-    int raws;   // int8 codes: stages of them as they are (0: 16-bit operands)
+    int raws, teams, a_cols;   // int8 codes: stages of them as they are (0: 16-bit operands), teams, TMEM column of the weight's
     uint32_t smem, recv_off, raw_off;
     int64_t tiles;
     float us;   // what it is expected to take
@@ -626,46 +674,61 @@ bool prefetch_pays(const SplitShape &s, int num_sms) {
 }
 
 // Shared memory and TMEM of a launch whose tiles and split are chosen; false if it has none.
-bool fit_split(SplitShape &s, int steps, int num_sms, bool codes) {
+bool fit_split(SplitShape &s, int steps, int num_sms, bool codes, bool w_kn) {
     const int most = (steps + s.split - 1) / s.split;   // stages of one CTA
     const int block_steps = kBlockDepth / (codes ? kDepth8 : kDepth);
-    // (the bytes of a 16-bit stage; of codes, those of a stage as it is, half of the widened one)
-    const uint32_t stage = codes ? static_cast<uint32_t>(kTileN + s.rows / s.group) * kDepth8
-                                 : kWBytes + static_cast<uint32_t>(s.rows / s.group) * kDepth * 2;
+    const uint32_t x_rows = static_cast<uint32_t>(s.rows / s.group);
+    const uint32_t stage = codes ? (kTileN + x_rows) * kDepth8 : kWBytes + x_rows * kDepth * 2;   // (of codes, as they are)
     const uint32_t room = s.per_sm == 2 ? 110u * 1024u : 220u * 1024u;
     const uint32_t sums = static_cast<uint32_t>(s.rows) * kTileN * 4;   // this CTA's, over the ring
     const uint32_t recv = static_cast<uint32_t>((s.split - 1) * ((s.rows + s.split - 1) / s.split)) * kTileN * 4;
-    // two widened stages: the MMAs take one while the other is filled
-    const uint32_t before = codes ? 2u * 2u * stage : 0u;
-    int full = static_cast<int>((room - before) / stage);
-    if (full > kMaxStages) full = kMaxStages;
-    if (full > most) full = most;
-    // the others' sums beside the ring, or, where that would shorten it, over it (256 tokens,
-    // 4096 x 4096, split in two: 0.6 us less than with a shorter ring)
-    int ring_stages = recv + before < room ? static_cast<int>((room - before - recv) / stage) : 0;
-    s.late = ring_stages < full && s.group == 2;
-    if (s.late || ring_stages > full) ring_stages = full;
-    if (ring_stages < 1) return false;
-    const uint32_t ring = before + ring_stages * stage;
-    s.stages = codes ? 2 : ring_stages;
-    s.raws = codes ? ring_stages : 0;
-    s.raw_off = before;
-    s.recv_off = s.late || ring < sums ? sums : ring;
-    const uint32_t bytes = ring > s.recv_off + recv ? ring : s.recv_off + recv;
-    s.smem = bytes + 1024;   // (slack to align the ring)
     const int blocks = (most + block_steps - 1) / block_steps;
     s.accs = (s.per_sm == 2 ? 256 : 512) / s.rows;
     // (integer sums stay exact in an accumulator of their own for each block)
     if (codes && s.accs < blocks) return false;
     if (s.accs > blocks) s.accs = blocks;
+    int columns = s.accs * s.rows, widened = 0, unit = 1;
+    s.teams = 0, s.a_cols = 0;
+    if (codes) {
+        // three widened stages and teams to fill them, where there is room for them beside a ring of six, or two
+        const uint32_t wide = (w_kn ? 2 * kWBytes : 0u) + x_rows * kDepth8 * 2;
+        widened = 3;
+        s.a_cols = (columns + 63) / 64 * 64;
+        if (3 * wide + 6 * stage > room || (!w_kn && s.a_cols + 3 * (kDepth8 / 2) > 512)) widened = 2;
+        if (!w_kn) columns = s.a_cols + widened * (kDepth8 / 2);
+        if (columns > 512) return false;
+        s.teams = unit = widened;
+        s.raw_off = widened * wide;
+    } else {
+        s.raw_off = 0;
+    }
+    int full = static_cast<int>((room - s.raw_off) / stage);
+    if (full > kMaxStages) full = kMaxStages;
+    if (codes)
+        full = full / unit * unit;   // (see the kernel)
+    else if (full > most)
+        full = most;
+    // the others' sums beside the ring, or, where that would shorten it, over it (256 tokens,
+    // 4096 x 4096, split in two: 0.6 us less than with a shorter ring)
+    int ring_stages = recv + s.raw_off < room ? static_cast<int>((room - s.raw_off - recv) / stage) : 0;
+    if (codes) ring_stages = ring_stages / unit * unit;
+    s.late = ring_stages < full && s.group == 2;
+    if (s.late || ring_stages > full) ring_stages = full;
+    if (ring_stages < unit) return false;
+    const uint32_t ring = s.raw_off + ring_stages * stage;
+    s.stages = codes ? widened : ring_stages;
+    s.raws = codes ? ring_stages : 0;
+    s.recv_off = s.late || ring < sums ? sums : ring;
+    const uint32_t bytes = ring > s.recv_off + recv ? ring : s.recv_off + recv;
+    s.smem = bytes + 1024;   // (slack to align the ring)
     s.tmem_cols = 32;
-    while (s.tmem_cols < s.accs * s.rows) s.tmem_cols *= 2;
+    while (s.tmem_cols < columns) s.tmem_cols *= 2;
     // A CTA that waits for TMEM while its cluster's others hold theirs could wait for
     // ever on a CTA that waits for it, were TMEM oversubscribed by launches of two
     // streams.  So a CTA that takes 1/2^i of TMEM takes at least that part of the
     // SM's shared memory too (its static part and the system's 1 KiB included):
     // CTAs that fit beside one another find their columns free.
-    const uint32_t share = static_cast<uint32_t>(s.tmem_cols) * (kSmemPerSm / 512) - kSmemOverhead;
+    const uint32_t share = static_cast<uint32_t>(s.tmem_cols) * (kSmemPerSm / 512) - 1024 - (codes ? kSmemStaticCodes : kSmemStatic);
     if (s.smem < share) s.smem = share;
     if (codes && s.smem > kMostSmemCodes) return false;
     s.prefetch = codes || prefetch_pays(s, num_sms);
@@ -764,7 +827,7 @@ SplitShape best_split(const LinearParams &p, int num_sms) {
             // two CTAs an SM where there are more than SMs and their stages are short: 0.2 us less for one token, 4096 x 4096;
             // but 1.7 us more for 32 tokens, 1024 x 8192, 64 CTAs
             s.per_sm = !codes && f.group == 1 && s.rows <= 32 && s.tiles > clusters_at_once(s.split, num_sms) ? 2 : 1;
-            if (!fit_split(s, steps, num_sms, codes)) continue;
+            if (!fit_split(s, steps, num_sms, codes, !p.w_nk)) continue;
             s.us = codes ? split_codes_us(s, p, steps, num_sms) : split_us(s, p, steps, num_sms);
             if (best.group == 0 || s.us < best.us) best = s;
         }
@@ -868,7 +931,7 @@ cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, 
     p.wait_limit_ns = host::kWaitLimitNs;
     if (lp.x_scale) {
         p.x_scale = lp.x_scale, p.w_scale = lp.w_scale, p.bias_f32 = lp.bias_f32;
-        p.raws = s.raws, p.raw_off = s.raw_off;
+        p.raws = s.raws, p.teams = s.teams, p.raw_off = s.raw_off, p.a_cols = static_cast<uint32_t>(s.a_cols);
         const auto words = [](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 8 == 0 && ld % 4 == 0; };
         p.words = words(lp.out, lp.ldo) && (!p.aux || words(p.aux, lp.ldaux));
         if (s.group == 1) return bf16 ? launch_split<true, EPI_SCALED, 1>(p, s, stream) : launch_split<false, EPI_SCALED, 1>(p, s, stream);

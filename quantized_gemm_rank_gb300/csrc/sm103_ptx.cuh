@@ -124,6 +124,12 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same, publishing to the arriving thread's own CTA only: for data that stay there, as the half of a pair's operand
+// that its own tensor core reads (a release to the cluster takes about a microsecond, for what it waits for).
+__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Arrive on an mbarrier of a CTA of this cluster without release semantics (the
 // caller has already consumed what it read).
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
@@ -458,6 +464,77 @@ __device__ __forceinline__ void mma_four_f16_ss(uint32_t d_tmem, uint32_t a_lo, 
             : "memory");
 }
 
+// The eight MMAs of a 128-deep stage whose A is in TMEM (eight columns a 16-deep slice) and B in two 64-deep halves, `b_half`
+// apart, and the commit that frees both.
+template <int kG>
+__device__ __forceinline__ void mma_stage_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t b_step, uint32_t b_half,
+                                                 uint32_t idesc, uint32_t accumulate, uint32_t bar, uint16_t mask) {
+    if constexpr (kG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t.reg .b32 al, bl, bh;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "mov.b32 al, %1;\n\tmov.b32 bl, %2;\n\tadd.u32 bh, %2, %7;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "setp.eq.b32 p, %5, %5;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\t"
+            "mov.b32 bl, bh;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(b_step), "r"(b_half), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t.reg .b32 al, bl, bh;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "mov.b32 al, %1;\n\tmov.b32 bl, %2;\n\tadd.u32 bh, %2, %7;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "setp.eq.b32 p, %5, %5;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\t"
+            "mov.b32 bl, bh;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+            "mov.b64 b, {bl, %3};\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%8], %9;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(b_step), "r"(b_half), "r"(bar), "h"(mask)
+            : "memory");
+}
+
 // Arrive on `bar` once all previously issued tcgen05 ops of this thread
 // complete; with kG = 2 the arrival goes to the barrier at the same offset in
 // both CTAs of the pair.
@@ -534,6 +611,17 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
         "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+// 32 columns.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
         : "memory");
 }
 // This thread's TMEM stores have completed.
