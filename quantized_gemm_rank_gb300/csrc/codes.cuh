@@ -170,6 +170,24 @@ __device__ __forceinline__ void decode_codes(uint2 w, int kind, float (&v)[8]) {
     }
 }
 
+// 16 codes of a row, of which `left` are in it (none: 0 or less); zeros behind them.  In one access where they are whole and
+// aligned, otherwise by the aligned words that hold one of them at least.  `again`: they will be read again (kept in L1).
+__device__ __forceinline__ uint4 load_codes16(const int8_t *from, int left, bool again = false) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(from);
+    if (left >= 16 && (a & 15) == 0) return again ? __ldg(reinterpret_cast<const uint4 *>(from)) : load_once(from);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~uintptr_t(3));
+    const int skip = static_cast<int>(a & 3), end = left > 0 ? min(left, 16) + skip : 0;   // in bytes from w on
+    uint32_t word[5], q[4];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) word[i] = 4 * i < end ? __ldg(w + i) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q[i] = __funnelshift_r(word[i], word[i + 1], skip * 8);
+        if (left < 4 * i + 4) q[i] = left > 4 * i ? q[i] & ((1u << (8 * (left - 4 * i))) - 1u) : 0;
+    }
+    return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
 // Columns of a group that share a scale.
 __host__ __device__ __forceinline__ int group_size(int qmode) { return qmode == QM_MX ? 32 : 128; }
 

@@ -38,6 +38,8 @@ struct QuantProduct {
     int bias_f32;   // (otherwise of out's type)
     void *workspace;
 };
+// One to eight tokens and an (n, k) weight, in any layout.
+cudaError_t launch_quant_tokens(bool bf16, const QuantProduct &p, cudaStream_t stream);
 size_t quant_product_workspace(const QuantProduct &p);
 // Kernels of a call, each followed by mark(ctx)
 using Mark = void (*)(void *ctx);

@@ -53,19 +53,8 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
         }
         const int8_t *from = t.src + r * t.ld + v * 16;
         const int64_t left = t.cols - v * 16;
-        uint32_t q[4];
-        if (left >= 16 && (reinterpret_cast<uintptr_t>(from) & 15u) == 0) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(from));
-            q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                q[i] = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * i + j < left) q[i] |= static_cast<uint32_t>(static_cast<uint8_t>(from[4 * i + j])) << (8 * j);
-            }
-        }
+        const uint4 codes = load_codes16(from, left < 16 ? static_cast<int>(left) : 16);
+        const uint32_t q[4] = {codes.x, codes.y, codes.z, codes.w};
         // (a row's last vector is whole, zeros behind its end)
         if constexpr (kWiden) {
             uint4 *to = reinterpret_cast<uint4 *>(static_cast<__half *>(t.dst) + r * t.pitch + v * 16);
@@ -174,7 +163,8 @@ struct Pieces {
 
 struct ProductPlan {
     size_t x = 0, w = 0, out = 0, total = 0;
-    bool split = false;        // the kernel of few tokens, on int8 operands
+    bool tokens = false;       // the kernel of one to eight tokens, on the matrices as they are
+    bool split = false;        // the one of few tokens, on int8 operands
     bool apart = false;        // the operands go through the workspace (the tiles': always)
     bool out_apart = false;    // the output, too
     bool residual_in = false;  // the residual is copied to where the output will be
@@ -194,12 +184,17 @@ LinearParams product_of(const QuantProduct &p) {
 
 ProductPlan plan_product(const QuantProduct &p) {
     ProductPlan at;
-    // which kernel, by the sizes alone: the tiles take 6.3 us and 0.3 a 64-deep stage for each wave of them, and widening
-    // three bytes a code at 5500 a ns and a launch
+    // one to four tokens (4096 x 4096: 3.8, 4.7 and 6.8 us for 1, 2 and 4, 7.7 to 7.9 in the kernel of few); to eight where the
+    // weight is small (1024 x 8192 4.5 against 6.6, 4096 x 4096 8.3 against 7.8)
+    at.tokens = p.w_nk && (p.m <= 4 || (p.m <= 8 && static_cast<int64_t>(p.n) * p.k <= 8ll << 20));
+    if (at.tokens) return at;
+    // Which kernel, by the sizes alone: the tiles take 9.4 us, 3.2 and 0.25 a 64-deep stage for each wave of them, and widening three
+    // bytes a code at 5000 a ns (1024 tokens, 4096 x 14336 112 us, 8192 x 4096 70; 4096 tokens, 4096 x 4096 106).  Where the two
+    // cross, with k = 4096: 512 tokens, n = 4096 24.6 us split, 31 in tiles; 1024 tokens, n = 8192 137 and 70.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256);
     const float steps = static_cast<float>((p.k + 63) / 64);
-    const float tiles_us = 9.3f + 0.3f * static_cast<float>((tiles + kPairs - 1) / kPairs) * steps +
-                           (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 3.0f / 5.5e6f;
+    const float tiles_us = 9.4f + static_cast<float>((tiles + kPairs - 1) / kPairs) * (3.2f + 0.2475f * steps) +
+                           (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 0.6e-6f;
     LinearParams l = product_of(p);
     l.x_scale = reinterpret_cast<const float *>(p.x);   // (codes; not read)
     const float split_us = linear_split_codes_us(l, kSms);
@@ -268,6 +263,11 @@ size_t quant_product_workspace(const QuantProduct &p) { return plan_product(p).t
 
 cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, cudaStream_t stream, Mark mark, void *ctx) {
     const ProductPlan at = plan_product(p);
+    if (at.tokens) {
+        const cudaError_t e = launch_quant_tokens(bf16, p, stream);
+        if (e == cudaSuccess) mark(ctx);
+        return e;
+    }
     char *ws = static_cast<char *>(p.workspace);
     LinearParams l = product_of(p);
     const int64_t w_rows = p.w_nk ? p.n : p.k, w_cols = p.w_nk ? p.k : p.n;
