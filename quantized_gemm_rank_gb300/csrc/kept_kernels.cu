@@ -17,7 +17,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 8;      // elements a thread takes at a time
-constexpr int kResident = 4;   // blocks of the covering kernels an SM holds
+// Blocks an SM holds and rows of a thread on their way at once, of the covering kernels.  8192 x 8192, in us: from codes to 16 bits
+// 35.5 with (8, 1), 38.2 (6, 1), 37.5 (4, 2); the gradient 68 with (5, 1), 69 (4, 2), 106 (8, 1: registers spill); to codes
+// with gelu 69 with (4, 2), 73 (8, 1), without an activation 44 and 41.
+constexpr int kToBlocks = 4, kToRows = 2, kFromBlocks = 8, kGradBlocks = 5;
 
 // f(activation with its form a constant): the choice is made once for all of a thread's elements.
 template <class F>
@@ -103,9 +106,9 @@ struct Cover {
 };
 
 // ------------------------------------------------------------------ from codes
-// Rows of whole chunks: every access is a whole one.  kRows rows of a thread are on their way at once.
-template <int kT, bool kGrad, int kQM, int kRows>
-__global__ void __launch_bounds__(kThreads, kResident) from_kept_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p, Activation act,
+// Rows of whole chunks: every access is a whole one.
+template <int kT, bool kGrad, int kQM>
+__global__ void __launch_bounds__(kThreads, kGrad ? kGradBlocks : kFromBlocks) from_kept_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p, Activation act,
                                                              void *out, int64_t ldo, Cover cover) {
     constexpr int kE = kT == ELEM_F32 ? 4 : 2;
     ptx::grid_dependency_wait();
@@ -115,38 +118,24 @@ __global__ void __launch_bounds__(kThreads, kResident) from_kept_kernel(const vo
     if (c >= cover.chunks) return;
     const int j = c * kChunk;
     const int64_t step = static_cast<int64_t>(gridDim.y) * per_block;
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * per_block + (threadIdx.x >> cover.lanes_log2); r0 < p.m; r0 += kRows * step) {
-        uint2 q[kRows];
-        Raw<kT> d[kRows];
-        float scale[kRows];
+    for (int64_t r = static_cast<int64_t>(blockIdx.y) * per_block + (threadIdx.x >> cover.lanes_log2); r < p.m; r += step) {
+        const uint2 q = load_codes(static_cast<const uint8_t *>(p.q) + r * p.h + j);
+        Raw<kT> d;
+        if constexpr (kGrad) d = load_raw<kT>(static_cast<const char *>(dy) + (r * lddy + j) * kE);
+        const float scale = scale_at<kQM>(p.scale, r, p.h, j);
+        float z[kChunk];
+        decode_codes(q, p.qkind, z);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int64_t r = r0 + i * step;
-            if (r < p.m) {
-                q[i] = load_codes(static_cast<const uint8_t *>(p.q) + r * p.h + j);
-                if constexpr (kGrad) d[i] = load_raw<kT>(static_cast<const char *>(dy) + (r * lddy + j) * kE);
-                scale[i] = scale_at<kQM>(p.scale, r, p.h, j);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int64_t r = r0 + i * step;
-            if (r < p.m) {
-                float z[kChunk];
-                decode_codes(q[i], p.qkind, z);
-#pragma unroll
-                for (int e = 0; e < kChunk; ++e) z[e] = __fmul_rn(z[e], scale[i]);
-                char *to = static_cast<char *>(out) + (r * ldo + j) * kE;
-                if constexpr (kGrad) {
-                    float g[kChunk];
-                    values<kT>(d[i], g);
-                    times_derivative(g, z, act);
-                    store_values<kT>(to, g);
-                } else {
-                    apply_act(z, act);
-                    store_values<kT>(to, z);
-                }
-            }
+        for (int e = 0; e < kChunk; ++e) z[e] = __fmul_rn(z[e], scale);
+        char *to = static_cast<char *>(out) + (r * ldo + j) * kE;
+        if constexpr (kGrad) {
+            float g[kChunk];
+            values<kT>(d, g);
+            times_derivative(g, z, act);
+            store_values<kT>(to, g);
+        } else {
+            apply_act(z, act);
+            store_values<kT>(to, z);
         }
     }
 }
@@ -280,8 +269,8 @@ __device__ __forceinline__ uint32_t largest_of(const float (&y)[kChunk]) {
 
 // Rows of whole chunks with scales of groups (16 or 4 neighbouring threads), or with one scale a row of at most 32
 // chunks (`lanes` threads): covered like from_kept_kernel.
-template <int kT, int kQM, int kRows>
-__global__ void __launch_bounds__(kThreads, kResident) act_quant_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act, Cover cover) {
+template <int kT, int kQM>
+__global__ void __launch_bounds__(kThreads, kToBlocks) act_quant_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act, Cover cover) {
     constexpr int kE = kT == ELEM_F32 ? 4 : 2;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
@@ -293,16 +282,16 @@ __global__ void __launch_bounds__(kThreads, kResident) act_quant_kernel(const vo
     const int groups = kQM == QM_TOKEN ? 1 : (p.h + group_size(kQM) - 1) / group_size(kQM);
     const int64_t step = static_cast<int64_t>(gridDim.y) * per_block;
     // (all threads of a block take as many turns, so that the groups' exchanges are whole)
-    for (int64_t first = static_cast<int64_t>(blockIdx.y) * per_block; first < p.m; first += kRows * step) {
+    for (int64_t first = static_cast<int64_t>(blockIdx.y) * per_block; first < p.m; first += kToRows * step) {
         const int64_t r0 = first + (threadIdx.x >> cover.lanes_log2);
-        Raw<kT> raw[kRows];
+        Raw<kT> raw[kToRows];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
+        for (int i = 0; i < kToRows; ++i) {
             const int64_t r = r0 + i * step;
             if (live && r < p.m) raw[i] = load_raw<kT>(static_cast<const char *>(z) + (r * ldz + j) * kE);
         }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
+        for (int i = 0; i < kToRows; ++i) {
             const int64_t r = r0 + i * step;
             const bool here = live && r < p.m;
             float y[kChunk];
@@ -452,8 +441,8 @@ cudaError_t launch_from(const void *dy, int64_t lddy, const Kept &p, int act, vo
     constexpr size_t kE = kT == ELEM_F32 ? 4 : 2;
     Cover cover;
     if (p.h % kChunk == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && whole_chunks(out, ldo, p.m, kE) && (!kGrad || whole_chunks(dy, lddy, p.m, kE))) {
-        const dim3 grid = cover_rows(p.h / kChunk, 1, p.m, num_sms, kResident, &cover);
-        return launch(from_kept_kernel<kT, kGrad, kQM, 2>, grid, kThreads, stream, dy, lddy, p, a, out, ldo, cover);
+        const dim3 grid = cover_rows(p.h / kChunk, 1, p.m, num_sms, kGrad ? kGradBlocks : kFromBlocks, &cover);
+        return launch(from_kept_kernel<kT, kGrad, kQM>, grid, kThreads, stream, dy, lddy, p, a, out, ldo, cover);
     }
     // (a row may begin inside its first chunk)
     const dim3 grid = cover_rows((p.h + 2 * kChunk - 2) / kChunk, 1, p.m, num_sms, 32, &cover);
@@ -478,11 +467,11 @@ cudaError_t launch_to(const void *z, int64_t ldz, const Kept &p, int act, int nu
         (p.qmode != QM_TOKEN || chunks <= 4 * 1024)) {
         Cover cover;
         if (p.qmode == QM_GROUP)
-            return launch(act_quant_kernel<kT, QM_GROUP, 2>, cover_rows(chunks, 16, p.m, num_sms, kResident, &cover), kThreads, stream, z, ldz, p, a, cover);
+            return launch(act_quant_kernel<kT, QM_GROUP>, cover_rows(chunks, 16, p.m, num_sms, kToBlocks, &cover), kThreads, stream, z, ldz, p, a, cover);
         if (p.qmode == QM_MX)
-            return launch(act_quant_kernel<kT, QM_MX, 2>, cover_rows(chunks, 4, p.m, num_sms, kResident, &cover), kThreads, stream, z, ldz, p, a, cover);
+            return launch(act_quant_kernel<kT, QM_MX>, cover_rows(chunks, 4, p.m, num_sms, kToBlocks, &cover), kThreads, stream, z, ldz, p, a, cover);
         if (chunks <= 32)
-            return launch(act_quant_kernel<kT, QM_TOKEN, 2>, cover_rows(chunks, 1, p.m, num_sms, kResident, &cover), kThreads, stream, z, ldz, p, a, cover);
+            return launch(act_quant_kernel<kT, QM_TOKEN>, cover_rows(chunks, 1, p.m, num_sms, kToBlocks, &cover), kThreads, stream, z, ldz, p, a, cover);
         // few rows: more threads a row; many: more chunks a thread
         const int v = p.m > 2 * num_sms || chunks > 2048 ? 4 : (chunks > 1024 ? 2 : 1);
         const int threads = ((chunks + v - 1) / v + 31) / 32 * 32;
