@@ -152,7 +152,7 @@ __device__ __forceinline__ uint2 load_bytes8(const uint8_t *p) {
 }
 
 // Rows of any width and alignment: the chunks are those of the output's aligned 16-byte units, the first and the
-// last of a row partial; codes come from any address, dy in whole chunks where it is aligned as dz is.
+// last of a row partial; codes and dy come from any address.
 template <int kT, bool kGrad, int kQM>
 __global__ void __launch_bounds__(kThreads) from_kept_any_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p, Activation act,
                                                                  void *out, int64_t ldo, Cover cover) {
@@ -184,8 +184,10 @@ __global__ void __launch_bounds__(kThreads) from_kept_any_kernel(const void *dy,
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) z[e] = __fmul_rn(z[e], kQM == QM_TOKEN || j0 + e < border ? first : last);
         if constexpr (kGrad) {
-            if (whole && ((reinterpret_cast<uintptr_t>(from) ^ reinterpret_cast<uintptr_t>(to)) & 15u) == 0) {
-                values<kT>(load_raw<kT>(from + j0), g);
+            if (whole && kT != ELEM_F32) {
+                Raw<kT> d;
+                d.v[0] = load_codes16(reinterpret_cast<const int8_t *>(from + j0), 16);
+                values<kT>(d, g);
             } else {
 #pragma unroll
                 for (int e = 0; e < kChunk; ++e) g[e] = j0 + e >= lo && j0 + e < hi ? Elem<kT>::load(from + j0 + e) : 0.0f;
@@ -349,55 +351,79 @@ __global__ void __launch_bounds__(kWarpRow ? kThreads : 1024) act_quant_row_kern
     }
 }
 
-// Any sizes, strides and alignments: one block a row, read once for its largest value and once for its codes.  A warp
-// takes whole groups of 32 or 128 elements, so that a group's scale is found inside one warp.
-template <int kT>
-__global__ void __launch_bounds__(kThreads) act_quant_any_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p,
-                                                                 Activation act) {
+// Any sizes, strides and alignments, element by element: a warp takes 128 of a row at a time (one group, or four of mx), lane l
+// elements l, l + 32, l + 64 and l + 96.  One scale a row: the row is read twice, by a warp, or (kBlockRow) by a block.
+template <int kT, int kQM, bool kBlockRow>
+__global__ void __launch_bounds__(kThreads) act_quant_any_kernel(const void *z, int64_t ldz, const __grid_constant__ Kept p, Activation act) {
     using T = typename Elem<kT>::type;
     __shared__ uint32_t slots[32];
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x;
-    const T *from = static_cast<const T *>(z) + row * ldz;
-    auto y_at = [&](int j) { return act2(both(Elem<kT>::load(from + j)), act).x; };
-    float token = 0.0f;
-    if (p.qmode == QM_TOKEN) {
-        float top = 0.0f;
-        for (int64_t j = threadIdx.x; j < p.h; j += kThreads) top = max_abs(top, y_at(static_cast<int>(j)));
-        token = __fmul_rn(__uint_as_float(block_max32(__float_as_uint(top), slots)), q_inverse(p.qkind));
-        if (threadIdx.x == 0) static_cast<float *>(p.scale)[row] = token;
-    }
-    const int group = group_size(p.qmode), groups = (p.h + group - 1) / group;
-    uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.h;
-    for (int g = warp; g < groups; g += kWarps) {
-        float y[4];
-        float top = 0.0f;
-        for (int i = 0; i < group / 32; ++i) {
-            const int j = g * group + 32 * i + lane;
-            y[i] = j < p.h ? y_at(j) : 0.0f;
-            top = max_abs(top, y[i]);
+    const int blocks = (p.h + 127) / 128;   // of a row
+    const auto load = [&](const T *from, int block, float (&y)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = block * 128 + 32 * i + lane;
+            y[i] = j < p.h ? Elem<kT>::load(from + j) : 0.0f;
         }
-        const uint32_t a = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
-        float step = token, inverse = 0.0f;
-        bool live;
-        if (p.qmode == QM_MX) {
-            const uint32_t code = mx_code(a, p.qkind);
-            if (lane == 0) static_cast<uint8_t *>(p.scale)[row * groups + g] = static_cast<uint8_t>(code);
-            live = code != 0xFFu;
-            inverse = mx_inverse(code);
-        } else {
-            if (p.qmode == QM_GROUP) {
-                step = __fmul_rn(__uint_as_float(a), q_inverse(p.qkind));
-                if (lane == 0) static_cast<float *>(p.scale)[row * groups + g] = step;
+        with_form(act, [&](const Activation &one) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const float2 v = act2(make_float2(y[i], y[i + 1]), one);
+                y[i] = v.x, y[i + 1] = v.y;
             }
-            live = usable(step);
+        });
+    };
+    const auto largest = [](const float (&y)[4]) {
+        return __float_as_uint(max_abs(max_abs(max_abs(max_abs(0.0f, y[0]), y[1]), y[2]), y[3]));
+    };
+    const auto store = [&](int64_t row, int block, const float (&r)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = block * 128 + 32 * i + lane;
+            if (j < p.h) static_cast<uint8_t *>(p.q)[row * p.h + j] = static_cast<uint8_t>(encode8(r[i], p.qkind));
         }
-        for (int i = 0; i < group / 32; ++i) {
-            const int j = g * group + 32 * i + lane;
-            if (j < p.h)
-                q[j] = live ? static_cast<uint8_t>(encode8(p.qmode == QM_MX ? y[i] * inverse : __fdiv_rn(y[i], step), p.qkind)) : 0;
+    };
+    float y[4], r[4];
+    if constexpr (kQM == QM_TOKEN) {
+        const int64_t row = kBlockRow ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+        const int first = kBlockRow ? warp : 0, step = kBlockRow ? kWarps : 1;
+        if (!kBlockRow && row >= p.m) return;
+        const T *from = static_cast<const T *>(z) + row * ldz;
+        uint32_t top = 0;
+        for (int b = first; b < blocks; b += step) {
+            load(from, b, y);
+            top = max(top, largest(y));
+        }
+        top = kBlockRow ? block_max32(top, slots) : __reduce_max_sync(0xFFFFFFFFu, top);
+        const float scale = __fmul_rn(__uint_as_float(top), q_inverse(p.qkind));
+        if (lane == 0 && first == 0) static_cast<float *>(p.scale)[row] = scale;
+        for (int b = first; b < blocks; b += step) {
+            load(from, b, y);
+            quotients(y, scale, r);
+            store(row, b, r);
+        }
+    } else {
+        const int64_t total = p.m * blocks, step = static_cast<int64_t>(gridDim.x) * kWarps;
+        const int groups = (p.h + group_size(kQM) - 1) / group_size(kQM);
+        for (int64_t e = static_cast<int64_t>(blockIdx.x) * kWarps + warp; e < total; e += step) {
+            const int64_t row = e / blocks;
+            const int b = static_cast<int>(e - row * blocks);
+            load(static_cast<const T *>(z) + row * ldz, b, y);
+            if constexpr (kQM == QM_GROUP) {
+                const float scale = __fmul_rn(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, largest(y))), q_inverse(p.qkind));
+                if (lane == 0) static_cast<float *>(p.scale)[row * groups + b] = scale;
+                quotients(y, scale, r);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t code = mx_code(__reduce_max_sync(0xFFFFFFFFu, abs_bits(y[i])), p.qkind);
+                    if (lane == 0 && b * 4 + i < groups) static_cast<uint8_t *>(p.scale)[row * groups + b * 4 + i] = static_cast<uint8_t>(code);
+                    r[i] = code != 0xFFu ? y[i] * mx_inverse(code) : 0.0f;
+                }
+            }
+            store(row, b, r);
         }
     }
 }
@@ -484,7 +510,14 @@ cudaError_t launch_to(const void *z, int64_t ldz, const Kept &p, int act, int nu
             default: return launch(act_quant_row_kernel<kT, 4, false>, grid, threads, stream, z, ldz, p, a);
         }
     }
-    return launch(act_quant_any_kernel<kT>, dim3(static_cast<unsigned>(p.m), 1, 1), kThreads, stream, z, ldz, p, a);
+    const int64_t units = (p.m * ((p.h + 127) / 128) + kWarps - 1) / kWarps, most = 64ll * num_sms;
+    const dim3 spread(static_cast<unsigned>(units < most ? units : most), 1, 1);
+    if (p.qmode == QM_GROUP) return launch(act_quant_any_kernel<kT, QM_GROUP, false>, spread, kThreads, stream, z, ldz, p, a);
+    if (p.qmode == QM_MX) return launch(act_quant_any_kernel<kT, QM_MX, false>, spread, kThreads, stream, z, ldz, p, a);
+    if (p.h <= 1024 && p.m > num_sms)
+        return launch(act_quant_any_kernel<kT, QM_TOKEN, false>, dim3(static_cast<unsigned>((p.m + kWarps - 1) / kWarps), 1, 1), kThreads, stream, z,
+                      ldz, p, a);
+    return launch(act_quant_any_kernel<kT, QM_TOKEN, true>, dim3(static_cast<unsigned>(p.m), 1, 1), kThreads, stream, z, ldz, p, a);
 }
 
 }  // namespace

@@ -69,12 +69,25 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
     }
 }
 
-// Rows of 16-bit elements from one layout to another, element by element.
+// Rows of 16-bit elements from one layout to another, by the aligned 16-byte units of the destination's rows (the first and
+// the last of them partial): a warp a row at a time.
 __global__ void __launch_bounds__(kThreads) copy_rows_kernel(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd, int64_t rows, int cols) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int c = threadIdx.x; c < cols; c += kThreads) dst[r * ldd + c] = src[r * lds + c];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kThreads / 32;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * warps + warp; r < rows; r += static_cast<int64_t>(gridDim.x) * warps) {
+        const uint16_t *from = src + r * lds;
+        uint16_t *to = dst + r * ldd;
+        for (int j = lane * 8 - static_cast<int>((reinterpret_cast<uintptr_t>(to) >> 1) & 7); j < cols; j += 32 * 8) {
+            if (j >= 0 && j + 8 <= cols) {
+                *reinterpret_cast<uint4 *>(to + j) = load_codes16(reinterpret_cast<const int8_t *>(from + j), 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (j + e >= 0 && j + e < cols) to[j + e] = from[j + e];
+            }
+        }
+    }
 }
 
 // dw and db from the parts' sums, added in order.  Four columns a thread; rows of dw are k elements, of a part ldp.
@@ -302,7 +315,7 @@ cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, 
     void *out = at.out_apart ? static_cast<void *>(ws + at.out) : p.out;
     const int64_t ldo = at.out_apart || p.m == 1 ? up8(p.n) : p.ldo;
     if (at.residual_in) {
-        e = launch(copy_rows_kernel, p.m < 4096 ? p.m : 4096, stream, static_cast<const uint16_t *>(p.residual), p.ldr,
+        e = launch(copy_rows_kernel, blocks_for(static_cast<int64_t>(p.m) * 32, num_sms), stream, static_cast<const uint16_t *>(p.residual), p.ldr,
                    static_cast<uint16_t *>(out), ldo, static_cast<int64_t>(p.m), p.n);
         if (e != cudaSuccess) return e;
         mark(ctx);
@@ -314,7 +327,7 @@ cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, 
     if (e != cudaSuccess) return e;
     mark(ctx);
     if (at.out_apart) {
-        e = launch(copy_rows_kernel, p.m < 4096 ? p.m : 4096, stream, static_cast<const uint16_t *>(out), ldo, static_cast<uint16_t *>(p.out),
+        e = launch(copy_rows_kernel, blocks_for(static_cast<int64_t>(p.m) * 32, num_sms), stream, static_cast<const uint16_t *>(out), ldo, static_cast<uint16_t *>(p.out),
                    p.ldo, static_cast<int64_t>(p.m), p.n);
         if (e != cudaSuccess) return e;
         mark(ctx);
@@ -335,7 +348,7 @@ cudaError_t launch_quant_weight_grad(bool bf16, const QuantWeightGrad &p, int nu
     int64_t lddy = p.m == 1 ? up8(p.n) : p.lddy;
     if (at.dy_apart) {
         dy = ws + at.dy, lddy = up8(p.n);
-        e = launch(copy_rows_kernel, p.m < 4096 ? p.m : 4096, stream, static_cast<const uint16_t *>(p.dy), p.lddy,
+        e = launch(copy_rows_kernel, blocks_for(static_cast<int64_t>(p.m) * 32, num_sms), stream, static_cast<const uint16_t *>(p.dy), p.lddy,
                    reinterpret_cast<uint16_t *>(ws + at.dy), lddy, static_cast<int64_t>(p.m), p.n);
         if (e != cudaSuccess) return e;
         mark(ctx);
