@@ -1,7 +1,8 @@
 """An MLP block on one GPU: the residual norm, the up projection with its
 activation, the down projection with the residual, and their backward; the same
-block for single tokens in a CUDA graph; and the norm's int8 codes into the
-all-to-all product, its per-group codes into the quantised all-reduce.
+block for single tokens in a CUDA graph; the block served in int8 and its backward
+from activations kept in 8 bits; and the norm's int8 codes into the all-to-all
+product, its per-group codes into the quantised all-reduce.
 
   python examples/mlp_block.py [--tokens 2048] [--hidden 4096] [--ffn 8192]
 
@@ -41,6 +42,28 @@ class Block:
         dz = mc2.mc2_matmul_act_grad(dy, self.w2, z, activation="gelu_tanh")
         dw2, db2 = mc2.mc2_matmul_weight_grad(dy, h)
         dw1, db1 = mc2.mc2_matmul_weight_grad(dz, n["out"])
+        dn, _ = mc2.mc2_matmul_bias_act(dz, self.w1, w_is_nk=False)
+        dx, dnorm = mc2.mc2_rms_norm_grad(dn, n["residual"], self.norm, n["rstd"], dres=dy)
+        return {"x": dx, "norm": dnorm, "w1": dw1, "b1": db1, "w2": dw2, "b2": db2}
+
+    def quantise(self):
+        """int8 weights, a scale for each of their rows (the output channels)."""
+        self.q1, self.q2 = mc2.mc2_act_quant(self.w1), mc2.mc2_act_quant(self.w2)
+
+    def forward8(self, x, residual, keep=False):
+        """The same in int8; what is kept is a byte an element: the norm's codes, and z's with a scale per 128 columns."""
+        n = mc2.mc2_add_rms_norm(x, self.norm, residual=residual, quant_mode=mc2.QUANT_PERTOKEN_DYNAMIC, with_rstd=keep)
+        z = mc2.mc2_quant_matmul(n["q"], n["scale"], *self.q1, bias=self.b1)
+        h = mc2.mc2_act_quant(z, activation="gelu_tanh")
+        y = mc2.mc2_quant_matmul(*h, *self.q2, bias=self.b2, residual=n["residual"])
+        return y, (n, mc2.mc2_act_quant(z, quant_mode=mc2.QUANT_PERGROUP)) if keep else None
+
+    def backward8(self, dy, kept):
+        n, z = kept
+        dw2, db2 = mc2.mc2_matmul_weight_grad_quant(dy, *z, activation="gelu_tanh")
+        dh, _ = mc2.mc2_matmul_bias_act(dy, self.w2, w_is_nk=False)
+        dz = mc2.mc2_act_grad_quant(dh, *z, activation="gelu_tanh", dz=dh)
+        dw1, db1 = mc2.mc2_matmul_weight_grad_quant(dz, n["q"], n["scale"])
         dn, _ = mc2.mc2_matmul_bias_act(dz, self.w1, w_is_nk=False)
         dx, dnorm = mc2.mc2_rms_norm_grad(dn, n["residual"], self.norm, n["rstd"], dres=dy)
         return {"x": dx, "norm": dnorm, "w1": dw1, "b1": db1, "w2": dw2, "b2": db2}
@@ -104,6 +127,20 @@ def main():
     with torch.cuda.graph(graph):
         ty, _ = block.forward(tx, tr)
     print(f"one token, captured: {microseconds(graph.replay, 200):.1f} us")
+
+    # the block in 8 bits: a quarter of the kept activations' bytes, and int8 weights
+    block.quantise()
+    _, k8 = block.forward8(x, r, keep=True)
+    print(f"forward in int8: {microseconds(lambda: block.forward8(x, r, keep=True)):.1f} us, "
+          f"backward from kept codes: {microseconds(lambda: block.backward8(dy, k8)):.1f} us")
+    ys, ks = block.forward8(x[:few], r[:few], keep=True)
+    gs = block.backward8(dy[:few], ks)
+    print("relative error against 64 bits:", ", ".join([f"y {off(ys, want):.1e}"] + [f"d{k} {off(v, wgrads[k]):.1e}" for k, v in gs.items()]))
+    graph8 = torch.cuda.CUDAGraph()
+    block.forward8(tx, tr)
+    with torch.cuda.graph(graph8):
+        ty8, _ = block.forward8(tx, tr)
+    print(f"one token in int8, captured: {microseconds(graph8.replay, 200):.1f} us")
 
     # the norm's int8 codes into the all-to-all product (four ranks' column blocks of the hidden state)
     ranks = 4

@@ -457,9 +457,10 @@ int mc2_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int a
  *     MC2_QUANT_MX                 scale e8m0 codes (m, ceil(h / 32)); fp8 codes only
  * and q (m, h) of MC2_I8, MC2_F8E4M3 or MC2_F8E5M2 and scale are contiguous.  A
  * code stands for q times its scale in fp32 (a scale that is a NaN or infinite makes
- * its zeros NaN, so that what could not be held is not lost).
+ * its zeros NaN, so that what could not be held is not lost; relu's derivative there is 0, as it is of a NaN).
  * Sizes are at most 2^30.  A call's tensors may have any alignment that suits their
- * elements, and its matrices any row stride.
+ * elements, and its matrices any row stride.  An output overlaps no other tensor of the call, but where its
+ * comment says that it may be an input itself.
  */
 
 /*
@@ -480,9 +481,9 @@ int mc2_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int a
  *   act        an mc2_activation
  *   residual   NULL or (m, n) of dtype, rows ldr apart
  *   dtype      MC2_F16 or MC2_BF16;  out (m, n), rows ldo apart; may be residual itself (same stride)
- *   workspace  device scratch of at least the bytes the query returns for the same matrices
- *              (0 where the product of few tokens reads its operands as they are: NULL is then fine), 16-byte
- *              aligned, no initialisation; reusable by calls ordered on one stream
+ *   workspace  device scratch of at least the bytes the query returns for the same matrices and sizes on the
+ *              same device (0 where the product of few tokens reads its operands as they are: NULL is then
+ *              fine), 16-byte aligned, no initialisation; reusable by calls ordered on one stream
  *
  * Returns MC2_OK or a negative mc2_status; nothing is launched on error.
  */
@@ -529,8 +530,9 @@ int mc2_act_grad_quant(const void *dy, int64_t lddy, const void *q, const void *
  *   dw[i, j] = sum_t dy[t, i] * act(q[t, j] * scale)       (n, k)
  *   db[i]    = sum_t dy[t, i]                              (n)
  *
- *   act(q * scale) is rounded to dtype, the tensor cores' operand type; sums are fp32, and
- *   dw and db rounded once.  Calls of the same sizes, types and layouts add in the same order.
+ *   act(q * scale) is rounded to dtype, the tensor cores' operand type (MC2_F16: beyond 65504 to infinity); sums are
+ *   fp32, and dw and db rounded once.  Calls of the same sizes, types, strides and alignment add in the same order
+ *   and give the same bits.
  *
  *   dy         (m, n), rows lddy apart;  q (m, k) with its scales
  *   dw         (n, k);  db NULL or (n);  dtype MC2_F16 or MC2_BF16 for dy, dw and db
@@ -569,7 +571,14 @@ int mc2_device_status(void);
  *   mc2_all_gather_mm, mc2_matmul_reduce_scatter   1: the GEMM
  *   mc2_matmul_weight_grad     1: the GEMM (which also forms db)
  *   mc2_quant_all_reduce       1: the reduction
- *   mc2_add_rms_norm, mc2_matmul_bias_act, mc2_matmul_act_grad, mc2_act_grad   1
+ *   mc2_add_rms_norm, mc2_matmul_bias_act, mc2_matmul_act_grad, mc2_act_grad,
+ *   mc2_act_quant, mc2_act_dequant, mc2_act_grad_quant   1
+ *   mc2_quant_matmul           1 for few tokens (2 where the matrices are not 16-byte aligned); for
+ *                              many the widening of both operands and the GEMM, with a copy of the
+ *                              residual before it or of the output after it where the tensor copies
+ *                              cannot take them (2 to 4)
+ *   mc2_matmul_weight_grad_quant   the values of the codes, the GEMM or its parts, and the sum of the parts
+ *                              (2 or 3), with a copy of dy before the GEMM where the tensor copies cannot take it
  *   mc2_rms_norm_grad          1, or 2 with dw: the gradient, the sum of its shares of dw
  *   mc2_alltoall_quant_mm      x1_quant_mode 7: 2 (the fused quant and x2
  *                              widening, the GEMM), or 3 when rank_size*h > 32768

@@ -18,6 +18,9 @@
 //   which keeps the tensor core's own accumulation error (it adds at the
 //   magnitude of the running sum) to the size of one block's partial sums.
 //
+//   * Products of the epilogue forms of epilogue.cuh, among them int8 codes held as fp16 with scales of rows and columns
+//     (EPI_SCALED: K blocks of 1024, added as integers) and a contraction in parts whose sums leave in fp32 (EPI_SUMS).
+//
 // Two shapes of the same kernel (template parameter kG):
 //   kG = 1  one CTA per tile: tile 128 x 256 x 64, tcgen05.mma.cta_group::1
 //           M=128 N=256, 4-stage ring of 48 KiB stages; or (kNarrow, outputs at

@@ -13,7 +13,7 @@
 //           tokens cost in L2 reads
 //   warp 1      TMEM allocation, MMA issue (the pair's first CTA)
 //   warps 0, 2  TMA producers, every other stage each
-//   the others  bring what the epilogue will read into L1
+//   the others  bring what the epilogue will read into L1; of int8 codes, widen them (below)
 //   all warps   then: partial sums from TMEM to shared memory, the sum over the
 //               cluster, and the epilogue, four columns a thread
 // Next to that, a stage's time was its issue: one lane took 460 clocks for a stage's two copies
@@ -27,6 +27,11 @@
 // the contraction goes to an accumulator of its own while TMEM has room, and
 // these are added in fp32 with round-to-nearest.  Beyond that they are used again (two for 256
 // tokens: 6144 deep each for 2000 x 1024 x 24576, split in two).
+//
+// Int8 codes (EPI_SCALED) come as bytes, 128 deep a stage, and warps bring them to fp16 between the copies and the MMAs: the
+// weight to TMEM, from where the MMA takes its A, the tokens (and an M-major weight) to shared memory.  Blocks of 1024 stay in
+// accumulators of their own, so every sum is an exact integer, in any shape.  A stage then takes 0.26 us and 2.7 ns a
+// token of the CTA (M-major 0.33 and 4.4): 64 tokens, 4096 x 4096 9.5 us, 256 13.7, 64 tokens, 28672 x 8192 57 (4.1 TB/s).
 #include <atomic>
 #include <cmath>
 #include <type_traits>

@@ -5,7 +5,8 @@
 // (4096 to 8192 deep this takes 1% more than one accumulator over all of it).
 // The tensor pipe bounds it, and called in turn the power limit: 8192 x 8192 x 7168 with bias, gelu and the
 // pre-activation 520 us (1852 TFLOP/s) in a graph of a few launches, 597 to 610 us in turn; without an
-// epilogue 493 in the graph.
+// epilogue 493 in the graph.  Two more forms: int8 codes held as fp16, whose blocks of 1024 are added as integers and scaled
+// by row and column (2048 tokens, 4096 x 4096: 41 us), and the parts of a weight gradient's sums in fp32.
 #include "gemm_tcgen05.cuh"
 #include "host.h"
 #include "internal.h"

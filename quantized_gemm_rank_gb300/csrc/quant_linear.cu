@@ -8,7 +8,8 @@
 // the fp32 sums of 1024 of their products; act(q scale) is rounded to dy's type.  The codes of few tokens are widened on
 // their way to the tensor cores (linear_split.cu): the weight is read once, as bytes.  The operands of many rows are
 // brought to 16 bits in the workspace, each element once, and multiplied by the GEMM of gemm_tcgen05.cuh; matrices that the
-// tensor copies cannot take go through the workspace, too.
+// tensor copies cannot take go through the workspace, too.  4096 tokens, 7168 x 8192: 303 us, of which widening takes 55 (4.9 TB/s); the
+// weight gradient 4096 x 7168 of 8192 tokens 292 us, from gelu(z) 311 (its values 36 and 56 us), the product itself 257.
 #include "kept.h"
 
 #include "codes.cuh"
@@ -29,19 +30,37 @@ struct Widened {
     void *dst;
     int64_t ld, pitch, rows;
     int64_t cols;
-    int64_t vectors;   // 16 columns each
+    int64_t vectors;   // of a row: 8 columns each as fp16, 16 as they are (16 bytes written)
+    int whole;         // one row of whole vectors, 16-byte aligned
 };
 
-// Both operands of a product in one launch: blocks [0, first) take a, the others b, 16 codes a thread at a time.
+// Both operands of a product in one launch: blocks [0, first) take a, the others b, 16 bytes written a thread at a time, so that
+// a warp's stores are one stretch (two of them a thread, 32 bytes apart, took 16.4 us for 25 M codes and these 11).
 template <bool kWiden>
 __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ Widened a, const __grid_constant__ Widened b, int first) {
+    constexpr int kVector = kWiden ? 8 : 16, kAhead = 4;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     const bool is_a = static_cast<int>(blockIdx.x) < first;
     const Widened &t = is_a ? a : b;
     const int64_t block = is_a ? blockIdx.x : blockIdx.x - first, blocks = is_a ? first : gridDim.x - first;
-    const int64_t total = t.rows * t.vectors;
-    for (int64_t e = block * kThreads + threadIdx.x; e < total; e += blocks * kThreads) {
+    const int64_t total = t.rows * t.vectors, step = blocks * kThreads;
+    int64_t e = block * kThreads + threadIdx.x;
+    if (kWiden && t.whole) {
+        uint4 *to = static_cast<uint4 *>(t.dst);
+        const uint2 *from = reinterpret_cast<const uint2 *>(t.src);
+        for (; e + (kAhead - 1) * step < total; e += kAhead * step) {
+            uint2 q[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) q[i] = __ldg(from + e + i * step);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const uint2 lo = widen4(q[i].x), hi = widen4(q[i].y);
+                to[e + i * step] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+        }
+    }
+    for (; e < total; e += step) {
         int64_t r = 0, v = e;
         if (t.rows > 1) {
             if (total <= UINT32_MAX) {
@@ -51,20 +70,14 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
             }
             v = e - r * t.vectors;
         }
-        const int8_t *from = t.src + r * t.ld + v * 16;
-        const int64_t left = t.cols - v * 16;
-        const uint4 codes = load_codes16(from, left < 16 ? static_cast<int>(left) : 16);
-        const uint32_t q[4] = {codes.x, codes.y, codes.z, codes.w};
         // (a row's last vector is whole, zeros behind its end)
+        const int64_t left = t.cols - v * kVector;
+        const uint4 q = load_codes16(t.src + r * t.ld + v * kVector, left < kVector ? static_cast<int>(left) : kVector);
         if constexpr (kWiden) {
-            uint4 *to = reinterpret_cast<uint4 *>(static_cast<__half *>(t.dst) + r * t.pitch + v * 16);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint2 lo = widen4(q[2 * i]), hi = widen4(q[2 * i + 1]);
-                to[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            }
+            const uint2 lo = widen4(q.x), hi = widen4(q.y);
+            *reinterpret_cast<uint4 *>(static_cast<__half *>(t.dst) + r * t.pitch + v * kVector) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         } else {
-            *reinterpret_cast<uint4 *>(static_cast<int8_t *>(t.dst) + r * t.pitch + v * 16) = make_uint4(q[0], q[1], q[2], q[3]);
+            *reinterpret_cast<uint4 *>(static_cast<int8_t *>(t.dst) + r * t.pitch + v * kVector) = q;
         }
     }
 }
@@ -290,9 +303,13 @@ cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, 
     l.w = p.w, l.ldw = w_rows == 1 ? up16(w_cols) : p.ldw;
     if (at.apart) {
         const auto taken = [&](const int8_t *src, int64_t ld, void *dst, int64_t rows, int64_t cols) {
-            Widened t = {src, dst, ld, up16(cols), rows, cols, (cols + 15) / 16};
+            const int vector = at.split ? 16 : 8;
+            Widened t = {src, dst, ld, up16(cols), rows, cols, (cols + vector - 1) / vector, 0};
             // matrices without gaps are one row
-            if (rows > 1 && ld == cols && cols % 16 == 0) t.cols = rows * cols, t.rows = 1, t.vectors = t.cols / 16;
+            if (ld == cols && cols % 16 == 0) {
+                t.cols = rows * cols, t.rows = 1, t.vectors = t.cols / vector;
+                t.whole = host::aligned16(src);
+            }
             return t;
         };
         const Widened a = taken(p.x, p.ldx, ws + at.x, p.m, p.k), b = taken(p.w, p.ldw, ws + at.w, w_rows, w_cols);

@@ -89,7 +89,7 @@ def test_workspace_queries():
     f = L.mc2_quant_matmul_workspace
     good = (FAKE, 4096, FAKE, 4096, 1, 4096, 4096, 4096, None, 0, FAKE, 4096, ref)
     assert f(*good) == mc2.MC2_OK and n.value >= 2 * 2 * 4096 * 4096   # both operands in 16 bits
-    few = (*good[:5], 1, *good[6:])
+    few = (*good[:5], 16, *good[6:])
     assert f(*few) == mc2.MC2_OK and n.value == 0
     assert f(FAKE + 1, *few[1:]) == mc2.MC2_OK and n.value > 4096 * 4096
     for at, value, status in ((0, None, mc2.MC2_ERR_NULL), (2, None, mc2.MC2_ERR_NULL), (10, None, mc2.MC2_ERR_NULL), (12, None, mc2.MC2_ERR_NULL),
