@@ -8,7 +8,7 @@
 // the fp32 sums of 1024 of their products; act(q scale) is rounded to dy's type.  The codes of few tokens are widened on
 // their way to the tensor cores (linear_split.cu): the weight is read once, as bytes.  The operands of many rows are
 // brought to 16 bits in the workspace, each element once, and multiplied by the GEMM of gemm_tcgen05.cuh; matrices that the
-// tensor copies cannot take go through the workspace, too.  4096 tokens, 7168 x 8192: 303 us, of which widening takes 55 (4.9 TB/s); the
+// tensor copies cannot take go through the workspace, too.  4096 tokens, 7168 x 8192: 282 to 295 us, of which widening takes 43; the
 // weight gradient 4096 x 7168 of 8192 tokens 292 us, from gelu(z) 311 (its values 36 and 56 us), the product itself 257.
 #include "kept.h"
 
@@ -35,7 +35,7 @@ struct Widened {
 };
 
 // Both operands of a product in one launch: blocks [0, first) take a, the others b, 16 bytes written a thread at a time, so that
-// a warp's stores are one stretch (two of them a thread, 32 bytes apart, took 16.4 us for 25 M codes and these 11).
+// a warp's stores are one stretch (92 M codes: 55 us with two of them a thread, 32 bytes apart, 43 this way, 6.4 TB/s).
 template <bool kWiden>
 __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ Widened a, const __grid_constant__ Widened b, int first) {
     constexpr int kVector = kWiden ? 8 : 16, kAhead = 4;
@@ -215,7 +215,7 @@ ProductPlan plan_product(const QuantProduct &p) {
     at.tokens = p.w_nk && (p.m <= 4 || (p.m <= 8 && static_cast<int64_t>(p.n) * p.k <= 8ll << 20));
     if (at.tokens) return at;
     // Which kernel, by the sizes alone: the tiles take 9.4 us, 3.2 and 0.25 a 64-deep stage for each wave of them, and widening three
-    // bytes a code at 5000 a ns (1024 tokens, 4096 x 14336 112 us, 8192 x 4096 70; 4096 tokens, 4096 x 4096 106).  Where the two
+    // bytes a code at 5000 a ns (since then 6400 where a matrix has no gaps) (1024 tokens, 4096 x 14336 112 us, 8192 x 4096 70; 4096 tokens, 4096 x 4096 106).  Where the two
     // cross, with k = 4096: 512 tokens, n = 4096 24.6 us split, 31 in tiles; 1024 tokens, n = 8192 137 and 70.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256);
     const float steps = static_cast<float>((p.k + 63) / 64);
