@@ -110,7 +110,7 @@ int mc2_quant_matmul_workspace(const int8_t *x, int64_t ldx, const int8_t *w, in
     if (!bytes) return fail(MC2_ERR_NULL, "bytes is NULL");
     mc2::QuantProduct p = {};
     if (int st = check_product(x, ldx, w, ldw, w_is_nk, m, n, k, residual, ldr, out, ldo, &p)) return st;
-    *bytes = mc2::quant_product_workspace(p);
+    *bytes = mc2::plan_quant_product(p).total;
     return MC2_OK;
 }
 
@@ -131,7 +131,8 @@ int mc2_quant_matmul(const int8_t *x, int64_t ldx, const float *x_scale, const i
             return fail(MC2_ERR_DTYPE, "the bias must be of the type of out or MC2_F32 (got %d)", bias_dtype);
         if (int st = check_rows("bias", bias, n, 1, n, elem_size(bias_dtype))) return st;
     }
-    if (int st = check_workspace(workspace, workspace_bytes, mc2::quant_product_workspace(p))) return st;
+    const mc2::ProductPlan plan = mc2::plan_quant_product(p);
+    if (int st = check_workspace(workspace, workspace_bytes, plan.total)) return st;
     DeviceInfo dev;
     if (int st = current_device(&dev)) return st;
     p.x_scale = x_scale, p.w_scale = w_scale, p.bias = bias;
@@ -140,7 +141,7 @@ int mc2_quant_matmul(const int8_t *x, int64_t ldx, const float *x_scale, const i
     p.workspace = workspace;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     LaunchMarks marks(s);
-    cudaError_t e = mc2::launch_quant_product(dtype == MC2_BF16, p, dev.num_sms, s, mark, &marks);
+    cudaError_t e = mc2::launch_quant_product(dtype == MC2_BF16, p, plan, dev.num_sms, s, mark, &marks);
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "quant_matmul launch: %s", cudaGetErrorString(e));
     return MC2_OK;
 }

@@ -1078,13 +1078,16 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                                 for (int i = 0; i < 4; ++i) v[4 * j + i] = __fmul_rn(__fmul_rn(v[4 * j + i], row_scale), t4[i]);
                             }
                         } else {
+                            // (columns past the last are zero: an activation works on pairs, and a last column without a
+                            // neighbour has the same one in every kernel)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                v[i] = __fmul_rn(__fmul_rn(v[i], row_scale), __ldg(p.x2_scale + min(colh + 32 * c + i, p.n - 1)));
+                                v[i] = __fmul_rn(__fmul_rn(v[i], row_scale), colh + 32 * c + i < p.n ? __ldg(p.x2_scale + colh + 32 * c + i) : 0.0f);
                         }
                         if (p.bias_f32 != nullptr) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __fadd_rn(v[i], __ldg(p.bias_f32 + min(colh + 32 * c + i, p.n - 1)));
+                            for (int i = 0; i < 32; ++i)
+                                if (colh + 32 * c + i < p.n) v[i] = __fadd_rn(v[i], __ldg(p.bias_f32 + colh + 32 * c + i));
                         }
                     }
                     if (bias_whole) {
@@ -1103,7 +1106,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     } else if (p.bias16 != nullptr) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            v[i] = __fadd_rn(v[i], load16<kBF16>(p.bias16, min(colh + 32 * c + i, p.n - 1)));
+                            if (kEpi != EPI_SCALED || colh + 32 * c + i < p.n)
+                                v[i] = __fadd_rn(v[i], load16<kBF16>(p.bias16, min(colh + 32 * c + i, p.n - 1)));
                     }
                     // with a pre-activation output: that through buffer 0, the output through buffer 1
                     const int i = p.has_pre ? 1 : c & 1;

@@ -40,10 +40,19 @@ struct QuantProduct {
 };
 // One to eight tokens and an (n, k) weight, in any layout.
 cudaError_t launch_quant_tokens(bool bf16, const QuantProduct &p, cudaStream_t stream);
-size_t quant_product_workspace(const QuantProduct &p);
+// How a product is computed, and the pieces of its workspace (in bytes from its start).
+struct ProductPlan {
+    size_t x = 0, w = 0, out = 0, total = 0;
+    bool tokens = false;       // the kernel of one to eight tokens, on the matrices as they are
+    bool split = false;        // the one of few tokens, on int8 operands
+    bool apart = false;        // the operands go through the workspace (the tiles': always)
+    bool out_apart = false;    // the output, too
+    bool residual_in = false;  // the residual is copied to where the output will be
+};
+ProductPlan plan_quant_product(const QuantProduct &p);   // by the matrices and sizes
 // Kernels of a call, each followed by mark(ctx)
 using Mark = void (*)(void *ctx);
-cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, cudaStream_t stream, Mark mark, void *ctx);
+cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, const ProductPlan &at, int num_sms, cudaStream_t stream, Mark mark, void *ctx);
 
 // dw (n, k) = dy^T act(q scale), db (n) = column sums of dy (or none); x is (m, k)
 struct QuantWeightGrad {

@@ -167,8 +167,11 @@ __device__ __forceinline__ void finish_tokens(const SplitParams &p, const float4
             for (int i = 0; i < 4; ++i) v[4 * u + i] = __fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[4 * u + i])), s), w4[i]);
         }
     }
+    // (codes: a sum's negative zero stays one without a bias, as in the other kernels)
+    if (!kCodes || p.bias) {
 #pragma unroll
-    for (int i = 0; i < 4 * kT; ++i) v[i] = __fadd_rn(v[i], b4[i & 3]);
+        for (int i = 0; i < 4 * kT; ++i) v[i] = __fadd_rn(v[i], b4[i & 3]);
+    }
     if (pre_row) {
 #pragma unroll
         for (int u = 0; u < kT; ++u) store4<kBF16>(pre_row + u * p.ldp, n, &v[4 * u], words);

@@ -187,15 +187,6 @@ struct Pieces {
     }
 };
 
-struct ProductPlan {
-    size_t x = 0, w = 0, out = 0, total = 0;
-    bool tokens = false;       // the kernel of one to eight tokens, on the matrices as they are
-    bool split = false;        // the one of few tokens, on int8 operands
-    bool apart = false;        // the operands go through the workspace (the tiles': always)
-    bool out_apart = false;    // the output, too
-    bool residual_in = false;  // the residual is copied to where the output will be
-};
-
 // The matrices and sizes as the product kernels take them.
 LinearParams product_of(const QuantProduct &p) {
     LinearParams l = {};
@@ -206,39 +197,6 @@ LinearParams product_of(const QuantProduct &p) {
     l.aux_mode = p.residual ? AUX_RESIDUAL : AUX_NONE;
     l.x_scale = p.x_scale, l.w_scale = p.w_scale;
     return l;
-}
-
-ProductPlan plan_product(const QuantProduct &p) {
-    ProductPlan at;
-    // one to four tokens (4096 x 4096: 3.8, 4.7 and 6.8 us for 1, 2 and 4, 7.7 to 7.9 in the kernel of few); to eight where the
-    // weight is small (1024 x 8192 4.5 against 6.6, 4096 x 4096 8.3 against 7.8)
-    at.tokens = p.w_nk && (p.m <= 4 || (p.m <= 8 && static_cast<int64_t>(p.n) * p.k <= 8ll << 20));
-    if (at.tokens) return at;
-    // Which kernel, by the sizes alone: the tiles take 9.4 us, 3.2 and 0.25 a 64-deep stage for each wave of them, and widening three
-    // bytes a code at 5000 a ns (since then 6400 where a matrix has no gaps) (1024 tokens, 4096 x 14336 112 us, 8192 x 4096 70; 4096 tokens, 4096 x 4096 106).  Where the two
-    // cross, with k = 4096: 512 tokens, n = 4096 24.6 us split, 31 in tiles; 1024 tokens, n = 8192 137 and 70.
-    const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256);
-    const float steps = static_cast<float>((p.k + 63) / 64);
-    const float tiles_us = 9.4f + static_cast<float>((tiles + kPairs - 1) / kPairs) * (3.2f + 0.2475f * steps) +
-                           (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 0.6e-6f;
-    LinearParams l = product_of(p);
-    l.x_scale = reinterpret_cast<const float *>(p.x);   // (codes; not read)
-    const float split_us = linear_split_codes_us(l, kSms);
-    at.split = split_us >= 0.0f && split_us < tiles_us;
-    Pieces ws;
-    const int64_t w_rows = p.w_nk ? p.n : p.k, w_cols = p.w_nk ? p.k : p.n;
-    at.apart = !at.split || !copies_read8(p.x, p.ldx, p.m) || !copies_read8(p.w, p.ldw, w_rows);
-    if (at.apart) {
-        at.x = ws.take(p.m * up16(p.k), at.split ? 1 : 2);
-        at.w = ws.take(w_rows * up16(w_cols), at.split ? 1 : 2);
-    }
-    if (!at.split) {
-        at.out_apart = !copies_write16(p.out, p.ldo, p.m, p.n);
-        at.residual_in = p.residual && (at.out_apart || !copies_read16(p.residual, p.ldr, p.m));
-        if (at.out_apart) at.out = ws.take(p.m * up8(p.n), 2);
-    }
-    at.total = ws.total;
-    return at;
 }
 
 // A contraction over m rows for few outputs is split: parts of it on CTA pairs that would have no tile, and their sums added by
@@ -285,10 +243,40 @@ WeightPlan plan_weight_grad(const QuantWeightGrad &p) {
 
 }  // namespace
 
-size_t quant_product_workspace(const QuantProduct &p) { return plan_product(p).total; }
+ProductPlan plan_quant_product(const QuantProduct &p) {
+    ProductPlan at;
+    // one to four tokens (4096 x 4096: 3.8, 4.7 and 6.8 us for 1, 2 and 4, 7.7 to 7.9 in the kernel of few); to eight where the
+    // weight is small (1024 x 8192 4.5 against 6.6, 4096 x 4096 8.3 against 7.8)
+    at.tokens = p.w_nk && (p.m <= 4 || (p.m <= 8 && static_cast<int64_t>(p.n) * p.k <= 8ll << 20));
+    if (at.tokens) return at;
+    // Which kernel, by the sizes alone: the tiles take 9.4 us, 3.2 and 0.25 a 64-deep stage for each wave of them, and widening three
+    // bytes a code at 5000 a ns (since then 6400 where a matrix has no gaps) (1024 tokens, 4096 x 14336 112 us, 8192 x 4096 70; 4096 tokens, 4096 x 4096 106).  Where the two
+    // cross, with k = 4096: 512 tokens, n = 4096 24.6 us split, 31 in tiles; 1024 tokens, n = 8192 137 and 70.
+    const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256);
+    const float steps = static_cast<float>((p.k + 63) / 64);
+    const float tiles_us = 9.4f + static_cast<float>((tiles + kPairs - 1) / kPairs) * (3.2f + 0.2475f * steps) +
+                           (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 0.6e-6f;
+    LinearParams l = product_of(p);
+    l.x_scale = reinterpret_cast<const float *>(p.x);   // (codes; not read)
+    const float split_us = linear_split_codes_us(l, kSms);
+    at.split = split_us >= 0.0f && split_us < tiles_us;
+    Pieces ws;
+    const int64_t w_rows = p.w_nk ? p.n : p.k, w_cols = p.w_nk ? p.k : p.n;
+    at.apart = !at.split || !copies_read8(p.x, p.ldx, p.m) || !copies_read8(p.w, p.ldw, w_rows);
+    if (at.apart) {
+        at.x = ws.take(p.m * up16(p.k), at.split ? 1 : 2);
+        at.w = ws.take(w_rows * up16(w_cols), at.split ? 1 : 2);
+    }
+    if (!at.split) {
+        at.out_apart = !copies_write16(p.out, p.ldo, p.m, p.n);
+        at.residual_in = p.residual && (at.out_apart || !copies_read16(p.residual, p.ldr, p.m));
+        if (at.out_apart) at.out = ws.take(p.m * up8(p.n), 2);
+    }
+    at.total = ws.total;
+    return at;
+}
 
-cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, int num_sms, cudaStream_t stream, Mark mark, void *ctx) {
-    const ProductPlan at = plan_product(p);
+cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, const ProductPlan &at, int num_sms, cudaStream_t stream, Mark mark, void *ctx) {
     if (at.tokens) {
         const cudaError_t e = launch_quant_tokens(bf16, p, stream);
         if (e == cudaSuccess) mark(ctx);

@@ -86,18 +86,32 @@ __global__ void __launch_bounds__(kThreads, resident(kM)) quant_tokens_kernel(co
             if (lane == 0) parts[warp][t * kRows + r] = sum;
         }
     __syncthreads();
-    // an output a thread: rows of the weight next to one another
-    for (int e = threadIdx.x; e < groups * kRows * kM; e += kThreads) {
-        const int t = e / (groups * kRows), g = (e / kRows) % groups, r = e % kRows;
+    // two outputs a thread, of neighbouring rows of the weight: an activation works on pairs, and these are the pairs of the
+    // other kernels (a last column without a neighbour has a zero beside it)
+    static_assert(kRows % 2 == 0, "pairs within a warp's rows");
+    for (int e = threadIdx.x; e < groups * (kRows / 2) * kM; e += kThreads) {
+        const int t = e / (groups * (kRows / 2)), g = (e / (kRows / 2)) % groups, r = e % (kRows / 2) * 2;
         const int j = (blockIdx.x * groups + g) * kRows + r;
         if (t >= p.m || j >= p.n) continue;
-        int sum = 0;
-        for (int i = 0; i < slices; ++i) sum += parts[g * slices + i][t * kRows + r];
-        float z = __fmul_rn(__fmul_rn(__int2float_rn(sum), p.x_scale[t]), p.w_scale[j]);
-        if (p.bias) z = __fadd_rn(z, p.bias_f32 ? static_cast<const float *>(p.bias)[j] : E::load(static_cast<const T *>(p.bias) + j));
-        float o = act2(both(z), act).x;
-        if (p.residual) o = __fadd_rn(o, E::load(static_cast<const T *>(p.residual) + t * p.ldr + j));
-        E::store(static_cast<T *>(p.out) + t * p.ldo + j, o);
+        float z[2] = {};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (j + c >= p.n) continue;
+            int sum = 0;
+            for (int i = 0; i < slices; ++i) sum += parts[g * slices + i][t * kRows + r + c];
+            z[c] = __fmul_rn(__fmul_rn(__int2float_rn(sum), p.x_scale[t]), p.w_scale[j + c]);
+            if (p.bias)
+                z[c] = __fadd_rn(z[c], p.bias_f32 ? static_cast<const float *>(p.bias)[j + c] : E::load(static_cast<const T *>(p.bias) + j + c));
+        }
+        const float2 a = act2(make_float2(z[0], z[1]), act);
+        const float o[2] = {a.x, a.y};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (j + c >= p.n) continue;
+            float v = o[c];
+            if (p.residual) v = __fadd_rn(v, E::load(static_cast<const T *>(p.residual) + t * p.ldr + j + c));
+            E::store(static_cast<T *>(p.out) + t * p.ldo + j + c, v);
+        }
     }
 }
 

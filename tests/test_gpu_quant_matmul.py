@@ -143,19 +143,27 @@ def test_the_deepest_product():
         assert torch.equal(out, sums(t, w, True).float().to(BF16))
 
 
-@pytest.mark.parametrize("n,k", [(512, 4096), (1000, 2056), (300, 1000)])
-def test_a_token_does_not_depend_on_the_others(n, k):
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("n,k", [(512, 4096), (1001, 2056), (333, 1000)])
+@pytest.mark.parametrize("bias_type", [None, BF16, torch.float32])
+def test_a_token_does_not_depend_on_the_others(n, k, act, bias_type):
     """The same bits for a row by itself, in a batch, and in a prompt; and from strided rows."""
     x, xs, w, ws = make(1200, n, k, 5)
-    bias = torch.randn(n, device="cuda")
-    whole = mc2.mc2_quant_matmul(x, xs, w, ws, bias=bias, activation="silu")
-    for m in (1, 2, 17, 64, 100, 250, 600):
-        part = mc2.mc2_quant_matmul(x[:m], xs[:m], w, ws, bias=bias, activation="silu")
-        assert torch.equal(part, whole[:m]), m
+    ws[::3] *= -1     # (negative zeros, too)
+    x[5] = 0
+    bias = None if bias_type is None else torch.randn(n, device="cuda").to(bias_type)
+
+    def bits(rows, scales):
+        return mc2.mc2_quant_matmul(rows, scales, w, ws, bias=bias, activation=act).view(torch.int16)
+
+    whole = bits(x, xs)
+    for m in (1, 2, 4, 7, 17, 64, 100, 250, 600):
+        assert torch.equal(bits(x[:m], xs[:m]), whole[:m]), m
+    for first in range(4, 1200, 149):
+        assert torch.equal(bits(x[first:first + 4], xs[first:first + 4]), whole[first:first + 4]), first
     wide = torch.zeros(70, k + 5, dtype=torch.int8, device="cuda")
     wide[:, 3:3 + k] = x[:70]
-    part = mc2.mc2_quant_matmul(wide[:, 3:3 + k], xs[:70], w, ws, bias=bias, activation="silu")
-    assert torch.equal(part, whole[:70])
+    assert torch.equal(bits(wide[:, 3:3 + k], xs[:70]), whole[:70])
 
 
 def test_scales_that_are_zero_or_not_numbers():
