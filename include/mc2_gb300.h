@@ -471,8 +471,8 @@ int mc2_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int a
  *   z   = (float(acc) * x_scale[t]) * w_scale[j] (+ bias[j])
  *   out = act(z) (+ residual)
  *
- *   The sums are exact integers, so an output depends on its row and its column alone: not on
- *   the other tokens of the call, on strides or alignment.  The rest is fp32; out is rounded once.
+ *   The sums are exact integers, so the bits of a token's outputs do not depend on the other tokens of
+ *   the call, on strides or on alignment.  The rest is fp32; out is rounded once.
  *
  *   x          (m, k) int8, rows ldx apart;  x_scale fp32 (m)
  *   w          (n, k) (the nn.Linear layout) or (k, n) int8, rows ldw apart;  w_scale fp32 (n)

@@ -156,9 +156,10 @@ __device__ __forceinline__ uint2 load_bytes8(const uint8_t *p) {
 // Rows of any width and alignment: the chunks are those of the output's aligned 16-byte units, the first and the
 // last of a row partial; codes and dy come from any address.
 template <int kT, bool kGrad, int kQM>
-__global__ void __launch_bounds__(kThreads) from_kept_any_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p, Activation act,
-                                                                 void *out, int64_t ldo, Cover cover) {
-    using T = typename Elem<kT>::type;
+__global__ void __launch_bounds__(kThreads, kGrad ? 4 : 6) from_kept_any_kernel(const void *dy, int64_t lddy, const __grid_constant__ Kept p,
+                                                                                Activation act, void *out, int64_t ldo, Cover cover) {
+    using E = Elem<kT>;
+    using T = typename E::type;
     constexpr int kE = kT == ELEM_F32 ? 4 : 2;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
@@ -170,42 +171,36 @@ __global__ void __launch_bounds__(kThreads) from_kept_any_kernel(const void *dy,
         const T *from = kGrad ? static_cast<const T *>(dy) + r * lddy : nullptr;
         const uint8_t *q = static_cast<const uint8_t *>(p.q) + r * p.h;
         const int j0 = c * kChunk - static_cast<int>(reinterpret_cast<uintptr_t>(to) / kE % kChunk);
-        const int lo = max(j0, 0), hi = min(j0 + kChunk, p.h);
-        if (lo >= hi) continue;
-        const bool whole = hi - lo == kChunk;
-        float z[kChunk], g[kChunk];
-        if (whole) {
-            decode_codes(load_bytes8(q + j0), p.qkind, z);
-        } else {
+        if (j0 >= 0 && j0 + kChunk <= p.h) {
+            float z[kChunk], g[kChunk];
+            const uint2 codes = load_bytes8(q + j0);
+            Raw<kT> d;
+            if constexpr (kGrad) d.v[0] = load_codes16(reinterpret_cast<const int8_t *>(from + j0), 16);
+            const float scale = scale_at<kQM>(p.scale, r, p.h, j0);
+            decode_codes(codes, p.qkind, z);
+            const int border = kQM == QM_TOKEN ? p.h : (j0 / group_size(kQM) + 1) * group_size(kQM);
+            if (border >= j0 + kChunk) {
 #pragma unroll
-            for (int e = 0; e < kChunk; ++e) z[e] = j0 + e >= lo && j0 + e < hi ? decode8(q[j0 + e], p.qkind) : 0.0f;
-        }
-        // a chunk reaches into two groups at most
-        const float first = scale_at<kQM>(p.scale, r, p.h, lo), last = scale_at<kQM>(p.scale, r, p.h, hi - 1);
-        const int border = (lo / group_size(kQM) + 1) * group_size(kQM);
+                for (int e = 0; e < kChunk; ++e) z[e] = __fmul_rn(z[e], scale);
+            } else {   // a chunk reaches into two groups at most
+                const float next = scale_at<kQM>(p.scale, r, p.h, border);
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e) z[e] = __fmul_rn(z[e], kQM == QM_TOKEN || j0 + e < border ? first : last);
-        if constexpr (kGrad) {
-            if (whole && kT != ELEM_F32) {
-                Raw<kT> d;
-                d.v[0] = load_codes16(reinterpret_cast<const int8_t *>(from + j0), 16);
-                values<kT>(d, g);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kChunk; ++e) g[e] = j0 + e >= lo && j0 + e < hi ? Elem<kT>::load(from + j0 + e) : 0.0f;
+                for (int e = 0; e < kChunk; ++e) z[e] = __fmul_rn(z[e], j0 + e < border ? scale : next);
             }
-            times_derivative(g, z, act);
+            if constexpr (kGrad) {
+                values<kT>(d, g);
+                times_derivative(g, z, act);
+                store_values<kT>(to + j0, g);
+            } else {
+                apply_act(z, act);
+                store_values<kT>(to + j0, z);
+            }
         } else {
-            apply_act(z, act);
-#pragma unroll
-            for (int e = 0; e < kChunk; ++e) g[e] = z[e];
-        }
-        if (whole) {
-            store_values<kT>(to + j0, g);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kChunk; ++e)
-                if (j0 + e >= lo && j0 + e < hi) Elem<kT>::store(to + j0 + e, g[e]);
+            // (elements are paired with themselves: an activation works on pairs)
+            for (int j = max(j0, 0); j < min(j0 + kChunk, p.h); ++j) {
+                const float z = __fmul_rn(decode8(q[j], p.qkind), scale_at<kQM>(p.scale, r, p.h, j));
+                E::store(to + j, kGrad ? E::load(from + j) * act_derivative2(both(z), act).x : act2(both(z), act).x);
+            }
         }
     }
 }
@@ -451,6 +446,14 @@ dim3 cover_rows(int chunks, int least, int64_t m, int num_sms, int resident, Cov
     cover->chunks = chunks;
     cover->lanes_log2 = 0;
     while ((1 << cover->lanes_log2) < kThreads && (1 << cover->lanes_log2) < (chunks > least ? chunks : least)) ++cover->lanes_log2;
+    // wide rows in pieces of 256 down to 32 threads, whichever leaves the fewest idle (513 chunks: 17 of 32, not 3 of 256, 8192 x 4097)
+    if (chunks > 32) {
+        int64_t least_work = INT64_MAX;
+        for (int log2 = 8; log2 >= 5; --log2) {
+            const int64_t work = (chunks + (1ll << log2) - 1) >> log2 << log2;
+            if (work < least_work) least_work = work, cover->lanes_log2 = log2;
+        }
+    }
     const int lanes = 1 << cover->lanes_log2;
     const int64_t across = (chunks + lanes - 1) / lanes, per_block = kThreads / lanes, down = (m + per_block - 1) / per_block;
     int64_t rows = (static_cast<int64_t>(num_sms) * resident + across - 1) / across;
@@ -473,7 +476,7 @@ cudaError_t launch_from(const void *dy, int64_t lddy, const Kept &p, int act, vo
         return launch(from_kept_kernel<kT, kGrad, kQM>, grid, kThreads, stream, dy, lddy, p, a, out, ldo, cover);
     }
     // (a row may begin inside its first chunk)
-    const dim3 grid = cover_rows((p.h + 2 * kChunk - 2) / kChunk, 1, p.m, num_sms, 32, &cover);
+    const dim3 grid = cover_rows((p.h + 2 * kChunk - 2) / kChunk, 1, p.m, num_sms, 16, &cover);
     return launch(from_kept_any_kernel<kT, kGrad, kQM>, grid, kThreads, stream, dy, lddy, p, a, out, ldo, cover);
 }
 
