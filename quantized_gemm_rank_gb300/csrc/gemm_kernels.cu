@@ -193,10 +193,14 @@ cudaError_t launch_gemm(GemmKind kind, int group, const GemmParams &p, int num_s
 // the contraction runs down the m rows of both; the same launch sums A's rows
 // over the contraction (the column sums of dY) into db
 cudaError_t launch_weight_grad_tiles(bool bf16, const void *dy, int64_t lddy, const void *x, int64_t ldx, int m, int n, int k, void *dw,
-                                     void *db, int num_sms, cudaStream_t stream) {
+                                     void *db, float *col_parts, int num_sms, cudaStream_t stream) {
     GemmParams p = {};
     const int group = gemm_group_for(n);
-    bool ok = host::make_map16(&p.a_maps[0], dy, n, m, 64, kBK, lddy);
+    bool ok = true;
+    if (host::make_map16_nmajor3d(&p.a_maps[0], dy, n, m, kBK, kBM / 64, lddy))
+        p.a_3d = 1;
+    else
+        ok = host::make_map16(&p.a_maps[0], dy, n, m, 64, kBK, lddy);
     if (host::make_map16_nmajor3d(&p.b_map, x, k, m, kBK, (kBN / group) / 64, ldx))
         p.b_3d = 1;
     else
@@ -209,7 +213,8 @@ cudaError_t launch_weight_grad_tiles(bool bf16, const void *dy, int64_t lddy, co
     p.m = n, p.n = k, p.k = m;
     p.kblock_tiles = 1024 / kBK;
     p.out = dw;
-    p.colsum_out = db;
+    p.colsum_out = col_parts ? col_parts : db;
+    p.col_share = col_parts != nullptr;
     p.wait_limit_ns = host::kWaitLimitNs;
     return launch_gemm(bf16 ? GEMM_BF16 : GEMM_F16, group, p, num_sms, stream);
 }

@@ -55,7 +55,7 @@
 //               (already complete: the MMA read it) and frees the stage, so
 //               the store never delays the MMAs.
 //   warps 2-3   (weight gradient with its bias gradient) on the first column of
-//               tiles, sum each stage's A rows over K from shared memory after
+//               tiles (col_share: on each, its share of the stages), sum each stage's A rows over K from shared memory after
 //               the MMAs have read it (the stage comes to them through the same
 //               "consumed" barrier), then free it; each tile's sums are the
 //               bias gradient of its 128 rows
@@ -128,6 +128,7 @@ struct GemmParams {
     int k_local;                    // A_KINTERLEAVE: columns per chunk
     int b_mn_major;
     int b_3d;                       // N-major B through a 3-D map [n/64][k][64]: one box per stage
+    int a_3d;                       // A_SINGLE_MN: the same for A, [m/64][k][64]
     int gather;
     int kblock_tiles;               // integer path: k-tiles per exact fp32 block
     void *out;                      // (m, n): dtype (float path) / bf16 (integer path)
@@ -156,6 +157,10 @@ struct GemmParams {
     // i.e. the sums of A's rows over K, rounded once to 16 bits into this (m)
     // vector (the bias gradient)
     void *colsum_out;
+    // ... or, col_share: each column of tiles sums the k-tiles that are its index modulo their number, into fp32
+    // [part][column of tiles][m] (the first column's two warps take longer for a stage than its MMAs: 8192 x 1024 x 4096
+    // 59 us, 44 without the sums)
+    int col_share;
     int out_rows;
     // rank r's output (out_rows, n) 16-bit, box 64 columns x 32 rows, 128-byte
     // swizzle; used when rs_tma (out_rows % 32 == 0: a warp's 32 rows are one rank's)
@@ -169,7 +174,7 @@ struct GemmParams {
     Activation act;
     const float *bias_f32;   // EPI_SCALED: (n), instead of bias16
     // EPI_SUMS: the contraction in `splits` parts of split_blocks K blocks, each with a launch id of its own (part by
-    // part); out_map: fp32 [part][m][n], boxes of 32 x 32, 128-byte swizzle; colsum_out: fp32 [part][m]
+    // part); out_map: fp32 [part][m][n], boxes of 32 x 32, 128-byte swizzle; with col_share
     int splits, split_blocks;
 };
 
@@ -378,6 +383,14 @@ struct TileWalk {
     }
 };
 
+// The first k-tile from kt_begin on that a tile of column nb shows to its gathered-store or summing warps, before it is
+// freed: all of the first column's, or (col_share) every num_n-th of each.
+__device__ __forceinline__ int next_shown(const GemmParams &p, int kt_begin, int nb, int num_n) {
+    if (!p.col_share) return nb == 0 ? kt_begin : INT32_MAX;
+    const int ahead = (nb - kt_begin) % num_n;
+    return kt_begin + (ahead < 0 ? ahead + num_n : ahead);
+}
+
 // Store 32 consecutive 16-bit outputs (columns col0 .. col0+31) of the row that
 // starts at row_ptr, masked at n.
 __device__ __forceinline__ void store_row32_16(uint16_t *row_ptr, int n, int col0, const uint32_t (&pk)[16]) {
@@ -514,8 +527,9 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
         bool ok = true;
         // B copy form, fixed for the launch: 0 K-major box, 1 N-major boxes, 2 one 3-D N-major box
         const int b_mode = !p.b_mn_major ? 0 : (p.b_3d ? 2 : 1);
-        // A form: the AMode, with the all-gather split into one box per k-tile (4) or several
-        const int a_form = p.a_mode == A_MCONCAT && p.a_box_rows == kBM ? 4 : p.a_mode;
+        // A form: the AMode, with the all-gather split into one box per k-tile (4) or several, and M-major A
+        // into one 3-D box (5) or two
+        const int a_form = p.a_mode == A_MCONCAT && p.a_box_rows == kBM ? 4 : (p.a_mode == A_SINGLE_MN && p.a_3d ? 5 : p.a_mode);
         // addresses of stage 0 (stage s adds s * 8 to a barrier, s * kStageBytes to a tile);
         // the pair's peer signals the leader's full barrier at the same offset
         const uint32_t full0 = ptx::smem_u32(&full_bar[0]);
@@ -570,6 +584,11 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     }
                     kl += kBK;
                     if (kl >= p.k_local) kl = 0, ++kc;
+                } else if constexpr (AF == 5) {
+                    if constexpr (kPair)
+                        ptx::tma_load_3d_pair(sA, &p.a_maps[0], 0, k0, m0 >> 6, bar);
+                    else
+                        ptx::tma_load_3d(sA, &p.a_maps[0], 0, k0, m0 >> 6, bar);
                 } else if constexpr (AF == A_SINGLE_MN) {
                     // M-major A: 64-wide M slabs of the (k, m) matrix, like an N-major B
 #pragma unroll
@@ -653,6 +672,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 case 4: with_b(std::integral_constant<int, 4>{}); break;
                 case A_MCONCAT: with_b(std::integral_constant<int, A_MCONCAT>{}); break;
                 case A_KINTERLEAVE: with_b(std::integral_constant<int, A_KINTERLEAVE>{}); break;
+                case 5: with_b(std::integral_constant<int, 5>{}); break;
                 case A_SINGLE_MN: with_b(std::integral_constant<int, A_SINGLE_MN>{}); break;
                 default: with_b(std::integral_constant<int, A_SINGLE>{}); break;
             }
@@ -696,9 +716,9 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
             const int kt_begin = w.kb0 * kblock, kt_end = min(num_k, w.kb1 * kblock);
             int mb, nb;
             tile_coords<kIntPath>(w.tile, num_m, num_n, mb, nb);
-            // stages of gathered tiles go to the gathered-store warp, and those of bias-gradient
-            // tiles to the summing warps, before being freed
-            const uint32_t release0 = ((p.gather || p.colsum_out != nullptr) && nb == 0) ? consumed0 : empty0;
+            // stages of gathered tiles go to the gathered-store warp, and those that bias-gradient
+            // warps sum to them, before being freed
+            int shown = (p.gather || p.colsum_out != nullptr) ? next_shown(p, kt_begin, nb, num_n) : INT32_MAX;
             int kin = 0;  // k-tile index inside the current K block
             for (int kt = kt_begin; kt < kt_end; ++kt) {
                 if (kin == 0) {
@@ -725,6 +745,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                 ptx::mma_f16_ss<kG>(d_tmem, ad + a_kk, bd + b_kk, idesc, 1u);
                 ptx::mma_f16_ss<kG>(d_tmem, ad + 2 * a_kk, bd + 2 * b_kk, idesc, 1u);
                 ptx::mma_f16_ss<kG>(d_tmem, ad + 3 * a_kk, bd + 3 * b_kk, idesc, 1u);
+                uint32_t release0 = empty0;
+                if (kt == shown) release0 = consumed0, shown += p.col_share ? num_n : 1;
                 ptx::mma_commit<kG>(release0 + 8u * stage);
                 if (++stage == S) {
                     stage = 0;
@@ -774,7 +796,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
             const int kt_begin = w.kb0 * p.kblock_tiles, kt_end = min(num_k, w.kb1 * p.kblock_tiles);
             int mb, nb;
             tile_coords<kIntPath>(w.tile, num_m, num_n, mb, nb);
-            if (nb != 0) {  // its stages are freed by the MMA directly
+            int shown = next_shown(p, kt_begin, nb, num_n);
+            if (!p.col_share && nb != 0) {  // its stages are freed by the MMA directly
                 stage = (stage + (kt_end - kt_begin)) % S;
                 continue;
             }
@@ -782,6 +805,11 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
             for (int kt = kt_begin; kt < kt_end; ++kt) {
+                if (kt != shown) {
+                    if (++stage == S) stage = 0;
+                    continue;
+                }
+                shown += p.col_share ? num_n : 1;
                 const bool got = __all_sync(0xffffffffu, wait_or_abort<kPair>(ptx::smem_u32(&consumed_bar[stage]),
                                                                               (consumed_parity >> stage) & 1u, p,
                                                                               abort_flag));
@@ -826,8 +854,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
             }
             const int col = mb * Cfg::kTileM + kBM * static_cast<int>(cr) + 64 * slab + 8 * c;
             if (g == 0 && col < p.m) {
-                if constexpr (kEpi == EPI_SUMS) {
-                    float *to = static_cast<float *>(p.colsum_out) + static_cast<int64_t>(w.split) * p.m + col;
+                if (p.col_share) {
+                    float *to = static_cast<float *>(p.colsum_out) + (static_cast<int64_t>(w.split) * num_n + nb) * p.m + col;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         if (col + e < p.m) to[e] = acc[e];

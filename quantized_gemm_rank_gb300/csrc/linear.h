@@ -58,7 +58,7 @@ float linear_split_codes_us(const LinearParams &p, int num_sms);
 bool linear_prefers_split(const LinearParams &p, int num_sms);
 
 // The sums of dy^T x, (n, k), over parts of the m rows, each to a matrix of its own in `parts` (fp32, rows ldp apart), and
-// dy's column sums to col_parts (splits, n) if given.  A part is split_blocks blocks of block_tiles 64-row stages; a
+// dy's column sums, in weight_grad_col_parts shares a part, to col_parts (splits x shares, n) if given.  A part is split_blocks blocks of block_tiles 64-row stages; a
 // block's sum stays in one accumulator, blocks are added in fp32 to nearest.
 struct WeightGradParts {
     const void *dy, *x;
@@ -68,9 +68,11 @@ struct WeightGradParts {
     int splits, split_blocks, block_tiles;
 };
 cudaError_t launch_weight_grad_parts(bool bf16, const WeightGradParts &w, cudaStream_t stream);
-// The whole of it in 16 bits: dw (n, k) with rows of a multiple of 8 elements, dw 16-byte aligned; db (n) or none.
+inline int weight_grad_col_parts(int k) { return (k + 255) / 256; }
+// The whole of it in 16 bits: dw (n, k) with rows of a multiple of 8 elements, dw 16-byte aligned; db (n) or none, or its
+// shares in col_parts (weight_grad_col_parts, n) instead.
 cudaError_t launch_weight_grad_tiles(bool bf16, const void *dy, int64_t lddy, const void *x, int64_t ldx, int m, int n, int k, void *dw,
-                                     void *db, int num_sms, cudaStream_t stream);
+                                     void *db, float *col_parts, int num_sms, cudaStream_t stream);
 
 // dz = dy * act'(z), (m, n)
 struct ActGradParams {

@@ -97,7 +97,11 @@ cudaError_t launch_linear_tiles(bool bf16, const LinearParams &lp, cudaStream_t 
 
 cudaError_t launch_weight_grad_parts(bool bf16, const WeightGradParts &w, cudaStream_t stream) {
     GemmParams p = {};
-    bool ok = host::make_map16(&p.a_maps[0], w.dy, w.n, w.m, 64, kBK, w.lddy);
+    bool ok = true;
+    if (host::make_map16_nmajor3d(&p.a_maps[0], w.dy, w.n, w.m, kBK, kBM / 64, w.lddy))
+        p.a_3d = 1;
+    else
+        ok = host::make_map16(&p.a_maps[0], w.dy, w.n, w.m, 64, kBK, w.lddy);
     if (host::make_map16_nmajor3d(&p.b_map, w.x, w.k, w.m, kBK, kBN / 2 / 64, w.ldx))
         p.b_3d = 1;
     else
@@ -111,6 +115,7 @@ cudaError_t launch_weight_grad_parts(bool bf16, const WeightGradParts &w, cudaSt
     p.kblock_tiles = w.block_tiles;
     p.splits = w.splits, p.split_blocks = w.split_blocks;
     p.colsum_out = w.col_parts;
+    p.col_share = 1;
     p.wait_limit_ns = host::kWaitLimitNs;
     p.status = device_status_word();
     return bf16 ? launch_tiles<true, EPI_SUMS>(p, stream) : launch_tiles<false, EPI_SUMS>(p, stream);

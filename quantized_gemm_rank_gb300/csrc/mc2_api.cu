@@ -533,7 +533,7 @@ int mc2_matmul_weight_grad(const void *dy, int64_t m, int64_t n, const void *x, 
     cudaError_t e = cudaSuccess;
     LaunchMarks marks(s);
     e = mc2::launch_weight_grad_tiles(dtype == MC2_BF16, dy, n, x, k, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), dw, db,
-                                      dev.num_sms, s);
+                                      nullptr, dev.num_sms, s);
     if (e != cudaSuccess) return fail(MC2_ERR_CUDA, "GEMM launch: %s", cudaGetErrorString(e));
     marks.launched();
     return MC2_OK;

@@ -103,18 +103,29 @@ __global__ void __launch_bounds__(kThreads) copy_rows_kernel(const uint16_t *src
     }
 }
 
-// dw and db from the parts' sums, added in order.  Four columns a thread; rows of dw are k elements, of a part ldp.
+// dw and db from the parts' sums, added in order (db's are col_count).  Four columns a thread; rows of dw are k elements, of a
+// part ldp.
 template <bool kBF16>
 __global__ void __launch_bounds__(kThreads) add_parts_kernel(const float *parts, int64_t ldp, int splits, int n, int k, void *dw,
-                                                             const float *col_parts, void *db, int dw_blocks) {
+                                                             const float *col_parts, int col_count, void *db, int dw_blocks) {
     using T = typename Elem<kBF16 ? ELEM_BF16 : ELEM_F16>::type;
     using E = Elem<kBF16 ? ELEM_BF16 : ELEM_F16>;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     if (static_cast<int>(blockIdx.x) >= dw_blocks) {
-        for (int i = (blockIdx.x - dw_blocks) * kThreads + threadIdx.x; i < n; i += (gridDim.x - dw_blocks) * kThreads) {
-            float s = 0.0f;
-            for (int p = 0; p < splits; ++p) s = __fadd_rn(s, col_parts[static_cast<int64_t>(p) * n + i]);
+        // 32 columns a block, a warp every eighth share, then the warps' sums in order
+        __shared__ float sums[kThreads / 32][32];
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = (blockIdx.x - dw_blocks) * 32 + lane;
+        float s = 0.0f;
+        if (i < n) {
+#pragma unroll 4
+            for (int p = warp; p < col_count; p += kThreads / 32) s = __fadd_rn(s, col_parts[static_cast<int64_t>(p) * n + i]);
+        }
+        sums[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && i < n) {
+#pragma unroll
+            for (int w = 1; w < kThreads / 32; ++w) s = __fadd_rn(s, sums[w][lane]);
             E::store(static_cast<T *>(db) + i, s);
         }
         return;
@@ -125,6 +136,7 @@ __global__ void __launch_bounds__(kThreads) add_parts_kernel(const float *parts,
         const int c = static_cast<int>(e - r * quads) * 4;
         const float4 *from = reinterpret_cast<const float4 *>(parts + r * ldp + c);
         float4 s = *from;
+#pragma unroll 4
         for (int p = 1; p < splits; ++p) {
             const float4 t = from[p * (part / 4)];
             s.x = __fadd_rn(s.x, t.x), s.y = __fadd_rn(s.y, t.y), s.z = __fadd_rn(s.z, t.z), s.w = __fadd_rn(s.w, t.w);
@@ -205,6 +217,7 @@ LinearParams product_of(const QuantProduct &p) {
 struct WeightPlan {
     size_t x = 0, dy = 0, parts = 0, col_parts = 0, total = 0;
     bool dy_apart = false, in_parts = false;
+    int col_count = 0;   // shares of db (0: it is written as it is)
     int splits = 1, split_blocks = 1, block_tiles = 16;
 };
 
@@ -222,9 +235,9 @@ WeightPlan plan_weight_grad(const QuantWeightGrad &p) {
     }
     at.in_parts = at.splits > 1 || !whole;
     if (at.in_parts) {
-        // equal blocks of at most 1024 rows, a whole number of them a part
+        // equal blocks of at most 2048 rows (as the tiles of linear.h's products), a whole number of them a part
         const int each = (steps + at.splits - 1) / at.splits;
-        at.split_blocks = (each + 15) / 16;
+        at.split_blocks = (each + 31) / 32;
         at.block_tiles = (each + at.split_blocks - 1) / at.split_blocks;
         const int blocks = (steps + at.block_tiles - 1) / at.block_tiles;
         at.splits = (blocks + at.split_blocks - 1) / at.split_blocks;
@@ -233,9 +246,13 @@ WeightPlan plan_weight_grad(const QuantWeightGrad &p) {
     at.x = ws.take(p.m * up8(p.k), 2);
     at.dy_apart = !copies_read16(p.dy, p.lddy, p.m);
     if (at.dy_apart) at.dy = ws.take(p.m * up8(p.n), 2);
-    if (at.in_parts) {
-        at.parts = ws.take(static_cast<int64_t>(at.splits) * p.n * ((p.k + 3ll) / 4 * 4), 4);
-        at.col_parts = ws.take(static_cast<int64_t>(at.splits) * p.n, 4);
+    if (at.in_parts) at.parts = ws.take(static_cast<int64_t>(at.splits) * p.n * ((p.k + 3ll) / 4 * 4), 4);
+    // db in shares of the columns of tiles: at no cost where the parts are added anyway, for a launch (2 us) otherwise, which
+    // pays from 1024 rows on (8192 x 1024 x 4096 73 -> 59 us, 1024 x 4096 x 4096 34.4 and 34)
+    const int shares = weight_grad_col_parts(p.k);
+    if (at.in_parts || (steps >= 16 && shares > 1)) {
+        at.col_count = at.splits * shares;
+        at.col_parts = ws.take(static_cast<int64_t>(at.col_count) * p.n, 4);
     }
     at.total = ws.total;
     return at;
@@ -358,23 +375,26 @@ cudaError_t launch_quant_weight_grad(bool bf16, const QuantWeightGrad &p, int nu
         if (e != cudaSuccess) return e;
         mark(ctx);
     }
-    if (!at.in_parts) {
-        e = launch_weight_grad_tiles(bf16, dy, lddy, ws + at.x, ldx, p.m, p.n, p.k, p.dw, p.db, num_sms, stream);
-        if (e == cudaSuccess) mark(ctx);
-        return e;
+    float *col_parts = p.db && at.col_count ? reinterpret_cast<float *>(ws + at.col_parts) : nullptr;
+    const float *parts = nullptr;
+    const int64_t ldp = (p.k + 3ll) / 4 * 4;
+    if (at.in_parts) {
+        WeightGradParts w = {};
+        w.dy = dy, w.x = ws + at.x, w.parts = reinterpret_cast<float *>(ws + at.parts), w.col_parts = col_parts;
+        w.lddy = lddy, w.ldx = ldx, w.ldp = ldp;
+        w.m = p.m, w.n = p.n, w.k = p.k;
+        w.splits = at.splits, w.split_blocks = at.split_blocks, w.block_tiles = at.block_tiles;
+        parts = w.parts;
+        e = launch_weight_grad_parts(bf16, w, stream);
+    } else {
+        e = launch_weight_grad_tiles(bf16, dy, lddy, ws + at.x, ldx, p.m, p.n, p.k, p.dw, p.db, col_parts, num_sms, stream);
     }
-    WeightGradParts w = {};
-    w.dy = dy, w.x = ws + at.x, w.parts = reinterpret_cast<float *>(ws + at.parts);
-    w.col_parts = p.db ? reinterpret_cast<float *>(ws + at.col_parts) : nullptr;
-    w.lddy = lddy, w.ldx = ldx, w.ldp = (p.k + 3ll) / 4 * 4;
-    w.m = p.m, w.n = p.n, w.k = p.k;
-    w.splits = at.splits, w.split_blocks = at.split_blocks, w.block_tiles = at.block_tiles;
-    e = launch_weight_grad_parts(bf16, w, stream);
     if (e != cudaSuccess) return e;
     mark(ctx);
-    const int64_t dw_blocks = blocks_for(p.n * ((p.k + 3ll) / 4), num_sms), db_blocks = p.db ? (p.n + kThreads - 1) / kThreads : 0;
-    e = launch(bf16 ? add_parts_kernel<true> : add_parts_kernel<false>, dw_blocks + db_blocks, stream, static_cast<const float *>(w.parts), w.ldp,
-               at.splits, p.n, p.k, p.dw, static_cast<const float *>(w.col_parts), p.db, static_cast<int>(dw_blocks));
+    if (!parts && !col_parts) return cudaSuccess;
+    const int64_t dw_blocks = parts ? blocks_for(p.n * ((p.k + 3ll) / 4), num_sms) : 0, db_blocks = col_parts ? (p.n + 31) / 32 : 0;
+    e = launch(bf16 ? add_parts_kernel<true> : add_parts_kernel<false>, dw_blocks + db_blocks, stream, parts, ldp, at.splits, p.n, p.k, p.dw,
+               static_cast<const float *>(col_parts), at.col_count, p.db, static_cast<int>(dw_blocks));
     if (e == cudaSuccess) mark(ctx);
     return e;
 }
