@@ -45,7 +45,7 @@ struct ProductPlan {
     size_t x = 0, w = 0, out = 0, total = 0;
     bool tokens = false;       // the kernel of one to eight tokens, on the matrices as they are
     bool split = false;        // the one of few tokens, on int8 operands
-    bool apart = false;        // the operands go through the workspace (the tiles': always)
+    bool x_apart = false, w_apart = false;   // the operands go through the workspace (the tiles': always)
     bool out_apart = false;    // the output, too
     bool residual_in = false;  // the residual is copied to where the output will be
 };

@@ -267,23 +267,22 @@ ProductPlan plan_quant_product(const QuantProduct &p) {
     at.tokens = p.w_nk && (p.m <= 4 || (p.m <= 8 && static_cast<int64_t>(p.n) * p.k <= 8ll << 20));
     if (at.tokens) return at;
     // Which kernel, by the sizes alone: the tiles take 9.4 us, 3.2 and 0.25 a 64-deep stage for each wave of them, and widening three
-    // bytes a code at 5000 a ns (since then 6400 where a matrix has no gaps) (1024 tokens, 4096 x 14336 112 us, 8192 x 4096 70; 4096 tokens, 4096 x 4096 106).  Where the two
-    // cross, with k = 4096: 512 tokens, n = 4096 24.6 us split, 31 in tiles; 1024 tokens, n = 8192 137 and 70.
+    // bytes a code at 6400 a ns (1024 tokens, 8192 x 4096 65 us; 2048 and 4096 tokens, 4096 x 4096 59.5 and 102).  Where the two
+    // cross, with k = 4096: 512 tokens, n = 4096 26 us split, 36 in tiles; 1024 tokens, n = 8192 137 and 65.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256);
     const float steps = static_cast<float>((p.k + 63) / 64);
     const float tiles_us = 9.4f + static_cast<float>((tiles + kPairs - 1) / kPairs) * (3.2f + 0.2475f * steps) +
-                           (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 0.6e-6f;
+                           (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 0.47e-6f;
     LinearParams l = product_of(p);
     l.x_scale = reinterpret_cast<const float *>(p.x);   // (codes; not read)
     const float split_us = linear_split_codes_us(l, kSms);
     at.split = split_us >= 0.0f && split_us < tiles_us;
     Pieces ws;
     const int64_t w_rows = p.w_nk ? p.n : p.k, w_cols = p.w_nk ? p.k : p.n;
-    at.apart = !at.split || !copies_read8(p.x, p.ldx, p.m) || !copies_read8(p.w, p.ldw, w_rows);
-    if (at.apart) {
-        at.x = ws.take(p.m * up16(p.k), at.split ? 1 : 2);
-        at.w = ws.take(w_rows * up16(w_cols), at.split ? 1 : 2);
-    }
+    at.x_apart = !at.split || !copies_read8(p.x, p.ldx, p.m);
+    at.w_apart = !at.split || !copies_read8(p.w, p.ldw, w_rows);
+    if (at.x_apart) at.x = ws.take(p.m * up16(p.k), at.split ? 1 : 2);
+    if (at.w_apart) at.w = ws.take(w_rows * up16(w_cols), at.split ? 1 : 2);
     if (!at.split) {
         at.out_apart = !copies_write16(p.out, p.ldo, p.m, p.n);
         at.residual_in = p.residual && (at.out_apart || !copies_read16(p.residual, p.ldr, p.m));
@@ -306,7 +305,7 @@ cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, const Product
     // (the stride of a single row is free: one that the tensor copies take)
     l.x = p.x, l.ldx = p.m == 1 ? up16(p.k) : p.ldx;
     l.w = p.w, l.ldw = w_rows == 1 ? up16(w_cols) : p.ldw;
-    if (at.apart) {
+    if (at.x_apart || at.w_apart) {
         const auto taken = [&](const int8_t *src, int64_t ld, void *dst, int64_t rows, int64_t cols) {
             const int vector = at.split ? 16 : 8;
             Widened t = {src, dst, ld, up16(cols), rows, cols, (cols + vector - 1) / vector, 0};
@@ -318,15 +317,16 @@ cudaError_t launch_quant_product(bool bf16, const QuantProduct &p, const Product
             return t;
         };
         const Widened a = taken(p.x, p.ldx, ws + at.x, p.m, p.k), b = taken(p.w, p.ldw, ws + at.w, w_rows, w_cols);
-        // blocks in proportion to the elements
-        const int64_t na = a.rows * a.vectors, nb = b.rows * b.vectors, blocks = blocks_for(na + nb, num_sms) + 1;
+        // blocks in proportion to the elements, at least one for each operand that is taken
+        const int64_t na = at.x_apart ? a.rows * a.vectors : 0, nb = at.w_apart ? b.rows * b.vectors : 0, blocks = blocks_for(na + nb, num_sms) + 1;
         int64_t first = static_cast<int64_t>(static_cast<double>(blocks) * na / (na + nb) + 0.5);
-        first = first < 1 ? 1 : (first > blocks - 1 ? blocks - 1 : first);
+        const int64_t least = na ? 1 : 0, most = nb ? blocks - 1 : blocks;
+        first = first < least ? least : (first > most ? most : first);
         e = launch(at.split ? widen_kernel<false> : widen_kernel<true>, blocks, stream, a, b, static_cast<int>(first));
         if (e != cudaSuccess) return e;
         mark(ctx);
-        l.x = ws + at.x, l.ldx = up16(p.k);
-        l.w = ws + at.w, l.ldw = up16(w_cols);
+        if (at.x_apart) l.x = ws + at.x, l.ldx = up16(p.k);
+        if (at.w_apart) l.w = ws + at.w, l.ldw = up16(w_cols);
     }
     if (at.split) {
         l.out = p.out, l.ldo = p.ldo, l.aux = p.residual, l.ldaux = p.ldr;

@@ -91,7 +91,9 @@ def test_workspace_queries():
     assert f(*good) == mc2.MC2_OK and n.value >= 2 * 2 * 4096 * 4096   # both operands in 16 bits
     few = (*good[:5], 16, *good[6:])
     assert f(*few) == mc2.MC2_OK and n.value == 0
-    assert f(FAKE + 1, *few[1:]) == mc2.MC2_OK and n.value > 4096 * 4096
+    # an operand that does not begin at 16 bytes goes through it
+    assert f(FAKE + 1, *few[1:]) == mc2.MC2_OK and 16 * 4096 <= n.value < 4096 * 4096
+    assert f(*few[:2], FAKE + 8, *few[3:]) == mc2.MC2_OK and n.value >= 4096 * 4096
     for at, value, status in ((0, None, mc2.MC2_ERR_NULL), (2, None, mc2.MC2_ERR_NULL), (10, None, mc2.MC2_ERR_NULL), (12, None, mc2.MC2_ERR_NULL),
                               (5, 0, mc2.MC2_ERR_SHAPE), (1, 8, mc2.MC2_ERR_SHAPE), (11, 31, mc2.MC2_ERR_SHAPE)):
         assert f(*good[:at], value, *good[at + 1:]) == status
