@@ -174,12 +174,12 @@ __device__ __forceinline__ void decode_codes(uint2 w, int kind, float (&v)[8]) {
 // aligned, otherwise by the aligned words that hold one of them at least.  `again`: they will be read again (kept in L1).
 __device__ __forceinline__ uint4 load_codes16(const int8_t *from, int left, bool again = false) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(from);
-    if (left >= 16 && (a & 15) == 0) return again ? __ldg(reinterpret_cast<const uint4 *>(from)) : load_once(from);
+    if (left >= 16 && (a & 15) == 0) return again ? *reinterpret_cast<const uint4 *>(from) : load_once(from);
     const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~uintptr_t(3));
     const int skip = static_cast<int>(a & 3), end = left > 0 ? min(left, 16) + skip : 0;   // in bytes from w on
     uint32_t word[5], q[4];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) word[i] = 4 * i < end ? __ldg(w + i) : 0;
+    for (int i = 0; i < 5; ++i) word[i] = 4 * i < end ? w[i] : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         q[i] = __funnelshift_r(word[i], word[i + 1], skip * 8);

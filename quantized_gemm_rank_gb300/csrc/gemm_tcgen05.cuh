@@ -1100,7 +1100,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                         if (scales_whole) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                const float4 t = __ldg(reinterpret_cast<const float4 *>(from) + j);
+                                const float4 t = reinterpret_cast<const float4 *>(from)[j];
                                 const float t4[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) v[4 * j + i] = __fmul_rn(__fmul_rn(v[4 * j + i], row_scale), t4[i]);
@@ -1110,12 +1110,12 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                             // neighbour has the same one in every kernel)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                v[i] = __fmul_rn(__fmul_rn(v[i], row_scale), colh + 32 * c + i < p.n ? __ldg(p.x2_scale + colh + 32 * c + i) : 0.0f);
+                                v[i] = __fmul_rn(__fmul_rn(v[i], row_scale), colh + 32 * c + i < p.n ? p.x2_scale[colh + 32 * c + i] : 0.0f);
                         }
                         if (p.bias_f32 != nullptr) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (colh + 32 * c + i < p.n) v[i] = __fadd_rn(v[i], __ldg(p.bias_f32 + colh + 32 * c + i));
+                                if (colh + 32 * c + i < p.n) v[i] = __fadd_rn(v[i], p.bias_f32[colh + 32 * c + i]);
                         }
                     }
                     if (bias_whole) {

@@ -147,9 +147,9 @@ __device__ __forceinline__ uint2 load_bytes8(const uint8_t *p) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~uintptr_t(3));
     const uint32_t shift = static_cast<uint32_t>(a & 3) * 8;
-    const uint32_t w0 = __ldg(w), w1 = __ldg(w + 1);
+    const uint32_t w0 = w[0], w1 = w[1];
     if (shift == 0) return make_uint2(w0, w1);
-    const uint32_t w2 = __ldg(w + 2);
+    const uint32_t w2 = w[2];
     return make_uint2(__funnelshift_r(w0, w1, shift), __funnelshift_r(w1, w2, shift));
 }
 

@@ -162,7 +162,7 @@ __device__ __forceinline__ void finish_tokens(const SplitParams &p, const float4
     if constexpr (kCodes) {
 #pragma unroll
         for (int u = 0; u < kT; ++u) {
-            const float s = __ldg(x_scale + u);
+            const float s = x_scale[u];
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[4 * u + i] = __fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[4 * u + i])), s), w4[i]);
         }

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
         for (; e + (kAhead - 1) * step < total; e += kAhead * step) {
             uint2 q[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) q[i] = __ldg(from + e + i * step);
+            for (int i = 0; i < kAhead; ++i) q[i] = from[e + i * step];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const uint2 lo = widen4(q[i].x), hi = widen4(q[i].y);

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, resident(kM)) quant_tokens_kernel(co
     int acc[kRows][kM] = {};
     const int8_t *x = p.x + k0;
     const auto load = [](const int8_t *from, int left, bool again) {
-        if (kAligned && left >= 16) return again ? __ldg(reinterpret_cast<const uint4 *>(from)) : load_once(from);
+        if (kAligned && left >= 16) return again ? *reinterpret_cast<const uint4 *>(from) : load_once(from);
         return load_codes16(from, left, again);
     };
     for (int k = k0; k < k1; k += kAhead * kTurn) {
