@@ -578,7 +578,7 @@ int mc2_device_status(void);
  *                              residual before it or of the output after it where the tensor copies
  *                              cannot take them (2 to 4)
  *   mc2_matmul_weight_grad_quant   the values of the codes, the GEMM or its parts, and the sum of the parts
- *                              (2 or 3), with a copy of dy before the GEMM where the tensor copies cannot take it
+ *                              or of the shares of db (2 or 3), with a copy of dy before the GEMM where the tensor copies cannot take it
  *   mc2_rms_norm_grad          1, or 2 with dw: the gradient, the sum of its shares of dw
  *   mc2_alltoall_quant_mm      x1_quant_mode 7: 2 (the fused quant and x2
  *                              widening, the GEMM), or 3 when rank_size*h > 32768

@@ -5,8 +5,8 @@
 //   dz = dy act'(q scale)                                                                        (act_grad_quant)
 // Arithmetic is fp32; codes and outputs are rounded once.  Memory bounds all of them without an activation, issue with gelu:
 // each element is read once, eight at a time (16 bytes of a 16-bit matrix, 8 of codes).  8192 x 8192 bf16, us (TB/s): to int8 per token
-// 36.5 (5.5), with gelu 57, per 128 columns 44 (4.6), with gelu 69; from int8 per 128 to 16 bits 33.6 to 35.5 (5.7 to 6.0),
-// with gelu 56; gelu' through it 66 (5.1).
+// 36.5 (5.5), with gelu 51, per 128 columns 44 (4.6), with gelu 62; from int8 per 128 to 16 bits 35 (5.7), with gelu 47.5;
+// gelu' through it 62 (5.4).
 #include "kept.h"
 
 #include "codes.cuh"
@@ -20,9 +20,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 8;      // elements a thread takes at a time
 // Blocks an SM holds and rows of a thread on their way at once, of the covering kernels.  8192 x 8192, in us: from codes to 16 bits
-// 35.5 with (8, 1), 38.2 (6, 1), 37.5 (4, 2); the gradient 68 with (5, 1), 69 (4, 2), 106 (8, 1: registers spill); to codes
-// with gelu 69 with (4, 2), 73 (8, 1), without an activation 44 and 41.
-constexpr int kToBlocks = 4, kToRows = 2, kFromBlocks = 8, kGradBlocks = 5;
+// 35 with (8, 1), 38 (6, 1), 37.5 (4, 2); the gradient 62 with (6, 1), 64 (5, 1), 69 (4, 2), 106 (8, 1: registers spill); to codes
+// per 128 without an activation and with gelu 44 and 62 with (4, 2), 43.5 and 67 (6, 1), 42 and 64 (4, 3), 46 and 62.5 (3, 3).
+constexpr int kToBlocks = 4, kToRows = 2, kFromBlocks = 8, kGradBlocks = 6;
 
 // f(activation with its form a constant): the choice is made once for all of a thread's elements.
 template <class F>
@@ -36,11 +36,41 @@ __device__ __forceinline__ void with_form(const Activation &act, F f) {
     }
 }
 
+// gelu by the tail T = Phi(-|z|) alone: z Phi(z) = max(z, 0) - |z| T, and Phi(z) + z phi(z) is u = |z| phi(z) - T above 1, or
+// -u below zero.  Two thirds of the instructions of act2, which selects T or 1 - T (8192 x 8192 bf16 to int8 per 128 69 us, so
+// 62; back 52.5 and 47.5), and eight registers fewer than act_derivative2 (65 and 62).  |z| is held where T is 0, so that an
+// infinity gives its limit; a NaN is kept out of the pair's common reciprocal and comes back by a factor.
+__device__ __forceinline__ float2 held_abs2(float2 z) { return make_float2(fminf(fabsf(z.x), kErfLimit), fminf(fabsf(z.y), kErfLimit)); }
+
+__device__ __forceinline__ float2 gelu2(float2 z) {
+    const float2 a = held_abs2(z);
+    float2 expo, top;
+    const float2 tail = normal_tail2(a, reciprocals(__ffma2_rn(a, both(kErfP), both(1.0f))), expo);
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(top.x) : "f"(z.x));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(top.y) : "f"(z.y));
+    return __ffma2_rn(make_float2(-a.x, -a.y), tail, top);
+}
+
+__device__ __forceinline__ float2 gelu_derivative2(float2 z) {
+    const float2 a = held_abs2(z);
+    float2 expo, c;
+    const float2 tail = normal_tail2(a, reciprocals(__ffma2_rn(a, both(kErfP), both(1.0f))), expo);
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(c.x) : "f"(fabsf(z.x)), "f"(kErfLimit));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(c.y) : "f"(fabsf(z.y)), "f"(kErfLimit));
+    const float2 u = __ffma2_rn(__fmul2_rn(c, both(kInvSqrt2Pi)), expo, make_float2(-tail.x, -tail.y));
+    return make_float2(z.x < 0.0f ? -u.x : 1.0f + u.x, z.y < 0.0f ? -u.y : 1.0f + u.y);
+}
+
+__device__ __forceinline__ float2 act_of(float2 z, const Activation &act) { return act.form == CASE_ERF ? gelu2(z) : act2(z, act); }
+__device__ __forceinline__ float2 derivative_of(float2 z, const Activation &act) {
+    return act.form == CASE_ERF ? gelu_derivative2(z) : act_derivative2(z, act);
+}
+
 __device__ __forceinline__ void apply_act(float (&y)[kChunk], const Activation &act) {
     with_form(act, [&](const Activation &one) {
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) {
-            const float2 v = act2(make_float2(y[e], y[e + 1]), one);
+            const float2 v = act_of(make_float2(y[e], y[e + 1]), one);
             y[e] = v.x, y[e + 1] = v.y;
         }
     });
@@ -50,7 +80,7 @@ __device__ __forceinline__ void times_derivative(float (&d)[kChunk], const float
     with_form(act, [&](const Activation &one) {
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) {
-            const float2 v = __fmul2_rn(make_float2(d[e], d[e + 1]), act_derivative2(make_float2(z[e], z[e + 1]), one));
+            const float2 v = __fmul2_rn(make_float2(d[e], d[e + 1]), derivative_of(make_float2(z[e], z[e + 1]), one));
             d[e] = v.x, d[e + 1] = v.y;
         }
     });
@@ -199,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, kGrad ? 4 : 6) from_kept_any_kernel(
             // (elements are paired with themselves: an activation works on pairs)
             for (int j = max(j0, 0); j < min(j0 + kChunk, p.h); ++j) {
                 const float z = __fmul_rn(decode8(q[j], p.qkind), scale_at<kQM>(p.scale, r, p.h, j));
-                E::store(to + j, kGrad ? E::load(from + j) * act_derivative2(both(z), act).x : act2(both(z), act).x);
+                E::store(to + j, kGrad ? E::load(from + j) * derivative_of(both(z), act).x : act_of(both(z), act).x);
             }
         }
     }
@@ -367,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) act_quant_any_kernel(const void *z, 
         with_form(act, [&](const Activation &one) {
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-                const float2 v = act2(make_float2(y[i], y[i + 1]), one);
+                const float2 v = act_of(make_float2(y[i], y[i + 1]), one);
                 y[i] = v.x, y[i + 1] = v.y;
             }
         });

@@ -107,16 +107,21 @@ __device__ __forceinline__ float2 sigmoid_form2(float2 c, const Activation &a) {
 // Functions, 7.1.26: for x >= 0, erf x = 1 - (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x),
 // to 1.5e-7; its exponential is the density's, so the derivative costs little more
 // than the value.
-__device__ __forceinline__ float2 normal_cdf2(float2 z, float2 &expo) {
-    constexpr float kP = 0.3275911f * kSqrtHalf;
-    const float2 t = reciprocals(make_float2(fmaf(fabsf(z.x), kP, 1.0f), fmaf(fabsf(z.y), kP, 1.0f)));
+// Phi(-|z|), with t = 1 / (1 + |z| kErfP), and its e^(-z^2 / 2)
+__device__ __forceinline__ float2 normal_tail2(float2 z, float2 t, float2 &expo) {
     const float2 x = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2e));
     expo = make_float2(exp2_f(x.x), exp2_f(x.y));
     float2 q = __ffma2_rn(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
     q = __ffma2_rn(q, t, both(0.5f * 1.421413741f));
     q = __ffma2_rn(q, t, both(0.5f * -0.284496736f));
     q = __ffma2_rn(q, t, both(0.5f * 0.254829592f));
-    const float2 tail = __fmul2_rn(__fmul2_rn(q, t), expo);   // Phi(-|z|)
+    return __fmul2_rn(__fmul2_rn(q, t), expo);
+}
+constexpr float kErfP = 0.3275911f * kSqrtHalf;
+
+__device__ __forceinline__ float2 normal_cdf2(float2 z, float2 &expo) {
+    const float2 t = reciprocals(make_float2(fmaf(fabsf(z.x), kErfP, 1.0f), fmaf(fabsf(z.y), kErfP, 1.0f)));
+    const float2 tail = normal_tail2(z, t, expo);
     return make_float2(z.x < 0.0f ? tail.x : 1.0f - tail.x, z.y < 0.0f ? tail.y : 1.0f - tail.y);
 }
 

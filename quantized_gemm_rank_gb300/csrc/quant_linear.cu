@@ -9,7 +9,7 @@
 // their way to the tensor cores (linear_split.cu): the weight is read once, as bytes.  The operands of many rows are
 // brought to 16 bits in the workspace, each element once, and multiplied by the GEMM of gemm_tcgen05.cuh; matrices that the
 // tensor copies cannot take go through the workspace, too.  4096 tokens, 7168 x 8192: 282 to 295 us, of which widening takes 43; the
-// weight gradient 4096 x 7168 of 8192 tokens 292 us, from gelu(z) 311 (its values 36 and 56 us), the product itself 257.
+// weight gradient 4096 x 7168 of 8192 tokens 286 us, from gelu(z) 294 to 303 (its values 36 and 44 us), the product itself 250.
 #include "kept.h"
 
 #include "codes.cuh"
