@@ -292,3 +292,29 @@ def test_more_dimensions():
         assert torch.equal(mc2.mc2_act_dequant(q, s).view(24, 256), mc2.mc2_act_dequant(q2, s2))
         assert torch.equal(mc2.mc2_act_grad_quant(z.view(2, 12, 256), q, s, activation="relu").view(24, 256),
                            mc2.mc2_act_grad_quant(z, q2, s2, activation="relu"))
+
+
+@pytest.mark.parametrize("h", [256, 259])
+@pytest.mark.parametrize("act", ACTS)
+def test_activations_of_infinite_codes_and_nans(h, act):
+    # every e5m2 code, infinities and NaN among them: each has its limit, and its neighbours are as without it
+    q = (torch.arange(h) % 256).repeat(2, 1).to(torch.uint8)
+    q[1] = q[1].roll(5)
+    q = q.view(E5M2).cuda()
+    scale = torch.ones(2, device="cuda")
+    z = q.double()
+    low, high, lost, fine = z == -torch.inf, z == torch.inf, z.isnan(), z.isfinite()
+    assert low.any() and high.any() and lost.any()
+    out = mc2.mc2_act_dequant(q, scale, activation=act, dtype=F32)
+    dz = mc2.mc2_act_grad_quant(torch.ones(2, h, dtype=F16, device="cuda"), q, scale, activation=act)
+    assert torch.equal(out.isnan(), lost) and (out[high] == torch.inf).all()
+    assert (out[low] == -torch.inf).all() if act == "none" else (out[low].abs() <= 1e-14).all()
+    known = torch.where(fine, z, 0.0)
+    bound = OWN * (1 + known.abs()) + 2.0 ** -22 * known.abs()
+    assert ((out.double() - plain_act(known, act)).abs() <= bound)[fine].all()
+    if act == "none":
+        assert (dz == 1).all()
+        return
+    assert (dz[lost] == 0).all() if act == "relu" else torch.equal(dz.isnan(), lost)
+    assert (dz[high] == 1).all() and (dz[low] == 0).all()
+    assert ((dz.double() - plain_derivative(known, act)).abs() <= 2.0 ** -11 * 1.2 + 2.0 ** -17 * (1 + known.abs()))[fine].all()
