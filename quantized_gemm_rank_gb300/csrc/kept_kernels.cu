@@ -5,7 +5,7 @@
 //   dz = dy act'(q scale)                                                                        (act_grad_quant)
 // Arithmetic is fp32; codes and outputs are rounded once.  Memory bounds all of them without an activation, issue with gelu:
 // each element is read once, eight at a time (16 bytes of a 16-bit matrix, 8 of codes).  8192 x 8192 bf16, us (TB/s): to int8 per token
-// 36.5 (5.5), with gelu 51, per 128 columns 44 (4.6), with gelu 62; from int8 per 128 to 16 bits 35 (5.7), with gelu 47.5;
+// 36.5 (5.5), with gelu 51, per 128 columns 41.4 (4.9), with gelu 62; from int8 per 128 to 16 bits 35 (5.7), with gelu 47.5;
 // gelu' through it 62 (5.4).
 #include "kept.h"
 
@@ -21,7 +21,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 8;      // elements a thread takes at a time
 // Blocks an SM holds and rows of a thread on their way at once, of the covering kernels.  8192 x 8192, in us: from codes to 16 bits
 // 35 with (8, 1), 38 (6, 1), 37.5 (4, 2); the gradient 62 with (6, 1), 64 (5, 1), 69 (4, 2), 106 (8, 1: registers spill); to codes
-// per 128 without an activation and with gelu 44 and 62 with (4, 2), 43.5 and 67 (6, 1), 42 and 64 (4, 3), 46 and 62.5 (3, 3).
+// per 128 without an activation and with gelu 44 and 62 with (4, 2), 43.5 and 67 (6, 1), 42 and 64 (4, 3), 46 and 62.5 (3, 3),
+// all of them by floats (below).
 constexpr int kToBlocks = 4, kToRows = 2, kFromBlocks = 8, kGradBlocks = 6;
 
 // f(activation with its form a constant): the choice is made once for all of a thread's elements.
@@ -318,6 +319,37 @@ __global__ void __launch_bounds__(kThreads, kToBlocks) act_quant_kernel(const vo
         for (int i = 0; i < kToRows; ++i) {
             const int64_t r = r0 + i * step;
             if (live && r < p.m) raw[i] = load_raw<kT>(static_cast<const char *>(z) + (r * ldz + j) * kE);
+        }
+        if constexpr (kT != ELEM_F32) {
+            static_assert(kToRows == 2, "a word holds the largest values of two rows");
+            if (act.form == CASE_NONE) {
+                // the largest values as 16-bit patterns without their sign (ordered like the values, a NaN above all), both
+                // rows' in one word (8192 x 8192 to int8 per 128 41.4 us, by floats 43.8; mx 39 and 42)
+                uint32_t m[kToRows] = {};
+#pragma unroll
+                for (int i = 0; i < kToRows; ++i) {
+                    if (!live || r0 + i * step >= p.m) continue;
+                    const uint4 v = raw[i].v[0];
+                    m[i] = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+                }
+                uint32_t both_tops = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+                for (int o = group / 2; o > 0; o >>= 1) both_tops = __vmaxu2(both_tops, __shfl_xor_sync(0xFFFFFFFFu, both_tops, o));
+                float2 tops;
+                if constexpr (kT == ELEM_BF16)
+                    tops = make_float2(__uint_as_float(both_tops << 16), __uint_as_float(both_tops & 0xFFFF0000u));
+                else
+                    tops = __half22float2(*reinterpret_cast<const __half2 *>(&both_tops));
+#pragma unroll
+                for (int i = 0; i < kToRows; ++i) {
+                    const int64_t r = r0 + i * step;
+                    if (!live || r >= p.m) continue;
+                    float y[kChunk];
+                    values<kT>(raw[i], y);
+                    encode_chunk<kQM>(p, y, __float_as_uint(i ? tops.y : tops.x), r * groups + (kQM == QM_TOKEN ? 0 : c / group),
+                                      (threadIdx.x & (group - 1)) == 0, r * p.h + j);
+                }
+                continue;
+            }
         }
 #pragma unroll
         for (int i = 0; i < kToRows; ++i) {

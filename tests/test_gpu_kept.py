@@ -318,3 +318,29 @@ def test_activations_of_infinite_codes_and_nans(h, act):
     assert (dz[lost] == 0).all() if act == "relu" else torch.equal(dz.isnan(), lost)
     assert (dz[high] == 1).all() and (dz[low] == 0).all()
     assert ((dz.double() - plain_derivative(known, act)).abs() <= 2.0 ** -11 * 1.2 + 2.0 ** -17 * (1 + known.abs()))[fine].all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("h", [96, 256, 264, 2048])
+@pytest.mark.parametrize("mode,kind", KINDS)
+def test_not_numbers_of_16_bits(mode, kind, h, dtype):
+    # one in a row each: its group is lost, and the rows and groups beside it are as without it
+    z = tensor(9, h, dtype, 9)
+    clean_q, clean_scale = mc2.mc2_act_quant(z, quant_mode=mode, q_dtype=kind)
+    odd = [float("nan"), float("inf"), -float("inf"), 0.0]
+    for i, v in enumerate(odd):
+        z[2 * i + 1, 37 + 9 * i] = v
+    z.view(torch.int16)[1, 38] = -1   # a NaN with its sign and every bit set
+    z[8] = 0
+    q, scale = mc2.mc2_act_quant(z, quant_mode=mode, q_dtype=kind)
+    step, clean_step = spread(scale, mode, h), spread(clean_scale, mode, h)
+    lost = torch.zeros(9, h, dtype=torch.bool, device="cuda")
+    same = torch.ones_like(lost)
+    for i, v in enumerate(odd):
+        group = torch.arange(h, device="cuda") // size_of(mode, h) == (37 + 9 * i) // size_of(mode, h)
+        same[2 * i + 1, group] = False
+        lost[2 * i + 1, group] = v != 0
+    same[8] = False
+    assert torch.equal(q.double()[same], clean_q.double()[same]) and torch.equal(step[same], clean_step[same])
+    assert not step[lost].isfinite().any() and (q.double()[lost] == 0).all() and step[~lost].isfinite().all()
+    assert (q.double()[8] == 0).all() and (step[8] <= 2.0 ** -127).all()
