@@ -1122,7 +1122,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                         const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias16) + colh + 32 * c);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint4 t = __ldg(from + j);
+                            const uint4 t = from[j];
                             const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -1429,8 +1429,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                     }
                     uint32_t pk[16];
                     if (col0 + 32 <= p.n) {
-                        // a whole chunk: its column scales and biases by 16-byte read-only
-                        // loads (16-byte aligned: col0 % 32 == 0), 8 columns at a time (with the
+                        // a whole chunk: its column scales and biases by 16-byte loads
+                        // (16-byte aligned: col0 % 32 == 0), 8 columns at a time (with the
                         // 128 running sums live, a group of 16 left too few registers)
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
@@ -1438,14 +1438,14 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                             float sc[8], bs[8];
 #pragma unroll
                             for (int q4 = 0; q4 < 2; ++q4) {
-                                const float4 t = __ldg(reinterpret_cast<const float4 *>(p.x2_scale + cg) + q4);
+                                const float4 t = reinterpret_cast<const float4 *>(p.x2_scale + cg)[q4];
                                 sc[4 * q4] = t.x;
                                 sc[4 * q4 + 1] = t.y;
                                 sc[4 * q4 + 2] = t.z;
                                 sc[4 * q4 + 3] = t.w;
                             }
                             if (p.bias_q_bf16) {
-                                const uint4 t = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias_q) + cg));
+                                const uint4 t = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias_q) + cg);
                                 const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
@@ -1455,8 +1455,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                             } else {
 #pragma unroll
                                 for (int q4 = 0; q4 < 2; ++q4) {
-                                    const float4 t =
-                                        __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias_q) + cg) + q4);
+                                    const float4 t = reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias_q) + cg)[q4];
                                     bs[4 * q4] = t.x;
                                     bs[4 * q4 + 1] = t.y;
                                     bs[4 * q4 + 2] = t.z;

@@ -78,11 +78,11 @@ __device__ __forceinline__ float weight_at(const void *w, int w_f32, int j, int 
 template <int kT>
 __device__ __forceinline__ void load_weights(const void *w, int w_f32, int c, float (&f)[Vec<kT>::kW]) {
     if (kT == ELEM_F32 || !w_f32) {
-        unpack<kT>(__ldg(static_cast<const uint4 *>(w) + c), f);
+        unpack<kT>(static_cast<const uint4 *>(w)[c], f);
     } else {
 #pragma unroll
         for (int i = 0; i < Vec<kT>::kW / 4; ++i) {
-            const float4 v = __ldg(static_cast<const float4 *>(w) + c * (Vec<kT>::kW / 4) + i);
+            const float4 v = static_cast<const float4 *>(w)[c * (Vec<kT>::kW / 4) + i];
             f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
         }
     }
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(1024) norm_grad_row_kernel(const __grid_consta
     constexpr bool kKeep = V == 1;
     const bool kept = kKeep && (kT == ELEM_F32 || !p.w_f32);
     uint4 wr = make_uint4(0, 0, 0, 0);
-    if (kept && threadIdx.x < nv) wr = __ldg(static_cast<const uint4 *>(p.w) + threadIdx.x);
+    if (kept && threadIdx.x < nv) wr = static_cast<const uint4 *>(p.w)[threadIdx.x];
     auto weights = [&](int k, float (&w)[kW]) {
         if (kept)
             unpack<kT>(wr, w);

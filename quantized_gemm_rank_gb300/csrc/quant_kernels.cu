@@ -234,7 +234,7 @@ __device__ __forceinline__ float2 mul_exact2(uint32_t x, uint32_t s) {
 
 template <bool kBF16>
 __device__ __forceinline__ uint4 smooth_vec(const uint16_t *smooth, int vi) {
-    if (smooth) return __ldg(reinterpret_cast<const uint4 *>(smooth + vi * 8));
+    if (smooth) return *reinterpret_cast<const uint4 *>(smooth + vi * 8);
     return kBF16 ? make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u)    // bf16 1.0
                  : make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);   // fp16 1.0
 }
@@ -242,13 +242,14 @@ __device__ __forceinline__ uint4 smooth_vec(const uint16_t *smooth, int vi) {
 template <bool kBF16>
 __global__ void __launch_bounds__(kPrologueThreads) a2a_prologue_kernel(
     const __grid_constant__ ChunkPtrs chunks, int h, int64_t bs_local, int rank_size,
-    const uint16_t *__restrict__ smooth, __half *__restrict__ qh, int8_t *__restrict__ q_out,
-    float *__restrict__ scale_out, const int8_t *__restrict__ x2, __half *__restrict__ x2h, int64_t x2_vecs,
+    const uint16_t *smooth, __half *__restrict__ qh, int8_t *__restrict__ q_out,
+    float *__restrict__ scale_out, const int8_t *x2, __half *__restrict__ x2h, int64_t x2_vecs,
     int64_t widen_ctas, uint16_t *__restrict__ comm_out, int *status,
     uint64_t wait_limit_ns) {
     extern __shared__ __align__(128) uint8_t prow[];   // the permuted row (K bf16/fp16), then its mbarrier
     // launched as a programmatic dependent of the stream's previous kernel:
-    // nothing in global memory is touched before that kernel has completed
+    // nothing in global memory is touched before that kernel has completed (and
+    // nothing is read by read-only loads: that kernel may write it while this one is resident)
     ptx::grid_dependency_wait();
     const int64_t b = blockIdx.x;
     const int64_t G = gridDim.x;
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kPrologueThreads) a2a_prologue_kernel(
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int64_t i = i0 + u * blockDim.x;
-                if (i < end) v[u] = __ldg(reinterpret_cast<const int4 *>(x2) + i);
+                if (i < end) v[u] = reinterpret_cast<const int4 *>(x2)[i];
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {

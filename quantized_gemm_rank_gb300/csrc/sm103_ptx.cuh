@@ -212,7 +212,9 @@ __device__ __forceinline__ void prefetch_l1(const void *p) {
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialisation may start while the previous kernel of the stream is still
 // running; grid_dependency_wait() blocks until that kernel has completed and
-// its memory operations are visible.  allow_dependent_launch() lets the next
+// its memory operations are visible.  What such a kernel reads, the previous one may
+// write during its lifetime, so it reads by ordinary loads: none through the read-only
+// path (__ldg, const pointers with __restrict__).  allow_dependent_launch() lets the next
 // kernel be launched once every CTA of this one has executed it (or exited).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_dependent_launch() {
