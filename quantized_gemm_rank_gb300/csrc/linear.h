@@ -53,7 +53,7 @@ cudaError_t launch_linear_tiles(bool bf16, const LinearParams &p, cudaStream_t s
 // products whose tiles would not fill the device.
 cudaError_t launch_linear_split(bool bf16, const LinearParams &p, int num_sms, cudaStream_t stream);
 // What the split kernel is expected to take for codes, in us; negative where it cannot sum them exactly.
-float linear_split_codes_us(const LinearParams &p, int num_sms);
+float linear_split_codes_us(const LinearParams &p);
 // Which of the two is expected to be faster for these sizes.
 bool linear_prefers_split(const LinearParams &p, int num_sms);
 

@@ -749,7 +749,10 @@ int clusters_at_once(int ctas, int num_sms) {
     if (ctas == 1) return num_sms;
     static std::atomic<int> known[64][kMaxCluster + 1];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return num_sms / ctas;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) {
+        (void)cudaGetLastError();
+        return num_sms / ctas;
+    }
     std::atomic<int> &slot = known[dev][ctas];
     int n = slot.load(std::memory_order_relaxed);
     if (n == 0) {
@@ -805,8 +808,11 @@ float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sm
 // The same for int8 codes, fitted to 2200 measurements (1 to 1024 tokens, 512 to 28672 columns, 1024 to 16384 deep): a 128-deep
 // stage is bound by what widens it; launch and set-up; the sums' way out for each wave, and another set-up for each
 // further one.  The shape that it chose took 0.6% more than the best one on average, and at most 10%.
-float split_codes_us(const SplitShape &s, const LinearParams &p, int steps, int num_sms) {
-    const int64_t clusters = clusters_at_once(s.group * s.split, num_sms);
+// Clusters that run at once are those of a GB300 (what the occupancy query says there), so that a plan, and with it the size of a
+// workspace, is the same wherever it is asked for.
+float split_codes_us(const SplitShape &s, const LinearParams &p, int steps) {
+    constexpr int kClusters[kMaxCluster + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    const int64_t clusters = kClusters[s.group * s.split];
     const float waves = static_cast<float>((s.tiles + clusters - 1) / clusters);
     const float x_rows = static_cast<float>(s.rows / s.group);
     const float stage = p.w_nk ? 0.261f + 0.0027f * x_rows : 0.331f + 0.0044f * x_rows;
@@ -836,7 +842,7 @@ SplitShape best_split(const LinearParams &p, int num_sms) {
             // but 1.7 us more for 32 tokens, 1024 x 8192, 64 CTAs
             s.per_sm = !codes && f.group == 1 && s.rows <= 32 && s.tiles > clusters_at_once(s.split, num_sms) ? 2 : 1;
             if (!fit_split(s, steps, num_sms, codes, !p.w_nk)) continue;
-            s.us = codes ? split_codes_us(s, p, steps, num_sms) : split_us(s, p, steps, num_sms);
+            s.us = codes ? split_codes_us(s, p, steps) : split_us(s, p, steps, num_sms);
             if (best.group == 0 || s.us < best.us) best = s;
         }
     }
@@ -903,8 +909,8 @@ bool linear_prefers_split(const LinearParams &p, int num_sms) {
     return s.us < us;
 }
 
-float linear_split_codes_us(const LinearParams &p, int num_sms) {
-    const SplitShape s = best_split(p, num_sms);
+float linear_split_codes_us(const LinearParams &p) {
+    const SplitShape s = best_split(p, 0);   // (asks for no number of SMs)
     return s.group == 0 ? -1.0f : s.us;
 }
 

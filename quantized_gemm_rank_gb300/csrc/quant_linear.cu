@@ -22,7 +22,7 @@ namespace mc2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSms = 152, kPairs = kSms / 2;   // of a GB300 (the plans, and so the workspace queries, ask no device)
+constexpr int kSms = 152, kPairs = kSms / 2;   // of a GB300 (the plans, and so the workspace queries, ask no device: here or in linear_split.cu)
 
 // A matrix of int8 and where it goes, in rows `pitch` apart (a multiple of 16): as fp16, or as it is.
 struct Widened {
@@ -275,7 +275,7 @@ ProductPlan plan_quant_product(const QuantProduct &p) {
                            (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 0.47e-6f;
     LinearParams l = product_of(p);
     l.x_scale = reinterpret_cast<const float *>(p.x);   // (codes; not read)
-    const float split_us = linear_split_codes_us(l, kSms);
+    const float split_us = linear_split_codes_us(l);
     at.split = split_us >= 0.0f && split_us < tiles_us;
     Pieces ws;
     const int64_t w_rows = p.w_nk ? p.n : p.k, w_cols = p.w_nk ? p.k : p.n;
