@@ -7,7 +7,7 @@
 // split over the CTAs (or CTA pairs) of a cluster, which send one another
 // their partial sums by bulk copies between shared memories and add them in rank
 // order (the result does not depend on timing).
-//   kG = 1  up to 64 tokens: a CTA takes 128 columns, M = 128
+//   kG = 1  up to 64 tokens, of int8 codes up to 128: a CTA takes 128 columns, M = 128
 //   kG = 2  more tokens: a CTA pair takes 256 columns, M = 256; each CTA loads 128
 //           columns of the weight and half the tokens, which halves what the
 //           tokens cost in L2 reads
@@ -30,8 +30,10 @@
 //
 // Int8 codes (EPI_SCALED) come as bytes, 128 deep a stage, and warps bring them to fp16 between the copies and the MMAs: the
 // weight to TMEM, from where the MMA takes its A, the tokens (and an M-major weight) to shared memory.  Blocks of 1024 stay in
-// accumulators of their own, so every sum is an exact integer, in any shape.  A stage then takes 0.26 us and 2.7 ns a
-// token of the CTA (M-major 0.33 and 4.4): 64 tokens, 4096 x 4096 9.5 us, 256 13.7, 64 tokens, 28672 x 8192 57 (4.1 TB/s).
+// accumulators of their own, so every sum is an exact integer, in any shape.  A stage then takes 0.26 us and 2.1 ns a
+// token where three teams of warps fit, 0.30 and 2.9 where two do (M-major 0.32 and 4.4): 64 tokens, 4096 x 4096 9.3 us, 256 15.2,
+// 64 tokens, 28672 x 8192 58 (4.0 TB/s).  Codes go by single CTAs: of a pair, one CTA's warps would have to tell the other's that their
+// half is widened, and an arrival that publishes to the cluster takes about a microsecond a stage (256 tokens 16.8 us).
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -249,6 +251,7 @@ __device__ __forceinline__ void finish(const SplitParams &p, const Place &at, in
 template <bool kBF16, int kEpi, int kG>
 __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) linear_split_kernel(const __grid_constant__ SplitParams p) {
     constexpr bool kCodes = kEpi == EPI_SCALED;   // int8 operands
+    static_assert(!kCodes || kG == 1, "codes by single CTAs");
     constexpr int kThreads = split_threads(kG, kCodes);
     constexpr int kStep = kCodes ? kDepth8 : kDepth;      // contraction a stage
     extern __shared__ uint8_t smem_raw[];
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
         ptx::tmem_relinquish<kG>();
     } else if (warp == 0) {
         if (lane < S) {
-            ptx::mbar_init(ptx::smem_u32(&full_bar[lane]), kCodes ? kWidenTeam * kG : 1);
+            ptx::mbar_init(ptx::smem_u32(&full_bar[lane]), kCodes ? kWidenTeam : 1);
             ptx::mbar_init(ptx::smem_u32(&empty_bar[lane]), 1);
         }
         if (kCodes && lane < p.raws) {
@@ -386,8 +389,6 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
         const uint32_t rows0 = static_cast<uint32_t>((member >> 1) * 1024 + row_in * 128);   // of the first turn, either side
         const uint32_t from0 = rows0 + (((4 * h + chunk) ^ row_in) << 4);
         const uint32_t to0 = rows0 + (((2 * chunk) ^ row_in) << 4), to1 = rows0 + (((2 * chunk + 1) ^ row_in) << 4);
-        const uint32_t full0 = ptx::smem_u32(&full_bar[0]);
-        const uint32_t ready0 = kG == 2 ? ptx::mapa(full0, crank - half) : full0;   // (the pair's first CTA counts both)
         // kTurns turns, 16 rows apart; from the fifth on `jump` further
         const auto widen = [&](const uint8_t *from, uint8_t *to, auto turns, uint32_t jump) {
             constexpr int kTurns = decltype(turns)::value;
@@ -454,10 +455,7 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
             __syncwarp();
             if (lane == 0) {
                 ptx::mbar_arrive(ptx::smem_u32(&raw_empty[rs]));
-                if (kG == 2)
-                    ptx::mbar_arrive_remote_cta(ready0 + 8u * stage);
-                else
-                    ptx::mbar_arrive(ready0 + 8u * stage);
+                ptx::mbar_arrive(ptx::smem_u32(&full_bar[stage]));
             }
             skip(p.teams);
         }
@@ -546,11 +544,11 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
                 if constexpr (kCodes) {
                     const uint32_t x_half = static_cast<uint32_t>(x_rows * 128) >> 4;
                     if (p.w_kn) {
-                        ptx::mma_four_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add);
+                        ptx::mma_four_f16_ss(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add);
                         ptx::mma_stage_f16_ss<kG>(d, w_lo + (kWBytes >> 4), w_hi, w_kk, x_lo + x_half, x_hi, x_kk, idesc, 1, bar, pair);
                     } else {
-                        ptx::mma_stage_f16_ts<kG>(d, tmem + p.a_cols + static_cast<uint32_t>((bar - to_empty - full0) * (kDepth8 / 16)), x_lo, x_hi, x_kk,
-                                                  x_half, idesc, add, bar, pair);
+                        ptx::mma_stage_f16_ts(d, tmem + p.a_cols + static_cast<uint32_t>((bar - to_empty - full0) * (kDepth8 / 16)), x_lo, x_hi, x_kk,
+                                              x_half, idesc, add, bar);
                     }
                 } else {
                     ptx::mma_stage_f16_ss<kG>(d, w_lo, w_hi, w_kk, x_lo, x_hi, x_kk, idesc, add, bar, pair);
@@ -687,7 +685,7 @@ bool fit_split(SplitShape &s, int steps, int num_sms, bool codes, bool w_kn) {
     const int block_steps = kBlockDepth / (codes ? kDepth8 : kDepth);
     const uint32_t x_rows = static_cast<uint32_t>(s.rows / s.group);
     const uint32_t stage = codes ? (kTileN + x_rows) * kDepth8 : kWBytes + x_rows * kDepth * 2;   // (of codes, as they are)
-    const uint32_t room = s.per_sm == 2 ? 110u * 1024u : 220u * 1024u;
+    const uint32_t room = s.per_sm == 2 ? 110u * 1024u : (codes ? 225u : 220u) * 1024u;
     const uint32_t sums = static_cast<uint32_t>(s.rows) * kTileN * 4;   // this CTA's, over the ring
     const uint32_t recv = static_cast<uint32_t>((s.split - 1) * ((s.rows + s.split - 1) / s.split)) * kTileN * 4;
     const int blocks = (most + block_steps - 1) / block_steps;
@@ -698,14 +696,19 @@ bool fit_split(SplitShape &s, int steps, int num_sms, bool codes, bool w_kn) {
     int columns = s.accs * s.rows, widened = 0, unit = 1;
     s.teams = 0, s.a_cols = 0;
     if (codes) {
-        // three widened stages and teams to fill them, where there is room for them beside a ring of six, or two
+        // teams and widened stages, the first of these that leave room for a ring of two stages a team.  A stage more than teams hides
+        // the MMAs of the last one: 64 tokens, 28672 x 4096 37.5 us with (3, 4), 38.4 with (3, 3), 40.6 with (2, 3); 256 of them
+        // 91.7 with (2, 3), 94.8 with (3, 3) and a ring of three, 100.9 with (2, 2).
+        const struct { int teams, widened; } forms[5] = {{3, 4}, {3, 3}, {2, 3}, {2, 2}, {1, 2}};
         const uint32_t wide = (w_kn ? 2 * kWBytes : 0u) + x_rows * kDepth8 * 2;
-        widened = 3;
         s.a_cols = (columns + 63) / 64 * 64;
-        if (3 * wide + 6 * stage > room || (!w_kn && s.a_cols + 3 * (kDepth8 / 2) > 512)) widened = 2;
+        for (const auto &f : forms) {
+            if (f.widened * wide + 2 * f.teams * stage > room || (!w_kn && s.a_cols + f.widened * (kDepth8 / 2) > 512)) continue;
+            widened = f.widened, s.teams = unit = f.teams;
+            break;
+        }
         if (!w_kn) columns = s.a_cols + widened * (kDepth8 / 2);
-        if (columns > 512) return false;
-        s.teams = unit = widened;
+        if (widened == 0 || columns > 512) return false;
         s.raw_off = widened * wide;
     } else {
         s.raw_off = 0;
@@ -720,7 +723,7 @@ bool fit_split(SplitShape &s, int steps, int num_sms, bool codes, bool w_kn) {
     // 4096 x 4096, split in two: 0.6 us less than with a shorter ring)
     int ring_stages = recv + s.raw_off < room ? static_cast<int>((room - s.raw_off - recv) / stage) : 0;
     if (codes) ring_stages = ring_stages / unit * unit;
-    s.late = ring_stages < full && s.group == 2;
+    s.late = ring_stages < full && (s.group == 2 || codes);
     if (s.late || ring_stages > full) ring_stages = full;
     if (ring_stages < unit) return false;
     const uint32_t ring = s.raw_off + ring_stages * stage;
@@ -805,32 +808,39 @@ float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sm
     return 2.1f + (s.group == 2 ? 0.17f : 0.0f) + stream + waves * join + 2.0f * (waves - 1.0f) - (s.prefetch ? fminf(0.5f, 0.1f * read) : 0.0f);
 }
 
-// The same for int8 codes, fitted to 2200 measurements (1 to 1024 tokens, 512 to 28672 columns, 1024 to 16384 deep): a 128-deep
-// stage is bound by what widens it; launch and set-up; the sums' way out for each wave, and another set-up for each
-// further one.  The shape that it chose took 0.6% more than the best one on average, and at most 10%.
-// Clusters that run at once are those of a GB300 (what the occupancy query says there), so that a plan, and with it the size of a
-// workspace, is the same wherever it is asked for.
+// The same for int8 codes, fitted to 60700 measurements (10 to 1024 tokens, 512 to 28672 columns, 1024 to 16384 deep): a 128-deep
+// stage is bound by what widens it, three teams or fewer, longer where they have no stage to spare; launch and set-up; per token of the tile
+// the way from TMEM to the output, and to the other CTAs; another set-up for each further wave.  The shape that it chose took
+// 0.4% more than the best one on average, 8% for one in a hundred, and at most 25%.  Clusters that run at once are those of a
+// GB300, so that a plan, and with it the size of a workspace, is the same wherever it is asked for: what the occupancy query says
+// there, but for clusters of 3 and 5, whose last one or two (of 46 and 28) often find no place beside the last kernel's.
 float split_codes_us(const SplitShape &s, const LinearParams &p, int steps) {
-    constexpr int kClusters[kMaxCluster + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
-    const int64_t clusters = kClusters[s.group * s.split];
+    constexpr int kClusters[kMaxCluster + 1] = {0, 152, 76, 45, 36, 26, 23, 15, 15};
+    const int64_t clusters = kClusters[s.split];
     const float waves = static_cast<float>((s.tiles + clusters - 1) / clusters);
-    const float x_rows = static_cast<float>(s.rows / s.group);
-    const float stage = p.w_nk ? 0.261f + 0.0027f * x_rows : 0.331f + 0.0044f * x_rows;
+    const float rows = static_cast<float>(s.rows);
+    float stage;
+    if (p.w_nk)
+        stage = (s.teams == 3 ? 0.258f + 0.0021f * rows : 0.302f + 0.0029f * rows) + (s.stages == s.teams ? 0.042f : 0.0f);
+    else
+        stage = s.teams > 1 ? 0.315f + 0.0044f * rows : 0.92f;
     const float stages = waves * ((steps + s.split - 1) / s.split) * stage;
-    const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 0.69f / 7.0e6f;
-    return 3.7f + (s.group == 2 ? 0.9f : 0.0f) + sqrtf(stages * stages + read * read) + waves * (0.022f * s.rows + (s.split > 1 ? 0.6f : 0.0f)) +
-           2.9f * (waves - 1.0f);
+    const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 1.08f / 7.0e6f;
+    float join = 0.0052f * rows;
+    if (s.split > 1) join += 0.0208f * rows * (s.split - 1) / s.split - 0.48f + (s.late ? 0.1f : 0.0f);
+    return 4.2f + sqrtf(stages * stages + read * read) + waves * join + 3.9f * (waves - 1.0f);
 }
 
 SplitShape best_split(const LinearParams &p, int num_sms) {
     const bool codes = p.x_scale != nullptr;
     const int steps = codes ? (p.k + kDepth8 - 1) / kDepth8 : (p.k + kDepth - 1) / kDepth;
     SplitShape best = {};
-    // tiles of at most 64 tokens by single CTAs; of 64, 128 or 256 by pairs
-    const struct { int group, most; } forms[4] = {{1, 64}, {2, 64}, {2, 128}, {2, 256}};
+    // tiles of at most 64 tokens by single CTAs; of 64, 128 or 256 by pairs, of codes of 128 by single CTAs
+    const struct { int group, most; } forms[4] = {{1, 64}, {codes ? 1 : 2, codes ? 128 : 64}, {2, 128}, {2, 256}};
     for (const auto &f : forms) {
+        if (codes && f.group == 2) break;
         if (f.group == 2 && p.m <= 32) continue;
-        if (f.group == 2 && f.most > 64 && p.m <= f.most / 2) continue;   // the smaller tile does the same
+        if (f.most > 64 && p.m <= f.most / 2) continue;   // the smaller tile does the same
         SplitShape s = {};
         s.group = f.group;
         const int unit = f.group == 1 ? 16 : 32, cols = kTileN * f.group;
@@ -948,8 +958,7 @@ cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, 
         p.raws = s.raws, p.teams = s.teams, p.raw_off = s.raw_off, p.a_cols = static_cast<uint32_t>(s.a_cols);
         const auto words = [](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 8 == 0 && ld % 4 == 0; };
         p.words = words(lp.out, lp.ldo) && (!p.aux || words(p.aux, lp.ldaux));
-        if (s.group == 1) return bf16 ? launch_split<true, EPI_SCALED, 1>(p, s, stream) : launch_split<false, EPI_SCALED, 1>(p, s, stream);
-        return bf16 ? launch_split<true, EPI_SCALED, 2>(p, s, stream) : launch_split<false, EPI_SCALED, 2>(p, s, stream);
+        return bf16 ? launch_split<true, EPI_SCALED, 1>(p, s, stream) : launch_split<false, EPI_SCALED, 1>(p, s, stream);
     }
     const bool back = lp.aux_mode == AUX_ACT_GRAD;
     if (s.group == 1) {

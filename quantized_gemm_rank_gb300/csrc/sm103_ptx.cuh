@@ -124,12 +124,6 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// The same, publishing to the arriving thread's own CTA only: for data that stay there, as the half of a pair's operand
-// that its own tensor core reads (a release to the cluster takes about a microsecond, for what it waits for).
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 // Arrive on an mbarrier of a CTA of this cluster without release semantics (the
 // caller has already consumed what it read).
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
@@ -431,115 +425,62 @@ __device__ __forceinline__ void mma_stage_f16_ss(uint32_t d_tmem, uint32_t a_lo,
             : "memory");
 }
 
-// The four MMAs alone.
-template <int kG>
+// The four MMAs alone, of one CTA.
 __device__ __forceinline__ void mma_four_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t a_step, uint32_t b_lo,
                                                 uint32_t b_hi, uint32_t b_step, uint32_t idesc, uint32_t accumulate) {
-    if constexpr (kG == 1)
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t.reg .b32 al, bl;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
-            "setp.eq.b32 p, %6, %6;\n\t"
-            "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %8;\n\t"
-            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
-            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
-            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
-            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
-            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t.reg .b32 al, bl;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
-            "setp.eq.b32 p, %6, %6;\n\t"
-            "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %8;\n\t"
-            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
-            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
-            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
-            "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
-            "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t.reg .b32 al, bl;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+        "setp.eq.b32 p, %6, %6;\n\t"
+        "add.u32 al, %1, %7;\n\tadd.u32 bl, %3, %8;\n\t"
+        "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+        "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+        "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+        "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\t"
+        "mov.b64 a, {al, %2};\n\tmov.b64 b, {bl, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step)
+        : "memory");
 }
 
 // The eight MMAs of a 128-deep stage whose A is in TMEM (eight columns a 16-deep slice) and B in two 64-deep halves, `b_half`
-// apart, and the commit that frees both.
-template <int kG>
+// apart, and the commit that frees both; of one CTA.
 __device__ __forceinline__ void mma_stage_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t b_step, uint32_t b_half,
-                                                 uint32_t idesc, uint32_t accumulate, uint32_t bar, uint16_t mask) {
-    if constexpr (kG == 1)
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t.reg .b32 al, bl, bh;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-            "mov.b32 al, %1;\n\tmov.b32 bl, %2;\n\tadd.u32 bh, %2, %7;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "setp.eq.b32 p, %5, %5;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\t"
-            "mov.b32 bl, bh;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t}" ::"r"(d_tmem),
-            "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(b_step), "r"(b_half), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t.reg .b32 al, bl, bh;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-            "mov.b32 al, %1;\n\tmov.b32 bl, %2;\n\tadd.u32 bh, %2, %7;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "setp.eq.b32 p, %5, %5;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\t"
-            "mov.b32 bl, bh;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
-            "mov.b64 b, {bl, %3};\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [al], b, %4, p;\n\t"
-            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%8], %9;\n\t}" ::"r"(d_tmem),
-            "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(b_step), "r"(b_half), "r"(bar), "h"(mask)
-            : "memory");
+                                                 uint32_t idesc, uint32_t accumulate, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t.reg .b32 al, bl, bh;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 al, %1;\n\tmov.b32 bl, %2;\n\tadd.u32 bh, %2, %7;\n\t"
+        "mov.b64 b, {bl, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+        "setp.eq.b32 p, %5, %5;\n\t"
+        "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+        "mov.b64 b, {bl, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+        "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+        "mov.b64 b, {bl, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+        "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+        "mov.b64 b, {bl, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+        "add.u32 al, al, 8;\n\t"
+        "mov.b32 bl, bh;\n\t"
+        "mov.b64 b, {bl, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+        "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+        "mov.b64 b, {bl, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+        "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+        "mov.b64 b, {bl, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+        "add.u32 al, al, 8;\n\tadd.u32 bl, bl, %6;\n\t"
+        "mov.b64 b, {bl, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], b, %4, p;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(b_step), "r"(b_half), "r"(bar)
+        : "memory");
 }
 
 // Arrive on `bar` once all previously issued tcgen05 ops of this thread
