@@ -451,22 +451,14 @@ PyObject *quant_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
         size_t need = 0, bytes = 0;
         const int8_t *xp = static_cast<int8_t *>(xr.p), *wp = static_cast<int8_t *>(wr.p);
         at::Tensor own;
-        if (!workspace(a[10], 0, x, cur, own, wk, bytes)) return irregular();
+        if (a[10] == Py_None && mc2_quant_matmul_workspace(xp, xr.ld, wp, wr.ld, nk, m, cols, k, rr.p, rr.ld, outr.p, outr.ld, &need) != MC2_OK)
+            return irregular();
+        if (!workspace(a[10], need, x, cur, own, wk, bytes)) return irregular();
         void *stream = handle(a[12]);
-        const auto call = [&] {
-            return unlocked([&] {
-                return mc2_quant_matmul(xp, xr.ld, static_cast<float *>(xs), wp, wr.ld, nk, static_cast<float *>(ws), m, cols, k, bp,
-                                        bias_type, act, rr.p, rr.ld, dtype_code(dt), outr.p, outr.ld, wk, bytes, stream);
-            });
-        };
-        // (few tokens need no workspace: how much others do is asked once it was missing)
-        int st = call();
-        if (st == MC2_ERR_WORKSPACE && a[10] == Py_None) {
-            if (mc2_quant_matmul_workspace(xp, xr.ld, wp, wr.ld, nk, m, cols, k, rr.p, rr.ld, outr.p, outr.ld, &need) != MC2_OK ||
-                !workspace(a[10], need, x, cur, own, wk, bytes))
-                return irregular();
-            st = call();
-        }
+        const int st = unlocked([&] {
+            return mc2_quant_matmul(xp, xr.ld, static_cast<float *>(xs), wp, wr.ld, nk, static_cast<float *>(ws), m, cols, k, bp, bias_type,
+                                    act, rr.p, rr.ld, dtype_code(dt), outr.p, outr.ld, wk, bytes, stream);
+        });
         return st != MC2_OK ? PyLong_FromLong(st) : out.take();
     });
 }

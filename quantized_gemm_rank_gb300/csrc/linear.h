@@ -25,6 +25,7 @@ struct LinearParams {
     int aux_mode;   // AuxMode
     // a product of int8 codes: out, aux and a 16-bit bias of the given type, z = float(acc) x_scale w_scale + bias.  The split
     // kernel takes x and w as they are (16-byte aligned, strides a multiple of 16; out and aux of any layout), the tiles as fp16
+    int codes;
     const float *x_scale, *w_scale;   // (m), (n)
     int bias_f32;
 };

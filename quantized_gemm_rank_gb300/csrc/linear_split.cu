@@ -831,8 +831,8 @@ float split_codes_us(const SplitShape &s, const LinearParams &p, int steps) {
     return 4.2f + sqrtf(stages * stages + read * read) + waves * join + 3.9f * (waves - 1.0f);
 }
 
-SplitShape best_split(const LinearParams &p, int num_sms) {
-    const bool codes = p.x_scale != nullptr;
+SplitShape search_split(const LinearParams &p, int num_sms) {
+    const bool codes = p.codes != 0;
     const int steps = codes ? (p.k + kDepth8 - 1) / kDepth8 : (p.k + kDepth - 1) / kDepth;
     SplitShape best = {};
     // tiles of at most 64 tokens by single CTAs; of 64, 128 or 256 by pairs, of codes of 128 by single CTAs
@@ -857,6 +857,15 @@ SplitShape best_split(const LinearParams &p, int num_sms) {
         }
     }
     return best;
+}
+
+// The shape for p.  A product of codes asks for it as its workspace is asked for, as it is planned and as it is launched, so a host
+// thread keeps the last one of these (it goes by the sizes alone; a search takes 1 us).
+SplitShape best_split(const LinearParams &p, int num_sms) {
+    if (!p.codes) return search_split(p, num_sms);
+    thread_local struct { int m, n, k, w_nk; SplitShape shape; } last = {};
+    if (last.m != p.m || last.n != p.n || last.k != p.k || last.w_nk != p.w_nk) last = {p.m, p.n, p.k, p.w_nk, search_split(p, num_sms)};
+    return last.shape;
 }
 
 template <bool kBF16, int kEpi, int kG>
@@ -930,19 +939,19 @@ cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, 
     SplitParams p = {};
     const uint64_t m = lp.m, n = lp.n, k = lp.k;
     bool ok;
-    if (lp.x_scale)
+    if (lp.codes)
         ok = host::make_map8(&p.x_map, lp.x, k, m, static_cast<uint32_t>(s.rows / s.group), lp.ldx) &&
              host::make_map8(&p.w_map, lp.w, lp.w_nk ? k : n, lp.w_nk ? n : k, 128, lp.ldw);
     else
         ok = host::make_map16(&p.x_map, lp.x, k, m, kDepth, static_cast<uint32_t>(s.rows / s.group), lp.ldx);
-    if (!lp.x_scale)
+    if (!lp.codes)
         ok = ok && (lp.w_nk ? host::make_map16(&p.w_map, lp.w, k, n, kDepth, kTileN, lp.ldw)
                             : host::make_map16(&p.w_map, lp.w, n, k, 64, kDepth, lp.ldw));
     if (!ok) return cudaErrorInvalidValue;
     p.bias = lp.bias, p.aux = lp.aux_mode == AUX_NONE ? nullptr : lp.aux, p.out = lp.out, p.preact = lp.preact;
     p.ldaux = lp.ldaux, p.ldo = lp.ldo, p.ldp = lp.ldp;
     p.m = lp.m, p.n = lp.n;
-    const int steps = lp.x_scale ? (lp.k + kDepth8 - 1) / kDepth8 : (lp.k + kDepth - 1) / kDepth;
+    const int steps = lp.codes ? (lp.k + kDepth8 - 1) / kDepth8 : (lp.k + kDepth - 1) / kDepth;
     p.steps = steps / s.split, p.more = steps % s.split;
     p.share = ((lp.m < s.rows ? lp.m : s.rows) + s.split - 1) / s.split;
     p.m_tiles_inv = UINT64_MAX / static_cast<uint64_t>(s.m_tiles) + 1;   // (0 for one tile: not used)
@@ -953,7 +962,7 @@ cudaError_t launch_linear_split(bool bf16, const LinearParams &lp, int num_sms, 
     p.act = activation_of(lp.act);
     p.status = device_status_word();
     p.wait_limit_ns = host::kWaitLimitNs;
-    if (lp.x_scale) {
+    if (lp.codes) {
         p.x_scale = lp.x_scale, p.w_scale = lp.w_scale, p.bias_f32 = lp.bias_f32;
         p.raws = s.raws, p.teams = s.teams, p.raw_off = s.raw_off, p.a_cols = static_cast<uint32_t>(s.a_cols);
         const auto words = [](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 8 == 0 && ld % 4 == 0; };

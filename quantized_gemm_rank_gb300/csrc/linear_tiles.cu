@@ -79,7 +79,7 @@ cudaError_t launch_linear_tiles(bool bf16, const LinearParams &lp, cudaStream_t 
     p.act = activation_of(lp.act);
     p.wait_limit_ns = host::kWaitLimitNs;
     p.status = device_status_word();
-    if (lp.x_scale) {
+    if (lp.codes) {
         p.kblock_tiles = 1024 / kBK;   // (an fp32 accumulator holds the sum of 1024 products of two int8 exactly)
         p.x1_scale = lp.x_scale, p.x2_scale = lp.w_scale;
         if (lp.bias_f32)

@@ -207,7 +207,7 @@ LinearParams product_of(const QuantProduct &p) {
     l.act = p.act;
     l.bias = p.bias, l.bias_f32 = p.bias_f32;
     l.aux_mode = p.residual ? AUX_RESIDUAL : AUX_NONE;
-    l.x_scale = p.x_scale, l.w_scale = p.w_scale;
+    l.codes = 1, l.x_scale = p.x_scale, l.w_scale = p.w_scale;
     return l;
 }
 
@@ -273,9 +273,7 @@ ProductPlan plan_quant_product(const QuantProduct &p) {
     const float steps = static_cast<float>((p.k + 63) / 64);
     const float tiles_us = 9.4f + static_cast<float>((tiles + kPairs - 1) / kPairs) * (3.2f + 0.2475f * steps) +
                            (static_cast<float>(p.m) + static_cast<float>(p.n)) * static_cast<float>(p.k) * 0.47e-6f;
-    LinearParams l = product_of(p);
-    l.x_scale = reinterpret_cast<const float *>(p.x);   // (codes; not read)
-    const float split_us = linear_split_codes_us(l);
+    const float split_us = linear_split_codes_us(product_of(p));
     at.split = split_us >= 0.0f && split_us < tiles_us;
     Pieces ws;
     const int64_t w_rows = p.w_nk ? p.n : p.k, w_cols = p.w_nk ? p.k : p.n;
