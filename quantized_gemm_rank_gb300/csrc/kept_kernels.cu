@@ -6,7 +6,8 @@
 // Arithmetic is fp32; codes and outputs are rounded once.  Memory bounds all of them without an activation, issue with gelu:
 // each element is read once, eight at a time (16 bytes of a 16-bit matrix, 8 of codes).  8192 x 8192 bf16, us (TB/s): to int8 per token
 // 36.5 (5.5), with gelu 51, per 128 columns 41.4 (4.9), with gelu 62; from int8 per 128 to 16 bits 35 (5.7), with gelu 47.5;
-// gelu' through it 62 (5.4).
+// gelu' through it 62 (5.4).  fp32 to int8 per token 50 (6.7), per 128 columns 55.5; from int8 per 128 to fp32 75 (4.5), with silu 84,
+// with gelu 143: an output of 32 bits is made with CUDA's own functions.
 #include "kept.h"
 
 #include "codes.cuh"
@@ -67,11 +68,29 @@ __device__ __forceinline__ float2 derivative_of(float2 z, const Activation &act)
     return act.form == CASE_ERF ? gelu_derivative2(z) : act_derivative2(z, act);
 }
 
+// The same for an output of 32 bits, by CUDA's own functions: erf's absolute 1.5e-7 above is 5e-4 of gelu(-4) and 1% of gelu(-8), the
+// rounded argument of 2^x above 2e-6 of silu(-40) (8192 x 8192 with gelu 143 us, with those 68).  z is held where the value is below
+// fp32's range.
+__device__ __forceinline__ float act32(float z, const Activation &act) {
+    constexpr float kLeast = -104.0f;   // e^-104 is below fp32's range
+    const float c = hold(z, act.form == CASE_ERF ? -kErfLimit - 1.0f : kLeast, __int_as_float(0x7F800000));
+    if (act.form == CASE_ERF) return c * normcdff(c);
+    const float w = fminf(c, -kLeast), e = expf(-fabsf(w * fmaf(w * w, act.c2, act.c1)));
+    return c * ((w < 0.0f ? e : 1.0f) / (1.0f + e));
+}
+template <int kT>
+__device__ __forceinline__ float2 value_of(float2 z, const Activation &act) {
+    if (kT == ELEM_F32 && (act.form == CASE_ERF || act.form == CASE_SIGMOID)) return make_float2(act32(z.x, act), act32(z.y, act));
+    return act_of(z, act);
+}
+
+// kT: the type of what becomes of it
+template <int kT>
 __device__ __forceinline__ void apply_act(float (&y)[kChunk], const Activation &act) {
     with_form(act, [&](const Activation &one) {
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) {
-            const float2 v = act_of(make_float2(y[e], y[e + 1]), one);
+            const float2 v = value_of<kT>(make_float2(y[e], y[e + 1]), one);
             y[e] = v.x, y[e + 1] = v.y;
         }
     });
@@ -167,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, kGrad ? kGradBlocks : kFromBlocks) f
             times_derivative(g, z, act);
             store_values<kT>(to, g);
         } else {
-            apply_act(z, act);
+            apply_act<kT>(z, act);
             store_values<kT>(to, z);
         }
     }
@@ -223,14 +242,14 @@ __global__ void __launch_bounds__(kThreads, kGrad ? 4 : 6) from_kept_any_kernel(
                 times_derivative(g, z, act);
                 store_values<kT>(to + j0, g);
             } else {
-                apply_act(z, act);
+                apply_act<kT>(z, act);
                 store_values<kT>(to + j0, z);
             }
         } else {
             // (elements are paired with themselves: an activation works on pairs)
             for (int j = max(j0, 0); j < min(j0 + kChunk, p.h); ++j) {
                 const float z = __fmul_rn(decode8(q[j], p.qkind), scale_at<kQM>(p.scale, r, p.h, j));
-                E::store(to + j, kGrad ? E::load(from + j) * derivative_of(both(z), act).x : act_of(both(z), act).x);
+                E::store(to + j, kGrad ? E::load(from + j) * derivative_of(both(z), act).x : value_of<kT>(both(z), act).x);
             }
         }
     }
@@ -358,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, kToBlocks) act_quant_kernel(const vo
             float y[kChunk];
             if (here) {
                 values<kT>(raw[i], y);
-                apply_act(y, act);
+                apply_act<ELEM_BF16>(y, act);   // (codes have fewer bits)
             } else {
 #pragma unroll
                 for (int e = 0; e < kChunk; ++e) y[e] = 0.0f;
@@ -396,7 +415,7 @@ __global__ void __launch_bounds__(kWarpRow ? kThreads : 1024) act_quant_row_kern
     for (int i = 0; i < V; ++i) {
         if (mine + i * T < chunks) {
             values<kT>(raw[i], y[i]);
-            apply_act(y[i], act);
+            apply_act<ELEM_BF16>(y[i], act);   // (codes have fewer bits)
             top = max(top, largest_of(y[i]));
         }
     }
