@@ -533,7 +533,8 @@ int mc2_act_grad_quant(const void *dy, int64_t lddy, const void *q, const void *
  *   dw[i, j] = sum_t dy[t, i] * act(q[t, j] * scale)       (n, k)
  *   db[i]    = sum_t dy[t, i]                              (n)
  *
- *   act(q * scale) is rounded to dtype, the tensor cores' operand type (MC2_F16: beyond 65504 to infinity); sums are
+ *   act(q * scale) is rounded to dtype, the tensor cores' operand type (MC2_F16: beyond 65504 to infinity, below 6.1e-5 to
+ *   fewer bits and below 3e-8 to zero); sums are
  *   fp32, and dw and db rounded once.  Calls of the same sizes, types, strides and alignment add in the same order
  *   and give the same bits.
  *
