@@ -391,6 +391,14 @@ __device__ __forceinline__ int next_shown(const GemmParams &p, int kt_begin, int
     return kt_begin + (ahead < 0 ? ahead + num_n : ahead);
 }
 
+// The integer path's column scales and biases.  The call's first kernel, whose end this one waits for, began to run once every kernel
+// before it had ended, and this one began after that: nobody writes them while it is resident, so they may come by the read-only
+// path, which lets the loads move ahead of the sums' (a2a-dyn 197.3 us, 199.3 by ordinary loads).
+template <class T>
+__device__ __forceinline__ T load_settled(const T *p) {
+    return __ldg(p);
+}
+
 // Store 32 consecutive 16-bit outputs (columns col0 .. col0+31) of the row that
 // starts at row_ptr, masked at n.
 __device__ __forceinline__ void store_row32_16(uint16_t *row_ptr, int n, int col0, const uint32_t (&pk)[16]) {
@@ -1438,14 +1446,14 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                             float sc[8], bs[8];
 #pragma unroll
                             for (int q4 = 0; q4 < 2; ++q4) {
-                                const float4 t = reinterpret_cast<const float4 *>(p.x2_scale + cg)[q4];
+                                const float4 t = load_settled(reinterpret_cast<const float4 *>(p.x2_scale + cg) + q4);
                                 sc[4 * q4] = t.x;
                                 sc[4 * q4 + 1] = t.y;
                                 sc[4 * q4 + 2] = t.z;
                                 sc[4 * q4 + 3] = t.w;
                             }
                             if (p.bias_q_bf16) {
-                                const uint4 t = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias_q) + cg);
+                                const uint4 t = load_settled(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias_q) + cg));
                                 const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
@@ -1455,7 +1463,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) mc2_gemm_kernel(const __grid_c
                             } else {
 #pragma unroll
                                 for (int q4 = 0; q4 < 2; ++q4) {
-                                    const float4 t = reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias_q) + cg)[q4];
+                                    const float4 t = load_settled(reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias_q) + cg) + q4);
                                     bs[4 * q4] = t.x;
                                     bs[4 * q4 + 1] = t.y;
                                     bs[4 * q4 + 2] = t.z;

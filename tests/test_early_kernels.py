@@ -1,5 +1,6 @@
 """Kernels that may begin before the stream's previous kernel ends read nothing through the read-only path: what they
-read, that kernel may write while they are resident, and read-only loads are for data that nobody writes meanwhile."""
+read, that kernel may write while they are resident, and read-only loads are for data that nobody writes meanwhile.
+(load_settled is for what the call's own first kernel has already waited for.)"""
 import glob
 import os
 import re
@@ -52,7 +53,7 @@ def test_no_read_only_loads():
         words = set(re.findall(r"\w+", text))
         todo += [d for d in parts if d[0] in words and "__global__" not in d[1] and id(d[1]) not in reached]
     assert any(n == "load_weights" for n, _ in reached.values())
-    bad = sorted({n for n, t in reached.values() if READ_ONLY.search(t)})
+    bad = sorted({n for n, t in reached.values() if READ_ONLY.search(t) and n != "load_settled"})
     assert not bad, f"read-only loads in {bad}"
 
 
