@@ -30,8 +30,8 @@
 //
 // Int8 codes (EPI_SCALED) come as bytes, 128 deep a stage, and warps bring them to fp16 between the copies and the MMAs: the
 // weight to TMEM, from where the MMA takes its A, the tokens (and an M-major weight) to shared memory.  Blocks of 1024 stay in
-// accumulators of their own, so every sum is an exact integer, in any shape.  A stage then takes 0.26 us and 2.1 ns a
-// token where three teams of warps fit, 0.30 and 2.9 where two do (M-major 0.32 and 4.4): 64 tokens, 4096 x 4096 9.3 us, 256 15.2,
+// accumulators of their own, so every sum is an exact integer, in any shape.  A stage then takes 0.24 us and 2.4 ns a
+// token where three teams of warps fit, 0.26 and 2.8 where two do (M-major 0.31 and 4.5): 64 tokens, 4096 x 4096 9.4 us, 256 15.5,
 // 64 tokens, 28672 x 8192 58 (4.0 TB/s).  Codes go by single CTAs: of a pair, one CTA's warps would have to tell the other's that their
 // half is widened, and an arrival that publishes to the cluster takes about a microsecond a stage (256 tokens 16.8 us).
 #include <atomic>
@@ -577,9 +577,15 @@ __global__ void __launch_bounds__(split_threads(kG, kEpi == EPI_SCALED), 1) line
     __syncthreads();
     bool ok = failed == 0;
     if (kG == 1 && ctas > 1) ptx::cluster_wait();
+    // Others' sums are about to be copied over the ring.  What was there of 16-bit operands only copies and MMAs wrote and read, and their ends
+    // have been waited for; codes were widened by this CTA's warps, whose loads and stores the arrival publishes (0.5 us).
     if (p.late) {
-        ptx::cluster_arrive_relaxed();
-        ptx::cluster_wait();
+        if constexpr (kCodes) {
+            ptx::cluster_sync();
+        } else {
+            ptx::cluster_arrive_relaxed();
+            ptx::cluster_wait();
+        }
     }
     float *part = reinterpret_cast<float *>(smem);   // [rows][128], over the ring
     // The sums leave TMEM a chunk of tokens at a time, four warps (one for each 32 columns) at a
@@ -698,12 +704,16 @@ bool fit_split(SplitShape &s, int steps, int num_sms, bool codes, bool w_kn) {
     if (codes) {
         // teams and widened stages, the first of these that leave room for a ring of two stages a team.  A stage more than teams hides
         // the MMAs of the last one: 64 tokens, 28672 x 4096 37.5 us with (3, 4), 38.4 with (3, 3), 40.6 with (2, 3); 256 of them
-        // 91.7 with (2, 3), 94.8 with (3, 3) and a ring of three, 100.9 with (2, 2).
+        // 91.7 with (2, 3), 94.8 with (3, 3) and a ring of three, 100.9 with (2, 2).  Not beside three where the others' sums then
+        // have no room beside the ring and would without it (64 tokens, 4096 x 4096 9.4 us with (3, 3), 9.7 with (3, 4); 256 of them 15.5
+        // with (2, 3), 16.9 with (2, 2) all the same).
         const struct { int teams, widened; } forms[5] = {{3, 4}, {3, 3}, {2, 3}, {2, 2}, {1, 2}};
         const uint32_t wide = (w_kn ? 2 * kWBytes : 0u) + x_rows * kDepth8 * 2;
         s.a_cols = (columns + 63) / 64 * 64;
         for (const auto &f : forms) {
-            if (f.widened * wide + 2 * f.teams * stage > room || (!w_kn && s.a_cols + f.widened * (kDepth8 / 2) > 512)) continue;
+            const uint32_t need = f.widened * wide + 2 * f.teams * stage;
+            if (need > room || (!w_kn && s.a_cols + f.widened * (kDepth8 / 2) > 512)) continue;
+            if (f.teams == 3 && f.widened > 3 && need + recv > room && need - wide + recv <= room) continue;
             widened = f.widened, s.teams = unit = f.teams;
             break;
         }
@@ -810,7 +820,7 @@ float split_us(const SplitShape &s, const LinearParams &p, int steps, int num_sm
 
 // The same for int8 codes, fitted to 60700 measurements (10 to 1024 tokens, 512 to 28672 columns, 1024 to 16384 deep): a 128-deep
 // stage is bound by what widens it, three teams or fewer, longer where they have no stage to spare; launch and set-up; per token of the tile
-// the way from TMEM to the output, and to the other CTAs; another set-up for each further wave.  The shape that it chose took
+// the way from TMEM to the output, and to the other CTAs, longer where the sums wait for the ring; another set-up for each further wave.  The shape that it chose took
 // 0.4% more than the best one on average, 8% for one in a hundred, and at most 25%.  Clusters that run at once are those of a
 // GB300, so that a plan, and with it the size of a workspace, is the same wherever it is asked for: what the occupancy query says
 // there, but for clusters of 3 and 5, whose last one or two (of 46 and 28) often find no place beside the last kernel's.
@@ -819,15 +829,17 @@ float split_codes_us(const SplitShape &s, const LinearParams &p, int steps) {
     const int64_t clusters = kClusters[s.split];
     const float waves = static_cast<float>((s.tiles + clusters - 1) / clusters);
     const float rows = static_cast<float>(s.rows);
-    float stage;
-    if (p.w_nk)
-        stage = (s.teams == 3 ? 0.258f + 0.0021f * rows : 0.302f + 0.0029f * rows) + (s.stages == s.teams ? 0.042f : 0.0f);
-    else
-        stage = s.teams > 1 ? 0.315f + 0.0044f * rows : 0.92f;
+    float stage, join = 0.0044f * rows;
+    if (p.w_nk) {
+        stage = s.teams == 3 ? 0.244f + 0.0024f * rows : 0.263f + 0.0028f * rows;
+        if (s.stages == s.teams) stage += s.teams == 3 ? 0.014f : 0.074f;
+        if (s.teams < 3) join += 0.23f;
+    } else {
+        stage = s.teams > 1 ? 0.309f + 0.0045f * rows : 0.92f;
+    }
     const float stages = waves * ((steps + s.split - 1) / s.split) * stage;
-    const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 1.08f / 7.0e6f;
-    float join = 0.0052f * rows;
-    if (s.split > 1) join += 0.0208f * rows * (s.split - 1) / s.split - 0.48f + (s.late ? 0.1f : 0.0f);
+    const float read = static_cast<float>(p.n) * static_cast<float>(p.k) * 1.09f / 7.0e6f;
+    if (s.split > 1) join += 0.0203f * rows * (s.split - 1) / s.split - 0.46f + (s.late ? 0.6f : 0.0f);
     return 4.2f + sqrtf(stages * stages + read * read) + waves * join + 3.9f * (waves - 1.0f);
 }
 

@@ -268,7 +268,7 @@ ProductPlan plan_quant_product(const QuantProduct &p) {
     if (at.tokens) return at;
     // Which kernel, by the sizes alone: the tiles take 9.4 us, 3.2 and 0.25 a 64-deep stage for each wave of them, and widening three
     // bytes a code at 6400 a ns (1024 tokens, 8192 x 4096 65 us; 2048 and 4096 tokens, 4096 x 4096 59.5 and 102).  Where the two
-    // cross, with k = 4096: 512 tokens, n = 4096 29 us split, 37 in tiles; 1024 tokens, n = 8192 65 in tiles.
+    // cross, with k = 4096: 512 tokens, n = 4096 30.5 us split, 37 in tiles; 1024 tokens, n = 8192 65 in tiles.
     const int64_t tiles = ((p.m + 255ll) / 256) * ((p.n + 255ll) / 256);
     const float steps = static_cast<float>((p.k + 63) / 64);
     const float tiles_us = 9.4f + static_cast<float>((tiles + kPairs - 1) / kPairs) * (3.2f + 0.2475f * steps) +
