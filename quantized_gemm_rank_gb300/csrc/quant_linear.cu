@@ -262,8 +262,8 @@ WeightPlan plan_weight_grad(const QuantWeightGrad &p) {
 
 ProductPlan plan_quant_product(const QuantProduct &p) {
     ProductPlan at;
-    // one to four tokens (4096 x 4096: 3.8, 4.7 and 6.8 us for 1, 2 and 4, 7.7 to 7.9 in the kernel of few); to eight where the
-    // weight is small (1024 x 8192 4.5 against 6.6, 4096 x 4096 8.3 against 7.8)
+    // one to four tokens (4096 x 4096: 4.3, 4.6 and 7.9 us for 1, 2 and 4, 7.9 in the kernel of few; 28672 x 8192 42.9, 43.9 and 55, there
+    // 49.5, but here a weight of any alignment is read as it is); to eight where the weight is small (1024 x 8192 5.5 against 6.7)
     at.tokens = p.w_nk && (p.m <= 4 || (p.m <= 8 && static_cast<int64_t>(p.n) * p.k <= 8ll << 20));
     if (at.tokens) return at;
     // Which kernel, by the sizes alone: the tiles take 9.4 us, 3.2 and 0.25 a 64-deep stage for each wave of them, and widening three

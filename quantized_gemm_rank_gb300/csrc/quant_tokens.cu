@@ -4,8 +4,8 @@
 //
 // Reading the weight once bounds it, so there is nothing between memory and the sums: a lane takes 16 codes of each of
 // four rows of the weight at a time, and the same 16 of every token (from L1), and adds their products four at a time
-// (dp4a, exact int32).  One token, 4096 x 4096: 3.8 us, 28672 x 4096 18.8 (6.2 TB/s).  The tensor cores need the codes widened
-// and an accumulator's way back: 7.7 us for 4096 x 4096 in linear_split.cu.  Rows share a block by slices of the depth, joined through shared memory.
+// (dp4a, exact int32).  One token, 4096 x 4096: 4.3 us, 28672 x 4096 22.6 (5.2 TB/s), 28672 x 8192 42 to 43 (5.5), weights by turns that L2 does
+// not hold.  The tensor cores need the codes widened and an accumulator's way back: 7.9 us for 4096 x 4096 in linear_split.cu.  Rows share a block by slices of the depth, joined through shared memory.
 #include "kept.h"
 
 #include "codes.cuh"
